@@ -82,6 +82,9 @@ long long layout_copy_max_rows(int d, int elem_bytes);
 constexpr size_t kNoAllocScratchBytes = static_cast<size_t>(128) << 20;
 void* noalloc_scratch();
 
+// Address of the device status word on the current device (null on failure).
+int* status_word();
+
 // Test-only failure injection behind dit_test_inject_stall.
 void set_stall_injection(int enable, long long wait_limit_cycles);
 

@@ -8,6 +8,7 @@ every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -24,7 +25,9 @@ EXPORTED_SYMBOLS = ("dit_attn_fwd", "dit_attn_fwd_strided", "dit_attn_chunk_fwd"
                     "dit_attn_stale_kv_fwd", "dit_attn_chunk_fwd_splitkv",
                     "dit_attn_splitkv_workspace_bytes", "dit_attn_splitkv_suggest",
                     "dit_attn_chunk_fwd_splitkv_noalloc",
-                    "dit_attn_check", "dit_test_inject_stall", "dit_test_set_grid_limit",
+                    "dit_paged_plan", "dit_paged_kv_write", "dit_paged_attn_fwd",
+                    "dit_paged_attn_workspace_bytes", "dit_paged_select",
+                    "dit_paged_select_workspace_bytes", "dit_attn_check", "dit_test_inject_stall", "dit_test_set_grid_limit",
                     "dit_status_string", "dit_version")
 
 
@@ -84,6 +87,20 @@ def lib() -> ctypes.CDLL:
         L.dit_attn_chunk_fwd_accumulate.argtypes = [P, P, P, P, P, I, I, I, I, I, LL, F, P]
         L.dit_attn_lse_merge.restype = I
         L.dit_attn_lse_merge.argtypes = [P, P, I, P, P, I, I, I, I, I, I, P]
+        L.dit_paged_plan.restype = I
+        L.dit_paged_plan.argtypes = [P, P, P, LL, P, P, P, P, P, P, I, I, I, I, I, I, P]
+        L.dit_paged_kv_write.restype = I
+        L.dit_paged_kv_write.argtypes = [P, SP, P, SP, P, P, SP, P, SP, P, I, I, I, I, I, P]
+        L.dit_paged_attn_fwd.restype = I
+        L.dit_paged_attn_fwd.argtypes = [P, SP, P, SP, P, SP, P, LL, P, P, I, P, P, I, I, I, I, I, I,
+                                         I, F, I, P, ctypes.c_size_t, P]
+        L.dit_paged_attn_workspace_bytes.restype = ctypes.c_size_t
+        L.dit_paged_attn_workspace_bytes.argtypes = [I, I, I, I]
+        L.dit_paged_select.restype = I
+        L.dit_paged_select.argtypes = [P, SP, P, P, LL, P, P, I, I, I, I, I, I, I, I, P,
+                                       ctypes.c_size_t, P]
+        L.dit_paged_select_workspace_bytes.restype = ctypes.c_size_t
+        L.dit_paged_select_workspace_bytes.argtypes = [I, I, I]
         L.dit_attn_check.restype = I
         L.dit_attn_check.argtypes = [P]
         L.dit_test_inject_stall.restype = None
@@ -700,3 +717,198 @@ def attention(q, k, v, scale=None, chunks=None, out_dtype=torch.float32,
         out, lse = chunk_attention(q, k, v, chunks, scale=scale, out_dtype=out_dtype,
                                    partial_dtype=partial_dtype)
     return out, lse
+
+
+# ------------------------------------------------------------------ paged key/value caches
+# One step of a batch of requests whose keys and values live in pages of one pool:
+#   lens, n_free, cu, slots = paged_plan(...)         pages and slots for the step's tokens
+#   paged_kv_write(k, v, slots, k_cache, v_cache, summary)
+#   selected = paged_select(q, summary, table, lens, ...)        (sparse attention only)
+#   out, lse = paged_attn_fwd(q, k_cache, v_cache, table, lens, selected=selected)
+# k_cache and v_cache are [n_pages, H_kv, page_size, D] views (a token-major cache
+# [n_pages, page_size, H_kv, D] is passed as x.transpose(1, 2)); block_table is int32
+# [B, max_pages], seq_lens int32 [B].
+
+
+def _launch_context(device, stream):
+    """The context a paged call allocates and launches in: `stream` becomes the current stream, so
+    that what the call allocates belongs to the stream that uses it."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _check_tensor(t, name, dtype, shape, device=None, contiguous=True):
+    """`t` is a CUDA tensor (on `device`) of `dtype` and `shape` (None: any extent)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(e is not None and e != x for e, x in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not contiguous and t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return t
+
+
+def _check_paged(k_cache, v_cache, device):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check_tensor(t, name, torch.bfloat16, (None,) * 4, device, contiguous=False)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape [n_pages, H_kv, page_size, D]")
+    return k_cache.shape
+
+
+def _check_table(block_table, seq_lens, B, device):
+    """(max_pages, table_stride) of the batch's block table."""
+    _check_tensor(seq_lens, "seq_lens", torch.int32, (B,), device)
+    _check_tensor(block_table, "block_table", torch.int32, (B, None), device, contiguous=False)
+    return block_table.shape[1], (block_table.stride(0) if B > 1 else block_table.shape[1])
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous() \
+            or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be a contiguous buffer of at least {need} bytes on {device}")
+    return workspace
+
+
+def paged_plan(new_lens, seq_lens, block_table, free_pages, n_free, page_size, n_pages, max_tokens,
+               seq_lens_out=None, n_free_out=None, cu_new=None, slots=None, stream=None):
+    """dit_paged_plan: grants the pages that new_lens [B] more tokens of each request need (from the
+    top of the stack free_pages[:n_free], into block_table in place) and maps the step's tokens
+    (packed in request order, at most max_tokens) to their slots.  All int32 but slots (int64).
+
+    Returns (seq_lens_out [B], n_free_out [1], cu_new [B + 1], slots [max_tokens]); seq_lens_out may
+    be seq_lens and n_free_out may be n_free (updated in place)."""
+    _check_tensor(new_lens, "new_lens", torch.int32, (None,))
+    dev, B = new_lens.device, new_lens.shape[0]
+    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    _check_tensor(free_pages, "free_pages", torch.int32, (None,), dev)
+    _check_tensor(n_free, "n_free", torch.int32, (1,), dev)
+    max_tokens = int(max_tokens)
+    for t, name, dt, n in ((seq_lens_out, "seq_lens_out", torch.int32, B),
+                           (n_free_out, "n_free_out", torch.int32, 1),
+                           (cu_new, "cu_new", torch.int32, B + 1),
+                           (slots, "slots", torch.int64, max_tokens)):
+        if t is not None:
+            _check_tensor(t, name, dt, (n,), dev)
+    with _launch_context(dev, stream):
+        if seq_lens_out is None:
+            seq_lens_out = torch.empty(B, dtype=torch.int32, device=dev)
+        if n_free_out is None:
+            n_free_out = torch.empty(1, dtype=torch.int32, device=dev)
+        if cu_new is None:
+            cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty(max(0, max_tokens), dtype=torch.int64, device=dev)
+        st = lib().dit_paged_plan(new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                                  stride, free_pages.data_ptr(), n_free.data_ptr(),
+                                  seq_lens_out.data_ptr(), n_free_out.data_ptr(), cu_new.data_ptr(),
+                                  slots.data_ptr(), B, max_pages, int(page_size), int(n_pages),
+                                  free_pages.shape[0], max_tokens, _stream(dev, stream))
+    if st != DIT_OK:
+        raise DitError(st, "dit_paged_plan")
+    return seq_lens_out, n_free_out, cu_new, slots
+
+
+def paged_kv_write(k_new, v_new, slots, k_cache, v_cache, summary=None, stream=None):
+    """dit_paged_kv_write: k_new, v_new bf16 [T, H_kv, D] views (slices of a fused projection need no
+    copy) into the slots (int64 [T], below 0: skipped) of the caches; with `summary` (bf16
+    [n_pages, H_kv, 2, D]) each touched page's channel minimum and maximum is kept up to date."""
+    _check_tensor(k_new, "k_new", torch.bfloat16, (None,) * 3, contiguous=False)
+    dev, (T, H, D) = k_new.device, k_new.shape
+    _check_tensor(v_new, "v_new", torch.bfloat16, (T, H, D), dev, contiguous=False)
+    n_pages, Hc, P, Dc = _check_paged(k_cache, v_cache, dev)
+    if (Hc, Dc) != (H, D):
+        raise ValueError(f"the caches hold {Hc} heads of {Dc}, the new rows {H} of {D}")
+    _check_tensor(slots, "slots", torch.int64, (T,), dev)
+    if summary is not None:
+        _check_tensor(summary, "summary", torch.bfloat16, (n_pages, H, 2, D), dev)
+    kn, vn = (Strides(D, t.stride(1), t.stride(0)) for t in (k_new, v_new))
+    ks, vs = view_strides(k_cache), view_strides(v_cache)
+    with _launch_context(dev, stream):
+        st = lib().dit_paged_kv_write(k_new.data_ptr(), kn, v_new.data_ptr(), vn, slots.data_ptr(),
+                                      k_cache.data_ptr(), ks, v_cache.data_ptr(), vs,
+                                      None if summary is None else summary.data_ptr(), T, H, D, P,
+                                      n_pages, _stream(dev, stream))
+    if st != DIT_OK:
+        raise DitError(st, "dit_paged_kv_write")
+
+
+def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, selected=None, out=None, lse=None,
+                   scale=None, out_dtype=torch.float32, workspace=None, stream=None, with_lse=True):
+    """dit_paged_attn_fwd: one query token of each request, q bf16 [B, H_q, D] (a view with contiguous
+    D), over the request's seq_lens[b] cached tokens; H_q is a multiple of the caches' H_kv.
+    `selected` (int32 [B, H_kv, n], paged_select's form) restricts each key/value head to the listed
+    pages.  The workspace is allocated with torch unless given.
+
+    Returns (out [B, H_q, D] of out_dtype, lse fp32 [B, H_q]); with_lse=False returns (out, None)."""
+    _check_tensor(q, "q", torch.bfloat16, (None,) * 3, contiguous=False)
+    dev, (B, Hq, D) = q.device, q.shape
+    n_pages, Hkv, P, Dc = _check_paged(k_cache, v_cache, dev)
+    if Dc != D:
+        raise ValueError(f"the caches hold heads of {Dc}, q of {D}")
+    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    if selected is not None:
+        _check_tensor(selected, "selected", torch.int32, (B, Hkv, None), dev)
+    _check_out(out, lse, (B, Hq, D), dev)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    L = lib()
+    with _launch_context(dev, stream):
+        if out is None:
+            out = torch.empty((B, Hq, D), device=dev, dtype=out_dtype)
+        if lse is None and with_lse:
+            lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
+        workspace = _workspace(workspace, L.dit_paged_attn_workspace_bytes(B, Hq, Hkv, D), dev)
+        st = L.dit_paged_attn_fwd(
+            q.data_ptr(), Strides(q.stride(0), q.stride(1), D), k_cache.data_ptr(),
+            view_strides(k_cache), v_cache.data_ptr(), view_strides(v_cache),
+            block_table.data_ptr(), stride, seq_lens.data_ptr(),
+            None if selected is None else selected.data_ptr(),
+            0 if selected is None else selected.shape[2], out.data_ptr(),
+            lse.data_ptr() if with_lse else None, B, Hq, Hkv, D, P, n_pages, max_pages, scale,
+            _dt(out.dtype), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream(dev, stream))
+    if st != DIT_OK:
+        raise DitError(st, "dit_paged_attn_fwd")
+    return out, (lse if with_lse else None)
+
+
+def paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected=None, workspace=None,
+                 stream=None):
+    """dit_paged_select: for each request and key/value head the newest page and the top_k - 1 others
+    whose summaries (bf16 [n_pages, H_kv, 2, D]) bound the highest scores for q bf16 [B, H_q, D].
+
+    Returns selected, int32 [B, H_kv, top_k]: table columns in ascending order, then -1."""
+    _check_tensor(q, "q", torch.bfloat16, (None,) * 3, contiguous=False)
+    dev, (B, Hq, D) = q.device, q.shape
+    _check_tensor(summary, "summary", torch.bfloat16, (None, None, 2, D), dev)
+    n_pages, Hkv = summary.shape[:2]
+    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    top_k = int(top_k)
+    if selected is not None:
+        _check_tensor(selected, "selected", torch.int32, (B, Hkv, top_k), dev)
+    L = lib()
+    with _launch_context(dev, stream):
+        if selected is None:
+            selected = torch.empty((B, Hkv, max(0, top_k)), device=dev, dtype=torch.int32)
+        workspace = _workspace(workspace, L.dit_paged_select_workspace_bytes(B, Hkv, max_pages), dev)
+        st = L.dit_paged_select(q.data_ptr(), Strides(q.stride(0), q.stride(1), D),
+                                summary.data_ptr(), block_table.data_ptr(), stride,
+                                seq_lens.data_ptr(), selected.data_ptr(), B, Hq, Hkv, D,
+                                int(page_size), n_pages, max_pages, top_k, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(dev, stream))
+    if st != DIT_OK:
+        raise DitError(st, "dit_paged_select")
+    return selected

@@ -286,6 +286,149 @@ dit_status dit_layout_copy(const void* src, const dit_strides* src_strides, void
                            const dit_strides* dst_strides, int B, int H, int N, int D,
                            dit_dtype dtype, dit_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged key/value caches: requests of different and growing lengths in pages of
+ * one pool, for generation with cached keys (text encoders and captioners of the
+ * pages' pipelines, autoregressive video blocks).  One step of a batch is
+ *   dit_paged_plan      pages and slots for the step's new tokens, from lengths
+ *   dit_paged_kv_write  their keys and values into the slots, page summaries
+ *   dit_paged_select    (sparse attention only) the best pages for each query
+ *   dit_paged_attn_fwd  one query token of each request against its pages
+ * All lengths, tables and slots live on the device, so that a step can be captured
+ * into a graph once and replayed as the lengths grow.
+ *
+ *  - A cache is a pool of n_pages pages: a [n_pages, H_kv, page_size, D] bf16 view
+ *    (dit_strides: b = page, h = head, n = row; NULL = contiguous).  page_size is a
+ *    multiple of 16 from 16 to 1024.  A token's slot is page * page_size + row.
+ *  - block_table: int32 [B, max_pages], rows table_stride >= max_pages entries apart;
+ *    entry (b, i) is the page that holds tokens i * page_size .. of request b.
+ *    max_pages * page_size < 2^31.  Entries past a request's length are never used.
+ *    An entry outside [0, n_pages) is a page without keys: nothing is read for it.
+ *  - seq_lens: int32 [B], the cached tokens of each request.  Values below 0 count as
+ *    0 and values above max_pages * page_size as that.
+ *  - Device contents cannot be refused; every value of the tables, lengths, slots and
+ *    lists is safe (no access outside the buffers), and what an unusual one means is
+ *    said at each call.
+ *  - Workspaces are scratch: 256-byte aligned, need no clearing, overwritten by every
+ *    call, and not to be shared by calls (or captured graphs) that can run at once.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Block tables and slot maps of one step from the requests' lengths.  Request b holds
+ * s_b = seq_lens[b] tokens in ceil(s_b / page_size) pages already in its table row and
+ * appends n_b = max(0, new_lens[b]) tokens (0: an idle request).  The step's tokens are
+ * packed in request order: request b's are rows cu_new[b] .. cu_new[b + 1] - 1 of the
+ * step's batch.  Pages are granted in request order from the top of the free-page stack
+ * (free_pages[n_free - 1] first) and written behind the request's pages in its table row;
+ * no other table entry changes.  Pages come back by writing them at free_pages[n_free ..]
+ * and raising n_free between steps.
+ *   new_lens, seq_lens : device int32 [B] (read)
+ *   block_table        : device int32 (read; granted entries written)
+ *   free_pages, n_free : device int32 [pool_capacity] and [1] (read); n_free counts as
+ *                        within [0, pool_capacity]
+ *   seq_lens_out       : device int32 [B] (written): the lengths after the step; may be
+ *                        seq_lens itself
+ *   n_free_out         : device int32 [1] (written): pages left; may be n_free itself
+ *   cu_new             : device int32 [B + 1] (written): prefix sums of n_b
+ *   slots              : device int64 [max_tokens] (written): the slot of each token of
+ *                        the batch, -1 for a token without one and behind the last token
+ * A token has no slot where the stack has run out, where its request's table row is full,
+ * or where its page's entry is outside [0, n_pages); tokens past max_tokens are dropped
+ * (cu_new stops there).  seq_lens_out counts the tokens that fitted, so that
+ * seq_lens_out[b] < s_b + n_b shows a request that ran out of pages.
+ *   B : 1 .. 8192 (above: DIT_ERR_UNSUPPORTED);  max_tokens : 1 .. 2^30
+ * Outputs must not overlap each other or the inputs, but for the two pairs named.
+ */
+dit_status dit_paged_plan(const int* new_lens, const int* seq_lens, int* block_table,
+                          long long table_stride, const int* free_pages, const int* n_free,
+                          int* seq_lens_out, int* n_free_out, int* cu_new, long long* slots, int B,
+                          int max_pages, int page_size, int n_pages, int pool_capacity,
+                          int max_tokens, dit_stream stream);
+
+/*
+ * Stores the keys and values of T tokens into their slots of the two caches, bit for bit.
+ *   k_new, v_new  : device bf16 views [T, H, D] (read); token t, head h starts
+ *                   t * s.n + h * s.h elements from the base (s.b is not used): slices of
+ *                   a fused projection need no copy.  NULL strides: contiguous [T, H, D].
+ *   slots         : device int64 [T]; a slot outside [0, n_pages * page_size) skips its
+ *                   token, and rows without a token are left as they are
+ *   k_cache, v_cache : paged caches (written)
+ *   summary       : device bf16 [n_pages, H, 2, D], contiguous, or NULL: for every page
+ *                   and channel the minimum (index 0) and maximum (1) of its keys.  A page
+ *                   whose row 0 is written starts anew from the rows of this call; any
+ *                   other touched page is widened by them.  NaN keys make it NaN.
+ * Slots are distinct, and with a summary the tokens of one page follow each other in
+ * ascending slots, as dit_paged_plan lays them out.  (Repeated slots or scattered rows of
+ * a page leave either row, and the page's summary, unspecified; nothing else.)
+ */
+dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_strides,
+                              const void* v_new, const dit_strides* v_new_strides,
+                              const long long* slots, void* k_cache,
+                              const dit_strides* k_strides, void* v_cache,
+                              const dit_strides* v_strides, void* summary, int T, int H, int D,
+                              int page_size, int n_pages, dit_stream stream);
+
+/*
+ * Attention of one new token of each request over its cached keys: for query head h of
+ * request b, with key/value head h / (H_q / H_kv),
+ *   s_j = scale * q_bh . k_j;  out_bh = sum_j softmax_j(s_j) v_j;  lse_bh = ln sum_j exp(s_j)
+ * over the seq_lens[b] first tokens (the new token's own key among them, once written).
+ * A request without keys gets out = 0, lse = -inf.  The keys' length is split over the GPU
+ * and the parts are joined exactly (the dit_attn_lse_merge combination), in an order that
+ * the lengths alone fix: equal calls give equal bits.
+ *   q           : device bf16 [B, H_q, D] view (s.b, s.h; s.n is not used); NULL strides:
+ *                 contiguous
+ *   k_cache, v_cache, block_table, seq_lens : as above (read).  Rows past a request's
+ *                 length may hold anything, NaN included.
+ *   selected    : device int32 [B, H_kv, n_selected], contiguous, or NULL (all pages): only
+ *                 the pages (table columns) listed for the key/value head take part, in
+ *                 dit_paged_select's form: ceil(seq_lens[b] / page_size) entries are
+ *                 looked at, at most n_selected.  An entry that is negative or past the
+ *                 request's last page is skipped; one that is repeated counts repeatedly.
+ *   out         : device [B, H_q, D] of out_dtype, contiguous, 16-byte aligned (written)
+ *   lse         : device fp32 [B, H_q] (written), or NULL
+ *   H_q         : a multiple of H_kv
+ *   workspace   : at least dit_paged_attn_workspace_bytes(B, H_q, H_kv, D) bytes
+ */
+dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const void* k_cache,
+                              const dit_strides* k_strides, const void* v_cache,
+                              const dit_strides* v_strides, const int* block_table,
+                              long long table_stride, const int* seq_lens, const int* selected,
+                              int n_selected, void* out, float* lse, int B, int H_q, int H_kv,
+                              int D, int page_size, int n_pages, int max_pages, float scale,
+                              dit_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                              dit_stream stream);
+
+/* Workspace bytes of a dit_paged_attn_fwd call with these sizes (0 when a size is not
+ * positive). */
+size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D);
+
+/*
+ * The pages whose keys can score highest, for attention over those alone.  For request b
+ * and key/value head g the score of page i is
+ *   max over the query heads h of the group of  sum_d max(q_hd * lo_d, q_hd * hi_d)
+ * with (lo, hi) the page's summary: no key of the page has a larger q . k.  Listed are the
+ * request's newest page and the top_k - 1 others with the highest scores (all pages where
+ * there are no more than top_k); equal scores go to the lower index, and a NaN score counts
+ * as +inf.  The choice is that of the scores in 64 bits.
+ *   q, block_table, seq_lens : as dit_paged_attn_fwd
+ *   summary  : device bf16 [n_pages, H_kv, 2, D], contiguous, as dit_paged_kv_write keeps it.
+ *              A page without keys (its entry outside [0, n_pages)) scores -inf.
+ *   selected : device int32 [B, H_kv, top_k], contiguous (written): table columns in
+ *              ascending order, then -1
+ *   top_k    : 1 .. max_pages
+ *   workspace: at least dit_paged_select_workspace_bytes(B, H_kv, max_pages) bytes
+ */
+dit_status dit_paged_select(const void* q, const dit_strides* q_strides, const void* summary,
+                            const int* block_table, long long table_stride, const int* seq_lens,
+                            int* selected, int B, int H_q, int H_kv, int D, int page_size,
+                            int n_pages, int max_pages, int top_k, void* workspace,
+                            size_t workspace_bytes, dit_stream stream);
+
+/* Workspace bytes of a dit_paged_select call with these sizes (0 when a size is not
+ * positive). */
+size_t dit_paged_select_workspace_bytes(int B, int H_kv, int max_pages);
+
 /*
  * Synchronises `stream`, then reads and clears the library's device status
  * word.  Returns DIT_ERR_TIMEOUT if any kernel since the last check gave up

@@ -1,0 +1,517 @@
+"""GPU parity of the paged key/value cache: dit_paged_plan, dit_paged_kv_write, dit_paged_select and
+dit_paged_attn_fwd against their plain 64-bit forms (paged_oracle), and a run of them together.
+
+Tolerances of the attention, from its arithmetic (S = scale max_j sum_d |q_d k_jd| for the row,
+A = sum_j p_j |v_j| for the channel):
+  - a score is a sum of D exact products in 32 bits, in D / 16 steps of 16 products and the running
+    sum, each term kept to within 2^-23 of the step's largest: off by at most
+    (D / 16) * 17 * 2^-23 * S =: E;
+  - a weight is off by a factor of at most exp(E) (score) and 2^-21 (exponential, in 32 bits), its
+    two or three 8-bit parts by 2^-17, a sum of them by 2^-20; numerator and denominator both:
+    |o - o_ref| <= (2 E + 2^-16) A, and half a step of the output's type;
+  - |lse - lse_ref| <= E + 2^-19 + 2^-23 |lse|.
+These are worst cases; over a whole output the errors are of random sign, so the 2-norm of the error
+is also held to 1e-5 (fp32 output) of the result's.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_oracle as po
+from diffusion_transformer_long_gb300 import ditattn as da
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+
+
+def dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x)).to(DEV, dtype)
+
+
+def rand(*shape, seed=0, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device=DEV) * scale).to(torch.bfloat16)
+
+
+def cache_view(n_pages, H, P, D, order, seed=0, scale=1.0):
+    """A [n_pages, H, P, D] view: head-major, token-major, or a part of a larger allocation."""
+    if order == "hnd":
+        return rand(n_pages, H, P, D, seed=seed, scale=scale)
+    if order == "nhd":
+        return rand(n_pages, P, H, D, seed=seed, scale=scale).transpose(1, 2)
+    return rand(n_pages, H + 1, P + 3, 2 * D, seed=seed, scale=scale)[:, 1:, 2:P + 2, D:]
+
+
+def tables(lens, P, seed=0, extra_pages=2, extra_cols=1):
+    """(block table with shuffled pages, -1 past each length; n_pages)."""
+    rng = np.random.default_rng(seed)
+    n = [-(-max(0, x) // P) for x in lens]
+    n_pages = sum(n) + extra_pages
+    order = rng.permutation(n_pages)
+    t = np.full((len(lens), max(1, max(n) + extra_cols)), -1, np.int64)
+    at = 0
+    for b, m in enumerate(n):
+        t[b, :m] = order[at:at + m]
+        at += m
+    return t, n_pages
+
+
+# ------------------------------------------------------------------ plan
+
+
+def check_plan(new, old, table, free_pages, n_free, P, n_pages, max_tokens, in_place=False):
+    want = po.plan(new, old, table, free_pages, n_free, P, n_pages, max_tokens)
+    td, sd, fd = dev(table), dev(old), dev([n_free])
+    kw = dict(seq_lens_out=sd, n_free_out=fd) if in_place else {}
+    got = da.paged_plan(dev(new), sd, td, dev(free_pages), fd, P, n_pages, max_tokens, **kw)
+    names = ("lens", "n_free", "cu", "slots")
+    for name, g, w in zip(names, got, want):
+        assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), name
+    assert np.array_equal(td.cpu().numpy(), want[4]), "table"
+    if not in_place:
+        assert np.array_equal(sd.cpu().numpy(), np.asarray(old)) and int(fd) == n_free
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,P,old_hi,new_lo,new_hi,pool", [
+    (1, 16, 40, 1, 1, 1.0), (1, 16, 0, 27280, 27280, 1.0), (5, 48, 200, 0, 90, 1.0),
+    (64, 16, 600, 1, 1, 1.0), (33, 32, 100, 0, 500, 0.6), (1000, 16, 70, 0, 3, 1.0),
+    (8192, 16, 40, 0, 2, 0.9), (3, 1024, 5000, 0, 3000, 1.0), (2047, 64, 300, 0, 40, 1.3)])
+def test_plan(B, P, old_hi, new_lo, new_hi, pool, in_place):
+    rng = np.random.default_rng(B + P)
+    old = rng.integers(0, old_hi + 1, B)
+    new = rng.integers(new_lo, new_hi + 1, B)
+    have = -(-old // P)
+    need = -(-(old + new) // P) - have
+    max_pages = int((-(-(old + new) // P)).max()) + 1
+    n_free = int(need.sum() * pool)
+    n_pages = int(have.sum()) + n_free + 4
+    order = rng.permutation(n_pages)
+    table = np.full((B, max_pages), -7, np.int64)
+    at = 0
+    for b in range(B):
+        table[b, :have[b]] = order[at:at + have[b]]
+        at += have[b]
+    free_pages = order[at:]
+    for max_tokens in {max(1, int(new.sum())), int(new.sum()) + 77, max(1, int(new.sum()) * 2 // 3)}:
+        check_plan(new, old, table, free_pages, n_free, P, n_pages, max_tokens, in_place)
+
+
+def test_plan_unusual_contents():
+    """Negative and huge lengths, a full table row, no free pages, a count past the stack, table and
+    stack entries outside the pool, a strided table."""
+    big = 2 ** 31 - 1
+    table = np.array([[3, -1, -1], [0, 99, -1], [1, 2, 4], [-5, -1, -1]])
+    free_pages = np.array([5, 77, 6, -2, 8])
+    for new, old in (([4, 20, 7, 9], [16, 20, 48, 3]), ([-3, 0, big, 1], [-8, 33, 40, 16]),
+                     ([big, big, big, big], [0, 0, 0, 0]), ([1, 1, 1, 1], [big, -big, 16, 32])):
+        for n_free in (0, 2, 5, 50, -4):
+            check_plan(new, old, table, free_pages, n_free, 16, 9, 100)
+    wide = torch.full((4, 10), -1, dtype=torch.int32, device=DEV)
+    wide[:, :3] = dev(table)
+    new, old = [4, 20, 7, 9], [16, 20, 40, 3]
+    got = da.paged_plan(dev(new), dev(old), wide[:, :3], dev(free_pages), dev([5]), 16, 9, 64)
+    want = po.plan(new, old, table, free_pages, 5, 16, 9, 64)
+    assert np.array_equal(got[3].cpu().numpy(), want[3])
+    assert np.array_equal(wide[:, :3].cpu().numpy(), want[4]) and (wide[:, 3:] == -1).all()
+
+
+# ------------------------------------------------------------------ write
+
+
+def check_write(T, H, D, P, order, slots, n_pages, with_summary, seed=0, k_new=None):
+    qkv = rand(T, 3 * H, D, seed=seed)
+    k_new = qkv[:, H:2 * H] if k_new is None else k_new
+    v_new = qkv[:, 2 * H:]
+    k, v = (cache_view(n_pages, H, P, D, order, seed=seed + i) for i in (1, 2))
+    summary = rand(n_pages, H, 2, D, seed=seed + 3) if with_summary else None
+    sl = dev(slots, torch.int64)
+    want_k, want_s = po.write(k_new.cpu(), sl.cpu(), k.cpu(), None if summary is None else summary.cpu())
+    want_v, _ = po.write(v_new.cpu(), sl.cpu(), v.cpu())
+    da.paged_kv_write(k_new, v_new, sl, k, v, summary=summary)
+    bits = lambda x: x.contiguous().cpu().view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(k), bits(want_k)) and torch.equal(bits(v), bits(want_v))
+    if with_summary:  # values: the zero of a page that holds both has either sign
+        s = summary.cpu()
+        assert torch.equal(s.isnan(), want_s.isnan())
+        assert torch.equal(s.nan_to_num(), want_s.nan_to_num())
+
+
+def plan_slots(old, new, P, seed=0, spare=0):
+    rng = np.random.default_rng(seed)
+    n_pages = sum(-(-(o + n) // P) for o, n in zip(old, new)) + 3
+    order = list(rng.permutation(n_pages))
+    slots = []
+    for o, n in zip(old, new):
+        pages = [order.pop() for _ in range(-(-(o + n) // P))]
+        slots += [pages[i // P] * P + i % P for i in range(o, o + n)]
+    return np.array(slots + [-1] * spare, np.int64), n_pages
+
+
+@pytest.mark.parametrize("with_summary", [False, True])
+@pytest.mark.parametrize("H,D,P,order,old,new,spare", [
+    (1, 64, 16, "hnd", [0], [1], 0), (8, 128, 16, "hnd", [0, 15, 16, 17, 31], [1, 1, 1, 1, 1], 3),
+    (2, 64, 48, "nhd", [3, 0, 47, 48, 100], [200, 1, 2, 90, 0], 5),
+    (3, 128, 16, "nhd", [5], [333], 0), (5, 128, 128, "part", [0, 100], [300, 57], 31),
+    (2, 64, 1024, "hnd", [1000], [1100], 1), (40, 128, 16, "hnd", list(range(70)), [1] * 70, 0),
+    (24, 128, 64, "hnd", [0], [5000], 0), (1, 64, 32, "part", [7] * 33, [35] * 33, 2)])
+def test_write(H, D, P, order, old, new, spare, with_summary):
+    slots, n_pages = plan_slots(old, new, P, seed=len(old), spare=spare)
+    check_write(len(slots), H, D, P, order, slots, n_pages, with_summary)
+
+
+def test_write_skips_and_nan():
+    """Slots outside the pool are skipped wherever they stand (a page's run goes on behind them, as a
+    run of its own rows), and a NaN key shows in its page's summary."""
+    P, n_pages, H, D = 16, 6, 2, 128
+    slots = [-1, 16, 17, 18, -9, 32, 96, 33 + 2 ** 40, 80, 81, 95, -1]
+    slots[10] = 82
+    k_new = rand(len(slots), H, D, seed=9)
+    k_new[2, 1, 7] = float("nan")
+    k_new[9, 0, 3] = float("inf")
+    for summary in (False, True):
+        check_write(len(slots), H, D, P, "hnd", slots, n_pages, summary, k_new=k_new)
+    check_write(4, H, D, P, "hnd", [-1, -1, 96, 2 ** 62], n_pages, True)
+
+
+# ------------------------------------------------------------------ attention
+
+
+def check_attn(o, lse, ref, bf16=False):
+    o_ref, lse_ref, (mag, pv) = ref
+    D = o_ref.shape[2]
+    E = (D // 16) * 17 * 2.0 ** -23 * mag
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    tol = (2 * E + 2.0 ** -16)[..., None] * pv + (2.0 ** -8 if bf16 else 2.0 ** -23) * np.abs(o_ref) + 1e-37
+    err = np.abs(o - o_ref)
+    assert (err <= tol).all(), f"out: {(err / tol).max():.3g} times its bound, {err.max():.3g}"
+    none = np.isinf(lse_ref)
+    assert (lse[none] == -math.inf).all() and (o[none] == 0).all()
+    lerr = np.abs(lse[~none] - lse_ref[~none])
+    ltol = E[~none] + 2.0 ** -19 + 2.0 ** -23 * np.abs(lse_ref[~none])
+    assert (lerr <= ltol).all(), f"lse: {(lerr / ltol).max():.3g} times its bound"
+    if not bf16 and np.abs(o_ref).max() > 0:
+        rel = np.linalg.norm(o - o_ref) / np.linalg.norm(o_ref)
+        assert rel <= 1e-5, f"2-norm of the error: {rel:.3g}"
+
+
+def make_case(lens, Hq, Hkv, D, P, order="hnd", seed=0, q_scale=1.5, k_scale=1.0):
+    table, n_pages = tables(lens, P, seed)
+    q = rand(len(lens), Hq, D, seed=seed + 1, scale=q_scale)
+    k = cache_view(n_pages, Hkv, P, D, order, seed=seed + 2, scale=k_scale)
+    v = cache_view(n_pages, Hkv, P, D, order, seed=seed + 3)
+    return q, k, v, dev(table), dev(lens)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Hq,Hkv,D,P,order,lens", [
+    (2, 2, 64, 16, "hnd", [1]), (2, 2, 64, 16, "nhd", [0, 1, 15, 16, 17, 63, 64, 65, 1024]),
+    (24, 8, 128, 16, "hnd", [0, 0, 1, 2, 4608]), (24, 24, 128, 32, "nhd", [31, 32, 33, 700]),
+    (40, 8, 128, 64, "hnd", [5, 1000, 63]), (16, 1, 64, 48, "part", [47, 48, 49, 2000]),
+    (24, 2, 128, 128, "hnd", [129, 1, 300]), (24, 1, 128, 16, "nhd", [513, 16]),
+    (64, 2, 64, 1024, "hnd", [1500, 1023]), (9, 1, 128, 16, "part", [100]),
+    (1, 1, 128, 16, "hnd", [27280]), (8, 8, 64, 16, "hnd", list(range(130)))])
+def test_attn(Hq, Hkv, D, P, order, lens, out_dtype):
+    q, k, v, table, sl = make_case(lens, Hq, Hkv, D, P, order, seed=Hq + len(lens))
+    o, lse = da.paged_attn_fwd(q, k, v, table, sl, out_dtype=out_dtype)
+    da.check()
+    ref = po.attend(q, k, v, table, sl, 1 / math.sqrt(D))
+    check_attn(o, lse, ref, out_dtype == torch.bfloat16)
+    o2, none = da.paged_attn_fwd(q, k, v, table, sl, out_dtype=out_dtype, with_lse=False)
+    assert none is None and torch.equal(o, o2)  # and equal calls give equal bits
+
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 48)])
+def test_attn_ignores_what_no_request_holds(D, P):
+    """Rows past a length and pages of nobody hold NaN and infinities; table entries past a length
+    are wild; entries inside a length that are outside the pool hold no keys."""
+    lens = [0, 1, P - 1, P, P + 1, 5 * P + 3, 777, 16, 3 * P]
+    q, k, v, table, sl = make_case(lens, 6, 2, D, P, seed=3)
+    used = torch.zeros(k.shape[0], P, dtype=torch.bool, device=DEV)
+    for b, n in enumerate(lens):
+        for page, row in po.rows_of(table.cpu().numpy(), b, n, P, k.shape[0]):
+            used[page, row] = True
+    for x, bad in ((k, float("nan")), (v, float("inf"))):
+        x.masked_fill_(~used[:, None, :, None], bad)
+    wild = table.clone()
+    wild[table < 0] = 2 ** 31 - 1
+    scale = 1 / math.sqrt(D)
+    ref = po.attend(q, k.nan_to_num(0, 0, 0), v.nan_to_num(0, 0, 0), table, sl, scale)
+    check_attn(*da.paged_attn_fwd(q, k, v, wild, sl), ref)
+    wild[5, 1] = -4                 # a page in the middle
+    wild[6, 777 // P] = k.shape[0]  # the last page
+    wild[3, 0] = 2 ** 30            # the only page: no keys at all
+    ref = po.attend(q, k.nan_to_num(0, 0, 0), v.nan_to_num(0, 0, 0), wild, sl, scale)
+    assert np.isinf(ref[1][3]).all()
+    check_attn(*da.paged_attn_fwd(q, k, v, wild, sl), ref)
+    # lengths below 0, and past the table (counted as the table's last row)
+    odd = sl.clone()
+    odd[1] = -(2 ** 31)
+    odd[2] = 2 ** 31 - 1
+    full = table.clone()
+    full[2] = torch.arange(table.shape[1], device=DEV, dtype=torch.int32) % k.shape[0]
+    kk, vv = k.nan_to_num(0, 0, 0), v.nan_to_num(0, 0, 0)
+    check_attn(*da.paged_attn_fwd(q, kk, vv, full, odd), po.attend(q, kk, vv, full, odd, scale))
+
+
+def test_attn_nan_and_infinite_keys_reach_their_own_row_only():
+    q, k, v, table, sl = make_case([40, 40, 40], 4, 2, 64, 16, seed=5)
+    k[table[0, 1], 0, 3] = float("nan")
+    v[table[1, 2], 1, 7, 5] = float("inf")
+    o, lse = (x.cpu() for x in da.paged_attn_fwd(q, k, v, table, sl))
+    assert o[0, :2].isnan().all() and lse[0, :2].isnan().all()
+    assert o[0, 2:].isfinite().all() and o[2].isfinite().all() and lse[1:].isfinite().all()
+    bad = torch.zeros(4, 64, dtype=torch.bool)
+    bad[2:, 5] = True
+    assert torch.equal(~o[1].isfinite(), bad)
+
+
+@pytest.mark.parametrize("q_scale,k_scale", [(8.0, 4.0), (0.0, 1.0), (1e-3, 1e-3)])
+def test_attn_peaked_and_flat(q_scale, k_scale):
+    q, k, v, table, sl = make_case([3000, 33, 1], 24, 8, 128, 16, seed=7, q_scale=q_scale, k_scale=k_scale)
+    check_attn(*da.paged_attn_fwd(q, k, v, table, sl), po.attend(q, k, v, table, sl, 128 ** -0.5))
+
+
+def test_attn_growing_scores():
+    """Every key beats the ones before it: the running maximum moves at each step."""
+    n, D, P = 2000, 64, 16
+    table, n_pages = tables([n], P, extra_pages=0, extra_cols=0)
+    q = torch.ones(1, 2, D, device=DEV, dtype=torch.bfloat16)
+    k, v = torch.zeros(n_pages, 2, P, D, device=DEV, dtype=torch.bfloat16), rand(n_pages, 2, P, D, seed=1)
+    at = dev(table[0], torch.int64)
+    ramp = torch.linspace(-80, 80, n, device=DEV).reshape(-1, P)
+    k[at, 0, :, 0] = ramp.to(torch.bfloat16)
+    k[at, 1, :, 0] = -ramp.to(torch.bfloat16)
+    t, sl = dev(table), dev([n])
+    for scale in (1.0, 10.0):
+        check_attn(*da.paged_attn_fwd(q, k, v, t, sl, scale=scale), po.attend(q, k, v, t, sl, scale))
+
+
+def test_attn_views_streams_workspace():
+    """Strided queries and tables, caller's outputs, a poisoned workspace of the exact size with a
+    guard behind it, another stream."""
+    lens = [100, 0, 3000, 17]
+    q, k, v, table, sl = make_case(lens, 10, 2, 128, 32, "part", seed=11)
+    fused = torch.zeros(4, 14, 192, device=DEV, dtype=torch.bfloat16)
+    fused[:, 2:12, 64:] = q
+    wide = torch.full((4, table.shape[1] + 5), 12345, device=DEV, dtype=torch.int32)
+    wide[:, 2:-3] = table
+    need = da.lib().dit_paged_attn_workspace_bytes(4, 10, 2, 128)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full((5, 10, 128), 7.0, device=DEV)
+    lse = torch.full((5, 10), 7.0, device=DEV)
+    da.paged_attn_fwd(fused[:, 2:12, 64:], k, v, wide[:, 2:-3], sl, out=out[:4], lse=lse[:4],
+                      workspace=ws[:need])
+    da.check()
+    ref = po.attend(q, k, v, table, sl, 128 ** -0.5)
+    check_attn(out[:4], lse[:4], ref)
+    assert (ws[need:] == 0xFF).all() and (out[4] == 7).all() and (lse[4] == 7).all()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o2, l2 = da.paged_attn_fwd(q, k, v, table, sl, stream=s)
+    s.synchronize()
+    assert torch.equal(o2, out[:4]) and torch.equal(l2, lse[:4])
+
+
+def test_attn_two_streams_at_once():
+    cases = [make_case([2000 + i, 900, 5], 24, 8, 128, 16, seed=20 + i) for i in range(2)]
+    alone = [da.paged_attn_fwd(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = [da.paged_attn_fwd(*c, stream=s) for c, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for (o, lse), (o1, l1) in zip(got, alone):
+            assert torch.equal(o, o1) and torch.equal(lse, l1)
+
+
+def test_attn_capped_grid():
+    """A capped grid walks many items per block: the same values up to the order of the joins."""
+    lens = [0, 700, 33, 1, 2500, 64]
+    q, k, v, table, sl = make_case(lens, 12, 4, 64, 16, seed=31)
+    ref = po.attend(q, k, v, table, sl, 64 ** -0.5)
+    try:
+        for cap in (1, 2, 7, 50):
+            da.set_grid_limit(cap)
+            check_attn(*da.paged_attn_fwd(q, k, v, table, sl), ref)
+    finally:
+        da.set_grid_limit(0)
+
+
+def test_attn_offsets_past_32_bits():
+    """Pages that begin more than 2^32 bytes and more than 2^31 elements into the cache."""
+    H, P, D = 2, 64, 128
+    n_pages = 2 ** 31 // (H * P * D) + 40
+    k = torch.empty(n_pages, H, P, D, device=DEV, dtype=torch.bfloat16)
+    k[:3] = rand(3, H, P, D, seed=1)
+    k[-3:] = rand(3, H, P, D, seed=2)
+    pages = [n_pages - 1, 0, n_pages - 3, 2, n_pages - 2, 1]
+    table, sl = dev([pages]), dev([6 * P - 5])
+    q = rand(1, 4, D, seed=3)
+    o, lse = da.paged_attn_fwd(q, k, k, table, sl)
+    small = torch.cat((k[:3], k[-3:]))
+    small_table = dev([[i if i < 3 else i - n_pages + 6 for i in pages]])
+    check_attn(o, lse, po.attend(q, small, small, small_table, sl, D ** -0.5))
+    # the write reaches the same pages
+    new = rand(3, H, D, seed=4)
+    slots = torch.tensor([(n_pages - 1) * P + 5, 2 * P + 1, n_pages * P], device=DEV)
+    v = torch.zeros(n_pages, H, P, D, device=DEV, dtype=torch.bfloat16)
+    da.paged_kv_write(new, new, slots, k, v)
+    assert torch.equal(k[-1, :, 5], new[0]) and torch.equal(v[-1, :, 5], new[0])
+    assert torch.equal(k[2, :, 1], new[1]) and torch.equal(v[2, :, 1], new[1])
+
+
+# ------------------------------------------------------------------ selection
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,P,lens,top_k", [
+    (2, 2, 64, 16, [1], 1), (24, 8, 128, 16, [0, 1, 16, 17, 500, 4608], 8),
+    (40, 8, 128, 32, [3000, 40], 1), (16, 1, 64, 16, [9000, 100, 5], 33),
+    (24, 24, 128, 48, [1000, 2000], 21), (24, 1, 128, 16, [700], 44), (64, 2, 64, 16, [1600, 320], 20),
+    (2, 2, 64, 16, [75600], 100), (4, 4, 128, 16, [27280, 27264], 1000)])
+def test_select(Hq, Hkv, D, P, lens, top_k):
+    table, n_pages = tables(lens, P, seed=top_k)
+    q = rand(len(lens), Hq, D, seed=1, scale=1.5)
+    a, b = rand(n_pages, Hkv, 1, D, seed=2), rand(n_pages, Hkv, 1, D, seed=3)
+    summary = torch.cat((torch.minimum(a, b), torch.maximum(a, b)), 2)
+    t, sl = dev(table), dev(lens)
+    top_k = min(top_k, table.shape[1])
+    got = da.paged_select(q, summary, t, sl, P, top_k)
+    assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k))
+
+
+@pytest.mark.parametrize("kind", ["equal", "few values", "near", "nan", "inf", "overflow", "tiny", "zero q",
+                                  "bad entries", "inf q"])
+def test_select_borders(kind):
+    """Scores that tie, that differ by less than a 32-bit sum resolves, that are no numbers, that pass
+    the range of 32 bits at either end."""
+    lens, P, Hq, Hkv, D, top_k = [2000, 1999, 130, 16], 16, 6, 2, 128, 37
+    table, n_pages = tables(lens, P, seed=8)
+    q = rand(len(lens), Hq, D, seed=1)
+    a, b = rand(n_pages, Hkv, 1, D, seed=2), rand(n_pages, Hkv, 1, D, seed=3)
+    summary = torch.cat((torch.minimum(a, b), torch.maximum(a, b)), 2)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    some = torch.rand(n_pages, Hkv, generator=g, device=DEV) < 0.2
+    if kind == "equal":
+        summary[:] = summary[:1].clone()
+    elif kind == "few values":
+        summary[:] = summary[torch.arange(n_pages, device=DEV) % 3]
+    elif kind == "near":  # one channel of a tiny query differs: the sums agree to about 2^-30
+        summary[:] = summary[:1].clone()
+        q[:, :, 5] = 2.0 ** -24
+        summary[:, :, :, 5] = rand(n_pages, Hkv, 1, seed=6)
+    elif kind == "nan":
+        summary[some, 1, 9] = float("nan")
+    elif kind == "inf":
+        summary[some, 0, 9] = -float("inf")
+        summary[~some, 1, 3] = float("inf")
+    elif kind == "overflow":
+        q *= 2.0 ** 70
+        summary *= 2.0 ** 66
+    elif kind == "tiny":
+        q *= 2.0 ** -75
+        summary *= 2.0 ** -70
+    elif kind == "zero q":
+        q.zero_()
+    elif kind == "bad entries":
+        table[0, 3:50] = -1
+        table[1, ::2] = n_pages
+        table[2, -2] = 2 ** 31 - 1
+    else:
+        q[0, 0, 0] = float("inf")
+        q[1, 4, 7] = float("nan")
+    t, sl = dev(table), dev(lens)
+    for k in (1, 2, top_k, table.shape[1]):
+        got = da.paged_select(q, summary, t, sl, P, k)
+        assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, k)), k
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,P,order", [(24, 8, 128, 16, "hnd"), (2, 2, 64, 48, "nhd"), (16, 1, 64, 64, "part")])
+def test_attn_over_selected_pages(Hq, Hkv, D, P, order):
+    """Lists as paged_select writes them, and any other list: skipped, repeated, unsorted entries."""
+    lens = [0, 1, P, P + 1, 40 * P - 3, 2000]
+    q, k, v, table, sl = make_case(lens, Hq, Hkv, D, P, order, seed=41)
+    rng = np.random.default_rng(5)
+    n = 6
+    sel = rng.integers(-2, 45, (len(lens), Hkv, n))
+    sel[4] = [[0, 39, 3, 3, -1, 38]] * Hkv
+    sel[3] = [[1, 0, -1, 7, 7, 7]] * Hkv
+    sd = dev(sel)
+    check_attn(*da.paged_attn_fwd(q, k, v, table, sl, selected=sd),
+               po.attend(q, k, v, table, sl, D ** -0.5, selected=sd))
+    every = dev(np.broadcast_to(np.arange(table.shape[1]), (len(lens), Hkv, table.shape[1])).copy())
+    ref = po.attend(q, k, v, table, sl, D ** -0.5)
+    check_attn(*da.paged_attn_fwd(q, k, v, table, sl, selected=every), ref)
+
+
+# ------------------------------------------------------------------ a run of them together
+
+
+def test_steps_together_eager_and_replayed():
+    """A batch that prefills, then decodes token by token: plan, write with summaries, select,
+    attention over all and over the selected pages, eagerly and as one captured step replayed as the
+    lengths grow; a request that is idle for some steps and one that runs out of pages."""
+    B, Hq, Hkv, D, P, top_k, n_pages, max_pages = 4, 6, 2, 64, 16, 3, 30, 12
+    scale = D ** -0.5
+    k, v = (torch.full((n_pages, Hkv, P, D), float("nan"), device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    summary = torch.full((n_pages, Hkv, 2, D), float("nan"), device=DEV, dtype=torch.bfloat16)
+    table = torch.full((B, max_pages), -1, device=DEV, dtype=torch.int32)
+    free = torch.randperm(n_pages, generator=torch.Generator().manual_seed(1)).to(DEV, torch.int32)
+    n_free, lens = dev([n_pages]), dev([0] * B)
+    keys = [[torch.zeros(0, Hkv, D), torch.zeros(0, Hkv, D)] for _ in range(B)]  # what each request holds
+
+    def step(new, qkv, max_tokens):
+        _, _, cu, slots = da.paged_plan(new, lens, table, free, n_free, P, n_pages, max_tokens,
+                                        seq_lens_out=lens, n_free_out=n_free)
+        da.paged_kv_write(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], slots, k, v, summary=summary)
+        q = qkv[:B, :Hq]
+        sel = da.paged_select(q, summary, table, lens, P, top_k)
+        return (cu, sel, *da.paged_attn_fwd(q, k, v, table, lens),
+                *da.paged_attn_fwd(q, k, v, table, lens, selected=sel))
+
+    def follow(new, qkv, res):
+        cu, sel, o, lse, os_, ls = res
+        da.check()
+        cu, x = cu.cpu(), qkv.cpu()
+        for b in range(B):
+            for i in range(2):
+                rows = x[cu[b]:cu[b + 1], Hq + i * Hkv:Hq + (i + 1) * Hkv].float()
+                keys[b][i] = torch.cat((keys[b][i], rows))[:int(lens[b])]
+        # what the requests hold, gathered by position, attended to as one page each
+        t = np.arange(B)[:, None]
+        most = max(1, int(lens.max()))
+        dense = [torch.zeros(B, Hkv, most, D) for _ in range(2)]
+        for b in range(B):
+            for i in range(2):
+                n = len(keys[b][i])
+                assert n == int(lens[b])
+                dense[i][b, :, :n] = keys[b][i].transpose(0, 1)
+        q = qkv[:B, :Hq]
+        check_attn(o, lse, po.attend(q, *dense, torch.as_tensor(t), lens, scale))
+        assert np.array_equal(sel.cpu().numpy(), po.select(q, summary, table, lens, P, top_k))
+        kk, vv = k.nan_to_num(0, 0, 0), v.nan_to_num(0, 0, 0)
+        check_attn(os_, ls, po.attend(q, kk, vv, table, lens, scale, selected=sel))
+
+    new = dev([40, 0, 75, 16])
+    qkv = rand(140, Hq + 2 * Hkv, D, seed=50)
+    follow(new, qkv, step(new, qkv, 140))
+    new = dev([1, 1, 1, 1])
+    qkv = rand(5, Hq + 2 * Hkv, D, seed=51)
+    follow(new, qkv, step(new, qkv, 5))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step(new, qkv, 5)
+    expect = np.array([41, 1, 76, 17])
+    for i in range(60):
+        fresh = [1, int(i % 3 == 0), 1, int(i < 9) * 2 - int(i == 4)]
+        new.copy_(dev(fresh))
+        qkv.copy_(rand(5, Hq + 2 * Hkv, D, seed=100 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        follow(new, qkv, res)
+        expect += np.maximum(fresh, 0)
+        if int(n_free) > 0:
+            assert np.array_equal(lens.cpu().numpy(), np.minimum(expect, max_pages * P))
