@@ -18,12 +18,9 @@ long long g_wait_limit = kDefaultWaitLimit;
 // Test-only cap on the persistent grid (0: one CTA per SM).
 int g_grid_limit = 0;
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
 
-EncodeTiledFn encoder() {
+EncodeTiledFn tensor_map_encoder() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -37,11 +34,13 @@ EncodeTiledFn encoder() {
   return fn;
 }
 
+namespace {
+
 // 4-D bf16 map (d, rows, heads, batch) of a strided [B, H, rows, d] view, with
 // 128-row x 64-column boxes and 128-byte swizzle; rows past `rows` read as zero.
 bool encode_view(CUtensorMap* m, const void* base, int d, int rows, int heads, int batch,
                  const Strides& st) {
-  EncodeTiledFn fn = encoder();
+  EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(batch)};
@@ -62,7 +61,7 @@ bool encode_view(CUtensorMap* m, const void* base, int d, int rows, int heads, i
 // be valid).
 bool encode_out_view(CUtensorMap* m, void* base, bool f32, int d, int rows, int heads, int batch,
                      int ranges, const Strides& st, long long range_stride) {
-  EncodeTiledFn fn = encoder();
+  EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
   const cuuint64_t es = f32 ? 4 : 2;
   const cuuint64_t dims[5] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
@@ -183,6 +182,13 @@ cudaError_t launch_attention(const AttnLaunch& a, cudaStream_t st) {
                      : host::launch_typed<64, false>(prm, st, g_grid_limit);
   return a.out_f32 ? host::launch_typed<128, true>(prm, st, g_grid_limit)
                    : host::launch_typed<128, false>(prm, st, g_grid_limit);
+}
+
+int grid_limit() { return g_grid_limit; }
+
+void stall_injection(int* enable, long long* wait_limit_cycles) {
+  *enable = g_stall_kv;
+  *wait_limit_cycles = g_wait_limit;
 }
 
 void set_grid_limit(int max_ctas) { g_grid_limit = max_ctas > 0 ? max_ctas : 0; }

@@ -3,6 +3,7 @@
 // attn_fwd_short.cu: the forms for short work items, whose softmax warpgroups drain O).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -10,6 +11,14 @@
 #include "attn_kernel.cuh"
 
 namespace ditattn {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// cuTensorMapEncodeTiled, looked up once (null if the driver has none).
+EncodeTiledFn tensor_map_encoder();
+
 namespace host {
 
 // Streaming multiprocessors of the current device, cached per device.

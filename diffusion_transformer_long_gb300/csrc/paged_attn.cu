@@ -1,14 +1,41 @@
 // Attention of one new token of each request over its paged keys and values:
 //   s_j = scale q . k_j,  m = max s_j,  l = sum exp(s_j - m),  o = sum exp(s_j - m) v_j / l,
-//   lse = m + ln l.
+//   lse = m + ln l
+// for the H_q / H_kv query heads that share a key/value head at once, each key and value read
+// once.  2 H_kv D bytes per key feed at most 4 H_q D operations: bound by HBM.
 //
-// One block per (request, query head); the warps take the keys in turn, a lane holds D / 32
-// channels of the running output, and the warps' states are joined at the end.
+// Work split.  A unit is 64 keys of one (request, key/value head, block of query heads).  The
+// units of the whole batch, counted from the lengths on the device, are dealt out evenly: each
+// block takes one run of consecutive units, whatever request they belong to, so that ragged
+// lengths and a single long request fill the GPU alike.  A run that ends inside an item leaves
+// fp32 partials (sum, m, l) in the workspace, at most two per block; a second, small launch
+// joins them in the order of the blocks (a fixed order: equal calls give equal bits).
+//
+// Inside a block every warp works alone: it takes every fourth 16-key tile of the run, keeps
+// its own ring of stages that its own lane 0 fills by TMA (one 16 x D box of one page for K and
+// one for V, 128-byte swizzle), and its own softmax state; the four states are joined through
+// shared memory where an item ends.  No block-wide barrier stands between the loads.
+//
+// Arithmetic.  Scores S^T = K Q^T on mma.sync m16n8k16 (keys x heads, 8 or 16 heads), so that a
+// column is a query head, padding to 8 heads and not to the 16 rows of an A operand, and the
+// running output O^T = V^T P^T has the same columns: a thread holds the statistics of the two
+// heads whose outputs it holds.  tcgen05 would need 64 or 128 rows for 1 to 16 heads and the
+// scores through tensor memory; at 1 to 16 operations per byte the tensor pipe is idle either
+// way.  P goes to bf16 in two parts (fp32 output: three), hi + lo (+ lo2), so that its rounding
+// (2^-18, fp32: 2^-27) does not show; each tile's product starts from zero and is added in
+// fp32, because the tensor core's own accumulation truncates, and over hundreds of tiles that
+// would pull the output towards zero.  The running maximum moves only when a tile exceeds it by
+// 2^8 (weights up to 256 cost no precision in fp32), and the row sum is compensated, since
+// thousands of like terms in turn would lose 2^-24 of the sum at each.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <mutex>
 
+#include "attn_host.cuh"
 #include "paged_launch.h"
 #include "sm103_ptx.cuh"
 
@@ -16,89 +43,672 @@ namespace ditattn {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kThreadsPaged = kWarps * 32;
+constexpr int kTile = 16;                    // keys of a warp's stage
+constexpr int kUnitTiles = kWarps;           // tiles of a unit
+constexpr int kMaxBlocks = 512;              // largest grid the workspace serves
+constexpr float kSlack = 8.f;                // log2 of the largest weight against the running maximum
 
 struct PagedParams {
-  PagedAttnLaunch a;
+  CUtensorMap tm_k, tm_v;
+  const __nv_bfloat16* q;
+  long long q_b, q_h;
+  const int* table;
+  long long table_stride;
+  const int* seq_lens;
+  const int* selected;
+  int n_selected;
+  void* out;
+  float* lse;
+  float* part_o;    // [blocks][2][R][D]
+  float2* part_ml;  // [blocks][2][R]: (maximum in units of log2, sum)
+  int4* meta;       // [blocks]: (request, item of it, parts, 0) of the item to join, parts = 0: none
+  int batch, h_q, h_kv, group, head_blocks;  // head_blocks: blocks of R query heads in a group
+  int page_size, page_tiles, n_pages, max_len;
+  float scale_log2;
+  int* status;
+  long long wait_limit;
+  int stall;
 };
 
-template <int D, typename OT>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_simple(const PagedParams p) {
-  constexpr int kC = D / 32;  // channels of a lane
-  __shared__ float sm_o[kWarps][D], sm_m[kWarps], sm_l[kWarps];
-  const PagedAttnLaunch& a = p.a;
-  const int b = blockIdx.x / a.h_q, h = blockIdx.x % a.h_q, hk = h / (a.h_q / a.h_kv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = a.page_size;
-  const int len = min(max(0, a.seq_lens[b]), a.max_pages * P);
-  const int pages = pages_of(len, P);
-  const int entries = a.selected ? min(pages, a.n_selected) : pages;
-  const int* sel = a.selected ? a.selected + (static_cast<long long>(b) * a.h_kv + hk) * a.n_selected : nullptr;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + h * a.q_h;
-  float qr[kC], o[kC], m = -INFINITY;
-  double l = 0.0;  // thousands of like terms in turn: 32 bits would lose 2^-24 of the sum at each
-#pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    qr[i] = __bfloat162float(q[lane + 32 * i]);
-    o[i] = 0.f;
+template <int D>
+struct PagedSmem {
+  static constexpr int kBox = kTile * D * 2;           // K or V of one tile
+  static constexpr int kStages = 96 * 1024 / (kWarps * 2 * kBox);  // 3 (D = 128) or 6
+  static constexpr int kRing = kWarps * kStages * 2 * kBox;
+  static constexpr int kJoin = kWarps * 8 * D * 4;     // eight heads' sums of each warp
+  static constexpr int kBars = kRing + kJoin;          // mbarriers
+  static constexpr int kValid = kBars + kWarps * kStages * 8;
+  static constexpr int kMl = kValid + kWarps * kStages * 4;
+  static constexpr int kScan = kMl + kWarps * 16 * 8;
+  static constexpr int kBytes = kScan + 64;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0,
+                                            int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+// The units of one request's item: 64-key blocks of its cached (or listed) keys, at least one,
+// so that a request without keys still gets its output written.
+struct Item {
+  int len, pages, tiles, units;
+};
+__device__ __forceinline__ Item item_of(const PagedParams& p, int b) {
+  Item x;
+  x.len = min(max(0, __ldg(p.seq_lens + b)), p.max_len);
+  x.pages = pages_of(x.len, p.page_size);
+  x.tiles = p.selected ? min(x.pages, p.n_selected) * p.page_tiles : pages_of(x.len, kTile);
+  x.units = max(1, (x.tiles + kUnitTiles - 1) / kUnitTiles);
+  return x;
+}
+
+// Walks a block's run of units item by item: units [u0, u1) of item j of request b.
+struct Walk {
+  int b, j, u0, u1;
+  long long left;  // units of the run behind u1
+  Item it;
+  __device__ __forceinline__ void start(const PagedParams& p, int b_, int j_, int u, long long n) {
+    b = b_;
+    j = j_;
+    it = item_of(p, b);
+    u0 = u;
+    left = n;
+    take();
   }
-  for (int e = 0; e < entries; ++e) {
-    const int i = sel ? sel[e] : e;
-    if (i < 0 || i >= pages) continue;
-    const int page = a.table[b * a.table_stride + i];
-    if (page < 0 || page >= a.n_pages) continue;
-    const int rows = min(P, len - i * P);
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k_cache) + page * a.ks.b_ + hk * a.ks.h_;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v_cache) + page * a.vs.b_ + hk * a.vs.h_;
-    for (int r = warp; r < rows; r += kWarps) {
-      float s = 0.f;
-#pragma unroll
-      for (int c = 0; c < kC; ++c) s = fmaf(qr[c], __bfloat162float(k[r * a.ks.n_ + lane + 32 * c]), s);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      s *= a.scale;
-      const float mn = fmaxf(m, s);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float f = expf(m - base), w = expf(s - base);
-      m = mn;
-      l = l * f + w;
-#pragma unroll
-      for (int c = 0; c < kC; ++c) o[c] = fmaf(w, __bfloat162float(v[r * a.vs.n_ + lane + 32 * c]), o[c] * f);
+  __device__ __forceinline__ void take() {
+    const int n = static_cast<int>(min(static_cast<long long>(it.units - u0), left));
+    u1 = u0 + n;
+    left -= n;
+  }
+  __device__ __forceinline__ void next(const PagedParams& p) {
+    if (++j == p.h_kv * p.head_blocks) {
+      j = 0;
+      it = item_of(p, ++b);
+    }
+    u0 = 0;
+    take();
+  }
+  // Tiles of the segment for one warp: first + 4 i < end.
+  __device__ __forceinline__ int first(int warp) const { return u0 * kUnitTiles + warp; }
+  __device__ __forceinline__ int end() const { return min(u1 * kUnitTiles, it.tiles); }
+};
+
+// One warp's loads, running ahead of its arithmetic over the same sequence of tiles.
+template <int D>
+struct Producer {
+  using S = PagedSmem<D>;
+  Walk w;
+  int i;           // the segment's next tile is first(warp) + 4 i
+  int page, spot;  // lane l: page of tile i / 32 * 32 + l, its first row | keys << 16
+  int count;       // tiles issued
+  __device__ __forceinline__ void look_up(const PagedParams& p, int warp, int lane) {
+    const int t = w.first(warp) + kUnitTiles * (i + lane);
+    page = 0;
+    spot = 0;
+    if (t < w.end()) {
+      int col = t / p.page_tiles;
+      const int row = (t - col * p.page_tiles) * kTile;
+      if (p.selected)
+        col = __ldg(p.selected + (static_cast<long long>(w.b) * p.h_kv + w.j / p.head_blocks) * p.n_selected + col);
+      if (col >= 0 && col < w.it.pages) {
+        page = __ldg(p.table + w.b * p.table_stride + col);
+        const int keys = min(kTile, w.it.len - col * p.page_size - row);
+        if (page >= 0 && page < p.n_pages && keys > 0) spot = row | keys << 16;
+      }
     }
   }
+  __device__ __forceinline__ void issue(const PagedParams& p, uint32_t ring, uint32_t bars, int* valid, int warp,
+                                        int lane) {
+    while (w.first(warp) + kUnitTiles * i >= w.end()) {
+      if (w.left == 0) return;
+      w.next(p);
+      i = 0;
+    }
+    if ((i & 31) == 0) look_up(p, warp, lane);
+    const int pg = __shfl_sync(~0u, page, i & 31), sp = __shfl_sync(~0u, spot, i & 31);
+    ++i;
+    const int stage = count % S::kStages;
+    ++count;
+    if (lane == 0) {
+      const uint32_t bar = bars + stage * 8, dst = ring + stage * 2 * S::kBox;
+      valid[stage] = sp >> 16;
+      if (sp == 0 || p.stall) {  // no key of this tile counts: nothing to load
+        if (!p.stall) ptx::mbar_arrive(bar);
+      } else {
+        const int head = w.j / p.head_blocks;
+        ptx::mbar_arrive_expect_tx(bar, 2 * S::kBox);
+        tma_load_5d(dst, &p.tm_k, bar, 0, sp & 0xffff, 0, head, pg);
+        tma_load_5d(dst + S::kBox, &p.tm_v, bar, 0, sp & 0xffff, 0, head, pg);
+      }
+    }
+  }
+};
+
+// kNb: blocks of eight query heads (R = 8 kNb).
+template <int D, int kNb, typename OT>
+__global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __grid_constant__ PagedParams p) {
+  using S = PagedSmem<D>;
+  constexpr int kSteps = D / 16;
+  constexpr int kParts = sizeof(OT) == 4 ? 3 : 2;
+  constexpr int R = 8 * kNb;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  float* join = reinterpret_cast<float*>(smem + S::kRing);
+  float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
+  long long* scan = reinterpret_cast<long long*>(smem + S::kScan);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = ptx::smem_addr(smem) + warp * S::kStages * 2 * S::kBox;
+  const uint32_t bars = ptx::smem_addr(smem + S::kBars) + warp * S::kStages * 8;
+  int* valid = reinterpret_cast<int*>(smem + S::kValid) + warp * S::kStages;
+  const int items = p.h_kv * p.head_blocks;  // of one request
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    ptx::tma_prefetch_desc(&p.tm_k);
+    ptx::tma_prefetch_desc(&p.tm_v);
+  }
   if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = static_cast<float>(l);
+    for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(bars + s * 8, 1);
+    ptx::fence_mbar_init();
   }
+  // All units of the batch, and where this block's run of them begins: each thread sums a chunk
+  // of the requests, the one whose chunk holds the run's first unit finds the request.
+  const int per = (p.batch + kThreadsPaged - 1) / kThreadsPaged;
+  const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) sum += item_of(p, b).units;
+  sum *= items;
+  long long upto = sum;
 #pragma unroll
-  for (int c = 0; c < kC; ++c) sm_o[warp][lane + 32 * c] = o[c];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < kWarps; ++w) L += sm_l[w] * expf(sm_m[w] - base);
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += sm_o[w][d] * expf(sm_m[w] - base);
-    static_cast<OT*>(a.out)[(static_cast<long long>(b) * a.h_q + h) * D + d] = static_cast<OT>(L == 0.f ? 0.f : x / L);
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += y;
   }
-  if (a.lse && threadIdx.x == 0) a.lse[static_cast<long long>(b) * a.h_q + h] = base + logf(L);
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += scan[w];
+    total += scan[w];
+  }
+  const long long blocks = min(static_cast<long long>(gridDim.x), total);
+  const long long c = blockIdx.x;
+  if (c >= blocks) {
+    if (threadIdx.x == 0) p.meta[c] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  const long long run0 = c * total / blocks, run1 = (c + 1) * total / blocks;
+  __syncthreads();
+  if (run0 < upto && run0 >= upto - sum) {
+    long long at = upto - sum;
+    int b = b0;
+    long long n = static_cast<long long>(item_of(p, b).units) * items;
+    while (at + n <= run0) {
+      at += n;
+      n = static_cast<long long>(item_of(p, ++b).units) * items;
+    }
+    scan[0] = b;
+    scan[1] = run0 - at;
+  }
+  __syncthreads();
+  Walk seg;
+  {
+    const int b = static_cast<int>(scan[0]);
+    const int units = item_of(p, b).units;
+    const int j = static_cast<int>(scan[1] / units);
+    seg.start(p, b, j, static_cast<int>(scan[1] - static_cast<long long>(j) * units), run1 - run0);
+  }
+  Producer<D> load;
+  load.w = seg;
+  load.i = 0;
+  load.count = 0;
+  for (int s = 0; s < S::kStages; ++s) load.issue(p, ring, bars, valid, warp, lane);
+
+  // ldmatrix addresses of this lane: row and 16-byte chunk of K (A operand, keys x channels) and
+  // of V read transposed (channels x keys); a row is 128 bytes per 64 channels, chunk ^ (row & 7).
+  const int r8 = lane & 7, mat = lane >> 3;
+  const int k_row = r8 + (mat & 1) * 8, k_chunk = mat >> 1;
+  const int v_row = r8 + (mat >> 1) * 8, v_chunk = mat & 1;
+
+  bool dead = false;
+  int consumed = 0, landed = 0;  // tiles passed; those whose copies have been waited for
+  int4 note = make_int4(0, 0, 0, 0);
+  for (;;) {
+    const int hk = seg.j / p.head_blocks, h0 = (seg.j - hk * p.head_blocks) * R;
+    // query fragments (B operand, channels x heads)
+    uint32_t qf[kNb][kSteps][2];
+#pragma unroll
+    for (int nb = 0; nb < kNb; ++nb) {
+      const int h = h0 + nb * 8 + (lane >> 2);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(
+          p.q + seg.b * p.q_b + static_cast<long long>(hk * p.group + h) * p.q_h + (lane & 3) * 2);
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        qf[nb][k][0] = h < p.group ? __ldg(q + k * 8) : 0;
+        qf[nb][k][1] = h < p.group ? __ldg(q + k * 8 + 4) : 0;
+      }
+    }
+    float o[kSteps][kNb][4];
+    float m[kNb][2], l[kNb][2], lc[kNb][2];  // lc: the sum's compensation
+#pragma unroll
+    for (int nb = 0; nb < kNb; ++nb) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[nb][i] = -INFINITY;
+        l[nb][i] = lc[nb][i] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) o[k][nb][0] = o[k][nb][1] = o[k][nb][2] = o[k][nb][3] = 0.f;
+    }
+
+    for (int t = seg.first(warp); t < seg.end(); t += kUnitTiles) {
+      const int stage = consumed % S::kStages;
+      if (!dead && !ptx::mbar_wait(bars + stage * 8, (consumed / S::kStages) & 1, p.wait_limit)) dead = true;
+      dead = __any_sync(~0u, dead);
+      ++consumed;
+      if (!dead) landed = consumed;
+      const int keys = dead ? 0 : valid[stage];
+      if (keys > 0) {
+        const uint32_t kb = ring + stage * 2 * S::kBox, vb = kb + S::kBox;
+        if (keys < kTile) {
+          // rows past the length may hold anything: their weight is 0, and 0 * NaN is not
+          const int n = (kTile - keys) * (D / 8);
+          for (int x = lane; x < n; x += 32) {
+            const int row = keys + x / (D / 8), ch = x % (D / 8);
+            const uint32_t a = vb + (ch >> 3) * (kTile * 128) + row * 128 + (ch & 7) * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+          }
+          __syncwarp();
+        }
+        float s[kNb][4];
+#pragma unroll
+        for (int nb = 0; nb < kNb; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a[4];
+          const int ch = (k & 3) * 2 + k_chunk;
+          ldsm4(kb + (k >> 2) * (kTile * 128) + k_row * 128 + ((ch ^ (k_row & 7)) << 4), a);
+#pragma unroll
+          for (int nb = 0; nb < kNb; ++nb) mma16816(s[nb], a, qf[nb][k]);
+        }
+        const bool in0 = (lane >> 2) < keys, in1 = (lane >> 2) + 8 < keys;
+        bool moves = false;
+#pragma unroll
+        for (int nb = 0; nb < kNb; ++nb) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            s[nb][i] = in0 ? s[nb][i] * p.scale_log2 : -INFINITY;
+            s[nb][i + 2] = in1 ? s[nb][i + 2] * p.scale_log2 : -INFINITY;
+            moves |= fmaxf(s[nb][i], s[nb][i + 2]) > m[nb][i] + kSlack;
+          }
+        }
+        if (__any_sync(~0u, moves)) {
+#pragma unroll
+          for (int nb = 0; nb < kNb; ++nb) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = fmaxf(m[nb][i], fmaxf(s[nb][i], s[nb][i + 2]));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+              const float f = x == -INFINITY ? 1.f : ptx::ex2_approx(m[nb][i] - x);
+              m[nb][i] = x;
+              l[nb][i] *= f;
+              lc[nb][i] *= f;
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) {
+                o[k][nb][i] *= f;
+                o[k][nb][i + 2] *= f;
+              }
+            }
+          }
+        }
+        uint32_t pf[kParts][kNb][2];  // B operand: keys x heads, P in parts
+#pragma unroll
+        for (int nb = 0; nb < kNb; ++nb) {
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float base = m[nb][i & 1] == -INFINITY ? 0.f : m[nb][i & 1];
+            w[i] = ptx::ex2_approx(s[nb][i] - base);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float y = (w[i] + w[i + 2]) - lc[nb][i];
+            const float z = l[nb][i] + y;
+            lc[nb][i] = (z - l[nb][i]) - y;
+            l[nb][i] = z;
+          }
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            const uint32_t a = ptx::pack_bf16x2(w[0], w[1]), b = ptx::pack_bf16x2(w[2], w[3]);
+            pf[part][nb][0] = transposed(a);
+            pf[part][nb][1] = transposed(b);
+            w[0] -= ptx::bf16lo(a);
+            w[1] -= ptx::bf16hi(a);
+            w[2] -= ptx::bf16lo(b);
+            w[3] -= ptx::bf16hi(b);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a[4];
+          const int ch = (k & 3) * 2 + v_chunk;
+          ldsm4_trans(vb + (k >> 2) * (kTile * 128) + v_row * 128 + ((ch ^ (v_row & 7)) << 4), a);
+#pragma unroll
+          for (int nb = 0; nb < kNb; ++nb) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int part = kParts - 1; part >= 0; --part) mma16816(d, a, pf[part][nb]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[k][nb][i] += d[i];
+          }
+        }
+        if (keys < kTile) ptx::fence_proxy_async_smem();  // the zeroed rows, before the next copy
+      }
+      __syncwarp();
+      if (!dead) load.issue(p, ring, bars, valid, warp, lane);
+    }
+
+    // ---- the four warps' states of this segment, joined
+    const bool whole = seg.u0 == 0 && seg.u1 == seg.it.units;
+    const int slot = seg.u0 > 0 ? 0 : 1;
+#pragma unroll
+    for (int nb = 0; nb < kNb; ++nb) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = l[nb][i] - lc[nb][i];
+        x += __shfl_xor_sync(~0u, x, 4);
+        x += __shfl_xor_sync(~0u, x, 8);
+        x += __shfl_xor_sync(~0u, x, 16);
+        if (lane < 4) ml[warp * 16 + nb * 8 + lane * 2 + i] = make_float2(m[nb][i], x);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nb = 0; nb < kNb; ++nb) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int head = (lane & 3) * 2 + i;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * 16 + nb * 8 + head].x);
+        const float f = M == -INFINITY ? 0.f : ptx::ex2_approx(m[nb][i] - M);
+        float* dst = join + (warp * 8 + head) * D;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const int d = k * 16 + (lane >> 2);
+          dst[d ^ ((lane & 3) << 3)] = o[k][nb][i] * f;
+          dst[(d + 8) ^ ((lane & 3) << 3)] = o[k][nb][i + 2] * f;
+        }
+      }
+      __syncthreads();
+      {
+        constexpr int kCols = 8 * D / kThreadsPaged;  // channels of a thread: 8 (D = 128) or 4
+        const int head = threadIdx.x / (D / kCols), d0 = threadIdx.x % (D / kCols) * kCols;
+        const int h = h0 + nb * 8 + head;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * 16 + nb * 8 + head].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 x = ml[w * 16 + nb * 8 + head];
+          L += M == -INFINITY ? 0.f : x.y * ptx::ex2_approx(x.x - M);
+        }
+        float x[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; i += 4) {
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 + head) * D + ((d0 + i) ^ ((head >> 1) << 3)));
+            acc.x += y.x;
+            acc.y += y.y;
+            acc.z += y.z;
+            acc.w += y.w;
+          }
+          x[i] = acc.x;
+          x[i + 1] = acc.y;
+          x[i + 2] = acc.z;
+          x[i + 3] = acc.w;
+        }
+        if (whole) {
+          if (h < p.group) {
+            const long long row = static_cast<long long>(seg.b) * p.h_q + hk * p.group + h;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            OT* dst = static_cast<OT*>(p.out) + row * D + d0;
+#pragma unroll
+            for (int i = 0; i < kCols; i += 4) {
+              if constexpr (sizeof(OT) == 4) {
+                *reinterpret_cast<float4*>(dst + i) = make_float4(x[i] * inv, x[i + 1] * inv, x[i + 2] * inv, x[i + 3] * inv);
+              } else {
+                *reinterpret_cast<uint2*>(dst + i) = make_uint2(ptx::pack_bf16x2(x[i] * inv, x[i + 1] * inv),
+                                                                ptx::pack_bf16x2(x[i + 2] * inv, x[i + 3] * inv));
+              }
+            }
+            if (p.lse && d0 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          }
+        } else {
+          const long long at = (c * 2 + slot) * R + nb * 8 + head;
+          float* dst = p.part_o + at * D + d0;
+#pragma unroll
+          for (int i = 0; i < kCols; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          if (d0 == 0) p.part_ml[at] = make_float2(M, L);
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole && slot == 1) {
+      // the item goes on in later blocks: up to the one that holds its last unit
+      const long long last = run1 - 1 + seg.it.units - seg.u1;
+      note = make_int4(seg.b, seg.j, static_cast<int>(((last + 1) * blocks - 1) / total - c) + 1, 0);
+    }
+    if (seg.left == 0) break;
+    seg.next(p);
+  }
+  if (threadIdx.x == 0) p.meta[c] = note;
+  if (dead) {
+    if (lane == 0) {
+      atomicMax(p.status, 1);
+      // leave only when the copies still in flight have landed (or this wait has run out too)
+      for (; landed < load.count && !p.stall; ++landed)
+        ptx::mbar_wait(bars + landed % S::kStages * 8, (landed / S::kStages) & 1, p.wait_limit);
+    }
+  }
+}
+
+// Joins the parts of the item that begins in block blockIdx.x and ends in a later one: part 0 is
+// that block's second, the others are the first of the blocks behind it.  One block of threads
+// per item and query head, a thread per channel quad and a quarter (D = 64: an eighth) of the parts.
+template <int D, int kNb, typename OT>
+__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int R = 8 * kNb, kQuads = D / 4, kSlices = 128 / kQuads;
+  __shared__ float4 acc_sm[kSlices][kQuads];
+  __shared__ float red[128 / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 note = p.meta[blockIdx.x];
+  const int n = note.z;
+  if (n == 0) return;
+  const int hk = note.y / p.head_blocks, head = blockIdx.y;
+  const int h = (note.y - hk * p.head_blocks) * R + head;
+  if (h >= p.group) return;
+  auto at = [&](int i) { return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0)) * R + head; };
+  float M = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += 128) M = fmaxf(M, p.part_ml[at(i)].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const int quad = threadIdx.x % kQuads, slice = threadIdx.x / kQuads;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
+#pragma unroll 4
+  for (int i = slice; i < n; i += kSlices) {
+    const float2 x = p.part_ml[at(i)];
+    const float4 y = *reinterpret_cast<const float4*>(p.part_o + at(i) * D + quad * 4);
+    const float f = M == -INFINITY ? 0.f : ptx::ex2_approx(x.x - M);
+    L = fmaf(f, x.y, L);
+    acc.x = fmaf(f, y.x, acc.x);
+    acc.y = fmaf(f, y.y, acc.y);
+    acc.z = fmaf(f, y.z, acc.z);
+    acc.w = fmaf(f, y.w, acc.w);
+  }
+  __shared__ float l_sm[kSlices];
+  acc_sm[slice][quad] = acc;
+  if (quad == 0) l_sm[slice] = L;
+  __syncthreads();
+  if (slice != 0) return;
+  for (int s = 1; s < kSlices; ++s) {
+    const float4 y = acc_sm[s][quad];
+    acc.x += y.x;
+    acc.y += y.y;
+    acc.z += y.z;
+    acc.w += y.w;
+  }
+  L = 0.f;
+  for (int s = 0; s < kSlices; ++s) L += l_sm[s];
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const long long row = static_cast<long long>(note.x) * p.h_q + hk * p.group + h;
+  OT* dst = static_cast<OT*>(p.out) + row * D + quad * 4;
+  if constexpr (sizeof(OT) == 4)
+    *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  else
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse && quad == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// 5-D map (64 channels, row, channel block, head, page) of a paged cache: boxes of 16 rows x D.
+bool encode_cache(CUtensorMap* m, const void* base, const Strides& s, int d, int page_size, int heads, int n_pages) {
+  const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(page_size), static_cast<cuuint64_t>(d / 64),
+                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n_pages)};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(s.n_) * 2, 128, static_cast<cuuint64_t>(s.h_) * 2,
+                                 static_cast<cuuint64_t>(s.b_) * 2};
+  const cuuint32_t box[5] = {64, kTile, static_cast<cuuint32_t>(d / 64), 1, 1};
+  const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+  EncodeTiledFn fn = tensor_map_encoder();
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, elem,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int row_block(int group) { return group <= 8 ? 8 : 16; }
+
+template <int D, int kNb, typename OT>
+cudaError_t launch_typed(const PagedParams& p, int blocks, cudaStream_t st) {
+  auto kern = paged_attn_kernel<D, kNb, OT>;
+  static std::mutex mu;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PagedSmem<D>::kBytes);
+      if (e != cudaSuccess) return e;
+      ready[dev] = true;
+    }
+  }
+  kern<<<blocks, kThreadsPaged, PagedSmem<D>::kBytes, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // The join may be scheduled while the attention still runs; it waits for its end itself.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, std::min(p.group, 8 * kNb));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kNb, OT>, p);
+}
+
+template <int D, int kNb>
+cudaError_t launch_out(const PagedParams& p, bool f32, int blocks, cudaStream_t st) {
+  return f32 ? launch_typed<D, kNb, float>(p, blocks, st) : launch_typed<D, kNb, __nv_bfloat16>(p, blocks, st);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int, int, int d) { return 512 * 2 * 16 * (static_cast<size_t>(d) + 2) * 4; }
+// Partials of two segments of each block: fp32 sums, (maximum, sum) pairs, and the join's notes.
+size_t paged_attn_workspace(int h_q, int h_kv, int d) {
+  const size_t rows = static_cast<size_t>(kMaxBlocks) * 2 * row_block(h_q / h_kv);
+  return rows * d * 4 + rows * 8 + kMaxBlocks * 16;
+}
 
 cudaError_t launch_paged_attn(const PagedAttnLaunch& a, cudaStream_t st) {
-  PagedParams p{a};
-  const unsigned grid = static_cast<unsigned>(a.batch) * a.h_q;
-  if (a.d == 64) {
-    if (a.out_f32) paged_attn_simple<64, float><<<grid, kWarps * 32, 0, st>>>(p);
-    else paged_attn_simple<64, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(p);
-  } else {
-    if (a.out_f32) paged_attn_simple<128, float><<<grid, kWarps * 32, 0, st>>>(p);
-    else paged_attn_simple<128, __nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  PagedParams p;
+  if (!encode_cache(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages) ||
+      !encode_cache(&p.tm_v, a.v_cache, a.vs, a.d, a.page_size, a.h_kv, a.n_pages))
+    return cudaErrorInvalidValue;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.q_b = a.q_b;
+  p.q_h = a.q_h;
+  p.table = a.table;
+  p.table_stride = a.table_stride;
+  p.seq_lens = a.seq_lens;
+  p.selected = a.selected;
+  p.n_selected = a.n_selected;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.batch = a.batch;
+  p.h_q = a.h_q;
+  p.h_kv = a.h_kv;
+  p.group = a.h_q / a.h_kv;
+  const int R = row_block(p.group);
+  p.head_blocks = (p.group + R - 1) / R;
+  p.page_size = a.page_size;
+  p.page_tiles = a.page_size / kTile;
+  p.n_pages = a.n_pages;
+  p.max_len = a.max_pages * a.page_size;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.status = a.status;
+  stall_injection(&p.stall, &p.wait_limit);
+  const size_t rows = static_cast<size_t>(kMaxBlocks) * 2 * R;
+  p.part_o = static_cast<float*>(a.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * a.d);
+  p.meta = reinterpret_cast<int4*>(p.part_ml + rows);
+  // Two blocks of 113 KB of shared memory fit one SM.
+  int blocks = std::min(kMaxBlocks, 2 * host::sm_count());
+  if (grid_limit() > 0) blocks = std::min(blocks, grid_limit());
+  if (a.d == 64)
+    return R == 8 ? launch_out<64, 1>(p, a.out_f32, blocks, st) : launch_out<64, 2>(p, a.out_f32, blocks, st);
+  return R == 8 ? launch_out<128, 1>(p, a.out_f32, blocks, st) : launch_out<128, 2>(p, a.out_f32, blocks, st);
 }
 
 }  // namespace ditattn

@@ -341,6 +341,25 @@ def test_attn_capped_grid():
         da.set_grid_limit(0)
 
 
+def test_attn_reports_a_wait_that_runs_out():
+    """With the copies withheld every wait runs out after its limit, the launch ends and the check
+    says so; the next call is right again."""
+    q, k, v, table, sl = make_case([500, 0, 40], 8, 2, 128, 16, seed=33)
+    good = da.paged_attn_fwd(q, k, v, table, sl)
+    da.check()
+    try:
+        da.inject_stall(True, 200_000)
+        da.paged_attn_fwd(q, k, v, table, sl)
+        with pytest.raises(da.DitError) as e:
+            da.check()
+        assert e.value.status == da.DIT_ERR_TIMEOUT
+    finally:
+        da.inject_stall(False)
+    o, lse = da.paged_attn_fwd(q, k, v, table, sl)
+    da.check()
+    assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+
+
 def test_attn_offsets_past_32_bits():
     """Pages that begin more than 2^32 bytes and more than 2^31 elements into the cache."""
     H, P, D = 2, 64, 128
