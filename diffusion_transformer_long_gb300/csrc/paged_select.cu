@@ -1,87 +1,441 @@
 // The pages whose keys can score highest for one query token of each request:
 //   score_i = max_h sum_d max(q_hd lo_id, q_hd hi_id)
-// over the query heads h of a key/value head's group, in 64 bits; listed are the newest page
-// and the top_k - 1 others with the highest scores, ties to the lower index.
+// over the query heads h of a key/value head's group; listed are the newest page and the
+// top_k - 1 others with the highest scores, ties to the lower index, by the scores in 64 bits.
 //
-// A block per (request, key/value head) scores its pages, ranks each against all others and
-// writes those of the first top_k in ascending order.
+// Scoring.  max(q lo, q hi) = max(q, 0) hi + min(q, 0) lo, so the scores of 16 pages against 8
+// heads are a matrix product over 2 D channels, on mma.sync straight from the summaries in
+// global memory: a lane's 16-byte loads hold its operands once the channels are renumbered (the
+// order of a sum's terms is free).  4 D bytes per page and head: bound by HBM, or by latency.
+//
+// Choosing.  Products of bf16 are exact in 32 bits but their sums are not, and two pages at the
+// border may differ by less.  A second product, of the magnitudes, bounds a score's error by
+// kErr sum |q| |k| =: e.  One block per (request, key/value head) narrows the score of the last
+// page in down to a histogram bin; a page more than 2 e above the bin is in, one more than 2 e
+// below is out, and those between, a handful, are scored again in 64 bits and ranked.  A score
+// that is not finite in 32 bits sends all pages of its row that way.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "paged_launch.h"
+#include "sm103_ptx.cuh"
 
 namespace ditattn {
 namespace {
 
-constexpr int kSelThreads = 256;
+constexpr int kScoreWarps = 8;
+constexpr int kChunk = 16;          // pages of a warp
+constexpr int kPickThreads = 512;
+constexpr int kBins = 1024;
+constexpr int kRanked = kPickThreads;  // pages between that are ranked pair by pair
+constexpr int kCached = 8192;       // keys held in shared memory
+// A 32-bit score is summed in 2 D / 16 <= 16 steps of 16 products and the running sum, each of
+// the 17 terms cut to within 2^-23 of the step's largest: at most 16 * 17 * 2^-23 of sum |q| |k|.
+constexpr double kErr = 16 * 17 / 8388608.0;
+constexpr uint32_t kLowest = 0x007FFFFFu;    // the key of -inf: a page without keys
+constexpr uint32_t kInfKey = 0xFF800000u;    // the key of +inf
+constexpr uint32_t kUnknown = 0xFFFFFFFFu;   // not finite in 32 bits
 
-__global__ void __launch_bounds__(kSelThreads) paged_select_simple(const SelectLaunch a) {
-  __shared__ int written;
-  const int b = blockIdx.x / a.h_kv, g = blockIdx.x % a.h_kv, group = a.h_q / a.h_kv;
-  const int P = a.page_size;
-  const int len = min(max(0, a.seq_lens[b]), a.max_pages * P);
-  const int n = pages_of(len, P);
-  int* out = a.selected + static_cast<long long>(blockIdx.x) * a.top_k;
-  double* score = static_cast<double*>(a.workspace) + static_cast<long long>(blockIdx.x) * a.max_pages;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + g * group * a.q_h;
-  for (int i = threadIdx.x; i < n; i += kSelThreads) {
-    double best = -INFINITY;
-    const int page = a.table[b * a.table_stride + i];
-    if (i == n - 1) {
-      best = INFINITY;
-    } else if (page >= 0 && page < a.n_pages) {
-      const __nv_bfloat16* lo = static_cast<const __nv_bfloat16*>(a.summary) + (static_cast<long long>(page) * a.h_kv + g) * 2 * a.d;
-      for (int h = 0; h < group; ++h) {
-        double s = 0;
-        for (int d = 0; d < a.d; ++d) {
-          const double x = static_cast<double>(__bfloat162float(q[h * a.q_h + d]));
-          const double u = x * static_cast<double>(__bfloat162float(lo[d])), v = x * static_cast<double>(__bfloat162float(lo[a.d + d]));
-          s += u != u ? u : v != v ? v : fmax(u, v);
-        }
-        if (s != s) s = INFINITY;
-        best = fmax(best, s);
+struct PickParams {
+  SelectLaunch a;
+  uint32_t* keys;   // [batch * h_kv][max_pages]: scores, as integers of the same order
+  float* bounds;    // [batch * h_kv][chunks]: the largest sum |q| |k| of 16 pages
+  double* exact;    // [batch * h_kv][max_pages]: 64-bit scores of the pages between
+  int chunks;
+};
+
+// Unsigned integers in the order of the floating-point numbers (no NaN).
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long key_of(double x) {
+  const unsigned long long b = __double_as_longlong(x == 0.0 ? 0.0 : x);  // -0 ties with +0
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t half_of(uint32_t w, bool positive) {
+  __nv_bfloat162 x, z = __float2bfloat162_rn(0.f);
+  memcpy(&x, &w, 4);
+  x = positive ? __hmax2_nan(x, z) : __hmin2_nan(x, z);
+  memcpy(&w, &x, 4);
+  return w;
+}
+
+__device__ __forceinline__ int pages_now(const SelectLaunch& a, int b) {
+  return pages_of(min(max(0, a.seq_lens[b]), a.max_pages * a.page_size), a.page_size);
+}
+
+// A warp scores 16 pages of one (request, key/value head).
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __grid_constant__ PickParams p) {
+  constexpr int kLoads = 2 * D / 32;  // 64-byte pieces of a page's [lo | hi]
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const SelectLaunch& a = p.a;
+  const int bg = blockIdx.y + blockIdx.z * gridDim.y;
+  if (bg >= a.batch * a.h_kv) return;
+  const int b = bg / a.h_kv, g = bg - b * a.h_kv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 3;
+  const int chunk = blockIdx.x * kScoreWarps + warp, i0 = chunk * kChunk;
+  const int n = pages_now(a, b);
+  if (i0 >= n || n <= a.top_k) return;  // nothing to choose
+  int page = -1;
+  if (lane < kChunk && i0 + lane < n) page = a.table[b * a.table_stride + i0 + lane];
+  if (page >= a.n_pages) page = -1;
+  const int p0 = __shfl_sync(~0u, page, lane >> 2), p1 = __shfl_sync(~0u, page, (lane >> 2) + 8);
+  uint4 x0[kLoads], x1[kLoads];
+  const uint4* s0 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.summary) +
+                                                   (static_cast<long long>(max(p0, 0)) * a.h_kv + g) * 2 * D) + j;
+  const uint4* s1 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.summary) +
+                                                   (static_cast<long long>(max(p1, 0)) * a.h_kv + g) * 2 * D) + j;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    x0[i] = p0 >= 0 ? __ldg(s0 + 4 * i) : none;
+    x1[i] = p1 >= 0 ? __ldg(s1 + 4 * i) : none;
+  }
+  const int group = a.h_q / a.h_kv;
+  float best0 = -INFINITY, best1 = -INFINITY, mag = 0.f;
+  bool odd0 = false, odd1 = false;
+  for (int h0 = 0; h0 < group; h0 += 8) {
+    const int h = h0 + (lane >> 2);
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b +
+                                                    static_cast<long long>(g * group + min(h, group - 1)) * a.q_h) + j;
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      // lane j's words of piece i: channels 8 j .. 8 j + 7 of 32, two products of 16
+      const bool hi = i >= kLoads / 2;
+      uint4 y = __ldg(q + 4 * (i % (kLoads / 2)));
+      y.x = half_of(y.x, hi);
+      y.y = half_of(y.y, hi);
+      y.z = half_of(y.z, hi);
+      y.w = half_of(y.w, hi);
+      constexpr uint32_t kAbs = 0x7fff7fffu;
+      mma16816(s, x0[i].x, x1[i].x, x0[i].y, x1[i].y, y.x, y.y);
+      mma16816(s, x0[i].z, x1[i].z, x0[i].w, x1[i].w, y.z, y.w);
+      mma16816(m, x0[i].x & kAbs, x1[i].x & kAbs, x0[i].y & kAbs, x1[i].y & kAbs, y.x & kAbs, y.y & kAbs);
+      mma16816(m, x0[i].z & kAbs, x1[i].z & kAbs, x0[i].w & kAbs, x1[i].w & kAbs, y.z & kAbs, y.w & kAbs);
+    }
+    // columns past the group repeat its last head: they change neither maximum
+    odd0 |= !(fabsf(s[0]) < INFINITY && fabsf(s[1]) < INFINITY);
+    odd1 |= !(fabsf(s[2]) < INFINITY && fabsf(s[3]) < INFINITY);
+    best0 = fmaxf(best0, fmaxf(s[0], s[1]));
+    best1 = fmaxf(best1, fmaxf(s[2], s[3]));
+    mag = fmaxf(fmaxf(mag, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+  }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    best0 = fmaxf(best0, __shfl_xor_sync(~0u, best0, d));
+    best1 = fmaxf(best1, __shfl_xor_sync(~0u, best1, d));
+    odd0 |= __shfl_xor_sync(~0u, static_cast<int>(odd0), d) != 0;
+    odd1 |= __shfl_xor_sync(~0u, static_cast<int>(odd1), d) != 0;
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) mag = fmaxf(mag, __shfl_xor_sync(~0u, mag, d));
+  uint32_t* keys = p.keys + static_cast<long long>(bg) * a.max_pages;
+  if (j == 0) {
+    const int i = i0 + (lane >> 2);
+    if (i < n) keys[i] = p0 < 0 ? kLowest : odd0 ? kUnknown : key_of(best0);
+    if (i + 8 < n) keys[i + 8] = p1 < 0 ? kLowest : odd1 ? kUnknown : key_of(best1);
+  }
+  if (lane == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
+}
+
+// Block-wide sums and extremes; `sm` is free again on return.
+template <typename T, typename F>
+__device__ __forceinline__ T block_all(T x, T* sm, F f) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = f(x, __shfl_xor_sync(~0u, x, d));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = sm[threadIdx.x & (kPickThreads / 32 - 1)];
+#pragma unroll
+  for (int d = kPickThreads / 64; d > 0; d >>= 1) x = f(x, __shfl_xor_sync(~0u, x, d));
+  return x;
+}
+// Sum over the lower threads, and over all.
+__device__ __forceinline__ int block_below(int x, int* sm, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int up = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(~0u, up, d);
+    if (lane >= d) up += y;
+  }
+  __syncthreads();
+  if (lane == 31) sm[warp] = up;
+  __syncthreads();
+  int w = lane < kPickThreads / 32 ? sm[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(~0u, w, d);
+    if (lane >= d) w += y;
+  }
+  all = __shfl_sync(~0u, w, kPickThreads / 32 - 1);
+  const int before = __shfl_sync(~0u, w, max(warp - 1, 0));
+  return up - x + (warp > 0 ? before : 0);
+}
+
+// The 64-bit score of table column i, by one warp.
+__device__ double exact_score(const SelectLaunch& a, int b, int g, int i) {
+  const int lane = threadIdx.x & 31, group = a.h_q / a.h_kv;
+  const int page = a.table[b * a.table_stride + i];
+  if (page < 0 || page >= a.n_pages) return -INFINITY;
+  const __nv_bfloat16* lo = static_cast<const __nv_bfloat16*>(a.summary) + (static_cast<long long>(page) * a.h_kv + g) * 2 * a.d;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + static_cast<long long>(g) * group * a.q_h;
+  double best = -INFINITY;
+  for (int h = 0; h < group; ++h) {
+    double s = 0.0;
+    for (int d = lane; d < a.d; d += 32) {
+      const double x = __bfloat162float(q[h * a.q_h + d]);
+      const double u = x * __bfloat162float(lo[d]), v = x * __bfloat162float(lo[a.d + d]);
+      s += u != u ? u : v != v ? v : fmax(u, v);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+    best = fmax(best, s != s ? static_cast<double>(INFINITY) : s);
+  }
+  return best;
+}
+
+__global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_constant__ PickParams p) {
+  __shared__ uint32_t cache[kCached];
+  __shared__ int bins[kBins];
+  __shared__ int between[kRanked];
+  __shared__ unsigned long long ranked[kRanked];
+  __shared__ unsigned long long red[kPickThreads / 32];
+  __shared__ int count, bin_found, bin_above;
+  __shared__ unsigned long long border_sm;
+  __shared__ int quota_sm;
+  int* red_i = reinterpret_cast<int*>(red);
+  uint32_t* red_u = reinterpret_cast<uint32_t*>(red);
+  float* red_f = reinterpret_cast<float*>(red);
+  const SelectLaunch& a = p.a;
+  const int bg = blockIdx.x, b = bg / a.h_kv, g = bg - b * a.h_kv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = pages_now(a, b);
+  int* out = a.selected + static_cast<long long>(bg) * a.top_k;
+  if (n <= a.top_k || a.top_k == 1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // a reader of the last call's list may still run
+    for (int i = tid; i < a.top_k; i += kPickThreads) out[i] = a.top_k == 1 ? n - 1 : i < n ? i : -1;
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int others = n - 1, want = a.top_k - 1;  // 1 <= want < others
+  const uint32_t* all_keys = p.keys + static_cast<long long>(bg) * a.max_pages;
+  double* exact = p.exact + static_cast<long long>(bg) * a.max_pages;
+  const bool cached = others <= kCached;
+  uint32_t lo = ~0u, hi = 0;
+  for (int i = tid; i < others; i += kPickThreads) {
+    const uint32_t k = all_keys[i];
+    if (cached) cache[i] = k;
+    lo = min(lo, k);
+    hi = max(hi, k);
+  }
+  float mag = 0.f;
+  for (int i = tid; i < (n + kChunk - 1) / kChunk; i += kPickThreads)
+    mag = fmaxf(mag, p.bounds[static_cast<long long>(bg) * p.chunks + i]);
+  lo = block_all(lo, red_u, [](uint32_t x, uint32_t y) { return min(x, y); });
+  hi = block_all(hi, red_u, [](uint32_t x, uint32_t y) { return max(x, y); });
+  mag = block_all(mag, red_f, [](float x, float y) { return fmaxf(x, y); });
+  const uint32_t* keys = cached ? cache : all_keys;
+  // (the magnitudes' own sum may be short by the same error; 2^-110: terms below 32 bits' range)
+  const double wide = 2.002 * (kErr * mag + 7.7e-34);
+  const bool unknown = hi >= kInfKey || !(mag < INFINITY);
+  double from = -INFINITY, to = INFINITY;  // pages scored above `to` are in, below `from` out
+  int above = 0;                           // pages above the range [lo, hi]
+  for (; !unknown;) {
+    const int bits = 32 - __clz(hi - lo);
+    const int shift = max(0, bits - 10);
+    for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < others; i += kPickThreads) {
+      const uint32_t k = keys[i];
+      if (k >= lo && k <= hi) atomicAdd(bins + ((k - lo) >> shift), 1);
+    }
+    __syncthreads();
+    // thread t holds bins 1023 - 2 t and 1022 - 2 t: sums run from the highest scores down
+    const int first = bins[kBins - 1 - 2 * tid], second = bins[kBins - 2 - 2 * tid];
+    int all;
+    const int over = above + block_below(first + second, red_i, all);
+    if (over < want && over + first + second >= want) {
+      const bool in_first = over + first >= want;
+      bin_found = in_first ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
+      bin_above = in_first ? over : over + first;
+    }
+    __syncthreads();
+    const uint32_t lo2 = lo + (static_cast<uint32_t>(bin_found) << shift);
+    hi = min(hi, lo2 + ((1u << shift) - 1));
+    lo = lo2;
+    above = bin_above;
+    from = static_cast<double>(value_of(lo)) - wide;
+    to = static_cast<double>(value_of(hi)) + wide;
+    int mine = 0;
+    for (int i = tid; i < others; i += kPickThreads) {
+      const double s = value_of(keys[i]);
+      if (s >= from && s <= to) ++mine;
+    }
+    const int sum = block_all(mine, red_i, [](int x, int y) { return x + y; });
+    if (sum <= kRanked || lo == hi) break;
+  }
+  // the pages between, scored in 64 bits
+  if (tid == 0) count = 0;
+  __syncthreads();
+  int sure = 0;
+  for (int i0 = 0; i0 < others; i0 += kPickThreads) {
+    const int i = i0 + tid;
+    bool mid = false;
+    if (i < others) {
+      if (unknown) {
+        mid = true;
+      } else {
+        const double s = value_of(keys[i]);
+        mid = s >= from && s <= to;
+        sure += s > to;
       }
     }
-    score[i] = best;
-  }
-  if (threadIdx.x == 0) written = 0;
-  __syncthreads();
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + threadIdx.x;
-    int in = 0;
-    if (i < n) {
-      int better = i == n - 1 ? 0 : 1;  // the newest page comes first, whatever the others score
-      for (int j = 0; j < n - 1 && i < n - 1; ++j)
-        better += score[j] > score[i] || (score[j] == score[i] && j < i);
-      in = better < a.top_k;
+    if (mid) {
+      const int at = atomicAdd(&count, 1);
+      if (at < kRanked) between[at] = i;
     }
-    __shared__ int warp_n[kSelThreads / 32];
-    const unsigned bal = __ballot_sync(~0u, in);
-    if ((threadIdx.x & 31) == 0) warp_n[threadIdx.x >> 5] = __popc(bal);
-    __syncthreads();
-    int at = written + __popc(bal & ((1u << (threadIdx.x & 31)) - 1));
-    for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) at += warp_n[w];
-    if (in) out[at] = i;
-    __syncthreads();
-    if (threadIdx.x == 0)
-      for (int w = 0; w < kSelThreads / 32; ++w) written += warp_n[w];
-    __syncthreads();
   }
-  for (int k = written + threadIdx.x; k < a.top_k; k += kSelThreads) out[k] = -1;
+  sure = block_all(sure, red_i, [](int x, int y) { return x + y; });
+  const int mids = count, rest = want - sure;  // 1 <= rest <= mids
+  unsigned long long border = 0;  // pages between with a higher 64-bit key are in,
+  int quota = others;             // and `quota` of those with this one
+  if (rest < mids) {
+    if (mids <= kRanked) {
+      for (int x = warp; x < mids; x += kPickThreads / 32) {
+        const double s = exact_score(a, b, g, between[x]);
+        if (lane == 0) {
+          ranked[x] = key_of(s);
+          exact[between[x]] = s;
+        }
+      }
+      __syncthreads();
+      if (tid < mids) {
+        const unsigned long long k = ranked[tid];
+        int higher = 0, same = 0;
+        for (int x = 0; x < mids; ++x) {
+          higher += ranked[x] > k;
+          same += ranked[x] == k;
+        }
+        if (higher < rest && higher + same >= rest) {
+          border_sm = k;
+          quota_sm = rest - higher;
+        }
+      }
+      __syncthreads();
+      border = border_sm;
+      quota = quota_sm;
+    } else {
+      // many alike (or not finite): the border by bisection of the 64-bit keys
+      for (int i = warp; i < others; i += kPickThreads / 32) {
+        const double k32 = unknown ? 0.0 : value_of(keys[i]);
+        if (!unknown && !(k32 >= from && k32 <= to)) continue;
+        const double s = exact_score(a, b, g, i);
+        if (lane == 0) exact[i] = s;
+      }
+      __syncthreads();
+      auto at_least = [&](unsigned long long k) {
+        int c = 0;
+        for (int i = tid; i < others; i += kPickThreads) {
+          const double k32 = unknown ? 0.0 : value_of(keys[i]);
+          if (unknown || (k32 >= from && k32 <= to)) c += key_of(exact[i]) >= k;
+        }
+        return block_all(c, red_i, [](int x, int y) { return x + y; });
+      };
+      for (int bit = 63; bit >= 0; --bit) {
+        const unsigned long long k = border | 1ull << bit;
+        if (at_least(k) >= rest) border = k;
+      }
+      quota = border == ~0ull ? rest : rest - at_least(border + 1);
+    }
+  }
+  // write the pages in, in ascending order: every thread takes a stretch of the columns
+  const int per = (others + kPickThreads - 1) / kPickThreads;
+  const int i0 = min(others, tid * per), i1 = min(others, i0 + per);
+  auto state = [&](int i) {  // 2: in, 1: at the border, 0: out
+    if (!unknown) {
+      const double s = value_of(keys[i]);
+      if (s > to) return 2;
+      if (s < from) return 0;
+    }
+    if (rest == mids) return 2;
+    const unsigned long long k = key_of(exact[i]);
+    return k > border ? 2 : k == border ? 1 : 0;
+  };
+  __syncthreads();
+  int in = 0, ties = 0, all;
+  for (int i = i0; i < i1; ++i) {
+    const int s = state(i);
+    in += s == 2;
+    ties += s == 1;
+  }
+  const int ties_before = block_below(ties, red_i, all);
+  in += max(0, min(ties, quota - ties_before));
+  int at = block_below(in, red_i, all), tie = ties_before;
+  for (int i = i0; i < i1; ++i) {
+    const int s = state(i);
+    if (s == 2 || (s == 1 && tie++ < quota)) out[at++] = i;
+  }
+  if (tid == 0) out[a.top_k - 1] = n - 1;
 }
+
+size_t aligned256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
+// Keys, bounds and 64-bit scores of every (request, key/value head).
 size_t paged_select_workspace(int batch, int h_kv, int max_pages) {
-  return static_cast<size_t>(batch) * h_kv * max_pages * 8;
+  const size_t rows = static_cast<size_t>(batch) * h_kv, chunks = (static_cast<size_t>(max_pages) + kChunk - 1) / kChunk;
+  return aligned256(rows * max_pages * 8) + aligned256(rows * max_pages * 4) + aligned256(rows * chunks * 4);
 }
 
 cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
-  paged_select_simple<<<static_cast<unsigned>(a.batch) * a.h_kv, kSelThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  PickParams p;
+  p.a = a;
+  p.chunks = static_cast<int>((static_cast<long long>(a.max_pages) + kChunk - 1) / kChunk);
+  const size_t rows = static_cast<size_t>(a.batch) * a.h_kv;
+  char* ws = static_cast<char*>(a.workspace);
+  p.exact = reinterpret_cast<double*>(ws);
+  p.keys = reinterpret_cast<uint32_t*>(ws + aligned256(rows * a.max_pages * 8));
+  p.bounds = reinterpret_cast<float*>(ws + aligned256(rows * a.max_pages * 8) + aligned256(rows * a.max_pages * 4));
+  if (rows > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+  const unsigned rows_y = static_cast<unsigned>(std::min<size_t>(rows, 32768));
+  const dim3 grid((p.chunks + kScoreWarps - 1) / kScoreWarps, rows_y, static_cast<unsigned>((rows + rows_y - 1) / rows_y));
+  if (a.d == 64) paged_score_kernel<64><<<grid, kScoreWarps * 32, 0, st>>>(p);
+  else paged_score_kernel<128><<<grid, kScoreWarps * 32, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(kPickThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_pick_kernel, p);
 }
 
 }  // namespace ditattn

@@ -8,8 +8,8 @@ every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -730,57 +730,78 @@ def attention(q, k, v, scale=None, chunks=None, out_dtype=torch.float32,
 # [B, max_pages], seq_lens int32 [B].
 
 
-def _launch_context(device, stream):
-    """The context a paged call allocates and launches in: `stream` becomes the current stream, so
-    that what the call allocates belongs to the stream that uses it."""
+def _elsewhere(device, stream):
+    """The context a paged call has to run in, or None where the current device and stream are the
+    ones asked for.  The call runs itself again inside it, so that what it allocates belongs to the
+    stream that uses it."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return None
 
 
-def _check_tensor(t, name, dtype, shape, device=None, contiguous=True):
-    """`t` is a CUDA tensor (on `device`) of `dtype` and `shape` (None: any extent)."""
+def _check_tensor(t, name, dtype, shape, index, rows=False):
+    """Raises unless `t` is a `dtype` tensor of `shape` (None: any extent) on CUDA device `index`,
+    contiguous, or (rows=True) with a contiguous last dimension."""
+    try:  # one cheap test for the usual case: these calls are bound by the host at small sizes
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != len(shape) or any(e is not None and e != x for e, x in zip(shape, t.shape)):
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if contiguous and not t.is_contiguous():
+    if not rows and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not contiguous and t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if rows and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
-    return t
 
 
-def _check_paged(k_cache, v_cache, device):
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check_tensor(t, name, torch.bfloat16, (None,) * 4, device, contiguous=False)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have one shape [n_pages, H_kv, page_size, D]")
+def _check_rows(t, name, dims):
+    """(device, CUDA device number) of a bf16 view of `dims` dimensions with a contiguous last one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    index = t.get_device()
+    _check_tensor(t, name, torch.bfloat16, (None,) * dims, index, rows=True)
+    return t.device, index
+
+
+def _check_caches(k_cache, v_cache, index):
+    """(n_pages, H_kv, page_size, D) of the two caches."""
+    _check_tensor(k_cache, "k_cache", torch.bfloat16, (None,) * 4, index, rows=True)
+    _check_tensor(v_cache, "v_cache", torch.bfloat16, k_cache.shape, index, rows=True)
     return k_cache.shape
 
 
-def _check_table(block_table, seq_lens, B, device):
+def _check_table(block_table, seq_lens, B, index):
     """(max_pages, table_stride) of the batch's block table."""
-    _check_tensor(seq_lens, "seq_lens", torch.int32, (B,), device)
-    _check_tensor(block_table, "block_table", torch.int32, (B, None), device, contiguous=False)
-    return block_table.shape[1], (block_table.stride(0) if B > 1 else block_table.shape[1])
+    _check_tensor(seq_lens, "seq_lens", torch.int32, (B,), index)
+    _check_tensor(block_table, "block_table", torch.int32, (B, None), index, rows=True)
+    max_pages = block_table.shape[1]
+    return max_pages, (block_table.stride(0) if B > 1 else max_pages)
+
+
+@functools.lru_cache(maxsize=None)
+def _attn_workspace_bytes(Hq, Hkv, D):
+    return lib().dit_paged_attn_workspace_bytes(1, Hq, Hkv, D)
 
 
 def _workspace(workspace, need, device):
+    """(pointer holder, bytes) of a call's workspace: the caller's, or a new one."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous() \
-            or workspace.numel() * workspace.element_size() < need:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    size = workspace.numel() * workspace.element_size()
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous() or size < need:
         raise ValueError(f"workspace must be a contiguous buffer of at least {need} bytes on {device}")
-    return workspace
+    return workspace, size
 
 
 def paged_plan(new_lens, seq_lens, block_table, free_pages, n_free, page_size, n_pages, max_tokens,
@@ -791,32 +812,42 @@ def paged_plan(new_lens, seq_lens, block_table, free_pages, n_free, page_size, n
 
     Returns (seq_lens_out [B], n_free_out [1], cu_new [B + 1], slots [max_tokens]); seq_lens_out may
     be seq_lens and n_free_out may be n_free (updated in place)."""
-    _check_tensor(new_lens, "new_lens", torch.int32, (None,))
-    dev, B = new_lens.device, new_lens.shape[0]
-    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
-    _check_tensor(free_pages, "free_pages", torch.int32, (None,), dev)
-    _check_tensor(n_free, "n_free", torch.int32, (1,), dev)
+    if not isinstance(new_lens, torch.Tensor) or not new_lens.is_cuda:
+        raise ValueError("new_lens must be a CUDA tensor")
+    dev, index = new_lens.device, new_lens.get_device()
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_plan(new_lens, seq_lens, block_table, free_pages, n_free, page_size, n_pages,
+                              max_tokens, seq_lens_out, n_free_out, cu_new, slots)
+    i32 = torch.int32
+    _check_tensor(new_lens, "new_lens", i32, (None,), index)
+    B = new_lens.shape[0]
+    max_pages, stride = _check_table(block_table, seq_lens, B, index)
+    _check_tensor(free_pages, "free_pages", i32, (None,), index)
+    _check_tensor(n_free, "n_free", i32, (1,), index)
     max_tokens = int(max_tokens)
-    for t, name, dt, n in ((seq_lens_out, "seq_lens_out", torch.int32, B),
-                           (n_free_out, "n_free_out", torch.int32, 1),
-                           (cu_new, "cu_new", torch.int32, B + 1),
-                           (slots, "slots", torch.int64, max_tokens)):
-        if t is not None:
-            _check_tensor(t, name, dt, (n,), dev)
-    with _launch_context(dev, stream):
-        if seq_lens_out is None:
-            seq_lens_out = torch.empty(B, dtype=torch.int32, device=dev)
-        if n_free_out is None:
-            n_free_out = torch.empty(1, dtype=torch.int32, device=dev)
-        if cu_new is None:
-            cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        if slots is None:
-            slots = torch.empty(max(0, max_tokens), dtype=torch.int64, device=dev)
-        st = lib().dit_paged_plan(new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-                                  stride, free_pages.data_ptr(), n_free.data_ptr(),
-                                  seq_lens_out.data_ptr(), n_free_out.data_ptr(), cu_new.data_ptr(),
-                                  slots.data_ptr(), B, max_pages, int(page_size), int(n_pages),
-                                  free_pages.shape[0], max_tokens, _stream(dev, stream))
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(B, dtype=i32, device=dev)
+    else:
+        _check_tensor(seq_lens_out, "seq_lens_out", i32, (B,), index)
+    if n_free_out is None:
+        n_free_out = torch.empty(1, dtype=i32, device=dev)
+    else:
+        _check_tensor(n_free_out, "n_free_out", i32, (1,), index)
+    if cu_new is None:
+        cu_new = torch.empty(B + 1, dtype=i32, device=dev)
+    else:
+        _check_tensor(cu_new, "cu_new", i32, (B + 1,), index)
+    if slots is None:
+        slots = torch.empty(max(0, max_tokens), dtype=torch.int64, device=dev)
+    else:
+        _check_tensor(slots, "slots", torch.int64, (max_tokens,), index)
+    st = lib().dit_paged_plan(new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                              stride, free_pages.data_ptr(), n_free.data_ptr(),
+                              seq_lens_out.data_ptr(), n_free_out.data_ptr(), cu_new.data_ptr(),
+                              slots.data_ptr(), B, max_pages, page_size, n_pages,
+                              free_pages.shape[0], max_tokens, torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_paged_plan")
     return seq_lens_out, n_free_out, cu_new, slots
@@ -826,22 +857,26 @@ def paged_kv_write(k_new, v_new, slots, k_cache, v_cache, summary=None, stream=N
     """dit_paged_kv_write: k_new, v_new bf16 [T, H_kv, D] views (slices of a fused projection need no
     copy) into the slots (int64 [T], below 0: skipped) of the caches; with `summary` (bf16
     [n_pages, H_kv, 2, D]) each touched page's channel minimum and maximum is kept up to date."""
-    _check_tensor(k_new, "k_new", torch.bfloat16, (None,) * 3, contiguous=False)
-    dev, (T, H, D) = k_new.device, k_new.shape
-    _check_tensor(v_new, "v_new", torch.bfloat16, (T, H, D), dev, contiguous=False)
-    n_pages, Hc, P, Dc = _check_paged(k_cache, v_cache, dev)
-    if (Hc, Dc) != (H, D):
+    dev, index = _check_rows(k_new, "k_new", 3)
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_kv_write(k_new, v_new, slots, k_cache, v_cache, summary)
+    T, H, D = k_new.shape
+    _check_tensor(v_new, "v_new", torch.bfloat16, (T, H, D), index, rows=True)
+    n_pages, Hc, P, Dc = _check_caches(k_cache, v_cache, index)
+    if Hc != H or Dc != D:
         raise ValueError(f"the caches hold {Hc} heads of {Dc}, the new rows {H} of {D}")
-    _check_tensor(slots, "slots", torch.int64, (T,), dev)
+    _check_tensor(slots, "slots", torch.int64, (T,), index)
     if summary is not None:
-        _check_tensor(summary, "summary", torch.bfloat16, (n_pages, H, 2, D), dev)
-    kn, vn = (Strides(D, t.stride(1), t.stride(0)) for t in (k_new, v_new))
-    ks, vs = view_strides(k_cache), view_strides(v_cache)
-    with _launch_context(dev, stream):
-        st = lib().dit_paged_kv_write(k_new.data_ptr(), kn, v_new.data_ptr(), vn, slots.data_ptr(),
-                                      k_cache.data_ptr(), ks, v_cache.data_ptr(), vs,
-                                      None if summary is None else summary.data_ptr(), T, H, D, P,
-                                      n_pages, _stream(dev, stream))
+        _check_tensor(summary, "summary", torch.bfloat16, (n_pages, H, 2, D), index)
+    kn, kh, _ = k_new.stride()
+    vn, vh, _ = v_new.stride()
+    st = lib().dit_paged_kv_write(k_new.data_ptr(), Strides(D, kh, kn), v_new.data_ptr(), Strides(D, vh, vn),
+                                  slots.data_ptr(), k_cache.data_ptr(), Strides(*k_cache.stride()[:3]),
+                                  v_cache.data_ptr(), Strides(*v_cache.stride()[:3]),
+                                  None if summary is None else summary.data_ptr(), T, H, D, P,
+                                  n_pages, torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_paged_kv_write")
 
@@ -854,35 +889,40 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, selected=None, ou
     pages.  The workspace is allocated with torch unless given.
 
     Returns (out [B, H_q, D] of out_dtype, lse fp32 [B, H_q]); with_lse=False returns (out, None)."""
-    _check_tensor(q, "q", torch.bfloat16, (None,) * 3, contiguous=False)
-    dev, (B, Hq, D) = q.device, q.shape
-    n_pages, Hkv, P, Dc = _check_paged(k_cache, v_cache, dev)
+    dev, index = _check_rows(q, "q", 3)
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, selected, out, lse, scale,
+                                  out_dtype, workspace, None, with_lse)
+    B, Hq, D = q.shape
+    n_pages, Hkv, P, Dc = _check_caches(k_cache, v_cache, index)
     if Dc != D:
         raise ValueError(f"the caches hold heads of {Dc}, q of {D}")
-    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    max_pages, stride = _check_table(block_table, seq_lens, B, index)
     if selected is not None:
-        _check_tensor(selected, "selected", torch.int32, (B, Hkv, None), dev)
-    _check_out(out, lse, (B, Hq, D), dev)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    L = lib()
-    with _launch_context(dev, stream):
-        if out is None:
-            out = torch.empty((B, Hq, D), device=dev, dtype=out_dtype)
-        if lse is None and with_lse:
-            lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
-        workspace = _workspace(workspace, L.dit_paged_attn_workspace_bytes(B, Hq, Hkv, D), dev)
-        st = L.dit_paged_attn_fwd(
-            q.data_ptr(), Strides(q.stride(0), q.stride(1), D), k_cache.data_ptr(),
-            view_strides(k_cache), v_cache.data_ptr(), view_strides(v_cache),
-            block_table.data_ptr(), stride, seq_lens.data_ptr(),
-            None if selected is None else selected.data_ptr(),
-            0 if selected is None else selected.shape[2], out.data_ptr(),
-            lse.data_ptr() if with_lse else None, B, Hq, Hkv, D, P, n_pages, max_pages, scale,
-            _dt(out.dtype), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _stream(dev, stream))
+        _check_tensor(selected, "selected", torch.int32, (B, Hkv, None), index)
+    if out is not None or lse is not None:
+        _check_out(out, lse, (B, Hq, D), dev)
+    if out is None:
+        out = torch.empty((B, Hq, D), device=dev, dtype=out_dtype)
+    if not with_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
+    workspace, size = _workspace(workspace, _attn_workspace_bytes(Hq, Hkv, D), dev)
+    qb, qh, _ = q.stride()
+    st = lib().dit_paged_attn_fwd(
+        q.data_ptr(), Strides(qb, qh, D), k_cache.data_ptr(), Strides(*k_cache.stride()[:3]),
+        v_cache.data_ptr(), Strides(*v_cache.stride()[:3]), block_table.data_ptr(), stride,
+        seq_lens.data_ptr(), None if selected is None else selected.data_ptr(),
+        0 if selected is None else selected.shape[2], out.data_ptr(),
+        None if lse is None else lse.data_ptr(), B, Hq, Hkv, D, P, n_pages, max_pages,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _dt(out.dtype), workspace.data_ptr(), size,
+        torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_paged_attn_fwd")
-    return out, (lse if with_lse else None)
+    return out, lse
 
 
 def paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected=None, workspace=None,
@@ -891,24 +931,27 @@ def paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected=N
     whose summaries (bf16 [n_pages, H_kv, 2, D]) bound the highest scores for q bf16 [B, H_q, D].
 
     Returns selected, int32 [B, H_kv, top_k]: table columns in ascending order, then -1."""
-    _check_tensor(q, "q", torch.bfloat16, (None,) * 3, contiguous=False)
-    dev, (B, Hq, D) = q.device, q.shape
-    _check_tensor(summary, "summary", torch.bfloat16, (None, None, 2, D), dev)
+    dev, index = _check_rows(q, "q", 3)
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected, workspace)
+    B, Hq, D = q.shape
+    _check_tensor(summary, "summary", torch.bfloat16, (None, None, 2, D), index)
     n_pages, Hkv = summary.shape[:2]
-    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    max_pages, stride = _check_table(block_table, seq_lens, B, index)
     top_k = int(top_k)
-    if selected is not None:
-        _check_tensor(selected, "selected", torch.int32, (B, Hkv, top_k), dev)
+    if selected is None:
+        selected = torch.empty((B, Hkv, max(0, top_k)), device=dev, dtype=torch.int32)
+    else:
+        _check_tensor(selected, "selected", torch.int32, (B, Hkv, top_k), index)
     L = lib()
-    with _launch_context(dev, stream):
-        if selected is None:
-            selected = torch.empty((B, Hkv, max(0, top_k)), device=dev, dtype=torch.int32)
-        workspace = _workspace(workspace, L.dit_paged_select_workspace_bytes(B, Hkv, max_pages), dev)
-        st = L.dit_paged_select(q.data_ptr(), Strides(q.stride(0), q.stride(1), D),
-                                summary.data_ptr(), block_table.data_ptr(), stride,
-                                seq_lens.data_ptr(), selected.data_ptr(), B, Hq, Hkv, D,
-                                int(page_size), n_pages, max_pages, top_k, workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream(dev, stream))
+    workspace, size = _workspace(workspace, L.dit_paged_select_workspace_bytes(B, Hkv, max_pages), dev)
+    qb, qh, _ = q.stride()
+    st = L.dit_paged_select(q.data_ptr(), Strides(qb, qh, D), summary.data_ptr(), block_table.data_ptr(),
+                            stride, seq_lens.data_ptr(), selected.data_ptr(), B, Hq, Hkv, D, page_size,
+                            n_pages, max_pages, top_k, workspace.data_ptr(), size,
+                            torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_paged_select")
     return selected
