@@ -554,7 +554,7 @@ template <int D, int kNb, typename OT>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedParams p) {
   constexpr int R = 8 * kNb, kQuads = D / 4, kSlices = 128 / kQuads;
   __shared__ float4 acc_sm[kSlices][kQuads];
-  __shared__ float red[128 / 32];
+  __shared__ float2 ml_sm[kSlices];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 note = p.meta[blockIdx.x];
   const int n = note.z;
@@ -563,41 +563,42 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int h = (note.y - hk * p.head_blocks) * R + head;
   if (h >= p.group) return;
   auto at = [&](int i) { return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0)) * R + head; };
-  float M = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += 128) M = fmaxf(M, p.part_ml[at(i)].x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  // each slice runs through its parts once, against its own running maximum; then the slices meet
   const int quad = threadIdx.x % kQuads, slice = threadIdx.x / kQuads;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
-#pragma unroll 4
-  for (int i = slice; i < n; i += kSlices) {
-    const float2 x = p.part_ml[at(i)];
-    const float4 y = *reinterpret_cast<const float4*>(p.part_o + at(i) * D + quad * 4);
-    const float f = M == -INFINITY ? 0.f : ptx::ex2_approx(x.x - M);
-    L = fmaf(f, x.y, L);
-    acc.x = fmaf(f, y.x, acc.x);
-    acc.y = fmaf(f, y.y, acc.y);
-    acc.z = fmaf(f, y.z, acc.z);
-    acc.w = fmaf(f, y.w, acc.w);
+  float M = -INFINITY, L = 0.f;
+  auto add = [&](float m, float l, const float4& y) {
+    const float top = fmaxf(M, m);
+    if (top == -INFINITY) return;
+    const float f = ptx::ex2_approx(M - top), w = ptx::ex2_approx(m - top);
+    M = top;
+    L = fmaf(w, l, L * f);
+    acc.x = fmaf(w, y.x, acc.x * f);
+    acc.y = fmaf(w, y.y, acc.y * f);
+    acc.z = fmaf(w, y.z, acc.z * f);
+    acc.w = fmaf(w, y.w, acc.w * f);
+  };
+  constexpr int kAhead = 8;
+  for (int i0 = slice; i0 < n; i0 += kSlices * kAhead) {
+    float2 x[kAhead];
+    float4 y[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kSlices;
+      if (i < n) {
+        x[k] = p.part_ml[at(i)];
+        y[k] = *reinterpret_cast<const float4*>(p.part_o + at(i) * D + quad * 4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kSlices < n) add(x[k].x, x[k].y, y[k]);
   }
-  __shared__ float l_sm[kSlices];
   acc_sm[slice][quad] = acc;
-  if (quad == 0) l_sm[slice] = L;
+  if (quad == 0) ml_sm[slice] = make_float2(M, L);
   __syncthreads();
   if (slice != 0) return;
-  for (int s = 1; s < kSlices; ++s) {
-    const float4 y = acc_sm[s][quad];
-    acc.x += y.x;
-    acc.y += y.y;
-    acc.z += y.z;
-    acc.w += y.w;
-  }
-  L = 0.f;
-  for (int s = 0; s < kSlices; ++s) L += l_sm[s];
+  for (int s = 1; s < min(n, kSlices); ++s) add(ml_sm[s].x, ml_sm[s].y, acc_sm[s][quad]);
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const long long row = static_cast<long long>(note.x) * p.h_q + hk * p.group + h;
   OT* dst = static_cast<OT*>(p.out) + row * D + quad * 4;

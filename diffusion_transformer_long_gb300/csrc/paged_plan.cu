@@ -8,13 +8,12 @@
 //   token t of request b sits at position s_b + t - cu_b of its request
 // Both sums are 32-bit and saturate (they are bounded by max_tokens and the grants).
 //
-// One thread block cluster does it in one launch: every block scans all lengths for itself
-// (B <= 8192: at most 8 per thread) into shared memory, the cluster meets once, so that no
-// length or count is overwritten in place before every block has read it, and then the
-// blocks share out the tokens and the grants; a token finds its request by bisection of the
-// prefix sums in shared memory.  Bound by latency: the launch, one dependent read of the
-// lengths, two block scans, one dependent read of the table.
-#include <cooperative_groups.h>
+// Every block scans all lengths for itself (B <= 8192) into shared memory and takes its share of
+// the tokens and the grants; a token finds its request by bisection of the prefix sums.  One
+// block serves up to kTokensPerBlock tokens alone.  Where several blocks share the tokens and
+// the lengths or the count are updated in place, those are written by a second launch, since
+// no block may overwrite what another has yet to read.  Bound by latency: the launch, one
+// dependent read of the lengths, two block scans, one dependent read of the table.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,13 +23,13 @@
 namespace ditattn {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kPlanThreads = 1024;
+constexpr int kTokensPerBlock = 2048;
 
 struct PlanParams {
   PlanLaunch a;
   int cap;  // tokens a table row can hold
+  int fill, commit;  // what this launch writes: slots, table and first tokens; lengths and count
 };
 
 __device__ __forceinline__ int sat_add(int x, int y) {
@@ -111,23 +110,22 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     run = sat_add(run, off[b + 1]);
     off[b + 1] = run;
   }
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();  // every block has read seq_lens and n_free: they may be written in place
+  __syncthreads();  // this block has read seq_lens and n_free: alone, it may write them in place
 
-  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
-  const int step = ranks * blockDim.x, first = rank * blockDim.x + threadIdx.x;
+  const int step = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
   const int grants = min(free, off[B]);
-  for (int b = first; b < B; b += step) {
-    const int have = pages_of(old[b], P);
-    const int got = min(max(0, free - off[b]), off[b + 1] - off[b]);
-    const int want = min(sat_add(old[b], cu[b + 1] - cu[b]), p.cap);
-    p.a.seq_lens_out[b] = static_cast<int>(min(static_cast<long long>(want), static_cast<long long>(have + got) * P));
-    p.a.cu_new[b + 1] = cu[b + 1];
+  if (p.commit) {
+    for (int b = first; b < B; b += step) {
+      const int have = pages_of(old[b], P);
+      const int got = min(max(0, free - off[b]), off[b + 1] - off[b]);
+      const int want = min(sat_add(old[b], cu[b + 1] - cu[b]), p.cap);
+      p.a.seq_lens_out[b] =
+          static_cast<int>(min(static_cast<long long>(want), static_cast<long long>(have + got) * P));
+    }
+    if (first == 0) *p.a.n_free_out = free - grants;
   }
-  if (first == 0) {
-    p.a.cu_new[0] = 0;
-    *p.a.n_free_out = free - grants;
-  }
+  if (!p.fill) return;
+  for (int b = first; b <= B; b += step) p.a.cu_new[b] = cu[b];
   for (int j = first; j < grants; j += step) {
     const int b = find(off, B, j);
     p.a.table[b * p.a.table_stride + pages_of(old[b], P) + j - off[b]] = p.a.free_pages[free - 1 - j];
@@ -167,21 +165,19 @@ cudaError_t launch_paged_plan(const PlanLaunch& a, cudaStream_t st) {
                                                (3 * kPlanMaxBatch + 2) * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return e;
   }
-  int blocks = 1;
-  while (blocks < 8 && blocks * 4 * kPlanThreads < a.max_tokens) blocks *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_plan_kernel, p);
+  // Few requests and tokens: a small block, whose scans and barriers are shorter.
+  const int threads = std::max(a.batch, std::min(a.max_tokens, kTokensPerBlock)) <= 512 ? 256 : kPlanThreads;
+  const int blocks = std::min((a.max_tokens + kTokensPerBlock - 1) / kTokensPerBlock, 256);
+  const bool in_place = a.seq_lens_out == a.seq_lens || a.n_free_out == a.n_free;
+  p.fill = 1;
+  p.commit = blocks == 1 || !in_place;
+  paged_plan_kernel<<<blocks, threads, smem, st>>>(p);
+  if (!p.commit) {
+    p.fill = 0;
+    p.commit = 1;
+    paged_plan_kernel<<<1, kPlanThreads, smem, st>>>(p);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace ditattn

@@ -44,11 +44,11 @@ struct PickParams {
   SelectLaunch a;
   uint32_t* keys;   // [batch * h_kv][max_pages]: scores, as integers of the same order
   float* bounds;    // [batch * h_kv][chunks]: the largest sum |q| |k| of 16 pages
-  double* exact;    // [batch * h_kv][max_pages]: 64-bit scores of the pages between
+  unsigned long long* exact;  // [batch * h_kv][max_pages]: 64-bit scores of the pages between, in order
   int chunks;
 };
 
-// Unsigned integers in the order of the floating-point numbers (no NaN).
+// Unsigned integers in the order of the floating-point numbers (no NaN, no -0).
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __g
   uint32_t* keys = p.keys + static_cast<long long>(bg) * a.max_pages;
   if (j == 0) {
     const int i = i0 + (lane >> 2);
-    if (i < n) keys[i] = p0 < 0 ? kLowest : odd0 ? kUnknown : key_of(best0);
-    if (i + 8 < n) keys[i + 8] = p1 < 0 ? kLowest : odd1 ? kUnknown : key_of(best1);
+    if (i < n) keys[i] = p0 < 0 ? kLowest : odd0 ? kUnknown : key_of(best0 + 0.f);
+    if (i + 8 < n) keys[i + 8] = p1 < 0 ? kLowest : odd1 ? kUnknown : key_of(best1 + 0.f);
   }
   if (lane == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
 }
@@ -194,26 +194,56 @@ __device__ __forceinline__ int block_below(int x, int* sm, int& all) {
   return up - x + (warp > 0 ? before : 0);
 }
 
-// The 64-bit score of table column i, by one warp.
-__device__ double exact_score(const SelectLaunch& a, int b, int g, int i) {
+// The 64-bit score of table column i as an integer of the same order, by one warp: a lane takes
+// two channels in every 64.  Sums are 64-bit integers in units of 1 / unit (a power of two for
+// which sum |q| |k| of every page stays below 2^62): each product, exact in 32 bits, is rounded
+// once, to 2^-61 of the largest page's sum or finer, so that the sum is exact but for that, in
+// any order, and far cheaper than in fp64, of which this GPU does two operations a clock and SM.
+// unit = 0 (some score is not finite in 32 bits, or all are near its underflow): fp64 after all.
+__device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, float unit) {
   const int lane = threadIdx.x & 31, group = a.h_q / a.h_kv;
   const int page = a.table[b * a.table_stride + i];
-  if (page < 0 || page >= a.n_pages) return -INFINITY;
-  const __nv_bfloat16* lo = static_cast<const __nv_bfloat16*>(a.summary) + (static_cast<long long>(page) * a.h_kv + g) * 2 * a.d;
+  if (page < 0 || page >= a.n_pages) return 0;
+  const uint32_t* lo = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.summary) +
+                                                         (static_cast<long long>(page) * a.h_kv + g) * 2 * a.d) + lane;
+  const uint32_t* hi = lo + a.d / 2;
+  const int parts = a.d / 64;
+  const uint32_t lo0 = lo[0], hi0 = hi[0], lo1 = parts > 1 ? lo[32] : 0, hi1 = parts > 1 ? hi[32] : 0;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + static_cast<long long>(g) * group * a.q_h;
+  const uint32_t* qh = reinterpret_cast<const uint32_t*>(q) + lane;
+  const long long q_step = a.q_h / 2;
+  if (unit > 0.f) {
+    auto term = [&](float x, float l, float h) { return __float2ll_rn(fmaxf(x * l, x * h) * unit); };
+    long long best = -(1ll << 63);
+#pragma unroll 4
+    for (int h = 0; h < group; ++h) {
+      const uint32_t q0 = __ldg(qh + h * q_step), q1 = parts > 1 ? __ldg(qh + h * q_step + 32) : 0;
+      long long s = term(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
+                    term(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
+                    term(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +
+                    term(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      best = max(best, s);
+    }
+    return static_cast<unsigned long long>(best) ^ 1ull << 63;
+  }
+  auto larger = [](float x, float l, float h) {  // NaN in either product is NaN
+    const double u = static_cast<double>(x) * l, v = static_cast<double>(x) * h;
+    return u != u ? u : v != v ? v : fmax(u, v);
+  };
   double best = -INFINITY;
   for (int h = 0; h < group; ++h) {
-    double s = 0.0;
-    for (int d = lane; d < a.d; d += 32) {
-      const double x = __bfloat162float(q[h * a.q_h + d]);
-      const double u = x * __bfloat162float(lo[d]), v = x * __bfloat162float(lo[a.d + d]);
-      s += u != u ? u : v != v ? v : fmax(u, v);
-    }
+    const uint32_t q0 = __ldg(qh + h * q_step), q1 = parts > 1 ? __ldg(qh + h * q_step + 32) : 0;
+    double s = larger(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
+               larger(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
+               larger(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +
+               larger(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
     best = fmax(best, s != s ? static_cast<double>(INFINITY) : s);
   }
-  return best;
+  return key_of(best);
 }
 
 __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_constant__ PickParams p) {
@@ -241,7 +271,7 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int others = n - 1, want = a.top_k - 1;  // 1 <= want < others
   const uint32_t* all_keys = p.keys + static_cast<long long>(bg) * a.max_pages;
-  double* exact = p.exact + static_cast<long long>(bg) * a.max_pages;
+  unsigned long long* exact = p.exact + static_cast<long long>(bg) * a.max_pages;
   const bool cached = others <= kCached;
   uint32_t lo = ~0u, hi = 0;
   for (int i = tid; i < others; i += kPickThreads) {
@@ -260,7 +290,10 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
   // (the magnitudes' own sum may be short by the same error; 2^-110: terms below 32 bits' range)
   const double wide = 2.002 * (kErr * mag + 7.7e-34);
   const bool unknown = hi >= kInfKey || !(mag < INFINITY);
-  double from = -INFINITY, to = INFINITY;  // pages scored above `to` are in, below `from` out
+  // 2^61 / 2^ceil(log2 mag): at least 2^61 units in mag, and every page's magnitudes below 2^62
+  // (mag may be short by kErr of itself); sums from 2^-40 up keep their products far from 2^-126
+  const float unit = !unknown && mag >= 0x1p-40f ? scalbnf(1.f, 60 - ilogbf(mag)) : 0.f;
+  uint32_t from = 0, to = ~0u;  // pages whose key is above `to` are in, below `from` out
   int above = 0;                           // pages above the range [lo, hi]
   for (; !unknown;) {
     const int bits = 32 - __clz(hi - lo);
@@ -286,15 +319,13 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
     hi = min(hi, lo2 + ((1u << shift) - 1));
     lo = lo2;
     above = bin_above;
-    from = static_cast<double>(value_of(lo)) - wide;
-    to = static_cast<double>(value_of(hi)) + wide;
+    from = key_of(__double2float_rd(value_of(lo) - wide));
+    to = key_of(__double2float_ru(value_of(hi) + wide));
     int mine = 0;
-    for (int i = tid; i < others; i += kPickThreads) {
-      const double s = value_of(keys[i]);
-      if (s >= from && s <= to) ++mine;
-    }
+    for (int i = tid; i < others; i += kPickThreads) mine += keys[i] >= from && keys[i] <= to;
     const int sum = block_all(mine, red_i, [](int x, int y) { return x + y; });
-    if (sum <= kRanked || lo == hi) break;
+    // a bin as narrow as the error, or so few that a warp has one page each, gains no more
+    if (sum <= kPickThreads / 32 || lo == hi || (sum <= kRanked && value_of(hi) - value_of(lo) <= wide)) break;
   }
   // the pages between, scored in 64 bits
   if (tid == 0) count = 0;
@@ -302,16 +333,8 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
   int sure = 0;
   for (int i0 = 0; i0 < others; i0 += kPickThreads) {
     const int i = i0 + tid;
-    bool mid = false;
-    if (i < others) {
-      if (unknown) {
-        mid = true;
-      } else {
-        const double s = value_of(keys[i]);
-        mid = s >= from && s <= to;
-        sure += s > to;
-      }
-    }
+    const bool mid = i < others && keys[i] >= from && keys[i] <= to;
+    sure += i < others && keys[i] > to;
     if (mid) {
       const int at = atomicAdd(&count, 1);
       if (at < kRanked) between[at] = i;
@@ -324,11 +347,8 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
   if (rest < mids) {
     if (mids <= kRanked) {
       for (int x = warp; x < mids; x += kPickThreads / 32) {
-        const double s = exact_score(a, b, g, between[x]);
-        if (lane == 0) {
-          ranked[x] = key_of(s);
-          exact[between[x]] = s;
-        }
+        const unsigned long long k = exact_key(a, b, g, between[x], unit);
+        if (lane == 0) ranked[x] = exact[between[x]] = k;
       }
       __syncthreads();
       if (tid < mids) {
@@ -349,18 +369,15 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
     } else {
       // many alike (or not finite): the border by bisection of the 64-bit keys
       for (int i = warp; i < others; i += kPickThreads / 32) {
-        const double k32 = unknown ? 0.0 : value_of(keys[i]);
-        if (!unknown && !(k32 >= from && k32 <= to)) continue;
-        const double s = exact_score(a, b, g, i);
-        if (lane == 0) exact[i] = s;
+        if (keys[i] < from || keys[i] > to) continue;
+        const unsigned long long k = exact_key(a, b, g, i, unit);
+        if (lane == 0) exact[i] = k;
       }
       __syncthreads();
       auto at_least = [&](unsigned long long k) {
         int c = 0;
-        for (int i = tid; i < others; i += kPickThreads) {
-          const double k32 = unknown ? 0.0 : value_of(keys[i]);
-          if (unknown || (k32 >= from && k32 <= to)) c += key_of(exact[i]) >= k;
-        }
+        for (int i = tid; i < others; i += kPickThreads)
+          if (keys[i] >= from && keys[i] <= to) c += exact[i] >= k;
         return block_all(c, red_i, [](int x, int y) { return x + y; });
       };
       for (int bit = 63; bit >= 0; --bit) {
@@ -374,13 +391,10 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
   const int per = (others + kPickThreads - 1) / kPickThreads;
   const int i0 = min(others, tid * per), i1 = min(others, i0 + per);
   auto state = [&](int i) {  // 2: in, 1: at the border, 0: out
-    if (!unknown) {
-      const double s = value_of(keys[i]);
-      if (s > to) return 2;
-      if (s < from) return 0;
-    }
+    if (keys[i] > to) return 2;
+    if (keys[i] < from) return 0;
     if (rest == mids) return 2;
-    const unsigned long long k = key_of(exact[i]);
+    const unsigned long long k = exact[i];
     return k > border ? 2 : k == border ? 1 : 0;
   };
   __syncthreads();
@@ -416,7 +430,7 @@ cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
   p.chunks = static_cast<int>((static_cast<long long>(a.max_pages) + kChunk - 1) / kChunk);
   const size_t rows = static_cast<size_t>(a.batch) * a.h_kv;
   char* ws = static_cast<char*>(a.workspace);
-  p.exact = reinterpret_cast<double*>(ws);
+  p.exact = reinterpret_cast<unsigned long long*>(ws);
   p.keys = reinterpret_cast<uint32_t*>(ws + aligned256(rows * a.max_pages * 8));
   p.bounds = reinterpret_cast<float*>(ws + aligned256(rows * a.max_pages * 8) + aligned256(rows * a.max_pages * 4));
   if (rows > 0x7fffffffu) return cudaErrorInvalidConfiguration;

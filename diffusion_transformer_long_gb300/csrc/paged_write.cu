@@ -90,7 +90,7 @@ __device__ __forceinline__ uint4 pack(const __nv_bfloat162 (&x)[4]) {
 }
 
 template <int kVpr>
-__global__ void __launch_bounds__(kWriteThreads) paged_write_runs(const WriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_runs(const WriteParams p) {
   constexpr int kRows = 32 / kVpr;  // rows a warp moves at once
   const long long w = (static_cast<long long>(blockIdx.x) * kWriteThreads + threadIdx.x) >> 5;
   if (w >= p.warps) return;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_runs(const WritePar
       const uint4 k = *reinterpret_cast<const uint4*>(ks + (sub < n ? sub : 0) * p.kn_n);
       e.take(k, true);
     }
-#pragma unroll 4
+#pragma unroll 2
     for (int r = sub; r < n; r += kRows) {
       const uint4 k = *reinterpret_cast<const uint4*>(ks + r * p.kn_n);
       const uint4 v = *reinterpret_cast<const uint4*>(vs + r * p.vn_n);
@@ -192,7 +192,7 @@ cudaError_t launch_paged_write(const WriteLaunch& a, cudaStream_t st) {
   p.heads = a.heads;
   p.page_size = a.page_size;
   p.window = 1;
-  while (p.window < 16 && static_cast<long long>(a.tokens) * a.heads > 16384LL * p.window) p.window *= 2;
+  while (p.window < 32 && static_cast<long long>(a.tokens) * a.heads > 16384LL * p.window) p.window *= 2;
   p.warps = (static_cast<long long>(a.tokens) + p.window - 1) / p.window * a.heads;
   return a.d == 64 ? launch<8>(p, st) : launch<16>(p, st);
 }

@@ -767,15 +767,28 @@ def _check_tensor(t, name, dtype, shape, index, rows=False):
 
 def _check_rows(t, name, dims):
     """(device, CUDA device number) of a bf16 view of `dims` dimensions with a contiguous last one."""
+    try:
+        index = t.get_device()
+        if index >= 0 and t.dtype is torch.bfloat16 and t.dim() == dims and t.stride(-1) == 1:
+            return t.device, index
+    except (AttributeError, IndexError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    index = t.get_device()
-    _check_tensor(t, name, torch.bfloat16, (None,) * dims, index, rows=True)
-    return t.device, index
+    _check_tensor(t, name, torch.bfloat16, (None,) * dims, t.get_device(), rows=True)
+    return t.device, t.get_device()
 
 
 def _check_caches(k_cache, v_cache, index):
     """(n_pages, H_kv, page_size, D) of the two caches."""
+    try:
+        shape = k_cache.shape
+        if (k_cache.dtype is torch.bfloat16 and v_cache.dtype is torch.bfloat16 and v_cache.shape == shape
+                and len(shape) == 4 and k_cache.get_device() == index and v_cache.get_device() == index
+                and k_cache.stride(3) == 1 and v_cache.stride(3) == 1):
+            return shape
+    except AttributeError:
+        pass
     _check_tensor(k_cache, "k_cache", torch.bfloat16, (None,) * 4, index, rows=True)
     _check_tensor(v_cache, "v_cache", torch.bfloat16, k_cache.shape, index, rows=True)
     return k_cache.shape
@@ -784,6 +797,14 @@ def _check_caches(k_cache, v_cache, index):
 def _check_table(block_table, seq_lens, B, index):
     """(max_pages, table_stride) of the batch's block table."""
     _check_tensor(seq_lens, "seq_lens", torch.int32, (B,), index)
+    try:
+        rows, max_pages = block_table.shape
+        stride, last = block_table.stride()
+        if (last == 1 and rows == B and block_table.dtype is torch.int32
+                and block_table.get_device() == index):
+            return max_pages, (stride if B > 1 else max_pages)
+    except (AttributeError, ValueError):
+        pass
     _check_tensor(block_table, "block_table", torch.int32, (B, None), index, rows=True)
     max_pages = block_table.shape[1]
     return max_pages, (block_table.stride(0) if B > 1 else max_pages)
@@ -821,10 +842,12 @@ def paged_plan(new_lens, seq_lens, block_table, free_pages, n_free, page_size, n
             return paged_plan(new_lens, seq_lens, block_table, free_pages, n_free, page_size, n_pages,
                               max_tokens, seq_lens_out, n_free_out, cu_new, slots)
     i32 = torch.int32
-    _check_tensor(new_lens, "new_lens", i32, (None,), index)
+    _check_tensor(new_lens, "new_lens", i32, new_lens.shape[:1] or (None,), index)
     B = new_lens.shape[0]
     max_pages, stride = _check_table(block_table, seq_lens, B, index)
-    _check_tensor(free_pages, "free_pages", i32, (None,), index)
+    if not isinstance(free_pages, torch.Tensor):
+        raise ValueError("free_pages must be a CUDA tensor")
+    _check_tensor(free_pages, "free_pages", i32, free_pages.shape[:1] or (None,), index)
     _check_tensor(n_free, "n_free", i32, (1,), index)
     max_tokens = int(max_tokens)
     if seq_lens_out is None:
@@ -901,7 +924,7 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, selected=None, ou
         raise ValueError(f"the caches hold heads of {Dc}, q of {D}")
     max_pages, stride = _check_table(block_table, seq_lens, B, index)
     if selected is not None:
-        _check_tensor(selected, "selected", torch.int32, (B, Hkv, None), index)
+        _check_tensor(selected, "selected", torch.int32, (B, Hkv, selected.shape[-1]), index)
     if out is not None or lse is not None:
         _check_out(out, lse, (B, Hq, D), dev)
     if out is None:
@@ -937,8 +960,10 @@ def paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected=N
         with elsewhere:
             return paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected, workspace)
     B, Hq, D = q.shape
-    _check_tensor(summary, "summary", torch.bfloat16, (None, None, 2, D), index)
+    if not isinstance(summary, torch.Tensor):
+        raise ValueError("summary must be a CUDA tensor")
     n_pages, Hkv = summary.shape[:2]
+    _check_tensor(summary, "summary", torch.bfloat16, (n_pages, Hkv, 2, D), index)
     max_pages, stride = _check_table(block_table, seq_lens, B, index)
     top_k = int(top_k)
     if selected is None:
