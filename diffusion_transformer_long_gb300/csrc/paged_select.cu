@@ -29,13 +29,13 @@ namespace {
 
 constexpr int kScoreWarps = 8;
 constexpr int kChunk = 16;          // pages of a warp
-constexpr int kPickThreads = 512;
+constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kRanked = kPickThreads;  // pages between that are ranked pair by pair
 constexpr int kCached = 8192;       // keys held in shared memory
 // A 32-bit score is summed in 2 D / 16 <= 16 steps of 16 products and the running sum, each of
 // the 17 terms cut to within 2^-23 of the step's largest: at most 16 * 17 * 2^-23 of sum |q| |k|.
-constexpr double kErr = 16 * 17 / 8388608.0;
+constexpr float kErr = 16 * 17 / 8388608.f;
 constexpr uint32_t kLowest = 0x007FFFFFu;    // the key of -inf: a page without keys
 constexpr uint32_t kInfKey = 0xFF800000u;    // the key of +inf
 constexpr uint32_t kUnknown = 0xFFFFFFFFu;   // not finite in 32 bits
@@ -45,7 +45,8 @@ struct PickParams {
   uint32_t* keys;   // [batch * h_kv][max_pages]: scores, as integers of the same order
   float* bounds;    // [batch * h_kv][chunks]: the largest sum |q| |k| of 16 pages
   unsigned long long* exact;  // [batch * h_kv][max_pages]: 64-bit scores of the pages between, in order
-  int chunks;
+  uint32_t* masks;  // [batch * h_kv][mask_words]: a bit for every page, where shared memory has no room
+  int chunks, mask_words;
 };
 
 // Unsigned integers in the order of the floating-point numbers (no NaN, no -0).
@@ -158,18 +159,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __g
   if (lane == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
 }
 
-// Block-wide sums and extremes; `sm` is free again on return.
-template <typename T, typename F>
-__device__ __forceinline__ T block_all(T x, T* sm, F f) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x = f(x, __shfl_xor_sync(~0u, x, d));
+// Sum over the block; `sm` is free again at the next barrier.
+__device__ __forceinline__ int block_sum(int x, int* sm) {
+  x = __reduce_add_sync(~0u, x);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
   __syncthreads();
-  x = sm[threadIdx.x & (kPickThreads / 32 - 1)];
-#pragma unroll
-  for (int d = kPickThreads / 64; d > 0; d >>= 1) x = f(x, __shfl_xor_sync(~0u, x, d));
-  return x;
+  return __reduce_add_sync(~0u, (threadIdx.x & 31) < kPickWarps ? sm[threadIdx.x & 31] : 0);
 }
 // Sum over the lower threads, and over all.
 __device__ __forceinline__ int block_below(int x, int* sm, int& all) {
@@ -183,13 +179,13 @@ __device__ __forceinline__ int block_below(int x, int* sm, int& all) {
   __syncthreads();
   if (lane == 31) sm[warp] = up;
   __syncthreads();
-  int w = lane < kPickThreads / 32 ? sm[lane] : 0;
+  int w = lane < kPickWarps ? sm[lane] : 0;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(~0u, w, d);
     if (lane >= d) w += y;
   }
-  all = __shfl_sync(~0u, w, kPickThreads / 32 - 1);
+  all = __shfl_sync(~0u, w, kPickWarps - 1);
   const int before = __shfl_sync(~0u, w, max(warp - 1, 0));
   return up - x + (warp > 0 ? before : 0);
 }
@@ -248,180 +244,194 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
 
 __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_constant__ PickParams p) {
   __shared__ uint32_t cache[kCached];
+  __shared__ uint32_t mask_sm[kCached / 32];
   __shared__ int bins[kBins];
   __shared__ int between[kRanked];
   __shared__ unsigned long long ranked[kRanked];
-  __shared__ unsigned long long red[kPickThreads / 32];
+  __shared__ uint32_t extremes[3][kPickWarps];
+  __shared__ int red[kPickWarps];
   __shared__ int count, bin_found, bin_above;
-  __shared__ unsigned long long border_sm;
-  __shared__ int quota_sm;
-  int* red_i = reinterpret_cast<int*>(red);
-  uint32_t* red_u = reinterpret_cast<uint32_t*>(red);
-  float* red_f = reinterpret_cast<float*>(red);
   const SelectLaunch& a = p.a;
   const int bg = blockIdx.x, b = bg / a.h_kv, g = bg - b * a.h_kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = pages_now(a, b);
   int* out = a.selected + static_cast<long long>(bg) * a.top_k;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n <= a.top_k || a.top_k == 1) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // a reader of the last call's list may still run
     for (int i = tid; i < a.top_k; i += kPickThreads) out[i] = a.top_k == 1 ? n - 1 : i < n ? i : -1;
     return;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int others = n - 1, want = a.top_k - 1;  // 1 <= want < others
   const uint32_t* all_keys = p.keys + static_cast<long long>(bg) * a.max_pages;
-  unsigned long long* exact = p.exact + static_cast<long long>(bg) * a.max_pages;
   const bool cached = others <= kCached;
-  uint32_t lo = ~0u, hi = 0;
+  uint32_t lo = ~0u, hi = 0, mag_bits = 0;  // magnitudes are >= 0 (or NaN): their bits are in order
+#pragma unroll 4
   for (int i = tid; i < others; i += kPickThreads) {
     const uint32_t k = all_keys[i];
     if (cached) cache[i] = k;
     lo = min(lo, k);
     hi = max(hi, k);
   }
-  float mag = 0.f;
   for (int i = tid; i < (n + kChunk - 1) / kChunk; i += kPickThreads)
-    mag = fmaxf(mag, p.bounds[static_cast<long long>(bg) * p.chunks + i]);
-  lo = block_all(lo, red_u, [](uint32_t x, uint32_t y) { return min(x, y); });
-  hi = block_all(hi, red_u, [](uint32_t x, uint32_t y) { return max(x, y); });
-  mag = block_all(mag, red_f, [](float x, float y) { return fmaxf(x, y); });
+    mag_bits = max(mag_bits, __float_as_uint(p.bounds[static_cast<long long>(bg) * p.chunks + i]));
+  lo = __reduce_min_sync(~0u, lo);
+  hi = __reduce_max_sync(~0u, hi);
+  mag_bits = __reduce_max_sync(~0u, mag_bits);
+  if (lane == 0) {
+    extremes[0][warp] = lo;
+    extremes[1][warp] = hi;
+    extremes[2][warp] = mag_bits;
+  }
+  for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
+  __syncthreads();
+  lo = __reduce_min_sync(~0u, extremes[0][lane % kPickWarps]);
+  hi = __reduce_max_sync(~0u, extremes[1][lane % kPickWarps]);
+  const float mag = __uint_as_float(__reduce_max_sync(~0u, extremes[2][lane % kPickWarps]));
   const uint32_t* keys = cached ? cache : all_keys;
-  // (the magnitudes' own sum may be short by the same error; 2^-110: terms below 32 bits' range)
-  const double wide = 2.002 * (kErr * mag + 7.7e-34);
+  // bit i: page i is in
+  uint32_t* mask = cached ? mask_sm : p.masks + static_cast<long long>(bg) * p.mask_words;
+  // twice the error (the magnitudes' own sum may be short by as much; 2^-110: terms below 32 bits'
+  // range), rounded up; in 32 bits, since every fp64 instruction costs a block 16 clocks a warp
+  const float wide = __fmul_ru(2.002f, __fmaf_ru(kErr, mag, 0x1p-110f));
   const bool unknown = hi >= kInfKey || !(mag < INFINITY);
-  // 2^61 / 2^ceil(log2 mag): at least 2^61 units in mag, and every page's magnitudes below 2^62
-  // (mag may be short by kErr of itself); sums from 2^-40 up keep their products far from 2^-126
+  // at least 2^60 units in mag, and every page's magnitudes (mag may be short by kErr of itself)
+  // below 2^62; sums from 2^-40 up keep the products that count far from 2^-126
   const float unit = !unknown && mag >= 0x1p-40f ? scalbnf(1.f, 60 - ilogbf(mag)) : 0.f;
   uint32_t from = 0, to = ~0u;  // pages whose key is above `to` are in, below `from` out
-  int above = 0;                           // pages above the range [lo, hi]
-  for (; !unknown;) {
-    const int bits = 32 - __clz(hi - lo);
-    const int shift = max(0, bits - 10);
-    for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < others; i += kPickThreads) {
-      const uint32_t k = keys[i];
-      if (k >= lo && k <= hi) atomicAdd(bins + ((k - lo) >> shift), 1);
-    }
-    __syncthreads();
-    // thread t holds bins 1023 - 2 t and 1022 - 2 t: sums run from the highest scores down
-    const int first = bins[kBins - 1 - 2 * tid], second = bins[kBins - 2 - 2 * tid];
-    int all;
-    const int over = above + block_below(first + second, red_i, all);
-    if (over < want && over + first + second >= want) {
-      const bool in_first = over + first >= want;
-      bin_found = in_first ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
-      bin_above = in_first ? over : over + first;
-    }
-    __syncthreads();
-    const uint32_t lo2 = lo + (static_cast<uint32_t>(bin_found) << shift);
-    hi = min(hi, lo2 + ((1u << shift) - 1));
-    lo = lo2;
-    above = bin_above;
-    from = key_of(__double2float_rd(value_of(lo) - wide));
-    to = key_of(__double2float_ru(value_of(hi) + wide));
-    int mine = 0;
-    for (int i = tid; i < others; i += kPickThreads) mine += keys[i] >= from && keys[i] <= to;
-    const int sum = block_all(mine, red_i, [](int x, int y) { return x + y; });
-    // a bin as narrow as the error, or so few that a warp has one page each, gains no more
-    if (sum <= kPickThreads / 32 || lo == hi || (sum <= kRanked && value_of(hi) - value_of(lo) <= wide)) break;
-  }
-  // the pages between, scored in 64 bits
-  if (tid == 0) count = 0;
-  __syncthreads();
-  int sure = 0;
-  for (int i0 = 0; i0 < others; i0 += kPickThreads) {
-    const int i = i0 + tid;
-    const bool mid = i < others && keys[i] >= from && keys[i] <= to;
-    sure += i < others && keys[i] > to;
-    if (mid) {
-      const int at = atomicAdd(&count, 1);
-      if (at < kRanked) between[at] = i;
-    }
-  }
-  sure = block_all(sure, red_i, [](int x, int y) { return x + y; });
-  const int mids = count, rest = want - sure;  // 1 <= rest <= mids
-  unsigned long long border = 0;  // pages between with a higher 64-bit key are in,
-  int quota = others;             // and `quota` of those with this one
-  if (rest < mids) {
-    if (mids <= kRanked) {
-      for (int x = warp; x < mids; x += kPickThreads / 32) {
-        const unsigned long long k = exact_key(a, b, g, between[x], unit);
-        if (lane == 0) ranked[x] = exact[between[x]] = k;
+  int above = 0;                // pages above the range [lo, hi]
+  int sure;                     // pages above `to`
+  for (;;) {
+    if (!unknown) {
+      // the bin that holds the want-th highest key
+      const int shift = max(0, 32 - __clz(hi - lo) - 10);
+#pragma unroll 4
+      for (int i = tid; i < others; i += kPickThreads) {
+        const uint32_t k = keys[i] - lo;
+        if (k <= hi - lo) atomicAdd(bins + (k >> shift), 1);
+      }
+      if (tid == 0) count = 0;
+      __syncthreads();
+      // thread t holds bins 1023 - 2 t and 1022 - 2 t: sums run from the highest scores down
+      const int first = bins[kBins - 1 - 2 * tid], second = bins[kBins - 2 - 2 * tid];
+      int all;
+      const int over = above + block_below(first + second, red, all);
+      if (over < want && over + first + second >= want) {
+        const bool in_first = over + first >= want;
+        bin_found = in_first ? kBins - 1 - 2 * tid : kBins - 2 - 2 * tid;
+        bin_above = in_first ? over : over + first;
       }
       __syncthreads();
-      if (tid < mids) {
-        const unsigned long long k = ranked[tid];
-        int higher = 0, same = 0;
-        for (int x = 0; x < mids; ++x) {
-          higher += ranked[x] > k;
-          same += ranked[x] == k;
-        }
-        if (higher < rest && higher + same >= rest) {
-          border_sm = k;
-          quota_sm = rest - higher;
-        }
-      }
-      __syncthreads();
-      border = border_sm;
-      quota = quota_sm;
+      const uint32_t lo2 = lo + (static_cast<uint32_t>(bin_found) << shift);
+      hi = min(hi, lo2 + ((1u << shift) - 1));
+      lo = lo2;
+      above = bin_above;
+      from = key_of(__fsub_rd(value_of(lo), wide) + 0.f);
+      to = key_of(__fadd_ru(value_of(hi), wide) + 0.f);
     } else {
-      // many alike (or not finite): the border by bisection of the 64-bit keys
-      for (int i = warp; i < others; i += kPickThreads / 32) {
-        if (keys[i] < from || keys[i] > to) continue;
-        const unsigned long long k = exact_key(a, b, g, i, unit);
-        if (lane == 0) exact[i] = k;
+      if (tid == 0) count = 0;
+      __syncthreads();
+    }
+    // the pages in for sure, and a list of those between
+    sure = 0;
+#pragma unroll 2
+    for (int i = tid; i - lane < others; i += kPickThreads) {
+      const uint32_t k = i < others ? keys[i] : 0;
+      const unsigned in = __ballot_sync(~0u, i < others && k > to);
+      if (lane == 0) mask[i >> 5] = in;
+      sure += __popc(in);
+      if (i < others && k - from <= to - from) {
+        const int x = atomicAdd(&count, 1);
+        if (x < kRanked) between[x] = i;
+      }
+    }
+    for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
+    sure = block_sum(lane == 0 ? sure : 0, red);
+    // a bin as narrow as the error, or so few that a warp has one page each, gains no more
+    if (unknown || count <= kPickWarps || lo == hi || (count <= kRanked && value_of(hi) - value_of(lo) <= wide)) break;
+    __syncthreads();
+  }
+  const int mids = count, rest = want - sure;  // 1 <= rest <= mids
+  if (mids <= kRanked) {
+    // scored in 64 bits and ranked pair by pair
+    if (rest < mids) {
+      for (int x = warp; x < mids; x += kPickWarps) {
+        const unsigned long long k = exact_key(a, b, g, between[x], unit);
+        if (lane == 0) ranked[x] = k;
       }
       __syncthreads();
-      auto at_least = [&](unsigned long long k) {
-        int c = 0;
-        for (int i = tid; i < others; i += kPickThreads)
-          if (keys[i] >= from && keys[i] <= to) c += exact[i] >= k;
-        return block_all(c, red_i, [](int x, int y) { return x + y; });
-      };
-      for (int bit = 63; bit >= 0; --bit) {
-        const unsigned long long k = border | 1ull << bit;
-        if (at_least(k) >= rest) border = k;
+    }
+    if (tid < mids) {
+      const int i = between[tid];
+      int better = 0;
+      if (rest < mids) {
+        const unsigned long long k = ranked[tid];
+        for (int x = 0; x < mids; ++x) better += ranked[x] > k || (ranked[x] == k && between[x] < i);
       }
-      quota = border == ~0ull ? rest : rest - at_least(border + 1);
+      if (better < rest) atomicOr(mask + (i >> 5), 1u << (i & 31));
+    }
+  } else if (rest == mids) {
+    for (int i = tid; i < others; i += kPickThreads)
+      if (keys[i] - from <= to - from) atomicOr(mask + (i >> 5), 1u << (i & 31));
+  } else {
+    // many alike (or not finite): the border by bisection of the 64-bit keys, ties in order
+    unsigned long long* exact = p.exact + static_cast<long long>(bg) * a.max_pages;
+    for (int i = warp; i < others; i += kPickWarps) {
+      if (keys[i] - from > to - from) continue;
+      const unsigned long long k = exact_key(a, b, g, i, unit);
+      if (lane == 0) exact[i] = k;
+    }
+    __syncthreads();
+    auto at_least = [&](unsigned long long k) {
+      int c = 0;
+      for (int i = tid; i < others; i += kPickThreads)
+        if (keys[i] - from <= to - from) c += exact[i] >= k;
+      return block_sum(c, red);
+    };
+    unsigned long long border = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const unsigned long long k = border | 1ull << bit;
+      if (at_least(k) >= rest) border = k;
+    }
+    const int higher = border == ~0ull ? 0 : at_least(border + 1);
+    __syncthreads();
+    if (warp == 0) {
+      int ties = rest - higher;  // to take, from the lowest columns up
+      for (int i0 = 0; i0 < others; i0 += 32) {
+        const int i = i0 + lane;
+        const bool mid = i < others && keys[i] - from <= to - from;
+        const unsigned long long k = mid ? exact[i] : 0;
+        const unsigned tied = __ballot_sync(~0u, mid && k == border);
+        const bool takes = mid && (k > border || (k == border && __popc(tied & ((1u << lane) - 1)) < ties));
+        const unsigned in = __ballot_sync(~0u, takes);
+        if (lane == 0) mask[i0 >> 5] |= in;
+        ties -= min(ties, __popc(tied));
+      }
     }
   }
-  // write the pages in, in ascending order: every thread takes a stretch of the columns
-  const int per = (others + kPickThreads - 1) / kPickThreads;
-  const int i0 = min(others, tid * per), i1 = min(others, i0 + per);
-  auto state = [&](int i) {  // 2: in, 1: at the border, 0: out
-    if (keys[i] > to) return 2;
-    if (keys[i] < from) return 0;
-    if (rest == mids) return 2;
-    const unsigned long long k = exact[i];
-    return k > border ? 2 : k == border ? 1 : 0;
-  };
   __syncthreads();
-  int in = 0, ties = 0, all;
-  for (int i = i0; i < i1; ++i) {
-    const int s = state(i);
-    in += s == 2;
-    ties += s == 1;
-  }
-  const int ties_before = block_below(ties, red_i, all);
-  in += max(0, min(ties, quota - ties_before));
-  int at = block_below(in, red_i, all), tie = ties_before;
-  for (int i = i0; i < i1; ++i) {
-    const int s = state(i);
-    if (s == 2 || (s == 1 && tie++ < quota)) out[at++] = i;
+  // the columns of the mask's bits, in ascending order
+  int done = 0;
+  for (int w0 = 0; w0 * 32 < others; w0 += kPickThreads) {
+    const int w = w0 + tid;
+    uint32_t bits = w * 32 < others ? mask[w] : 0;
+    int all;
+    int at = done + block_below(__popc(bits), red, all);
+    for (; bits; bits &= bits - 1) out[at++] = w * 32 + __ffs(bits) - 1;
+    done += all;
   }
   if (tid == 0) out[a.top_k - 1] = n - 1;
 }
 
 size_t aligned256(size_t x) { return (x + 255) / 256 * 256; }
+size_t mask_words(int max_pages) { return (static_cast<size_t>(max_pages) + 31) / 32; }
 
 }  // namespace
 
 // Keys, bounds and 64-bit scores of every (request, key/value head).
 size_t paged_select_workspace(int batch, int h_kv, int max_pages) {
   const size_t rows = static_cast<size_t>(batch) * h_kv, chunks = (static_cast<size_t>(max_pages) + kChunk - 1) / kChunk;
-  return aligned256(rows * max_pages * 8) + aligned256(rows * max_pages * 4) + aligned256(rows * chunks * 4);
+  return aligned256(rows * max_pages * 8) + aligned256(rows * max_pages * 4) + aligned256(rows * chunks * 4) +
+         aligned256(rows * mask_words(max_pages) * 4);
 }
 
 cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
@@ -433,6 +443,8 @@ cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
   p.exact = reinterpret_cast<unsigned long long*>(ws);
   p.keys = reinterpret_cast<uint32_t*>(ws + aligned256(rows * a.max_pages * 8));
   p.bounds = reinterpret_cast<float*>(ws + aligned256(rows * a.max_pages * 8) + aligned256(rows * a.max_pages * 4));
+  p.mask_words = static_cast<int>(mask_words(a.max_pages));
+  p.masks = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(p.bounds) + aligned256(rows * p.chunks * 4));
   if (rows > 0x7fffffffu) return cudaErrorInvalidConfiguration;
   const unsigned rows_y = static_cast<unsigned>(std::min<size_t>(rows, 32768));
   const dim3 grid((p.chunks + kScoreWarps - 1) / kScoreWarps, rows_y, static_cast<unsigned>((rows + rows_y - 1) / rows_y));
