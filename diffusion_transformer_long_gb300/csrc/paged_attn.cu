@@ -36,6 +36,7 @@
 #include <mutex>
 
 #include "attn_host.cuh"
+#include "paged_device.cuh"
 #include "paged_launch.h"
 #include "sm103_ptx.cuh"
 
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
   int* valid = reinterpret_cast<int*>(smem + S::kValid) + warp * S::kStages;
   const int items = p.h_kv * p.head_blocks;  // of one request
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
   if (threadIdx.x == 0) {
     ptx::tma_prefetch_desc(&p.tm_k);
     ptx::tma_prefetch_desc(&p.tm_v);
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(bars + s * 8, 1);
     ptx::fence_mbar_init();
   }
+  wait_for_inputs();
   // All units of the batch, and where this block's run of them begins: each thread sums a chunk
   // of the requests, the one whose chunk holds the run's first unit finds the request.
   const int per = (p.batch + kThreadsPaged - 1) / kThreadsPaged;
@@ -555,7 +557,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   constexpr int R = 8 * kNb, kQuads = D / 4, kSlices = 128 / kQuads;
   __shared__ float4 acc_sm[kSlices][kQuads];
   __shared__ float2 ml_sm[kSlices];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  launch_dependents();
+  wait_for_inputs();
   const int4 note = p.meta[blockIdx.x];
   const int n = note.z;
   if (n == 0) return;
@@ -643,20 +646,9 @@ cudaError_t launch_typed(const PagedParams& p, int blocks, cudaStream_t st) {
       ready[dev] = true;
     }
   }
-  kern<<<blocks, kThreadsPaged, PagedSmem<D>::kBytes, st>>>(p);
-  e = cudaGetLastError();
+  e = launch_after(kern, dim3(blocks), dim3(kThreadsPaged), PagedSmem<D>::kBytes, st, p);
   if (e != cudaSuccess) return e;
-  // The join may be scheduled while the attention still runs; it waits for its end itself.
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, std::min(p.group, 8 * kNb));
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, kNb, OT>, p);
+  return launch_after(paged_join_kernel<D, kNb, OT>, dim3(blocks, std::min(p.group, 8 * kNb)), dim3(128), 0, st, p);
 }
 
 template <int D, int kNb>

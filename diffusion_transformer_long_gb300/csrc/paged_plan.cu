@@ -18,6 +18,7 @@
 
 #include <algorithm>
 
+#include "paged_device.cuh"
 #include "paged_launch.h"
 
 namespace ditattn {
@@ -74,6 +75,8 @@ __device__ __forceinline__ int find(const int* first, int n, int x) {
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p) {
   extern __shared__ int sm[];
+  launch_dependents();
+  wait_for_inputs();
   __shared__ int warp_sums[32];
   const int B = p.a.batch, P = p.a.page_size;
   int* cu = sm;               // [B + 1]
@@ -171,13 +174,13 @@ cudaError_t launch_paged_plan(const PlanLaunch& a, cudaStream_t st) {
   const bool in_place = a.seq_lens_out == a.seq_lens || a.n_free_out == a.n_free;
   p.fill = 1;
   p.commit = blocks == 1 || !in_place;
-  paged_plan_kernel<<<blocks, threads, smem, st>>>(p);
-  if (!p.commit) {
+  cudaError_t e = launch_after(paged_plan_kernel, dim3(blocks), dim3(threads), smem, st, p);
+  if (e == cudaSuccess && !p.commit) {
     p.fill = 0;
     p.commit = 1;
-    paged_plan_kernel<<<1, kPlanThreads, smem, st>>>(p);
+    e = launch_after(paged_plan_kernel, dim3(1), dim3(kPlanThreads), smem, st, p);
   }
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace ditattn

@@ -21,6 +21,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "paged_device.cuh"
 #include "paged_launch.h"
 #include "sm103_ptx.cuh"
 
@@ -87,7 +88,8 @@ __device__ __forceinline__ int pages_now(const SelectLaunch& a, int b) {
 template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __grid_constant__ PickParams p) {
   constexpr int kLoads = 2 * D / 32;  // 64-byte pieces of a page's [lo | hi]
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  launch_dependents();
+  wait_for_inputs();
   const SelectLaunch& a = p.a;
   const int bg = blockIdx.y + blockIdx.z * gridDim.y;
   if (bg >= a.batch * a.h_kv) return;
@@ -190,14 +192,14 @@ __device__ __forceinline__ int block_below(int x, int* sm, int& all) {
   return up - x + (warp > 0 ? before : 0);
 }
 
-// The 64-bit score of table column i as an integer of the same order, by one warp: a lane takes
-// two channels in every 64.  Sums are 64-bit integers in units of 1 / unit (a power of two for
+// The 64-bit score of table column i, over heads h_first .. h_end - 1 of the group, as an integer of
+// the same order, by one warp: a lane takes two channels in every 64.  Sums are 64-bit integers in units of 1 / unit (a power of two for
 // which sum |q| |k| of every page stays below 2^62): each product, exact in 32 bits, is rounded
 // once, to 2^-61 of the largest page's sum or finer, so that the sum is exact but for that, in
 // any order, and far cheaper than in fp64, of which this GPU does two operations a clock and SM.
 // unit = 0 (some score is not finite in 32 bits, or all are near its underflow): fp64 after all.
-__device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, float unit) {
-  const int lane = threadIdx.x & 31, group = a.h_q / a.h_kv;
+__device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, float unit, int h_first, int h_end) {
+  const int lane = threadIdx.x & 31;
   const int page = a.table[b * a.table_stride + i];
   if (page < 0 || page >= a.n_pages) return 0;
   const uint32_t* lo = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.summary) +
@@ -205,14 +207,14 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
   const uint32_t* hi = lo + a.d / 2;
   const int parts = a.d / 64;
   const uint32_t lo0 = lo[0], hi0 = hi[0], lo1 = parts > 1 ? lo[32] : 0, hi1 = parts > 1 ? hi[32] : 0;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + static_cast<long long>(g) * group * a.q_h;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + static_cast<long long>(g) * (a.h_q / a.h_kv) * a.q_h;
   const uint32_t* qh = reinterpret_cast<const uint32_t*>(q) + lane;
   const long long q_step = a.q_h / 2;
   if (unit > 0.f) {
     auto term = [&](float x, float l, float h) { return __float2ll_rn(fmaxf(x * l, x * h) * unit); };
     long long best = -(1ll << 63);
 #pragma unroll 4
-    for (int h = 0; h < group; ++h) {
+    for (int h = h_first; h < h_end; ++h) {
       const uint32_t q0 = __ldg(qh + h * q_step), q1 = parts > 1 ? __ldg(qh + h * q_step + 32) : 0;
       long long s = term(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
                     term(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
@@ -229,7 +231,7 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
     return u != u ? u : v != v ? v : fmax(u, v);
   };
   double best = -INFINITY;
-  for (int h = 0; h < group; ++h) {
+  for (int h = h_first; h < h_end; ++h) {
     const uint32_t q0 = __ldg(qh + h * q_step), q1 = parts > 1 ? __ldg(qh + h * q_step + 32) : 0;
     double s = larger(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
                larger(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
@@ -254,9 +256,10 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
   const SelectLaunch& a = p.a;
   const int bg = blockIdx.x, b = bg / a.h_kv, g = bg - b * a.h_kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  launch_dependents();
+  wait_for_inputs();
   const int n = pages_now(a, b);
   int* out = a.selected + static_cast<long long>(bg) * a.top_k;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n <= a.top_k || a.top_k == 1) {
     for (int i = tid; i < a.top_k; i += kPickThreads) out[i] = a.top_k == 1 ? n - 1 : i < n ? i : -1;
     return;
@@ -346,17 +349,21 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
     }
     for (int i = tid; i < kBins; i += kPickThreads) bins[i] = 0;
     sure = block_sum(lane == 0 ? sure : 0, red);
-    // a bin as narrow as the error, or so few that a warp has one page each, gains no more
-    if (unknown || count <= kPickWarps || lo == hi || (count <= kRanked && value_of(hi) - value_of(lo) <= wide)) break;
+    // all between are in, or a narrower bin would not part them
+    if (unknown || count == want - sure || lo == hi || (count <= kRanked && value_of(hi) - value_of(lo) <= wide)) break;
     __syncthreads();
   }
   const int mids = count, rest = want - sure;  // 1 <= rest <= mids
   if (mids <= kRanked) {
     // scored in 64 bits and ranked pair by pair
     if (rest < mids) {
-      for (int x = warp; x < mids; x += kPickWarps) {
-        const unsigned long long k = exact_key(a, b, g, between[x], unit);
-        if (lane == 0) ranked[x] = k;
+      const int group = a.h_q / a.h_kv;
+      if (tid < mids) ranked[tid] = 0;
+      __syncthreads();
+      for (long long x = warp; x < static_cast<long long>(mids) * group; x += kPickWarps) {
+        const int i = static_cast<int>(x / group), h = static_cast<int>(x - static_cast<long long>(i) * group);
+        const unsigned long long k = exact_key(a, b, g, between[i], unit, h, h + 1);
+        if (lane == 0) atomicMax(ranked + i, k);
       }
       __syncthreads();
     }
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
     unsigned long long* exact = p.exact + static_cast<long long>(bg) * a.max_pages;
     for (int i = warp; i < others; i += kPickWarps) {
       if (keys[i] - from > to - from) continue;
-      const unsigned long long k = exact_key(a, b, g, i, unit);
+      const unsigned long long k = exact_key(a, b, g, i, unit, 0, a.h_q / a.h_kv);
       if (lane == 0) exact[i] = k;
     }
     __syncthreads();
@@ -448,20 +455,9 @@ cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
   if (rows > 0x7fffffffu) return cudaErrorInvalidConfiguration;
   const unsigned rows_y = static_cast<unsigned>(std::min<size_t>(rows, 32768));
   const dim3 grid((p.chunks + kScoreWarps - 1) / kScoreWarps, rows_y, static_cast<unsigned>((rows + rows_y - 1) / rows_y));
-  if (a.d == 64) paged_score_kernel<64><<<grid, kScoreWarps * 32, 0, st>>>(p);
-  else paged_score_kernel<128><<<grid, kScoreWarps * 32, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows));
-  cfg.blockDim = dim3(kPickThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_pick_kernel, p);
+  const cudaError_t e = a.d == 64 ? launch_after(paged_score_kernel<64>, grid, dim3(kScoreWarps * 32), 0, st, p)
+                                  : launch_after(paged_score_kernel<128>, grid, dim3(kScoreWarps * 32), 0, st, p);
+  return e != cudaSuccess ? e : launch_after(paged_pick_kernel, dim3(static_cast<unsigned>(rows)), dim3(kPickThreads), 0, st, p);
 }
 
 }  // namespace ditattn

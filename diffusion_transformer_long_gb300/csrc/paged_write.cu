@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "paged_device.cuh"
 #include "paged_launch.h"
 
 namespace ditattn {
@@ -37,7 +38,9 @@ struct WriteParams {
 
 // kVpr: 16-byte vectors per row.  One thread per vector of a (token, head) row.
 template <int kVpr>
-__global__ void __launch_bounds__(kWriteThreads) paged_write_rows(const WriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads) paged_write_rows(const __grid_constant__ WriteParams p) {
+  launch_dependents();
+  wait_for_inputs();
   const long long i = static_cast<long long>(blockIdx.x) * kWriteThreads + threadIdx.x;
   const long long row = i / kVpr;
   const int t = static_cast<int>(row / p.heads), h = static_cast<int>(row - static_cast<long long>(t) * p.heads);
@@ -90,7 +93,9 @@ __device__ __forceinline__ uint4 pack(const __nv_bfloat162 (&x)[4]) {
 }
 
 template <int kVpr>
-__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_runs(const WriteParams p) {
+__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_runs(const __grid_constant__ WriteParams p) {
+  launch_dependents();
+  wait_for_inputs();
   constexpr int kRows = 32 / kVpr;  // rows a warp moves at once
   const long long w = (static_cast<long long>(blockIdx.x) * kWriteThreads + threadIdx.x) >> 5;
   if (w >= p.warps) return;
@@ -160,11 +165,9 @@ cudaError_t launch(const WriteParams& p, cudaStream_t st) {
   const long long threads = p.summary ? p.warps * 32 : static_cast<long long>(p.tokens) * p.heads * kVpr;
   const long long blocks = (threads + kWriteThreads - 1) / kWriteThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (p.summary)
-    paged_write_runs<kVpr><<<static_cast<unsigned>(blocks), kWriteThreads, 0, st>>>(p);
-  else
-    paged_write_rows<kVpr><<<static_cast<unsigned>(blocks), kWriteThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return p.summary ? launch_after(paged_write_runs<kVpr>, grid, dim3(kWriteThreads), 0, st, p)
+                   : launch_after(paged_write_rows<kVpr>, grid, dim3(kWriteThreads), 0, st, p);
 }
 
 }  // namespace

@@ -328,6 +328,49 @@ def test_attn_two_streams_at_once():
             assert torch.equal(o, o1) and torch.equal(lse, l1)
 
 
+def test_captured_between_copies_and_two_graphs_of_one_workspace():
+    """Captured behind a copy, a fill and each other; two graphs that share the workspaces, replayed
+    in turn, and one call captured twice into the same graph."""
+    P, top_k = 16, 9
+    q, k, v, table, sl = make_case([1500, 40, 0, 333], 6, 2, 64, P, seed=61)
+    summary = torch.stack((k.amin(2), k.amax(2)), 2)
+    src = torch.empty_like(q)
+    ws = torch.empty(da.lib().dit_paged_attn_workspace_bytes(4, 6, 2, 64), dtype=torch.uint8, device=DEV)
+    wsel = torch.empty(da.lib().dit_paged_select_workspace_bytes(4, 2, table.shape[1]), dtype=torch.uint8, device=DEV)
+    ws.fill_(0x5A)
+    wsel.fill_(0xA5)
+    x = q.clone()
+
+    def step(out, lse):
+        x.copy_(src)
+        sel = da.paged_select(x, summary, table, sl, P, top_k, workspace=wsel)
+        out.fill_(3)
+        da.paged_attn_fwd(x, k, v, table, sl, selected=sel, out=out, lse=lse, workspace=ws)
+        return sel
+
+    graphs, outs = [], []
+    for _ in range(2):
+        out, lse = torch.empty(2, 4, 6, 64, device=DEV), torch.empty(2, 4, 6, device=DEV)
+        src.copy_(q)
+        step(out[0], lse[0])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sel = [step(out[i], lse[i]) for i in range(2)]
+        graphs.append(g)
+        outs.append((out, lse, sel))
+    for i in range(12):
+        src.copy_(rand(4, 6, 64, seed=70 + i, scale=1.5))
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        out, lse, sel = outs[i % 2]
+        want = po.select(src, summary, table, sl, P, top_k)
+        ref = po.attend(src, k, v, table, sl, 64 ** -0.5, selected=dev(want))
+        for c in range(2):
+            assert np.array_equal(sel[c].cpu().numpy(), want)
+            check_attn(out[c], lse[c], ref)
+
+
 def test_attn_capped_grid():
     """A capped grid walks many items per block: the same values up to the order of the joins."""
     lens = [0, 700, 33, 1, 2500, 64]
