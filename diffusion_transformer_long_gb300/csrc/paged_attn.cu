@@ -75,7 +75,7 @@ struct PagedParams {
 template <int D>
 struct PagedSmem {
   static constexpr int kBox = kTile * D * 2;           // K or V of one tile
-  static constexpr int kStages = 96 * 1024 / (kWarps * 2 * kBox);  // 3 (D = 128) or 6
+  static constexpr int kStages = 64 * 1024 / (kWarps * 2 * kBox);  // 2 (D = 128) or 4
   static constexpr int kRing = kWarps * kStages * 2 * kBox;
   static constexpr int kJoin = kWarps * 8 * D * 4;     // eight heads' sums of each warp
   static constexpr int kBars = kRing + kJoin;          // mbarriers
