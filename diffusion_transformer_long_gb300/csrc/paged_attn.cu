@@ -4,9 +4,9 @@
 // for the H_q / H_kv query heads that share a key/value head at once, each key and value read
 // once.  2 H_kv D bytes per key feed at most 4 H_q D operations: bound by HBM.
 //
-// Work split.  A unit is 64 keys of one (request, key/value head, block of query heads).  The
-// units of the whole batch, counted from the lengths on the device, are dealt out evenly: each
-// block takes one run of consecutive units, whatever request they belong to, so that ragged
+// Work split.  A unit is 64 keys of one item (request, key/value head, block of query heads).  The
+// units of the whole batch, counted from the lengths on the device, and a fixed cost for each item
+// are dealt out evenly: each block takes one run of consecutive units, whatever request they belong to, so that ragged
 // lengths and a single long request fill the GPU alike.  A run that ends inside an item leaves
 // fp32 partials (sum, m, l) in the workspace, at most two per block; a second, small launch
 // joins them in the order of the blocks (a fixed order: equal calls give equal bits).
@@ -47,6 +47,7 @@ constexpr int kWarps = 4;
 constexpr int kThreadsPaged = kWarps * 32;
 constexpr int kTile = 16;                    // keys of a warp's stage
 constexpr int kUnitTiles = kWarps;           // tiles of a unit
+constexpr int kItemCost = 2;                 // what an item costs beside its units, in units
 constexpr int kMaxBlocks = 512;              // largest grid the workspace serves
 constexpr float kSlack = 8.f;                // log2 of the largest weight against the running maximum
 
@@ -118,10 +119,13 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The units of one request's item: 64-key blocks of its cached (or listed) keys, at least one,
-// so that a request without keys still gets its output written.
+// One request's item: the 64-key units of its cached (or listed) keys, at least one, so that a
+// request without keys still gets its output written.  Its cost adds what its queries, look-ups and
+// joining take (2.3 us, about as long as a block's share of HBM needs for 1.6 units), so that a
+// block with many short items is not dealt as many keys as one with a few long ones.
 struct Item {
   int len, pages, tiles, units;
+  __device__ __forceinline__ int cost() const { return units + kItemCost; }
 };
 __device__ __forceinline__ Item item_of(const PagedParams& p, int b) {
   Item x;
@@ -132,22 +136,24 @@ __device__ __forceinline__ Item item_of(const PagedParams& p, int b) {
   return x;
 }
 
-// Walks a block's run of units item by item: units [u0, u1) of item j of request b.
+// Walks a block's run item by item: units [u0, u1) (none, where the run meets only the item's
+// extra cost) of item j of request b.
 struct Walk {
-  int b, j, u0, u1;
-  long long left;  // units of the run behind u1
+  int b, j, c0, u0, u1;  // c0: where the run meets the item, in its cost
+  long long left;        // of the run's cost, behind this item
   Item it;
-  __device__ __forceinline__ void start(const PagedParams& p, int b_, int j_, int u, long long n) {
+  __device__ __forceinline__ void start(const PagedParams& p, int b_, int j_, int c, long long n) {
     b = b_;
     j = j_;
     it = item_of(p, b);
-    u0 = u;
+    c0 = c;
     left = n;
     take();
   }
   __device__ __forceinline__ void take() {
-    const int n = static_cast<int>(min(static_cast<long long>(it.units - u0), left));
-    u1 = u0 + n;
+    const int n = static_cast<int>(min(static_cast<long long>(it.cost() - c0), left));
+    u0 = min(c0, it.units);
+    u1 = min(c0 + n, it.units);
     left -= n;
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
@@ -155,7 +161,7 @@ struct Walk {
       j = 0;
       it = item_of(p, ++b);
     }
-    u0 = 0;
+    c0 = 0;
     take();
   }
   // Tiles of the segment for one warp: first + 4 i < end.
@@ -163,52 +169,77 @@ struct Walk {
   __device__ __forceinline__ int end() const { return min(u1 * kUnitTiles, it.tiles); }
 };
 
-// One warp's loads, running ahead of its arithmetic over the same sequence of tiles.
+// One warp's loads, running ahead of its arithmetic over the same sequence of tiles.  The pages of
+// up to 32 tiles are looked up at once, a tile a lane, one such batch ahead of the one in use.
 template <int D>
 struct Producer {
   using S = PagedSmem<D>;
+  struct Batch {
+    int n, head;     // tiles (0: the run is over), key/value head
+    int page, spot;  // the lane's tile: page, first row | keys << 16 (0: no key of it counts)
+  };
   Walk w;
-  int i;           // the segment's next tile is first(warp) + 4 i
-  int page, spot;  // lane l: page of tile i / 32 * 32 + l, its first row | keys << 16
-  int count;       // tiles issued
-  __device__ __forceinline__ void look_up(const PagedParams& p, int warp, int lane) {
-    const int t = w.first(warp) + kUnitTiles * (i + lane);
-    page = 0;
-    spot = 0;
-    if (t < w.end()) {
+  int at;  // tiles of w's segment that are in batches
+  Batch now, ahead;
+  int i;      // the batch's next tile
+  int count;  // tiles issued
+  __device__ __forceinline__ Batch look_up(const PagedParams& p, int warp, int lane) {
+    Batch x;
+    x.n = 0;
+    while (w.first(warp) + kUnitTiles * at >= w.end()) {
+      if (w.left == 0) return x;
+      w.next(p);
+      at = 0;
+    }
+    const int first = w.first(warp) + kUnitTiles * at;
+    x.n = min(32, (w.end() - first + kUnitTiles - 1) / kUnitTiles);
+    x.head = w.j / p.head_blocks;
+    x.page = 0;
+    x.spot = 0;
+    at += x.n;
+    const int t = first + kUnitTiles * lane;
+    if (lane < x.n) {
       int col = t / p.page_tiles;
       const int row = (t - col * p.page_tiles) * kTile;
-      if (p.selected)
-        col = __ldg(p.selected + (static_cast<long long>(w.b) * p.h_kv + w.j / p.head_blocks) * p.n_selected + col);
+      if (p.selected) col = __ldg(p.selected + (static_cast<long long>(w.b) * p.h_kv + x.head) * p.n_selected + col);
       if (col >= 0 && col < w.it.pages) {
-        page = __ldg(p.table + w.b * p.table_stride + col);
+        x.page = __ldg(p.table + w.b * p.table_stride + col);
         const int keys = min(kTile, w.it.len - col * p.page_size - row);
-        if (page >= 0 && page < p.n_pages && keys > 0) spot = row | keys << 16;
+        if (keys > 0) x.spot = row | keys << 16;
       }
     }
+    return x;
+  }
+  __device__ __forceinline__ void start(const PagedParams& p, const Walk& first, int warp, int lane) {
+    w = first;
+    at = i = count = 0;
+    now = look_up(p, warp, lane);
+    ahead.n = 0;
+    if (now.n) ahead = look_up(p, warp, lane);
   }
   __device__ __forceinline__ void issue(const PagedParams& p, uint32_t ring, uint32_t bars, int* valid, int warp,
                                         int lane) {
-    while (w.first(warp) + kUnitTiles * i >= w.end()) {
-      if (w.left == 0) return;
-      w.next(p);
+    if (i == now.n) {
+      if (ahead.n == 0) return;
+      now = ahead;
       i = 0;
+      ahead = look_up(p, warp, lane);
     }
-    if ((i & 31) == 0) look_up(p, warp, lane);
-    const int pg = __shfl_sync(~0u, page, i & 31), sp = __shfl_sync(~0u, spot, i & 31);
+    const int page = __shfl_sync(~0u, now.page, i);
+    int spot = __shfl_sync(~0u, now.spot, i);
+    if (page < 0 || page >= p.n_pages) spot = 0;
     ++i;
     const int stage = count % S::kStages;
     ++count;
     if (lane == 0) {
       const uint32_t bar = bars + stage * 8, dst = ring + stage * 2 * S::kBox;
-      valid[stage] = sp >> 16;
-      if (sp == 0 || p.stall) {  // no key of this tile counts: nothing to load
+      valid[stage] = spot >> 16;
+      if (spot == 0 || p.stall) {  // nothing to load
         if (!p.stall) ptx::mbar_arrive(bar);
       } else {
-        const int head = w.j / p.head_blocks;
         ptx::mbar_arrive_expect_tx(bar, 2 * S::kBox);
-        tma_load_5d(dst, &p.tm_k, bar, 0, sp & 0xffff, 0, head, pg);
-        tma_load_5d(dst + S::kBox, &p.tm_v, bar, 0, sp & 0xffff, 0, head, pg);
+        tma_load_5d(dst, &p.tm_k, bar, 0, spot & 0xffff, 0, now.head, page);
+        tma_load_5d(dst + S::kBox, &p.tm_v, bar, 0, spot & 0xffff, 0, now.head, page);
       }
     }
   }
@@ -241,12 +272,12 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     ptx::fence_mbar_init();
   }
   wait_for_inputs();
-  // All units of the batch, and where this block's run of them begins: each thread sums a chunk
-  // of the requests, the one whose chunk holds the run's first unit finds the request.
+  // The batch's cost, and where this block's run begins: each thread sums a chunk
+  // of the requests, the one whose chunk holds the run's beginning finds the request.
   const int per = (p.batch + kThreadsPaged - 1) / kThreadsPaged;
   const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += item_of(p, b).units;
+  for (int b = b0; b < b1; ++b) sum += item_of(p, b).cost();
   sum *= items;
   long long upto = sum;
 #pragma unroll
@@ -273,10 +304,10 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
   if (run0 < upto && run0 >= upto - sum) {
     long long at = upto - sum;
     int b = b0;
-    long long n = static_cast<long long>(item_of(p, b).units) * items;
+    long long n = static_cast<long long>(item_of(p, b).cost()) * items;
     while (at + n <= run0) {
       at += n;
-      n = static_cast<long long>(item_of(p, ++b).units) * items;
+      n = static_cast<long long>(item_of(p, ++b).cost()) * items;
     }
     scan[0] = b;
     scan[1] = run0 - at;
@@ -285,14 +316,12 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
   Walk seg;
   {
     const int b = static_cast<int>(scan[0]);
-    const int units = item_of(p, b).units;
-    const int j = static_cast<int>(scan[1] / units);
-    seg.start(p, b, j, static_cast<int>(scan[1] - static_cast<long long>(j) * units), run1 - run0);
+    const int cost = item_of(p, b).cost();
+    const int j = static_cast<int>(scan[1] / cost);
+    seg.start(p, b, j, static_cast<int>(scan[1] - static_cast<long long>(j) * cost), run1 - run0);
   }
   Producer<D> load;
-  load.w = seg;
-  load.i = 0;
-  load.count = 0;
+  load.start(p, seg, warp, lane);
   for (int s = 0; s < S::kStages; ++s) load.issue(p, ring, bars, valid, warp, lane);
 
   // ldmatrix addresses of this lane: row and 16-byte chunk of K (A operand, keys x channels) and
@@ -304,7 +333,14 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
   bool dead = false;
   int consumed = 0, landed = 0;  // tiles passed; those whose copies have been waited for
   int4 note = make_int4(0, 0, 0, 0);
+  long long pos = run0;  // of c0 in the batch's cost
   for (;;) {
+    if (seg.u0 == seg.u1) {
+      if (seg.left == 0) break;
+      pos += seg.it.cost() - seg.c0;
+      seg.next(p);
+      continue;
+    }
     const int hk = seg.j / p.head_blocks, h0 = (seg.j - hk * p.head_blocks) * R;
     // query fragments (B operand, channels x heads)
     uint32_t qf[kNb][kSteps][2];
@@ -532,10 +568,11 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     }
     if (!whole && slot == 1) {
       // the item goes on in later blocks: up to the one that holds its last unit
-      const long long last = run1 - 1 + seg.it.units - seg.u1;
+      const long long last = pos - seg.c0 + seg.it.units - 1;
       note = make_int4(seg.b, seg.j, static_cast<int>(((last + 1) * blocks - 1) / total - c) + 1, 0);
     }
     if (seg.left == 0) break;
+    pos += seg.it.cost() - seg.c0;
     seg.next(p);
   }
   if (threadIdx.x == 0) p.meta[c] = note;
