@@ -316,6 +316,30 @@ def test_attn_views_streams_workspace():
     assert torch.equal(o2, out[:4]) and torch.equal(l2, lse[:4])
 
 
+@pytest.mark.parametrize("B", [700, 5000])
+def test_attn_many_requests(B):
+    """More requests than a block has threads: lengths 0 to 40, one longer; rows in a strided query."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 41, B)
+    lens[B // 3] = 900
+    q, k, v, table, sl = make_case(list(lens), 4, 2, 64, 16, seed=81)
+    check_attn(*da.paged_attn_fwd(q, k, v, table, sl), po.attend(q, k, v, table, sl, 0.125))
+
+
+def test_attn_scores_without_a_finite_one():
+    """Keys that score -inf weigh nothing; a request all of whose keys do is one without keys."""
+    q, k, v, table, sl = make_case([40, 20], 2, 2, 64, 16, seed=83)
+    q[:, :, 0] = 1.0
+    k[table[0, 1], :, :, 0] = -float("inf")
+    k[table[1, :2].long(), :, :, 0] = -float("inf")
+    o, lse = da.paged_attn_fwd(q, k, v, table, sl)
+    cut = table.clone()
+    cut[0, 1] = -1
+    cut[1] = -1
+    check_attn(o, lse, po.attend(q, k.nan_to_num(neginf=0), v, cut, sl, 0.125))
+    assert (lse[1] == -float("inf")).all() and (o[1] == 0).all()
+
+
 def test_attn_two_streams_at_once():
     cases = [make_case([2000 + i, 900, 5], 24, 8, 128, 16, seed=20 + i) for i in range(2)]
     alone = [da.paged_attn_fwd(*c) for c in cases]
@@ -487,6 +511,30 @@ def test_select_borders(kind):
         q[1, 4, 7] = float("nan")
     t, sl = dev(table), dev(lens)
     for k in (1, 2, top_k, table.shape[1]):
+        got = da.paged_select(q, summary, t, sl, P, k)
+        assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, k)), k
+
+
+@pytest.mark.parametrize("n,kind", [(700, "equal"), (700, "nan"), (3000, "two values"), (9001, "random"),
+                                    (9001, "equal"), (9001, "two values"), (9001, "inf")])
+def test_select_among_many_pages(n, kind):
+    """More pages at the border than are ranked pair by pair, and more pages than shared memory holds."""
+    P, Hq, Hkv, D = 16, 3, 1, 64
+    table, n_pages = tables([n * P, n * P - 5], P, seed=n)
+    q = rand(2, Hq, D, seed=1)
+    a, b = rand(n_pages, Hkv, 1, D, seed=2), rand(n_pages, Hkv, 1, D, seed=3)
+    summary = torch.cat((torch.minimum(a, b), torch.maximum(a, b)), 2)
+    some = torch.rand(n_pages, generator=torch.Generator(device=DEV).manual_seed(4), device=DEV) < 0.4
+    if kind == "equal":
+        summary[:] = summary[:1].clone()
+    elif kind == "two values":
+        summary[:] = summary[some.int()]
+    elif kind == "nan":
+        summary[some, 0, 1, 9] = float("nan")
+    elif kind == "inf":
+        summary[some, 0, 0, 9] = -float("inf")
+    t, sl = dev(table), dev([n * P, n * P - 5])
+    for k in (2, 17, n // 3, n - 1):
         got = da.paged_select(q, summary, t, sl, P, k)
         assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, k)), k
 
