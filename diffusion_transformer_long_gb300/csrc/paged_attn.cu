@@ -16,11 +16,11 @@
 // one for V, 128-byte swizzle), and its own softmax state; the four states are joined through
 // shared memory where an item ends.  No block-wide barrier stands between the loads.
 //
-// Arithmetic.  Scores S^T = K Q^T on mma.sync m16n8k16 (keys x heads, 8 or 16 heads), so that a
+// Arithmetic.  Scores S^T = K Q^T on mma.sync m16n8k16 (keys x heads, 8 to 32 heads), so that a
 // column is a query head, padding to 8 heads and not to the 16 rows of an A operand, and the
 // running output O^T = V^T P^T has the same columns: a thread holds the statistics of the two
-// heads whose outputs it holds.  tcgen05 would need 64 or 128 rows for 1 to 16 heads and the
-// scores through tensor memory; at 1 to 16 operations per byte the tensor pipe is idle either
+// heads whose outputs it holds.  tcgen05 would need 64 or 128 rows for 1 to 32 heads and the
+// scores through tensor memory; at 1 to 32 operations per byte the tensor pipe is idle either
 // way.  P goes to bf16 in two parts (fp32 output: three), hi + lo (+ lo2), so that its rounding
 // (2^-18, fp32: 2^-27) does not show; each tile's product starts from zero and is added in
 // fp32, because the tensor core's own accumulation truncates, and over hundreds of tiles that
@@ -46,6 +46,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreadsPaged = kWarps * 32;
 constexpr int kTile = 16;                    // keys of a warp's stage
+constexpr int kMaxRows = 32;                 // query heads that a block holds
 constexpr int kUnitTiles = kWarps;           // tiles of a unit
 constexpr int kItemCost = 2;                 // what an item costs beside its units, in units
 constexpr int kMaxBlocks = 512;              // largest grid the workspace serves
@@ -82,8 +83,9 @@ struct PagedSmem {
   static constexpr int kBars = kRing + kJoin;          // mbarriers
   static constexpr int kValid = kBars + kWarps * kStages * 8;
   static constexpr int kMl = kValid + kWarps * kStages * 4;
-  static constexpr int kScan = kMl + kWarps * 16 * 8;
-  static constexpr int kBytes = kScan + 64;
+  static constexpr int kScan = kMl + kWarps * kMaxRows * 8;
+  static constexpr int kQ = kScan + 64;                // query fragments, where registers have no room
+  static constexpr int bytes(int nb) { return kQ + (nb > 2 ? nb * (D / 16) * 32 * 8 : 0); }
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
   constexpr int kSteps = D / 16;
   constexpr int kParts = sizeof(OT) == 4 ? 3 : 2;
   constexpr int R = 8 * kNb;
+  constexpr bool kQShared = kNb > 2;  // 32 registers of queries for 16 heads fit beside the output's 64
   extern __shared__ __align__(1024) unsigned char smem[];
   float* join = reinterpret_cast<float*>(smem + S::kRing);
   float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
@@ -343,18 +346,26 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     }
     const int hk = seg.j / p.head_blocks, h0 = (seg.j - hk * p.head_blocks) * R;
     // query fragments (B operand, channels x heads)
-    uint32_t qf[kNb][kSteps][2];
+    uint32_t qf[kQShared ? 1 : kNb][kSteps][2];
+    uint2* q_sm = reinterpret_cast<uint2*>(smem + S::kQ);  // [nb][step][lane]
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) {
+      if (kQShared && nb % kWarps != warp) continue;  // shared: each warp fetches its part
       const int h = h0 + nb * 8 + (lane >> 2);
       const uint32_t* q = reinterpret_cast<const uint32_t*>(
           p.q + seg.b * p.q_b + static_cast<long long>(hk * p.group + h) * p.q_h + (lane & 3) * 2);
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        qf[nb][k][0] = h < p.group ? __ldg(q + k * 8) : 0;
-        qf[nb][k][1] = h < p.group ? __ldg(q + k * 8 + 4) : 0;
+        const uint2 x = h < p.group ? make_uint2(__ldg(q + k * 8), __ldg(q + k * 8 + 4)) : make_uint2(0, 0);
+        if constexpr (kQShared) {
+          q_sm[(nb * kSteps + k) * 32 + lane] = x;
+        } else {
+          qf[nb][k][0] = x.x;
+          qf[nb][k][1] = x.y;
+        }
       }
     }
+    if constexpr (kQShared) __syncthreads();  // (the last item's barriers have freed the buffer)
     float o[kSteps][kNb][4];
     float m[kNb][2], l[kNb][2], lc[kNb][2];  // lc: the sum's compensation
 #pragma unroll
@@ -396,7 +407,15 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
           const int ch = (k & 3) * 2 + k_chunk;
           ldsm4(kb + (k >> 2) * (kTile * 128) + k_row * 128 + ((ch ^ (k_row & 7)) << 4), a);
 #pragma unroll
-          for (int nb = 0; nb < kNb; ++nb) mma16816(s[nb], a, qf[nb][k]);
+          for (int nb = 0; nb < kNb; ++nb) {
+            if constexpr (kQShared) {
+              const uint2 x = q_sm[(nb * kSteps + k) * 32 + lane];
+              const uint32_t b[2] = {x.x, x.y};
+              mma16816(s[nb], a, b);
+            } else {
+              mma16816(s[nb], a, qf[nb][k]);
+            }
+          }
         }
         const bool in0 = (lane >> 2) < keys, in1 = (lane >> 2) + 8 < keys;
         bool moves = false;
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
         x += __shfl_xor_sync(~0u, x, 4);
         x += __shfl_xor_sync(~0u, x, 8);
         x += __shfl_xor_sync(~0u, x, 16);
-        if (lane < 4) ml[warp * 16 + nb * 8 + lane * 2 + i] = make_float2(m[nb][i], x);
+        if (lane < 4) ml[warp * kMaxRows + nb * 8 + lane * 2 + i] = make_float2(m[nb][i], x);
       }
     }
     __syncthreads();
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
         const int head = (lane & 3) * 2 + i;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * 16 + nb * 8 + head].x);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kMaxRows + nb * 8 + head].x);
         const float f = M == -INFINITY ? 0.f : ptx::ex2_approx(m[nb][i] - M);
         float* dst = join + (warp * 8 + head) * D;
 #pragma unroll
@@ -516,10 +535,10 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
         const int h = h0 + nb * 8 + head;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * 16 + nb * 8 + head].x);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kMaxRows + nb * 8 + head].x);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float2 x = ml[w * 16 + nb * 8 + head];
+          const float2 x = ml[w * kMaxRows + nb * 8 + head];
           L += M == -INFINITY ? 0.f : x.y * ptx::ex2_approx(x.x - M);
         }
         float x[kCols];
@@ -664,7 +683,8 @@ bool encode_cache(CUtensorMap* m, const void* base, const Strides& s, int d, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int row_block(int group) { return group <= 8 ? 8 : 16; }
+// Query heads that share one pass over the keys: the group's, in eights, up to 32.
+int row_block(int group) { return std::min((group + 7) / 8 * 8, kMaxRows); }
 
 template <int D, int kNb, typename OT>
 cudaError_t launch_typed(const PagedParams& p, int blocks, cudaStream_t st) {
@@ -678,12 +698,12 @@ cudaError_t launch_typed(const PagedParams& p, int blocks, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PagedSmem<D>::kBytes);
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PagedSmem<D>::bytes(kNb));
       if (e != cudaSuccess) return e;
       ready[dev] = true;
     }
   }
-  e = launch_after(kern, dim3(blocks), dim3(kThreadsPaged), PagedSmem<D>::kBytes, st, p);
+  e = launch_after(kern, dim3(blocks), dim3(kThreadsPaged), PagedSmem<D>::bytes(kNb), st, p);
   if (e != cudaSuccess) return e;
   return launch_after(paged_join_kernel<D, kNb, OT>, dim3(blocks, std::min(p.group, 8 * kNb)), dim3(128), 0, st, p);
 }
@@ -691,6 +711,16 @@ cudaError_t launch_typed(const PagedParams& p, int blocks, cudaStream_t st) {
 template <int D, int kNb>
 cudaError_t launch_out(const PagedParams& p, bool f32, int blocks, cudaStream_t st) {
   return f32 ? launch_typed<D, kNb, float>(p, blocks, st) : launch_typed<D, kNb, __nv_bfloat16>(p, blocks, st);
+}
+
+template <int D>
+cudaError_t launch_rows(const PagedParams& p, int rows, bool f32, int blocks, cudaStream_t st) {
+  switch (rows) {
+    case 8: return launch_out<D, 1>(p, f32, blocks, st);
+    case 16: return launch_out<D, 2>(p, f32, blocks, st);
+    case 24: return launch_out<D, 3>(p, f32, blocks, st);
+    default: return launch_out<D, 4>(p, f32, blocks, st);
+  }
 }
 
 }  // namespace
@@ -736,9 +766,7 @@ cudaError_t launch_paged_attn(const PagedAttnLaunch& a, cudaStream_t st) {
   // Two blocks of 113 KB of shared memory fit one SM.
   int blocks = std::min(kMaxBlocks, 2 * host::sm_count());
   if (grid_limit() > 0) blocks = std::min(blocks, grid_limit());
-  if (a.d == 64)
-    return R == 8 ? launch_out<64, 1>(p, a.out_f32, blocks, st) : launch_out<64, 2>(p, a.out_f32, blocks, st);
-  return R == 8 ? launch_out<128, 1>(p, a.out_f32, blocks, st) : launch_out<128, 2>(p, a.out_f32, blocks, st);
+  return a.d == 64 ? launch_rows<64>(p, R, a.out_f32, blocks, st) : launch_rows<128>(p, R, a.out_f32, blocks, st);
 }
 
 }  // namespace ditattn
