@@ -337,23 +337,16 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
   int consumed = 0, landed = 0;  // tiles passed; those whose copies have been waited for
   int4 note = make_int4(0, 0, 0, 0);
   long long pos = run0;  // of c0 in the batch's cost
-  for (;;) {
-    if (seg.u0 == seg.u1) {
-      if (seg.left == 0) break;
-      pos += seg.it.cost() - seg.c0;
-      seg.next(p);
-      continue;
-    }
-    const int hk = seg.j / p.head_blocks, h0 = (seg.j - hk * p.head_blocks) * R;
-    // query fragments (B operand, channels x heads)
-    uint32_t qf[kQShared ? 1 : kNb][kSteps][2];
-    uint2* q_sm = reinterpret_cast<uint2*>(smem + S::kQ);  // [nb][step][lane]
+  uint32_t qf[kQShared ? 1 : kNb][kSteps][2];          // query fragments (B operand, channels x heads)
+  uint2* q_sm = reinterpret_cast<uint2*>(smem + S::kQ);  // [nb][step][lane]
+  auto load_queries = [&](const Walk& w) {
+    const int hk = w.j / p.head_blocks, h0 = (w.j - hk * p.head_blocks) * R;
 #pragma unroll
     for (int nb = 0; nb < kNb; ++nb) {
       if (kQShared && nb % kWarps != warp) continue;  // shared: each warp fetches its part
       const int h = h0 + nb * 8 + (lane >> 2);
       const uint32_t* q = reinterpret_cast<const uint32_t*>(
-          p.q + seg.b * p.q_b + static_cast<long long>(hk * p.group + h) * p.q_h + (lane & 3) * 2);
+          p.q + w.b * p.q_b + static_cast<long long>(hk * p.group + h) * p.q_h + (lane & 3) * 2);
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
         const uint2 x = h < p.group ? make_uint2(__ldg(q + k * 8), __ldg(q + k * 8 + 4)) : make_uint2(0, 0);
@@ -365,7 +358,21 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
         }
       }
     }
-    if constexpr (kQShared) __syncthreads();  // (the last item's barriers have freed the buffer)
+  };
+  // The run's next item with units (false: the run is over); `at` follows its place in the batch's cost.
+  auto advance = [&](Walk& w, long long& at) {
+    do {
+      if (w.left == 0) return false;
+      at += w.it.cost() - w.c0;
+      w.next(p);
+    } while (w.u0 == w.u1);
+    return true;
+  };
+  bool more = seg.u0 < seg.u1 || advance(seg, pos);
+  if (more) load_queries(seg);
+  while (more) {
+    if constexpr (kQShared) __syncthreads();
+    const int hk = seg.j / p.head_blocks, h0 = (seg.j - hk * p.head_blocks) * R;
     float o[kSteps][kNb][4];
     float m[kNb][2], l[kNb][2], lc[kNb][2];  // lc: the sum's compensation
 #pragma unroll
@@ -496,7 +503,13 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
       if (!dead) load.issue(p, ring, bars, valid, warp, lane);
     }
 
-    // ---- the four warps' states of this segment, joined
+    // The next item's queries are on their way while this one's states are joined.
+    Walk next = seg;
+    long long next_pos = pos;
+    more = advance(next, next_pos);
+    if (more && !kQShared) load_queries(next);
+
+    // ---- the four warps' states of this segment, joined: the output, or a part of it
     const bool whole = seg.u0 == 0 && seg.u1 == seg.it.units;
     const int slot = seg.u0 > 0 ? 0 : 1;
 #pragma unroll
@@ -508,24 +521,12 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
         x += __shfl_xor_sync(~0u, x, 8);
         x += __shfl_xor_sync(~0u, x, 16);
         if (lane < 4) ml[warp * kMaxRows + nb * 8 + lane * 2 + i] = make_float2(m[nb][i], x);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int nb = 0; nb < kNb; ++nb) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int head = (lane & 3) * 2 + i;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kMaxRows + nb * 8 + head].x);
-        const float f = M == -INFINITY ? 0.f : ptx::ex2_approx(m[nb][i] - M);
-        float* dst = join + (warp * 8 + head) * D;
+        float* dst = join + (warp * 8 + (lane & 3) * 2 + i) * D;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           const int d = k * 16 + (lane >> 2);
-          dst[d ^ ((lane & 3) << 3)] = o[k][nb][i] * f;
-          dst[(d + 8) ^ ((lane & 3) << 3)] = o[k][nb][i + 2] * f;
+          dst[d ^ ((lane & 3) << 3)] = o[k][nb][i];
+          dst[(d + 8) ^ ((lane & 3) << 3)] = o[k][nb][i + 2];
         }
       }
       __syncthreads();
@@ -533,54 +534,43 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
         constexpr int kCols = 8 * D / kThreadsPaged;  // channels of a thread: 8 (D = 128) or 4
         const int head = threadIdx.x / (D / kCols), d0 = threadIdx.x % (D / kCols) * kCols;
         const int h = h0 + nb * 8 + head;
-        float M = -INFINITY, L = 0.f;
+        float M = -INFINITY, L = 0.f, f[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kMaxRows + nb * 8 + head].x);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float2 x = ml[w * kMaxRows + nb * 8 + head];
-          L += M == -INFINITY ? 0.f : x.y * ptx::ex2_approx(x.x - M);
+          f[w] = M == -INFINITY ? 0.f : ptx::ex2_approx(x.x - M);
+          L = fmaf(f[w], x.y, L);
         }
-        float x[kCols];
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const long long row = static_cast<long long>(seg.b) * p.h_q + hk * p.group + h;
+        const long long part = (c * 2 + slot) * R + nb * 8 + head;
 #pragma unroll
         for (int i = 0; i < kCols; i += 4) {
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float4 y = *reinterpret_cast<const float4*>(join + (w * 8 + head) * D + ((d0 + i) ^ ((head >> 1) << 3)));
-            acc.x += y.x;
-            acc.y += y.y;
-            acc.z += y.z;
-            acc.w += y.w;
+            x.x = fmaf(f[w], y.x, x.x);
+            x.y = fmaf(f[w], y.y, x.y);
+            x.z = fmaf(f[w], y.z, x.z);
+            x.w = fmaf(f[w], y.w, x.w);
           }
-          x[i] = acc.x;
-          x[i + 1] = acc.y;
-          x[i + 2] = acc.z;
-          x[i + 3] = acc.w;
+          if (!whole) {
+            *reinterpret_cast<float4*>(p.part_o + part * D + d0 + i) = x;
+          } else if (h < p.group) {
+            OT* dst = static_cast<OT*>(p.out) + row * D + d0 + i;
+            if constexpr (sizeof(OT) == 4)
+              *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+            else
+              *reinterpret_cast<uint2*>(dst) =
+                  make_uint2(ptx::pack_bf16x2(x.x * inv, x.y * inv), ptx::pack_bf16x2(x.z * inv, x.w * inv));
+          }
         }
-        if (whole) {
-          if (h < p.group) {
-            const long long row = static_cast<long long>(seg.b) * p.h_q + hk * p.group + h;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            OT* dst = static_cast<OT*>(p.out) + row * D + d0;
-#pragma unroll
-            for (int i = 0; i < kCols; i += 4) {
-              if constexpr (sizeof(OT) == 4) {
-                *reinterpret_cast<float4*>(dst + i) = make_float4(x[i] * inv, x[i + 1] * inv, x[i + 2] * inv, x[i + 3] * inv);
-              } else {
-                *reinterpret_cast<uint2*>(dst + i) = make_uint2(ptx::pack_bf16x2(x[i] * inv, x[i + 1] * inv),
-                                                                ptx::pack_bf16x2(x[i + 2] * inv, x[i + 3] * inv));
-              }
-            }
-            if (p.lse && d0 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-          }
-        } else {
-          const long long at = (c * 2 + slot) * R + nb * 8 + head;
-          float* dst = p.part_o + at * D + d0;
-#pragma unroll
-          for (int i = 0; i < kCols; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-          if (d0 == 0) p.part_ml[at] = make_float2(M, L);
+        if (d0 == 0) {
+          if (!whole) p.part_ml[part] = make_float2(M, L);
+          else if (p.lse && h < p.group) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         }
       }
       __syncthreads();
@@ -590,9 +580,9 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
       const long long last = pos - seg.c0 + seg.it.units - 1;
       note = make_int4(seg.b, seg.j, static_cast<int>(((last + 1) * blocks - 1) / total - c) + 1, 0);
     }
-    if (seg.left == 0) break;
-    pos += seg.it.cost() - seg.c0;
-    seg.next(p);
+    if (more && kQShared) load_queries(next);
+    seg = next;
+    pos = next_pos;
   }
   if (threadIdx.x == 0) p.meta[c] = note;
   if (dead) {
