@@ -17,9 +17,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libditattn.so")
 SOURCES = ["attn_fwd.cu", "attn_fwd_short.cu", "lse_merge.cu", "layout_copy.cu", "noalloc.cu", "ditattn_api.cu",
-           "paged_api.cu", "paged_plan.cu", "paged_write.cu", "paged_attn.cu", "paged_select.cu"]
+           "paged_api.cu", "paged_plan.cu", "paged_write.cu", "paged_attn.cu", "paged_attn_few.cu",
+           "paged_select.cu"]
 HEADERS = ["attn_kernel.cuh", "attn_host.cuh", "merge_math.cuh", "sm103_ptx.cuh", "launch.h", "api_checks.h",
-           "paged_launch.h", "paged_device.cuh"]
+           "paged_launch.h", "paged_device.cuh", "paged_attn_kernel.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

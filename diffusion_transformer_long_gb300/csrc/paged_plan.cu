@@ -75,7 +75,6 @@ __device__ __forceinline__ int find(const int* first, int n, int x) {
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p) {
   extern __shared__ int sm[];
-  launch_dependents();
   wait_for_inputs();
   __shared__ int warp_sums[32];
   const int B = p.a.batch, P = p.a.page_size;

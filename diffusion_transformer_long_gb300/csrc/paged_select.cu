@@ -14,6 +14,7 @@
 // page in down to a histogram bin; a page more than 2 e above the bin is in, one more than 2 e
 // below is out, and those between, a handful, are scored again in 64 bits and ranked.  A score
 // that is not finite in 32 bits sends all pages of its row that way.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -21,6 +22,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "attn_host.cuh"
 #include "paged_device.cuh"
 #include "paged_launch.h"
 #include "sm103_ptx.cuh"
@@ -84,20 +86,12 @@ __device__ __forceinline__ int pages_now(const SelectLaunch& a, int b) {
   return pages_of(min(max(0, a.seq_lens[b]), a.max_pages * a.page_size), a.page_size);
 }
 
-// A warp scores 16 pages of one (request, key/value head).
-template <int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __grid_constant__ PickParams p) {
+// A warp scores 16 pages of one (request, key/value head), the n table columns' from 16 chunk on:
+// store(i, key) gets each one's, by one lane.  Returns the largest sum |q| |k|.
+template <int D, typename Store>
+__device__ __forceinline__ float score_pages(const SelectLaunch& a, int b, int g, int n, int chunk, Store store) {
   constexpr int kLoads = 2 * D / 32;  // 64-byte pieces of a page's [lo | hi]
-  launch_dependents();
-  wait_for_inputs();
-  const SelectLaunch& a = p.a;
-  const int bg = blockIdx.y + blockIdx.z * gridDim.y;
-  if (bg >= a.batch * a.h_kv) return;
-  const int b = bg / a.h_kv, g = bg - b * a.h_kv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 3;
-  const int chunk = blockIdx.x * kScoreWarps + warp, i0 = chunk * kChunk;
-  const int n = pages_now(a, b);
-  if (i0 >= n || n <= a.top_k) return;  // nothing to choose
+  const int lane = threadIdx.x & 31, j = lane & 3, i0 = chunk * kChunk;
   int page = -1;
   if (lane < kChunk && i0 + lane < n) page = a.table[b * a.table_stride + i0 + lane];
   if (page >= a.n_pages) page = -1;
@@ -152,13 +146,27 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __g
   }
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) mag = fmaxf(mag, __shfl_xor_sync(~0u, mag, d));
-  uint32_t* keys = p.keys + static_cast<long long>(bg) * a.max_pages;
   if (j == 0) {
     const int i = i0 + (lane >> 2);
-    if (i < n) keys[i] = p0 < 0 ? kLowest : odd0 ? kUnknown : key_of(best0 + 0.f);
-    if (i + 8 < n) keys[i + 8] = p1 < 0 ? kLowest : odd1 ? kUnknown : key_of(best1 + 0.f);
+    if (i < n) store(i, p0 < 0 ? kLowest : odd0 ? kUnknown : key_of(best0 + 0.f));
+    if (i + 8 < n) store(i + 8, p1 < 0 ? kLowest : odd1 ? kUnknown : key_of(best1 + 0.f));
   }
-  if (lane == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
+  return mag;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __grid_constant__ PickParams p) {
+  wait_for_inputs();
+  const SelectLaunch& a = p.a;
+  const int bg = blockIdx.y + blockIdx.z * gridDim.y;
+  if (bg >= a.batch * a.h_kv) return;
+  const int b = bg / a.h_kv, g = bg - b * a.h_kv;
+  const int chunk = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
+  const int n = pages_now(a, b);
+  if (chunk * kChunk >= n || n <= a.top_k) return;  // nothing to choose
+  uint32_t* keys = p.keys + static_cast<long long>(bg) * a.max_pages;
+  const float mag = score_pages<D>(a, b, g, n, chunk, [&](int i, uint32_t key) { keys[i] = key; });
+  if ((threadIdx.x & 31) == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
 }
 
 // Sum over the block; `sm` is free again at the next barrier.
@@ -244,39 +252,47 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
   return key_of(best);
 }
 
-__global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_constant__ PickParams p) {
-  __shared__ uint32_t cache[kCached];
-  __shared__ uint32_t mask_sm[kCached / 32];
-  __shared__ int bins[kBins];
-  __shared__ int between[kRanked];
-  __shared__ unsigned long long ranked[kRanked];
-  __shared__ uint32_t extremes[3][kPickWarps];
-  __shared__ int red[kPickWarps];
-  __shared__ int count, bin_found, bin_above;
+struct PickSmem {
+  uint32_t cache[kCached];  // the pages' keys
+  uint32_t mask[kCached / 32];
+  int bins[kBins];
+  int between[kRanked];
+  unsigned long long ranked[kRanked];
+  uint32_t extremes[3][kPickWarps];
+  int red[kPickWarps];
+  int count, bin_found, bin_above;
+};
+
+// Chooses top_k of one row's n > top_k > 1 pages, by a whole block.  kHeld: the keys are in sm.cache
+// (the block has met since) and mag_bits is this thread's share of the magnitudes; else both are
+// read from the workspace.
+template <bool kHeld>
+__device__ __forceinline__ void pick_pages(const PickParams& p, PickSmem& sm, int bg, int b, int g, int n, int* out,
+                                           uint32_t mag_bits) {
   const SelectLaunch& a = p.a;
-  const int bg = blockIdx.x, b = bg / a.h_kv, g = bg - b * a.h_kv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  launch_dependents();
-  wait_for_inputs();
-  const int n = pages_now(a, b);
-  int* out = a.selected + static_cast<long long>(bg) * a.top_k;
-  if (n <= a.top_k || a.top_k == 1) {
-    for (int i = tid; i < a.top_k; i += kPickThreads) out[i] = a.top_k == 1 ? n - 1 : i < n ? i : -1;
-    return;
-  }
+  uint32_t* const cache = sm.cache;
+  uint32_t* const mask_sm = sm.mask;
+  int* const bins = sm.bins;
+  int* const between = sm.between;
+  unsigned long long* const ranked = sm.ranked;
+  auto& extremes = sm.extremes;
+  int* const red = sm.red;
+  int &count = sm.count, &bin_found = sm.bin_found, &bin_above = sm.bin_above;
   const int others = n - 1, want = a.top_k - 1;  // 1 <= want < others
   const uint32_t* all_keys = p.keys + static_cast<long long>(bg) * a.max_pages;
-  const bool cached = others <= kCached;
-  uint32_t lo = ~0u, hi = 0, mag_bits = 0;  // magnitudes are >= 0 (or NaN): their bits are in order
+  const bool cached = kHeld || others <= kCached;
+  uint32_t lo = ~0u, hi = 0;  // magnitudes are >= 0 (or NaN): their bits are in order
 #pragma unroll 4
   for (int i = tid; i < others; i += kPickThreads) {
-    const uint32_t k = all_keys[i];
-    if (cached) cache[i] = k;
+    const uint32_t k = kHeld ? cache[i] : all_keys[i];
+    if (!kHeld && cached) cache[i] = k;
     lo = min(lo, k);
     hi = max(hi, k);
   }
-  for (int i = tid; i < (n + kChunk - 1) / kChunk; i += kPickThreads)
-    mag_bits = max(mag_bits, __float_as_uint(p.bounds[static_cast<long long>(bg) * p.chunks + i]));
+  if constexpr (!kHeld)
+    for (int i = tid; i < (n + kChunk - 1) / kChunk; i += kPickThreads)
+      mag_bits = max(mag_bits, __float_as_uint(p.bounds[static_cast<long long>(bg) * p.chunks + i]));
   lo = __reduce_min_sync(~0u, lo);
   hi = __reduce_max_sync(~0u, hi);
   mag_bits = __reduce_max_sync(~0u, mag_bits);
@@ -429,6 +445,52 @@ __global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_c
   if (tid == 0) out[a.top_k - 1] = n - 1;
 }
 
+// The list of a row that has nothing to choose: all its pages, or (top_k = 1) the newest alone.
+__device__ __forceinline__ void list_all(const SelectLaunch& a, int n, int* out, int threads) {
+  for (int i = threadIdx.x; i < a.top_k; i += threads) out[i] = a.top_k == 1 ? n - 1 : i < n ? i : -1;
+}
+
+__global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_constant__ PickParams p) {
+  __shared__ PickSmem sm;
+  wait_for_inputs();
+  const SelectLaunch& a = p.a;
+  const int bg = blockIdx.x, b = bg / a.h_kv, g = bg - b * a.h_kv;
+  const int n = pages_now(a, b);
+  int* out = a.selected + static_cast<long long>(bg) * a.top_k;
+  if (n <= a.top_k || a.top_k == 1) list_all(a, n, out, kPickThreads);
+  else pick_pages<false>(p, sm, bg, b, g, n, out, 0);
+}
+
+// Few rows: a cluster of eight blocks scores a row's pages, the keys going straight to the first
+// block's shared memory, which then chooses.  One launch, and nothing through the workspace.
+constexpr int kSelectCluster = 8;
+template <int D>
+__global__ void __launch_bounds__(kPickThreads) paged_select_few_kernel(const __grid_constant__ PickParams p) {
+  __shared__ PickSmem sm;
+  __shared__ uint32_t mags[kSelectCluster * kPickWarps];
+  const auto cluster = cooperative_groups::this_cluster();
+  cluster.sync();  // the first block's shared memory is there
+  const SelectLaunch& a = p.a;
+  const int bg = blockIdx.x / kSelectCluster, rank = blockIdx.x % kSelectCluster;
+  const int b = bg / a.h_kv, g = bg - b * a.h_kv, warp = threadIdx.x >> 5;
+  const int n = pages_now(a, b);
+  int* out = a.selected + static_cast<long long>(bg) * a.top_k;
+  if (n <= a.top_k || a.top_k == 1) {
+    if (rank == 0) list_all(a, n, out, kPickThreads);
+    return;
+  }
+  uint32_t* keys = cluster.map_shared_rank(sm.cache, 0);
+  float mag = 0.f;
+  for (int chunk = warp * kSelectCluster + rank; chunk * kChunk < n; chunk += kSelectCluster * kPickWarps) {
+    const float x = score_pages<D>(a, b, g, n, chunk, [&](int i, uint32_t key) { keys[i] = key; });
+    mag = x > mag || x != x ? x : mag;
+  }
+  if ((threadIdx.x & 31) == 0) cluster.map_shared_rank(mags, 0)[rank * kPickWarps + warp] = __float_as_uint(mag);
+  cluster.sync();
+  if (rank == 0)
+    pick_pages<true>(p, sm, bg, b, g, n, out, threadIdx.x < kSelectCluster * kPickWarps ? mags[threadIdx.x] : 0);
+}
+
 size_t aligned256(size_t x) { return (x + 255) / 256 * 256; }
 size_t mask_words(int max_pages) { return (static_cast<size_t>(max_pages) + 31) / 32; }
 
@@ -453,6 +515,15 @@ cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
   p.mask_words = static_cast<int>(mask_words(a.max_pages));
   p.masks = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(p.bounds) + aligned256(rows * p.chunks * 4));
   if (rows > 0x7fffffffu) return cudaErrorInvalidConfiguration;
+  // One block of 512 threads and their registers fits an SM: clusters for all rows at once, or none.
+  // Against two launches (in a graph; each launch also costs the host 2 us): 8 rows of 500 pages 7.4
+  // and 8.7 us, of 1705 pages 10.8 and 12.3, of 4725 pages 15.9 and 15.7, of 8000 pages 21.3 and 20.2.
+  if (rows * kSelectCluster <= static_cast<size_t>(host::sm_count()) && a.max_pages <= 2048) {
+    static_assert(2048 <= kCached, "a row's keys fit the first block");
+    const dim3 grid(static_cast<unsigned>(rows * kSelectCluster));
+    return a.d == 64 ? launch_after<kSelectCluster>(paged_select_few_kernel<64>, grid, dim3(kPickThreads), 0, st, p)
+                     : launch_after<kSelectCluster>(paged_select_few_kernel<128>, grid, dim3(kPickThreads), 0, st, p);
+  }
   const unsigned rows_y = static_cast<unsigned>(std::min<size_t>(rows, 32768));
   const dim3 grid((p.chunks + kScoreWarps - 1) / kScoreWarps, rows_y, static_cast<unsigned>((rows + rows_y - 1) / rows_y));
   const cudaError_t e = a.d == 64 ? launch_after(paged_score_kernel<64>, grid, dim3(kScoreWarps * 32), 0, st, p)

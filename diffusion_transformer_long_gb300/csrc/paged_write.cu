@@ -41,7 +41,6 @@ struct WriteParams {
 // kVpr: 16-byte vectors per row.  One thread per vector of a (token, head) row.
 template <int kVpr>
 __global__ void __launch_bounds__(kWriteThreads) paged_write_rows(const __grid_constant__ WriteParams p) {
-  launch_dependents();
   wait_for_inputs();
   const long long i = static_cast<long long>(blockIdx.x) * kWriteThreads + threadIdx.x;
   const long long row = i / kVpr;
@@ -112,7 +111,6 @@ __device__ __forceinline__ Place place_of(long long slot, long long n_slots, int
 template <int kVpr>
 __global__ void __launch_bounds__(kWriteThreads) paged_write_runs(const __grid_constant__ WriteParams p) {
   constexpr int kAhead = 4;  // tokens in flight
-  launch_dependents();
   wait_for_inputs();
   const long long id = static_cast<long long>(blockIdx.x) * kWriteThreads + threadIdx.x;
   if (id >= p.threads) return;
@@ -193,7 +191,6 @@ template <int kVpr>
 __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_few(const __grid_constant__ WriteParams p) {
   constexpr int kRows = 32 / kVpr, kWarps = kWriteThreads / 32;  // rows a warp moves at once
   __shared__ Ext of_warp[kWarps][kVpr];
-  launch_dependents();
   wait_for_inputs();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = static_cast<int>(blockIdx.x % p.heads), t0 = static_cast<int>(blockIdx.x / p.heads) * p.window;

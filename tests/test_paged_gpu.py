@@ -560,6 +560,51 @@ def test_attn_over_selected_pages(Hq, Hkv, D, P, order):
 # ------------------------------------------------------------------ a run of them together
 
 
+@pytest.mark.parametrize("grid_limit", [0, 1000])  # 1000: the launches for many items, at any size
+@pytest.mark.parametrize("sparse", [False, True])
+def test_replayed_steps_are_in_order(sparse, grid_limit):
+    """Three decode steps captured back to back, each kernel behind the last with nothing between: every
+    step sees what the one before wrote (the lengths, the table, the new keys), replay after replay."""
+    B, Hq, Hkv, D, P, n_pages, steps = 4, 6, 2, 64, 16, 40, 3
+    k, v = (torch.zeros(n_pages, Hkv, P, D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    summary = torch.zeros(n_pages, Hkv, 2, D, device=DEV, dtype=torch.bfloat16)
+    table = torch.full((B, 10), -1, device=DEV, dtype=torch.int32)
+    free, n_free, lens = dev(np.arange(n_pages)), dev([n_pages]), dev([0] * B)
+    new, qkv = dev([1] * B), rand(steps, B, Hq + 2 * Hkv, D, seed=1)
+
+    def step(i):
+        da.paged_plan(new, lens, table, free, n_free, P, n_pages, B, seq_lens_out=lens, n_free_out=n_free, slots=slots)
+        da.paged_kv_write(qkv[i, :, Hq:Hq + Hkv], qkv[i, :, Hq + Hkv:], slots, k, v, summary=summary)
+        sel = da.paged_select(qkv[i, :, :Hq], summary, table, lens, P, 3) if sparse else None
+        return (*da.paged_attn_fwd(qkv[i, :, :Hq], k, v, table, lens, selected=sel), sel)
+
+    slots = torch.empty(B, dtype=torch.int64, device=DEV)
+    try:
+        da.set_grid_limit(grid_limit)
+        step(0)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            res = [step(i) for i in range(steps)]
+        for it in range(12):
+            qkv.copy_(rand(steps, B, Hq + 2 * Hkv, D, seed=it))
+            before = lens.clone()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(lens, before + steps)
+            for i, (o, lse, sel) in enumerate(res):
+                # the last steps' rows are there already; each step's own length hides them
+                then = before + i + 1
+                if sparse and i < steps - 1:
+                    continue  # later rows of the same page are in its summary by now
+                if sparse:
+                    want = po.select(qkv[i, :, :Hq], summary, table, then, P, 3)
+                    assert np.array_equal(sel.cpu().numpy(), want)
+                check_attn(o, lse, po.attend(qkv[i, :, :Hq], k, v, table, then, D ** -0.5, selected=sel))
+    finally:
+        da.set_grid_limit(0)
+
+
 def test_steps_together_eager_and_replayed():
     """A batch that prefills, then decodes token by token: plan, write with summaries, select,
     attention over all and over the selected pages, eagerly and as one captured step replayed as the
