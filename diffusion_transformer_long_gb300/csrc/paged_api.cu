@@ -1,5 +1,6 @@
 // C entry points of the paged key/value cache (declared in include/ditattn.h): argument
-// validation and dispatch.  Validation runs before any CUDA call.
+// validation and dispatch.  Validation makes no CUDA call but the workspace sizes' look at the device's
+// SM count.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -178,9 +179,9 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
   return done(ditattn::launch_paged_write(a, static_cast<cudaStream_t>(stream)));
 }
 
-size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D) {
-  if (B < 1 || H_q < 1 || H_kv < 1 || D < 1) return 0;
-  return ditattn::paged_attn_workspace(H_q, H_kv, D);
+size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D, int page_size, int pages) {
+  if (B < 1 || H_kv < 1 || H_q < H_kv || D < 1 || page_size < 1 || pages < 1) return 0;
+  return ditattn::paged_attn_workspace(B, H_q, H_kv, D, static_cast<long long>(pages) * page_size);
 }
 
 dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const void* k_cache,
@@ -206,8 +207,8 @@ dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const
     return DIT_ERR_INVALID_ARG;
   if (selected && (n_selected < 1 || n_selected > max_pages)) return DIT_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || !valid_dtype(out_dtype)) return DIT_ERR_INVALID_ARG;
-  const size_t need = dit_paged_attn_workspace_bytes(B, H_q, H_kv, D);
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return DIT_ERR_INVALID_ARG;
+  const size_t need = dit_paged_attn_workspace_bytes(B, H_q, H_kv, D, page_size, selected ? n_selected : max_pages);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return DIT_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(B) * H_q;
   const Range outs[] = {span(out, rows * D * dtype_bytes(out_dtype)), span(lse, lse ? rows * 4 : 0),
                         span(workspace, static_cast<long long>(need))};
@@ -276,7 +277,7 @@ dit_status dit_paged_select(const void* q, const dit_strides* q_strides, const v
     return DIT_ERR_INVALID_ARG;
   if (top_k < 1 || top_k > max_pages) return DIT_ERR_INVALID_ARG;
   const size_t need = dit_paged_select_workspace_bytes(B, H_kv, max_pages);
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return DIT_ERR_INVALID_ARG;
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return DIT_ERR_INVALID_ARG;
   const Range outs[] = {span(selected, 4LL * B * H_kv * top_k),
                         span(workspace, static_cast<long long>(need))};
   const Range ins[] = {span(q, view_span(qs, B, H_q, 1, D, 2)), span(summary, 4LL * n_pages * H_kv * D),

@@ -31,10 +31,22 @@ bool encode_cache(CUtensorMap* m, const void* base, const Strides& s, int d, int
 // Query heads that share one pass over the keys: the group's, in eights, up to 32.
 int row_block(int group) { return std::min((group + 7) / 8 * 8, kMaxRows); }
 
+// Few short items get a cluster of blocks each: against the runs, 8 items of 1024 keys 4.9 and 7.4 us, of
+// 4096 keys 8.5 and 9.2, of 8192 keys 14.2 and 12.0.  So does one request whose heads' clusters fill
+// most of the GPU (24 heads, 32768 keys: 63.0 and 65.8 us); several may be of very different lengths.
+bool few_items(int batch, int h_q, int h_kv, long long keys) {
+  const int group = h_q / h_kv, R = row_block(group);
+  const long long blocks = static_cast<long long>(batch) * h_kv * ((group + R - 1) / R) * kCluster;
+  const int slots = 2 * host::sm_count();  // two blocks fit an SM (registers, 82 to 92 KB of shared memory)
+  return grid_limit() == 0 && blocks <= slots && (keys <= 4096 || (batch == 1 && 5 * blocks >= 3 * slots));
+}
+
 }  // namespace
 
 // Partials of two segments of each block: fp32 sums, (maximum, sum) pairs, and the join's notes.
-size_t paged_attn_workspace(int h_q, int h_kv, int d) {
+// Clusters need none.
+size_t paged_attn_workspace(int batch, int h_q, int h_kv, int d, long long keys) {
+  if (few_items(batch, h_q, h_kv, keys)) return 0;
   const size_t rows = static_cast<size_t>(kMaxBlocks) * 2 * row_block(h_q / h_kv);
   return rows * d * 4 + rows * 8 + kMaxBlocks * 16;
 }
@@ -71,17 +83,9 @@ cudaError_t launch_paged_attn(const PagedAttnLaunch& a, cudaStream_t st) {
   p.part_o = static_cast<float*>(a.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + rows * a.d);
   p.meta = reinterpret_cast<int4*>(p.part_ml + rows);
-  // Two blocks fit one SM (their registers, and 82 to 92 KB of shared memory).  Few short items get a
-  // cluster of blocks each: against the runs, 8 items of 1024 keys 4.9 and 7.4 us, of 4096 keys 8.5
-  // and 9.2, of 8192 keys 14.2 and 12.0.  So does one request whose heads' clusters fill most of the
-  // GPU (24 heads, 32768 keys: 63.0 and 65.8 us); several may be of very different lengths.
-  const long long items = static_cast<long long>(a.batch) * a.h_kv * p.head_blocks;
-  const long long keys = static_cast<long long>(a.selected ? a.n_selected : a.max_pages) * a.page_size;
-  const int slots = 2 * host::sm_count();
-  if (grid_limit() == 0 && items * kCluster <= slots &&
-      (keys <= 4096 || (a.batch == 1 && 5 * items * kCluster >= 3 * slots)))
-    return launch_few(p, a.d, R, a.out_f32, static_cast<int>(items), st);
-  int blocks = std::min(kMaxBlocks, slots);
+  if (few_items(a.batch, a.h_q, a.h_kv, static_cast<long long>(a.selected ? a.n_selected : a.max_pages) * a.page_size))
+    return launch_few(p, a.d, R, a.out_f32, a.batch * a.h_kv * p.head_blocks, st);
+  int blocks = std::min(kMaxBlocks, 2 * host::sm_count());
   if (grid_limit() > 0) blocks = std::min(blocks, grid_limit());
   return for_sizes(a.d, R, a.out_f32, [&](auto D, auto nb, auto zero) {
     using OT = decltype(zero);

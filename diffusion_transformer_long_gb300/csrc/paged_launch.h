@@ -64,7 +64,8 @@ struct PagedAttnLaunch {
   int* status;  // device status word
 };
 cudaError_t launch_paged_attn(const PagedAttnLaunch& a, cudaStream_t st);
-size_t paged_attn_workspace(int h_q, int h_kv, int d);
+// Workspace bytes on the current device; `keys`: the most that a request can attend to.
+size_t paged_attn_workspace(int batch, int h_q, int h_kv, int d, long long keys);
 
 struct SelectLaunch {
   const void* q;

@@ -36,6 +36,8 @@ constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kRanked = kPickThreads;  // pages between that are ranked pair by pair
 constexpr int kCached = 8192;       // keys held in shared memory
+constexpr int kFewPages = 2048;     // pages of a row that a cluster scores; it holds their 64-bit scores too
+static_assert(kFewPages * 4 + kFewPages * 8 <= kCached * 4, "keys and 64-bit scores");
 // A 32-bit score is summed in 2 D / 16 <= 16 steps of 16 products and the running sum, each of
 // the 17 terms cut to within 2^-23 of the step's largest: at most 16 * 17 * 2^-23 of sum |q| |k|.
 constexpr float kErr = 16 * 17 / 8388608.f;
@@ -397,7 +399,8 @@ __device__ __forceinline__ void pick_pages(const PickParams& p, PickSmem& sm, in
       if (keys[i] - from <= to - from) atomicOr(mask + (i >> 5), 1u << (i & 31));
   } else {
     // many alike (or not finite): the border by bisection of the 64-bit keys, ties in order
-    unsigned long long* exact = p.exact + static_cast<long long>(bg) * a.max_pages;
+    unsigned long long* exact = kHeld ? reinterpret_cast<unsigned long long*>(cache + kFewPages)
+                                      : p.exact + static_cast<long long>(bg) * a.max_pages;
     for (int i = warp; i < others; i += kPickWarps) {
       if (keys[i] - from > to - from) continue;
       const unsigned long long k = exact_key(a, b, g, i, unit, 0, a.h_q / a.h_kv);
@@ -494,10 +497,18 @@ __global__ void __launch_bounds__(kPickThreads) paged_select_few_kernel(const __
 size_t aligned256(size_t x) { return (x + 255) / 256 * 256; }
 size_t mask_words(int max_pages) { return (static_cast<size_t>(max_pages) + 31) / 32; }
 
+// One block of 512 threads and their registers fits an SM: clusters for all rows at once, or none.
+// Against two launches (in a graph; each launch also costs the host 2 us): 8 rows of 500 pages 7.4
+// and 8.7 us, of 1705 pages 10.8 and 12.3, of 4725 pages 15.9 and 15.7, of 8000 pages 21.3 and 20.2.
+bool few_rows(size_t rows, int max_pages) {
+  return rows * kSelectCluster <= static_cast<size_t>(host::sm_count()) && max_pages <= kFewPages;
+}
+
 }  // namespace
 
-// Keys, bounds and 64-bit scores of every (request, key/value head).
+// Keys, bounds and 64-bit scores of every (request, key/value head).  Clusters need none.
 size_t paged_select_workspace(int batch, int h_kv, int max_pages) {
+  if (few_rows(static_cast<size_t>(batch) * h_kv, max_pages)) return 0;
   const size_t rows = static_cast<size_t>(batch) * h_kv, chunks = (static_cast<size_t>(max_pages) + kChunk - 1) / kChunk;
   return aligned256(rows * max_pages * 8) + aligned256(rows * max_pages * 4) + aligned256(rows * chunks * 4) +
          aligned256(rows * mask_words(max_pages) * 4);
@@ -515,11 +526,7 @@ cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
   p.mask_words = static_cast<int>(mask_words(a.max_pages));
   p.masks = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(p.bounds) + aligned256(rows * p.chunks * 4));
   if (rows > 0x7fffffffu) return cudaErrorInvalidConfiguration;
-  // One block of 512 threads and their registers fits an SM: clusters for all rows at once, or none.
-  // Against two launches (in a graph; each launch also costs the host 2 us): 8 rows of 500 pages 7.4
-  // and 8.7 us, of 1705 pages 10.8 and 12.3, of 4725 pages 15.9 and 15.7, of 8000 pages 21.3 and 20.2.
-  if (rows * kSelectCluster <= static_cast<size_t>(host::sm_count()) && a.max_pages <= 2048) {
-    static_assert(2048 <= kCached, "a row's keys fit the first block");
+  if (few_rows(rows, a.max_pages)) {
     const dim3 grid(static_cast<unsigned>(rows * kSelectCluster));
     return a.d == 64 ? launch_after<kSelectCluster>(paged_select_few_kernel<64>, grid, dim3(kPickThreads), 0, st, p)
                      : launch_after<kSelectCluster>(paged_select_few_kernel<128>, grid, dim3(kPickThreads), 0, st, p);

@@ -95,7 +95,7 @@ def lib() -> ctypes.CDLL:
         L.dit_paged_attn_fwd.argtypes = [P, SP, P, SP, P, SP, P, LL, P, P, I, P, P, I, I, I, I, I, I,
                                          I, F, I, P, ctypes.c_size_t, P]
         L.dit_paged_attn_workspace_bytes.restype = ctypes.c_size_t
-        L.dit_paged_attn_workspace_bytes.argtypes = [I, I, I, I]
+        L.dit_paged_attn_workspace_bytes.argtypes = [I, I, I, I, I, I]
         L.dit_paged_select.restype = I
         L.dit_paged_select.argtypes = [P, SP, P, P, LL, P, P, I, I, I, I, I, I, I, I, P,
                                        ctypes.c_size_t, P]
@@ -566,6 +566,7 @@ def inject_stall(enable: bool, wait_limit_cycles: int = 0):
 def set_grid_limit(max_ctas: int):
     """TEST ONLY: cap the persistent attention grid (0 restores one CTA per SM)."""
     lib().dit_test_set_grid_limit(int(max_ctas))
+    _attn_need.cache_clear()  # with a cap, no call takes the launch that needs no workspace
 
 
 def chunk_attention(q, k, v, chunks, scale=None, out_dtype=torch.float32,
@@ -810,19 +811,29 @@ def _check_table(block_table, seq_lens, B, index):
     return max_pages, (block_table.stride(0) if B > 1 else max_pages)
 
 
-@functools.lru_cache(maxsize=None)
-def _attn_workspace_bytes(Hq, Hkv, D):
-    return lib().dit_paged_attn_workspace_bytes(1, Hq, Hkv, D)
+@functools.lru_cache(maxsize=4096)
+def _attn_need(index, B, Hq, Hkv, D, page_size, pages):
+    """dit_paged_attn_workspace_bytes on the current device, number `index`."""
+    return lib().dit_paged_attn_workspace_bytes(B, Hq, Hkv, D, page_size, pages)
+
+
+@functools.lru_cache(maxsize=4096)
+def _select_need(index, B, Hkv, max_pages):
+    """dit_paged_select_workspace_bytes on the current device, number `index`."""
+    return lib().dit_paged_select_workspace_bytes(B, Hkv, max_pages)
 
 
 def _workspace(workspace, need, device):
-    """(pointer holder, bytes) of a call's workspace: the caller's, or a new one."""
+    """(buffer or None, its address or None, bytes) of a call's workspace: the caller's, or a new one."""
+    if need == 0:
+        return None, None, 0
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     size = workspace.numel() * workspace.element_size()
     if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous() or size < need:
         raise ValueError(f"workspace must be a contiguous buffer of at least {need} bytes on {device}")
-    return workspace, size
+    return workspace, workspace.data_ptr(), size
 
 
 def paged_plan(new_lens, seq_lens, block_table, free_pages, n_free, page_size, n_pages, max_tokens,
@@ -933,7 +944,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, selected=None, ou
         lse = None
     elif lse is None:
         lse = torch.empty((B, Hq), device=dev, dtype=torch.float32)
-    workspace, size = _workspace(workspace, _attn_workspace_bytes(Hq, Hkv, D), dev)
+    pages = max_pages if selected is None else selected.shape[2]
+    workspace, ws, size = _workspace(workspace, _attn_need(index, B, Hq, Hkv, D, P, pages), dev)
     qb, qh, _ = q.stride()
     st = lib().dit_paged_attn_fwd(
         q.data_ptr(), Strides(qb, qh, D), k_cache.data_ptr(), Strides(*k_cache.stride()[:3]),
@@ -941,7 +953,7 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, selected=None, ou
         seq_lens.data_ptr(), None if selected is None else selected.data_ptr(),
         0 if selected is None else selected.shape[2], out.data_ptr(),
         None if lse is None else lse.data_ptr(), B, Hq, Hkv, D, P, n_pages, max_pages,
-        1.0 / math.sqrt(D) if scale is None else float(scale), _dt(out.dtype), workspace.data_ptr(), size,
+        1.0 / math.sqrt(D) if scale is None else float(scale), _dt(out.dtype), ws, size,
         torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_paged_attn_fwd")
@@ -970,12 +982,11 @@ def paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected=N
         selected = torch.empty((B, Hkv, max(0, top_k)), device=dev, dtype=torch.int32)
     else:
         _check_tensor(selected, "selected", torch.int32, (B, Hkv, top_k), index)
-    L = lib()
-    workspace, size = _workspace(workspace, L.dit_paged_select_workspace_bytes(B, Hkv, max_pages), dev)
+    workspace, ws, size = _workspace(workspace, _select_need(index, B, Hkv, max_pages), dev)
     qb, qh, _ = q.stride()
-    st = L.dit_paged_select(q.data_ptr(), Strides(qb, qh, D), summary.data_ptr(), block_table.data_ptr(),
+    st = lib().dit_paged_select(q.data_ptr(), Strides(qb, qh, D), summary.data_ptr(), block_table.data_ptr(),
                             stride, seq_lens.data_ptr(), selected.data_ptr(), B, Hq, Hkv, D, page_size,
-                            n_pages, max_pages, top_k, workspace.data_ptr(), size,
+                            n_pages, max_pages, top_k, ws, size,
                             torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_paged_select")

@@ -389,7 +389,8 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
  *   out         : device [B, H_q, D] of out_dtype, contiguous, 16-byte aligned (written)
  *   lse         : device fp32 [B, H_q] (written), or NULL
  *   H_q         : a multiple of H_kv
- *   workspace   : at least dit_paged_attn_workspace_bytes(B, H_q, H_kv, D) bytes
+ *   workspace   : at least dit_paged_attn_workspace_bytes(B, H_q, H_kv, D, page_size, pages) bytes,
+ *                 pages = n_selected with `selected`, else max_pages; NULL where that is 0
  */
 dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const void* k_cache,
                               const dit_strides* k_strides, const void* v_cache,
@@ -400,9 +401,9 @@ dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const
                               dit_dtype out_dtype, void* workspace, size_t workspace_bytes,
                               dit_stream stream);
 
-/* Workspace bytes of a dit_paged_attn_fwd call with these sizes (0 when a size is not
- * positive). */
-size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D);
+/* Workspace bytes of a dit_paged_attn_fwd call with these sizes on the current device: 0 for
+ * few requests of few keys, which need none, and when a size is not positive. */
+size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D, int page_size, int pages);
 
 /*
  * The pages whose keys can score highest, for attention over those alone.  For request b
@@ -418,7 +419,8 @@ size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D);
  *   selected : device int32 [B, H_kv, top_k], contiguous (written): table columns in
  *              ascending order, then -1
  *   top_k    : 1 .. max_pages
- *   workspace: at least dit_paged_select_workspace_bytes(B, H_kv, max_pages) bytes
+ *   workspace: at least dit_paged_select_workspace_bytes(B, H_kv, max_pages) bytes; NULL where
+ *              that is 0
  */
 dit_status dit_paged_select(const void* q, const dit_strides* q_strides, const void* summary,
                             const int* block_table, long long table_stride, const int* seq_lens,
@@ -426,8 +428,8 @@ dit_status dit_paged_select(const void* q, const dit_strides* q_strides, const v
                             int n_pages, int max_pages, int top_k, void* workspace,
                             size_t workspace_bytes, dit_stream stream);
 
-/* Workspace bytes of a dit_paged_select call with these sizes (0 when a size is not
- * positive). */
+/* Workspace bytes of a dit_paged_select call with these sizes on the current device: 0 for few
+ * requests of few pages, which need none, and when a size is not positive. */
 size_t dit_paged_select_workspace_bytes(int B, int H_kv, int max_pages);
 
 /*

@@ -116,9 +116,10 @@ def test_select_validation(lib, kw, status):
 
 
 def test_workspace_sizes(lib):
-    assert lib.dit_paged_attn_workspace_bytes(0, 8, 2, 128) == 0
-    assert lib.dit_paged_attn_workspace_bytes(1, 8, 0, 128) == 0
-    assert lib.dit_paged_attn_workspace_bytes(1, 8, 2, 128) > 0
+    assert lib.dit_paged_attn_workspace_bytes(0, 8, 2, 128, 16, 9) == 0
+    assert lib.dit_paged_attn_workspace_bytes(1, 8, 0, 128, 16, 9) == 0
+    assert lib.dit_paged_attn_workspace_bytes(1, 8, 2, 128, 0, 9) == 0
+    assert lib.dit_paged_attn_workspace_bytes(64, 8, 2, 128, 16, 900) > 0
     assert lib.dit_paged_select_workspace_bytes(1, 0, 5) == 0
     assert lib.dit_paged_select_workspace_bytes(64, 8, 1 << 20) >= 64 * 8 * (1 << 20)  # no 32-bit wrap
 
@@ -154,7 +155,8 @@ def test_binding_refusals():
                   (dict(seq_lens=i.cpu()), ValueError), (dict(selected=t), ValueError),
                   (dict(selected=torch.zeros(2, 2, 5, dtype=torch.int32, device=dev)), da.DitError),
                   (dict(out=torch.zeros(2, 4, 32, device=dev)), ValueError), (dict(lse=torch.zeros(2, 5, device=dev)), ValueError),
-                  (dict(workspace=torch.zeros(64, dtype=torch.uint8, device=dev)), ValueError), (dict(scale=-1.0), da.DitError),
+                  (dict(workspace=torch.zeros(64, dtype=torch.uint8, device=dev),
+                        block_table=torch.zeros(2, 500, dtype=torch.int32, device=dev)), ValueError), (dict(scale=-1.0), da.DitError),
                   (dict(out_dtype=torch.float16), TypeError),
                   (dict(q=torch.zeros(2, 3, 64, dtype=torch.bfloat16, device=dev)), da.DitError)):
         with pytest.raises(e):

@@ -59,6 +59,23 @@ def tables(lens, P, seed=0, extra_pages=2, extra_cols=1):
     return t, n_pages
 
 
+@pytest.fixture(params=["as chosen", "many items"])
+def launch(request):
+    """The launch that the sizes choose (a cluster for each of few items), and the one for many items."""
+    da.set_grid_limit(1000 if request.param == "many items" else 0)
+    yield request.param
+    da.set_grid_limit(0)
+
+
+def widened(table, launch):
+    """For the selection: the same table with room for more pages than a cluster takes on."""
+    if launch == "as chosen":
+        return table
+    wide = torch.full((table.shape[0], 2100), -1, device=DEV, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
 # ------------------------------------------------------------------ plan
 
 
@@ -214,7 +231,7 @@ def make_case(lens, Hq, Hkv, D, P, order="hnd", seed=0, q_scale=1.5, k_scale=1.0
     (24, 2, 128, 128, "hnd", [129, 1, 300]), (24, 1, 128, 16, "nhd", [513, 16]),
     (64, 2, 64, 1024, "hnd", [1500, 1023]), (9, 1, 128, 16, "part", [100]),
     (1, 1, 128, 16, "hnd", [27280]), (8, 8, 64, 16, "hnd", list(range(130)))])
-def test_attn(Hq, Hkv, D, P, order, lens, out_dtype):
+def test_attn(Hq, Hkv, D, P, order, lens, out_dtype, launch):
     q, k, v, table, sl = make_case(lens, Hq, Hkv, D, P, order, seed=Hq + len(lens))
     o, lse = da.paged_attn_fwd(q, k, v, table, sl, out_dtype=out_dtype)
     da.check()
@@ -225,7 +242,7 @@ def test_attn(Hq, Hkv, D, P, order, lens, out_dtype):
 
 
 @pytest.mark.parametrize("D,P", [(64, 16), (128, 48)])
-def test_attn_ignores_what_no_request_holds(D, P):
+def test_attn_ignores_what_no_request_holds(D, P, launch):
     """Rows past a length and pages of nobody hold NaN and infinities; table entries past a length
     are wild; entries inside a length that are outside the pool hold no keys."""
     lens = [0, 1, P - 1, P, P + 1, 5 * P + 3, 777, 16, 3 * P]
@@ -257,7 +274,7 @@ def test_attn_ignores_what_no_request_holds(D, P):
     check_attn(*da.paged_attn_fwd(q, kk, vv, full, odd), po.attend(q, kk, vv, full, odd, scale))
 
 
-def test_attn_nan_and_infinite_keys_reach_their_own_row_only():
+def test_attn_nan_and_infinite_keys_reach_their_own_row_only(launch):
     q, k, v, table, sl = make_case([40, 40, 40], 4, 2, 64, 16, seed=5)
     k[table[0, 1], 0, 3] = float("nan")
     v[table[1, 2], 1, 7, 5] = float("inf")
@@ -270,12 +287,12 @@ def test_attn_nan_and_infinite_keys_reach_their_own_row_only():
 
 
 @pytest.mark.parametrize("q_scale,k_scale", [(8.0, 4.0), (0.0, 1.0), (1e-3, 1e-3)])
-def test_attn_peaked_and_flat(q_scale, k_scale):
+def test_attn_peaked_and_flat(q_scale, k_scale, launch):
     q, k, v, table, sl = make_case([3000, 33, 1], 24, 8, 128, 16, seed=7, q_scale=q_scale, k_scale=k_scale)
     check_attn(*da.paged_attn_fwd(q, k, v, table, sl), po.attend(q, k, v, table, sl, 128 ** -0.5))
 
 
-def test_attn_growing_scores():
+def test_attn_growing_scores(launch):
     """Every key beats the ones before it: the running maximum moves at each step."""
     n, D, P = 2000, 64, 16
     table, n_pages = tables([n], P, extra_pages=0, extra_cols=0)
@@ -297,13 +314,14 @@ def test_attn_views_streams_workspace():
     q, k, v, table, sl = make_case(lens, 10, 2, 128, 32, "part", seed=11)
     fused = torch.zeros(4, 14, 192, device=DEV, dtype=torch.bfloat16)
     fused[:, 2:12, 64:] = q
-    wide = torch.full((4, table.shape[1] + 5), 12345, device=DEV, dtype=torch.int32)
-    wide[:, 2:-3] = table
-    need = da.lib().dit_paged_attn_workspace_bytes(4, 10, 2, 128)
+    wide = torch.full((4, 160), 12345, device=DEV, dtype=torch.int32)
+    wide[:, 2:2 + table.shape[1]] = table
+    need = da.lib().dit_paged_attn_workspace_bytes(4, 10, 2, 128, 32, 150)
+    assert need > 0
     ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
     out = torch.full((5, 10, 128), 7.0, device=DEV)
     lse = torch.full((5, 10), 7.0, device=DEV)
-    da.paged_attn_fwd(fused[:, 2:12, 64:], k, v, wide[:, 2:-3], sl, out=out[:4], lse=lse[:4],
+    da.paged_attn_fwd(fused[:, 2:12, 64:], k, v, wide[:, 2:152], sl, out=out[:4], lse=lse[:4],
                       workspace=ws[:need])
     da.check()
     ref = po.attend(q, k, v, table, sl, 128 ** -0.5)
@@ -311,9 +329,12 @@ def test_attn_views_streams_workspace():
     assert (ws[need:] == 0xFF).all() and (out[4] == 7).all() and (lse[4] == 7).all()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    o2, l2 = da.paged_attn_fwd(q, k, v, table, sl, stream=s)
+    o2, l2 = da.paged_attn_fwd(q, k, v, wide[:, 2:152], sl, stream=s)
     s.synchronize()
     assert torch.equal(o2, out[:4]) and torch.equal(l2, lse[:4])
+    # few keys at most: clusters, and no workspace
+    assert da.lib().dit_paged_attn_workspace_bytes(4, 10, 2, 128, 32, table.shape[1]) == 0
+    check_attn(*da.paged_attn_fwd(fused[:, 2:12, 64:], k, v, table, sl, stream=s), ref)
 
 
 @pytest.mark.parametrize("B", [700, 5000])
@@ -326,7 +347,7 @@ def test_attn_many_requests(B):
     check_attn(*da.paged_attn_fwd(q, k, v, table, sl), po.attend(q, k, v, table, sl, 0.125))
 
 
-def test_attn_scores_without_a_finite_one():
+def test_attn_scores_without_a_finite_one(launch):
     """Keys that score -inf weigh nothing; a request all of whose keys do is one without keys."""
     q, k, v, table, sl = make_case([40, 20], 2, 2, 64, 16, seed=83)
     q[:, :, 0] = 1.0
@@ -340,7 +361,7 @@ def test_attn_scores_without_a_finite_one():
     assert (lse[1] == -float("inf")).all() and (o[1] == 0).all()
 
 
-def test_attn_two_streams_at_once():
+def test_attn_two_streams_at_once(launch):
     cases = [make_case([2000 + i, 900, 5], 24, 8, 128, 16, seed=20 + i) for i in range(2)]
     alone = [da.paged_attn_fwd(*c) for c in cases]
     torch.cuda.synchronize()
@@ -352,15 +373,16 @@ def test_attn_two_streams_at_once():
             assert torch.equal(o, o1) and torch.equal(lse, l1)
 
 
-def test_captured_between_copies_and_two_graphs_of_one_workspace():
+def test_captured_between_copies_and_two_graphs_of_one_workspace(launch):
     """Captured behind a copy, a fill and each other; two graphs that share the workspaces, replayed
     in turn, and one call captured twice into the same graph."""
     P, top_k = 16, 9
     q, k, v, table, sl = make_case([1500, 40, 0, 333], 6, 2, 64, P, seed=61)
+    table = widened(table, launch)
     summary = torch.stack((k.amin(2), k.amax(2)), 2)
     src = torch.empty_like(q)
-    ws = torch.empty(da.lib().dit_paged_attn_workspace_bytes(4, 6, 2, 64), dtype=torch.uint8, device=DEV)
-    wsel = torch.empty(da.lib().dit_paged_select_workspace_bytes(4, 2, table.shape[1]), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    wsel = torch.empty(da.lib().dit_paged_select_workspace_bytes(4, 2, 5000), dtype=torch.uint8, device=DEV)
     ws.fill_(0x5A)
     wsel.fill_(0xA5)
     x = q.clone()
@@ -408,7 +430,7 @@ def test_attn_capped_grid():
         da.set_grid_limit(0)
 
 
-def test_attn_reports_a_wait_that_runs_out():
+def test_attn_reports_a_wait_that_runs_out(launch):
     """With the copies withheld every wait runs out after its limit, the launch ends and the check
     says so; the next call is right again."""
     q, k, v, table, sl = make_case([500, 0, 40], 8, 2, 128, 16, seed=33)
@@ -427,7 +449,7 @@ def test_attn_reports_a_wait_that_runs_out():
     assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
 
 
-def test_attn_offsets_past_32_bits():
+def test_attn_offsets_past_32_bits(launch):
     """Pages that begin more than 2^32 bytes and more than 2^31 elements into the cache."""
     H, P, D = 2, 64, 128
     n_pages = 2 ** 31 // (H * P * D) + 40
@@ -458,12 +480,12 @@ def test_attn_offsets_past_32_bits():
     (40, 8, 128, 32, [3000, 40], 1), (16, 1, 64, 16, [9000, 100, 5], 33),
     (24, 24, 128, 48, [1000, 2000], 21), (24, 1, 128, 16, [700], 44), (64, 2, 64, 16, [1600, 320], 20),
     (2, 2, 64, 16, [75600], 100), (4, 4, 128, 16, [27280, 27264], 1000)])
-def test_select(Hq, Hkv, D, P, lens, top_k):
+def test_select(Hq, Hkv, D, P, lens, top_k, launch):
     table, n_pages = tables(lens, P, seed=top_k)
     q = rand(len(lens), Hq, D, seed=1, scale=1.5)
     a, b = rand(n_pages, Hkv, 1, D, seed=2), rand(n_pages, Hkv, 1, D, seed=3)
     summary = torch.cat((torch.minimum(a, b), torch.maximum(a, b)), 2)
-    t, sl = dev(table), dev(lens)
+    t, sl = widened(dev(table), launch) if table.shape[1] < 2100 else dev(table), dev(lens)
     top_k = min(top_k, table.shape[1])
     got = da.paged_select(q, summary, t, sl, P, top_k)
     assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k))
@@ -471,7 +493,7 @@ def test_select(Hq, Hkv, D, P, lens, top_k):
 
 @pytest.mark.parametrize("kind", ["equal", "few values", "near", "nan", "inf", "overflow", "tiny", "zero q",
                                   "bad entries", "inf q"])
-def test_select_borders(kind):
+def test_select_borders(kind, launch):
     """Scores that tie, that differ by less than a 32-bit sum resolves, that are no numbers, that pass
     the range of 32 bits at either end."""
     lens, P, Hq, Hkv, D, top_k = [2000, 1999, 130, 16], 16, 6, 2, 128, 37
@@ -509,13 +531,13 @@ def test_select_borders(kind):
     else:
         q[0, 0, 0] = float("inf")
         q[1, 4, 7] = float("nan")
-    t, sl = dev(table), dev(lens)
+    t, sl = widened(dev(table), launch), dev(lens)
     for k in (1, 2, top_k, table.shape[1]):
         got = da.paged_select(q, summary, t, sl, P, k)
         assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, k)), k
 
 
-@pytest.mark.parametrize("n,kind", [(700, "equal"), (700, "nan"), (3000, "two values"), (9001, "random"),
+@pytest.mark.parametrize("n,kind", [(700, "equal"), (700, "nan"), (2047, "two values"), (3000, "two values"), (9001, "random"),
                                     (9001, "equal"), (9001, "two values"), (9001, "inf")])
 def test_select_among_many_pages(n, kind):
     """More pages at the border than are ranked pair by pair, and more pages than shared memory holds."""
@@ -540,7 +562,7 @@ def test_select_among_many_pages(n, kind):
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,P,order", [(24, 8, 128, 16, "hnd"), (2, 2, 64, 48, "nhd"), (16, 1, 64, 64, "part")])
-def test_attn_over_selected_pages(Hq, Hkv, D, P, order):
+def test_attn_over_selected_pages(Hq, Hkv, D, P, order, launch):
     """Lists as paged_select writes them, and any other list: skipped, repeated, unsorted entries."""
     lens = [0, 1, P, P + 1, 40 * P - 3, 2000]
     q, k, v, table, sl = make_case(lens, Hq, Hkv, D, P, order, seed=41)
@@ -560,15 +582,14 @@ def test_attn_over_selected_pages(Hq, Hkv, D, P, order):
 # ------------------------------------------------------------------ a run of them together
 
 
-@pytest.mark.parametrize("grid_limit", [0, 1000])  # 1000: the launches for many items, at any size
 @pytest.mark.parametrize("sparse", [False, True])
-def test_replayed_steps_are_in_order(sparse, grid_limit):
+def test_replayed_steps_are_in_order(sparse, launch):
     """Three decode steps captured back to back, each kernel behind the last with nothing between: every
     step sees what the one before wrote (the lengths, the table, the new keys), replay after replay."""
     B, Hq, Hkv, D, P, n_pages, steps = 4, 6, 2, 64, 16, 40, 3
     k, v = (torch.zeros(n_pages, Hkv, P, D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
     summary = torch.zeros(n_pages, Hkv, 2, D, device=DEV, dtype=torch.bfloat16)
-    table = torch.full((B, 10), -1, device=DEV, dtype=torch.int32)
+    table = widened(torch.full((B, 10), -1, device=DEV, dtype=torch.int32), launch)
     free, n_free, lens = dev(np.arange(n_pages)), dev([n_pages]), dev([0] * B)
     new, qkv = dev([1] * B), rand(steps, B, Hq + 2 * Hkv, D, seed=1)
 
@@ -579,33 +600,29 @@ def test_replayed_steps_are_in_order(sparse, grid_limit):
         return (*da.paged_attn_fwd(qkv[i, :, :Hq], k, v, table, lens, selected=sel), sel)
 
     slots = torch.empty(B, dtype=torch.int64, device=DEV)
-    try:
-        da.set_grid_limit(grid_limit)
-        step(0)
+    step(0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = [step(i) for i in range(steps)]
+    for it in range(12):
+        qkv.copy_(rand(steps, B, Hq + 2 * Hkv, D, seed=it))
+        before = lens.clone()
+        graph.replay()
         torch.cuda.synchronize()
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            res = [step(i) for i in range(steps)]
-        for it in range(12):
-            qkv.copy_(rand(steps, B, Hq + 2 * Hkv, D, seed=it))
-            before = lens.clone()
-            graph.replay()
-            torch.cuda.synchronize()
-            assert torch.equal(lens, before + steps)
-            for i, (o, lse, sel) in enumerate(res):
-                # the last steps' rows are there already; each step's own length hides them
-                then = before + i + 1
-                if sparse and i < steps - 1:
-                    continue  # later rows of the same page are in its summary by now
-                if sparse:
-                    want = po.select(qkv[i, :, :Hq], summary, table, then, P, 3)
-                    assert np.array_equal(sel.cpu().numpy(), want)
-                check_attn(o, lse, po.attend(qkv[i, :, :Hq], k, v, table, then, D ** -0.5, selected=sel))
-    finally:
-        da.set_grid_limit(0)
+        assert torch.equal(lens, before + steps)
+        for i, (o, lse, sel) in enumerate(res):
+            # the last steps' rows are there already; each step's own length hides them
+            then = before + i + 1
+            if sparse and i < steps - 1:
+                continue  # later rows of the same page are in its summary by now
+            if sparse:
+                want = po.select(qkv[i, :, :Hq], summary, table, then, P, 3)
+                assert np.array_equal(sel.cpu().numpy(), want)
+            check_attn(o, lse, po.attend(qkv[i, :, :Hq], k, v, table, then, D ** -0.5, selected=sel))
 
 
-def test_steps_together_eager_and_replayed():
+def test_steps_together_eager_and_replayed(launch):
     """A batch that prefills, then decodes token by token: plan, write with summaries, select,
     attention over all and over the selected pages, eagerly and as one captured step replayed as the
     lengths grow; a request that is idle for some steps and one that runs out of pages."""
