@@ -226,8 +226,14 @@ struct Producer {
     w = first;
     at = i = count = 0;
     now = look_up(p, warp, lane);
+  }
+  // The first tiles, and only then the look-up of the batch behind theirs.
+  __device__ __forceinline__ void begin(const PagedParams& p, uint32_t ring, uint32_t bars, int* valid, int warp,
+                                        int lane) {
+    for (int s = 0; s < S::kStages && i < now.n; ++s) put(p, ring, bars, valid, lane);
     ahead.n = 0;
     if (now.n) ahead = look_up(p, warp, lane);
+    while (count < S::kStages && (i < now.n || ahead.n)) issue(p, ring, bars, valid, warp, lane);
   }
   __device__ __forceinline__ void issue(const PagedParams& p, uint32_t ring, uint32_t bars, int* valid, int warp,
                                         int lane) {
@@ -237,6 +243,9 @@ struct Producer {
       i = 0;
       ahead = look_up(p, warp, lane);
     }
+    put(p, ring, bars, valid, lane);
+  }
+  __device__ __forceinline__ void put(const PagedParams& p, uint32_t ring, uint32_t bars, int* valid, int lane) {
     const int page = __shfl_sync(~0u, now.page, i);
     int spot = __shfl_sync(~0u, now.spot, i);
     if (page < 0 || page >= p.n_pages) spot = 0;
@@ -256,6 +265,11 @@ struct Producer {
     }
   }
 };
+
+// x / y of non-negative numbers, in 32 bits where they fit (several times cheaper).
+__device__ __forceinline__ long long divided(long long x, long long y) {
+  return (x | y) >> 32 ? x / y : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
+}
 
 // kNb: blocks of eight query heads (R = 8 kNb).  kClusters: a cluster for each item instead of a run
 // of units for each block.
@@ -283,9 +297,11 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     for (int s = 0; s < S::kStages; ++s) ptx::mbar_init(bars + s * 8, 1);
     ptx::fence_mbar_init();
   }
+  __syncwarp();
   wait_for_inputs();
   const long long c = blockIdx.x;
-  long long total = 0, blocks = 0, run0 = 0;
+  long long total = 0, blocks = 0, run0 = 0;  // blocks with a run, and where this one's begins
+  long long share = 0, extra = 0;             // runs: share + 1 each for the first `extra`, share for the others
   Walk seg;
   if constexpr (kClusters) {
     // Block r of a cluster takes the r-th eighth of its item.
@@ -297,10 +313,11 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     seg.u1 = static_cast<int>(static_cast<long long>(seg.it.units) * (r + 1) / kCluster);
     seg.left = 0;
   } else {
-    // The batch's cost, and where this block's run begins: each thread sums a chunk
-    // of the requests, the one whose chunk holds the run's beginning finds the request.
-    const int per = (p.batch + kThreadsPaged - 1) / kThreadsPaged;
-    const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+    // The batch's cost, and where this block's run begins: lane l (of up to 32 requests) or thread t
+    // (of a chunk of the requests) sums, and the one that holds the run's beginning finds the request.
+    const int per = p.batch <= 32 ? 1 : (p.batch + kThreadsPaged - 1) / kThreadsPaged;
+    const int who = p.batch <= 32 ? lane : threadIdx.x;
+    const int b0 = min(p.batch, who * per), b1 = min(p.batch, b0 + per);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) sum += item_of(p, b).cost();
     sum *= items;
@@ -310,44 +327,54 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
       const long long y = __shfl_up_sync(~0u, upto, d);
       if (lane >= d) upto += y;
     }
-    if (lane == 31) scan[warp] = upto;
-    __syncthreads();
-    total = 0;
+    if (p.batch <= 32) {
+      total = __shfl_sync(~0u, upto, 31);
+    } else {
+      if (lane == 31) scan[warp] = upto;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) upto += scan[w];
-      total += scan[w];
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) upto += scan[w];
+        total += scan[w];
+      }
     }
     blocks = min(static_cast<long long>(gridDim.x), total);
     if (c >= blocks) {
       if (threadIdx.x == 0) p.meta[c] = make_int4(0, 0, 0, 0);
       return;
     }
-    run0 = c * total / blocks;
-    const long long run1 = (c + 1) * total / blocks;
-    __syncthreads();
-    if (run0 < upto && run0 >= upto - sum) {
-      long long at = upto - sum;
-      int b = b0;
-      long long n = static_cast<long long>(item_of(p, b).cost()) * items;
-      while (at + n <= run0) {
-        at += n;
-        n = static_cast<long long>(item_of(p, ++b).cost()) * items;
+    share = divided(total, blocks);
+    extra = total - share * blocks;
+    run0 = c * share + min(c, extra);
+    const long long run = share + (c < extra);
+    const bool holds = run0 < upto && run0 >= upto - sum;
+    long long at = upto - sum;
+    int b = b0;
+    if (p.batch <= 32) {
+      b = __ffs(__ballot_sync(~0u, holds)) - 1;
+      at = __shfl_sync(~0u, at, b);
+    } else {
+      __syncthreads();
+      if (holds) {
+        long long n = static_cast<long long>(item_of(p, b).cost()) * items;
+        while (at + n <= run0) {
+          at += n;
+          n = static_cast<long long>(item_of(p, ++b).cost()) * items;
+        }
+        scan[0] = b;
+        scan[1] = at;
       }
-      scan[0] = b;
-      scan[1] = run0 - at;
+      __syncthreads();
+      b = static_cast<int>(scan[0]);
+      at = scan[1];
     }
-    __syncthreads();
-    {
-      const int b = static_cast<int>(scan[0]);
-      const int cost = item_of(p, b).cost();
-      const int j = static_cast<int>(scan[1] / cost);
-      seg.start(p, b, j, static_cast<int>(scan[1] - static_cast<long long>(j) * cost), run1 - run0);
-    }
+    const int cost = item_of(p, b).cost();
+    const int j = static_cast<int>(divided(run0 - at, cost));
+    seg.start(p, b, j, static_cast<int>(run0 - at - static_cast<long long>(j) * cost), run);
   }
   Producer<D> load;
   load.start(p, seg, warp, lane);
-  for (int s = 0; s < S::kStages; ++s) load.issue(p, ring, bars, valid, warp, lane);
+  load.begin(p, ring, bars, valid, warp, lane);
 
   // ldmatrix addresses of this lane: row and 16-byte chunk of K (A operand, keys x channels) and
   // of V read transposed (channels x keys); a row is 128 bytes per 64 channels, chunk ^ (row & 7).
@@ -609,7 +636,9 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     if (!kClusters && !whole && slot == 1) {
       // the item goes on in later blocks: up to the one that holds its last unit
       const long long last = pos - seg.c0 + seg.it.units - 1;
-      note = make_int4(seg.b, seg.j, static_cast<int>(((last + 1) * blocks - 1) / total - c) + 1, 0);
+      const long long longer = extra * (share + 1);
+      const long long owner = last < longer ? divided(last, share + 1) : extra + divided(last - longer, share);
+      note = make_int4(seg.b, seg.j, static_cast<int>(owner - c) + 1, 0);
     }
     if (more && kQShared) load_queries(next);
     seg = next;
