@@ -13,7 +13,8 @@
 // block serves up to kTokensPerBlock tokens alone.  Where several blocks share the tokens and
 // the lengths or the count are updated in place, those are written by a second launch, since
 // no block may overwrite what another has yet to read.  Bound by latency: the launch, one
-// dependent read of the lengths, two block scans, one dependent read of the table.
+// dependent read of the lengths, two block scans, one dependent read of the table (256 requests
+// of one token 3.9 us, 63 of 75569 tokens 5.0 us, in a captured graph).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -14,6 +14,9 @@
 // page in down to a histogram bin; a page more than 2 e above the bin is in, one more than 2 e
 // below is out, and those between, a handful, are scored again in 64 bits and ranked.  A score
 // that is not finite in 32 bits sends all pages of its row that way.
+//
+// Measured (in a captured graph): 8 rows of 4725 pages 14 us; 256 rows of up to 853 pages 24 us, of
+// which 14 for 56 MB of summaries; 14 rows of up to 427 pages 8 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

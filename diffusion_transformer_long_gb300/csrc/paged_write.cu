@@ -9,7 +9,9 @@
 // window has 8 channels of one head: it moves them for all of the run's tokens, keeps their
 // running extremes in registers and merges them with the page's earlier summary (or starts it
 // anew, where the run holds row 0): no atomics, no exchange between threads, and neighbouring
-// threads read whole tokens, as without a summary.
+// threads read whole tokens, as without a summary.  Measured: 27280 tokens of 24 heads of 128, pages
+// of 64: 110 us, 6.1 TB/s (without summaries 104 us; a copy's rate here is 6.8 TB/s); 64 tokens of 8
+// heads 2.4 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

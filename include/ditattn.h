@@ -446,6 +446,7 @@ dit_status dit_attn_check(dit_stream stream);
  * after `wait_limit_cycles` SM clocks (<= 0 keeps the default of about two
  * seconds); the kernel then records DIT_ERR_TIMEOUT in the status word and
  * exits cleanly, and dit_attn_check() reports it.  Nothing faults or hangs.
+ * dit_paged_attn_fwd withholds its copies and reports in the same way.
  * Call with enable = 0 to restore normal operation.  Not thread-safe with
  * concurrent launches from other host threads.
  */
@@ -456,6 +457,9 @@ void dit_test_inject_stall(int enable, long long wait_limit_cycles);
  * (normally one per SM; max_ctas <= 0 restores that).  With a small cap every
  * CTA walks many work items, which exercises the cross-item pipeline on small
  * inputs.  Affects later launches from this process; results do not change.
+ * dit_paged_attn_fwd takes the cap too and, while one is set, deals its work
+ * out over the capped grid at any size (its results change by the rounding of
+ * the joins).
  */
 void dit_test_set_grid_limit(int max_ctas);
 
