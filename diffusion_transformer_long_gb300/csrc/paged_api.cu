@@ -44,8 +44,8 @@ dit_strides cache_strides(const dit_strides* s, int n_pages, int H, int page_siz
   return x;
 }
 
-bool valid_cache(const void* p, const dit_strides& s, int n_pages) {
-  return p && aligned(p, 16) && valid_strides(s) && s.b <= kMaxSpan / n_pages;
+bool valid_cache(const void* p, const dit_strides& s, int n_pages, int H) {
+  return p && aligned(p, 16) && valid_strides(s) && s.b <= kMaxSpan / n_pages && s.h <= kMaxSpan / H;
 }
 
 Range cache_range(const void* p, const dit_strides& s, int n_pages, int H, int page_size, int D) {
@@ -61,8 +61,8 @@ dit_strides query_strides(const dit_strides* s, int B, int H, int D) {
   return x;
 }
 
-bool valid_query(const void* q, const dit_strides& s, int B) {
-  return q && aligned(q, 16) && valid_strides(s) && s.b <= kMaxSpan / B;
+bool valid_query(const void* q, const dit_strides& s, int B, int H) {
+  return q && aligned(q, 16) && valid_strides(s) && s.b <= kMaxSpan / B && s.h <= kMaxSpan / H;
 }
 
 dit_status check_heads(int B, int H_q, int H_kv, int D) {
@@ -137,10 +137,11 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
   const dit_strides ks = cache_strides(k_strides, n_pages, H, page_size, D);
   const dit_strides vs = cache_strides(v_strides, n_pages, H, page_size, D);
   if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16) || !valid_strides(kn) ||
-      !valid_strides(vn) || kn.n > kMaxSpan / T || vn.n > kMaxSpan / T)
+      !valid_strides(vn) || kn.n > kMaxSpan / T || vn.n > kMaxSpan / T || kn.h > kMaxSpan / H ||
+      vn.h > kMaxSpan / H)
     return DIT_ERR_INVALID_ARG;
-  if (!slots || !aligned(slots, 8) || !valid_cache(k_cache, ks, n_pages) ||
-      !valid_cache(v_cache, vs, n_pages) || !aligned(summary, 16) ||
+  if (!slots || !aligned(slots, 8) || !valid_cache(k_cache, ks, n_pages, H) ||
+      !valid_cache(v_cache, vs, n_pages, H) || !aligned(summary, 16) ||
       H > kMaxSpan / (static_cast<long long>(n_pages) * D))
     return DIT_ERR_INVALID_ARG;
   if (!no_self_overlap(ks, n_pages, H, page_size, D) ||
@@ -199,8 +200,8 @@ dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const
   const dit_strides qs = query_strides(q_strides, B, H_q, D);
   const dit_strides ks = cache_strides(k_strides, n_pages, H_kv, page_size, D);
   const dit_strides vs = cache_strides(v_strides, n_pages, H_kv, page_size, D);
-  if (!valid_query(q, qs, B) || !valid_cache(k_cache, ks, n_pages) ||
-      !valid_cache(v_cache, vs, n_pages))
+  if (!valid_query(q, qs, B, H_q) || !valid_cache(k_cache, ks, n_pages, H_kv) ||
+      !valid_cache(v_cache, vs, n_pages, H_kv))
     return DIT_ERR_INVALID_ARG;
   if (!valid_table(block_table, table_stride, B, max_pages) || !seq_lens || !aligned(seq_lens, 4) ||
       !aligned(selected, 4) || !out || !aligned(out, 16) || !aligned(lse, 4))
@@ -269,7 +270,7 @@ dit_status dit_paged_select(const void* q, const dit_strides* q_strides, const v
   s = check_pages(page_size, n_pages, max_pages);
   if (s != DIT_OK) return s;
   const dit_strides qs = query_strides(q_strides, B, H_q, D);
-  if (!valid_query(q, qs, B) || !summary || !aligned(summary, 16) ||
+  if (!valid_query(q, qs, B, H_q) || !summary || !aligned(summary, 16) ||
       H_kv > kMaxSpan / (static_cast<long long>(n_pages) * D))
     return DIT_ERR_INVALID_ARG;
   if (!valid_table(block_table, table_stride, B, max_pages) || !seq_lens || !aligned(seq_lens, 4) ||

@@ -166,12 +166,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __g
   const int bg = blockIdx.y + blockIdx.z * gridDim.y;
   if (bg >= a.batch * a.h_kv) return;
   const int b = bg / a.h_kv, g = bg - b * a.h_kv;
-  const int chunk = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
   const int n = pages_now(a, b);
-  if (chunk * kChunk >= n || n <= a.top_k) return;  // nothing to choose
+  if (n <= a.top_k) return;  // nothing to choose
   uint32_t* keys = p.keys + static_cast<long long>(bg) * a.max_pages;
-  const float mag = score_pages<D>(a, b, g, n, chunk, [&](int i, uint32_t key) { keys[i] = key; });
-  if ((threadIdx.x & 31) == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
+  for (int chunk = blockIdx.x * kScoreWarps + (threadIdx.x >> 5); chunk * kChunk < n; chunk += gridDim.x * kScoreWarps) {
+    const float mag = score_pages<D>(a, b, g, n, chunk, [&](int i, uint32_t key) { keys[i] = key; });
+    if ((threadIdx.x & 31) == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
+  }
 }
 
 // Sum over the block; `sm` is free again at the next barrier.
@@ -225,7 +226,7 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
   const long long q_step = a.q_h / 2;
   if (unit > 0.f) {
     auto term = [&](float x, float l, float h) { return __float2ll_rn(fmaxf(x * l, x * h) * unit); };
-    long long best = -(1ll << 63);
+    long long best = static_cast<long long>(1ull << 63);  // below every sum
 #pragma unroll 4
     for (int h = h_first; h < h_end; ++h) {
       const uint32_t q0 = __ldg(qh + h * q_step), q1 = parts > 1 ? __ldg(qh + h * q_step + 32) : 0;
@@ -535,7 +536,12 @@ cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
                      : launch_after<kSelectCluster>(paged_select_few_kernel<128>, grid, dim3(kPickThreads), 0, st, p);
   }
   const unsigned rows_y = static_cast<unsigned>(std::min<size_t>(rows, 32768));
-  const dim3 grid((p.chunks + kScoreWarps - 1) / kScoreWarps, rows_y, static_cast<unsigned>((rows + rows_y - 1) / rows_y));
+  // A block for every 128 pages that the table has room for, up to 32 an SM: tables are often far wider
+  // than the requests are long, and each empty block costs its start.
+  const size_t most = std::max<size_t>(1, 32 * static_cast<size_t>(host::sm_count()) / rows);
+  const size_t needed = (static_cast<size_t>(p.chunks) + kScoreWarps - 1) / kScoreWarps;
+  const dim3 grid(static_cast<unsigned>(std::min(needed, most)), rows_y,
+                  static_cast<unsigned>((rows + rows_y - 1) / rows_y));
   const cudaError_t e = a.d == 64 ? launch_after(paged_score_kernel<64>, grid, dim3(kScoreWarps * 32), 0, st, p)
                                   : launch_after(paged_score_kernel<128>, grid, dim3(kScoreWarps * 32), 0, st, p);
   return e != cudaSuccess ? e : launch_after(paged_pick_kernel, dim3(static_cast<unsigned>(rows)), dim3(kPickThreads), 0, st, p);

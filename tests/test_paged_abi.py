@@ -90,7 +90,7 @@ def attn(lib, **kw):
     (dict(ws=A[7] + 128), INVALID), (dict(out=A[5] + 8), INVALID), (dict(lse=A[6] + 2), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=math.nan), INVALID), (dict(dt=3), INVALID),
     (dict(sel=A[8], n_sel=0), INVALID), (dict(sel=A[8], n_sel=11), INVALID), (dict(sel=A[8] + 2, n_sel=2), INVALID),
-    (dict(qs=S(1024, 100, 0)), INVALID), (dict(ks=S(0, 2048, 128)), INVALID), (dict(out=A[0] + 1024), INVALID),
+    (dict(qs=S(1024, 100, 0)), INVALID), (dict(ks=S(1 << 38, 1 << 38, 128), B=1, Hq=1 << 23, Hkv=1 << 23), INVALID), (dict(ks=S(0, 2048, 128)), INVALID), (dict(out=A[0] + 1024), INVALID),
     (dict(lse=A[4]), INVALID), (dict(ws=A[2] + 256), INVALID), (dict(out=A[7] + 4096), INVALID),
     (dict(lse=A[5] + 64), INVALID), (dict(B=1 << 16, Hq=1 << 16), INVALID)])
 def test_attn_validation(lib, kw, status):

@@ -14,6 +14,9 @@ These are worst cases; over a whole output the errors are of random sign, so the
 is also held to 1e-5 (fp32 output) of the result's.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -229,6 +232,7 @@ def make_case(lens, Hq, Hkv, D, P, order="hnd", seed=0, q_scale=1.5, k_scale=1.0
     (24, 8, 128, 16, "hnd", [0, 0, 1, 2, 4608]), (24, 24, 128, 32, "nhd", [31, 32, 33, 700]),
     (40, 8, 128, 64, "hnd", [5, 1000, 63]), (16, 1, 64, 48, "part", [47, 48, 49, 2000]),
     (24, 2, 128, 128, "hnd", [129, 1, 300]), (24, 1, 128, 16, "nhd", [513, 16]),
+    (40, 1, 128, 16, "hnd", [700, 3]), (70, 2, 64, 32, "nhd", [333, 0, 64]),
     (64, 2, 64, 1024, "hnd", [1500, 1023]), (9, 1, 128, 16, "part", [100]),
     (1, 1, 128, 16, "hnd", [27280]), (8, 8, 64, 16, "hnd", list(range(130)))])
 def test_attn(Hq, Hkv, D, P, order, lens, out_dtype, launch):
@@ -559,6 +563,52 @@ def test_select_among_many_pages(n, kind):
     for k in (2, 17, n // 3, n - 1):
         got = da.paged_select(q, summary, t, sl, P, k)
         assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, k)), k
+
+
+def test_tables_far_wider_than_the_requests():
+    """Room for 2^20 pages a request, a few of them held: nothing takes the room for the length."""
+    lens, P = [100, 0, 3000], 16
+    q, k, v, table, sl = make_case(lens, 6, 2, 64, P, seed=91)
+    wide = torch.full((3, 1 << 20), -1, device=DEV, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    summary = torch.stack((k.amin(2), k.amax(2)), 2)
+    sel = da.paged_select(q, summary, wide, sl, P, 20)
+    assert np.array_equal(sel.cpu().numpy(), po.select(q, summary, table, sl, P, 20))
+    check_attn(*da.paged_attn_fwd(q, k, v, wide, sl), po.attend(q, k, v, table, sl, 0.125))
+    check_attn(*da.paged_attn_fwd(q, k, v, wide, sl, selected=sel),
+               po.attend(q, k, v, table, sl, 0.125, selected=sel))
+    free = dev(np.arange(40))
+    got = da.paged_plan(dev([20, 5, 1]), sl, wide, free, dev([40]), P, 500, 26)
+    want = po.plan([20, 5, 1], lens, table.cpu().numpy(), np.arange(40), 40, P, 500, 26)
+    assert np.array_equal(got[3].cpu().numpy(), want[3]) and np.array_equal(got[0].cpu().numpy(), want[0])
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """A fresh process captures its first calls: nothing of their setup is forbidden in a capture."""
+    code = """
+import torch
+from diffusion_transformer_long_gb300 import ditattn as da
+i32 = dict(dtype=torch.int32, device="cuda")
+B, H, D, P, n = 3, 2, 64, 16, 30
+new, lens, table = torch.full((B,), 5, **i32), torch.zeros(B, **i32), torch.full((B, 8), -1, **i32)
+free, n_free = torch.arange(n, **i32), torch.full((1,), n, **i32)
+k, v = (torch.zeros(n, H, P, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+s = torch.zeros(n, H, 2, D, dtype=torch.bfloat16, device="cuda")
+x = torch.randn(15, 3 * H, D, device="cuda").bfloat16()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    _, _, _, slots = da.paged_plan(new, lens, table, free, n_free, P, n, 15, seq_lens_out=lens, n_free_out=n_free)
+    da.paged_kv_write(x[:, H:2 * H], x[:, 2 * H:], slots, k, v, summary=s)
+    sel = da.paged_select(x[:B, :H], s, table, lens, P, 2)
+    o, lse = da.paged_attn_fwd(x[:B, :H], k, v, table, lens, selected=sel)
+g.replay()
+da.check()
+assert lens.tolist() == [5] * B and o.isfinite().all() and lse.isfinite().all() and o.abs().sum() > 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,P,order", [(24, 8, 128, 16, "hnd"), (2, 2, 64, 48, "nhd"), (16, 1, 64, 64, "part")])
