@@ -24,7 +24,7 @@
 namespace ditattn {
 namespace {
 
-constexpr int kWriteThreads = 256;
+constexpr int kWriteThreads = 128;  // (256: 0.5 to 1 % slower for long prefills)
 
 struct WriteParams {
   const char* k_new;
@@ -36,7 +36,7 @@ struct WriteParams {
   long long ks_p, ks_h, ks_r, vs_p, vs_h, vs_r;  // page, head, row strides (bytes)
   char* summary;
   long long n_slots;
-  long long threads;  // with a summary: windows * columns (16 bytes of a head), or * heads * block
+  long long threads;  // with a summary: windows * columns (16 bytes of a head), or * heads (blocks)
   int tokens, heads, page_size, window, few;
 };
 
@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_runs(const __grid_c
 
 // The same for launches that a thread per column would leave with too few threads: a block for each
 // window and head shares out a run's rows over its warps and lanes.  Short runs (decoded tokens)
-// go to every eighth head's block, a head to each warp.
-template <int kVpr>
-__global__ void __launch_bounds__(kWriteThreads, 4) paged_write_few(const __grid_constant__ WriteParams p) {
-  constexpr int kRows = 32 / kVpr, kWarps = kWriteThreads / 32;  // rows a warp moves at once
+// go to every kWarps-th head's block, a head to each warp.
+template <int kVpr, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 32 / kWarps) paged_write_few(const __grid_constant__ WriteParams p) {
+  constexpr int kRows = 32 / kVpr;  // rows a warp moves at once
   __shared__ Ext of_warp[kWarps][kVpr];
   wait_for_inputs();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -264,12 +264,15 @@ __global__ void __launch_bounds__(kWriteThreads, 4) paged_write_few(const __grid
 template <int kVpr>
 cudaError_t launch(const WriteParams& p, cudaStream_t st) {
   const long long threads = p.summary ? p.threads : static_cast<long long>(p.tokens) * p.heads * kVpr;
-  const long long blocks = (threads + kWriteThreads - 1) / kWriteThreads;
+  const long long blocks = p.few ? threads : (threads + kWriteThreads - 1) / kWriteThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kWriteThreads);
   if (!p.summary) return launch_after(paged_write_rows<kVpr>, grid, block, 0, st, p);
-  return p.few ? launch_after(paged_write_few<kVpr>, grid, block, 0, st, p)
-               : launch_after(paged_write_runs<kVpr>, grid, block, 0, st, p);
+  if (!p.few) return launch_after(paged_write_runs<kVpr>, grid, block, 0, st, p);
+  // Four warps for a run of up to 64 rows (24 heads of 128, 64 decoded tokens: 4.0 us, eight warps 5.3),
+  // eight for longer ones (8 heads, 300 tokens, pages of 512: 8.8 us, four warps 12.0).
+  return p.page_size <= 64 ? launch_after(paged_write_few<kVpr, 4>, grid, dim3(128), 0, st, p)
+                           : launch_after(paged_write_few<kVpr, 8>, grid, dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -300,14 +303,14 @@ cudaError_t launch_paged_write(const WriteLaunch& a, cudaStream_t st) {
   // Threads that would hold a run each: the two forms meet at 30 to 50 thousand (8 heads of 128, pages
   // of 64: 18432 tokens; at 300 tokens the block form takes 5 us, the other 16; at 27280, 51 and 44).
   // Runs of at most 16 tokens are short enough for one thread at any size.
-  p.few = a.page_size > 16 && a.tokens * columns / a.page_size < 32768;
+  p.few = a.summary && a.page_size > 16 && a.tokens * columns / a.page_size < 32768;
   // A window per token (and head) where there are few, longer ones where every SM has work anyway.
   p.window = 1;
   if (p.few)
     while (p.window < 32 && static_cast<long long>(a.tokens) * a.heads > 2048LL * p.window) p.window *= 2;
   else
     while (p.window < 16 && a.tokens * columns > 65536LL * p.window) p.window *= 2;
-  p.threads = (static_cast<long long>(a.tokens) + p.window - 1) / p.window * (p.few ? a.heads * static_cast<long long>(kWriteThreads) : columns);
+  p.threads = (static_cast<long long>(a.tokens) + p.window - 1) / p.window * (p.few ? a.heads : columns);
   return a.d == 64 ? launch<8>(p, st) : launch<16>(p, st);
 }
 
