@@ -51,15 +51,15 @@ inline bool valid_strides(const dit_strides& s) {
   return true;
 }
 
-// True if no two elements of the view share an address: sorted by stride, every stride
-// must clear the span of the dimensions below it.
+// True if no two elements of the view, or of `copies` of it `distance` elements apart, share an
+// address: sorted by stride, every stride must clear the span of the dimensions below it.
 inline bool no_self_overlap(const dit_strides& s, long long B, long long H, long long N,
-                            long long D) {
+                            long long D, long long distance = 0, long long copies = 1) {
   struct Dim {
     long long stride, extent;
-  } d[3] = {{s.n, N}, {s.h, H}, {s.b, B}};
-  for (int i = 0; i < 3; ++i)  // sort by stride
-    for (int j = i + 1; j < 3; ++j)
+  } d[4] = {{s.n, N}, {s.h, H}, {s.b, B}, {distance, copies}};
+  for (int i = 0; i < 4; ++i)  // sort by stride
+    for (int j = i + 1; j < 4; ++j)
       if (d[j].stride < d[i].stride) std::swap(d[i], d[j]);
   long long span = D;
   for (const Dim& x : d) {

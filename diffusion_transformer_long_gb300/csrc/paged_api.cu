@@ -52,6 +52,18 @@ Range cache_range(const void* p, const dit_strides& s, int n_pages, int H, int p
   return span(p, view_span(s, n_pages, H, page_size, D, 2));
 }
 
+// True if the two caches share no element: apart, or of equal strides and interleaved (pages, rows or
+// heads of K and V in turn in one allocation), which the pair as one view with the distance between
+// them as a further dimension shows.
+bool caches_apart(const void* k, const dit_strides& ks, const void* v, const dit_strides& vs, int n_pages,
+                  int H, int page_size, int D) {
+  if (!overlap(cache_range(k, ks, n_pages, H, page_size, D), cache_range(v, vs, n_pages, H, page_size, D)))
+    return true;
+  if (ks.b != vs.b || ks.h != vs.h || ks.n != vs.n) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(k), b = reinterpret_cast<uintptr_t>(v);
+  return no_self_overlap(ks, n_pages, H, page_size, D, static_cast<long long>((a > b ? a - b : b - a) / 2), 2);
+}
+
 // A [B, H, D] query view: its strides (b, h) in the manner of cache_strides.
 dit_strides query_strides(const dit_strides* s, int B, int H, int D) {
   dit_strides x = s ? *s : dit_strides{static_cast<long long>(H) * D, D, D};
@@ -153,9 +165,9 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
   const Range ins[] = {span(k_new, view_span(kn, 1, H, T, D, 2)),
                        span(v_new, view_span(vn, 1, H, T, D, 2)), span(slots, 8LL * T)};
   const int n_out = summary ? 3 : 2;
+  if (!caches_apart(k_cache, ks, v_cache, vs, n_pages, H, page_size, D)) return DIT_ERR_INVALID_ARG;
   for (int i = 0; i < n_out; ++i) {
-    for (int j = i + 1; j < n_out; ++j)
-      if (overlap(outs[i], outs[j])) return DIT_ERR_INVALID_ARG;
+    if (i < 2 && summary && overlap(outs[i], outs[2])) return DIT_ERR_INVALID_ARG;
     for (const Range& in : ins)
       if (overlap(outs[i], in)) return DIT_ERR_INVALID_ARG;
   }

@@ -727,7 +727,8 @@ def attention(q, k, v, scale=None, chunks=None, out_dtype=torch.float32,
 #   selected = paged_select(q, summary, table, lens, ...)        (sparse attention only)
 #   out, lse = paged_attn_fwd(q, k_cache, v_cache, table, lens, selected=selected)
 # k_cache and v_cache are [n_pages, H_kv, page_size, D] views (a token-major cache
-# [n_pages, page_size, H_kv, D] is passed as x.transpose(1, 2)); block_table is int32
+# [n_pages, page_size, H_kv, D] is passed as x.transpose(1, 2), the halves of one that holds keys and
+# values in turn as x[:, 0] and x[:, 1]); block_table is int32
 # [B, max_pages], seq_lens int32 [B].
 
 

@@ -352,7 +352,9 @@ dit_status dit_paged_plan(const int* new_lens, const int* seq_lens, int* block_t
  *                   a fused projection need no copy.  NULL strides: contiguous [T, H, D].
  *   slots         : device int64 [T]; a slot outside [0, n_pages * page_size) skips its
  *                   token, and rows without a token are left as they are
- *   k_cache, v_cache : paged caches (written)
+ *   k_cache, v_cache : paged caches (written); they may be interleaved in one allocation
+ *                   ([n_pages, 2, H, page_size, D], [n_pages, page_size, 2, H, D] ..) where
+ *                   their strides are equal and no element is shared
  *   summary       : device bf16 [n_pages, H, 2, D], contiguous, or NULL: for every page
  *                   and channel the minimum (index 0) and maximum (1) of its keys.  A page
  *                   whose row 0 is written starts anew from the rows of this call; any

@@ -66,6 +66,13 @@ def write(lib, **kw):
     (dict(kcs=S(2048, 1024, 32)), INVALID),      # rows overlap
     (dict(kcs=S(1024, 1024, 64)), INVALID),      # pages overlap
     (dict(kcs=S(1 << 39, 1024, 64)), INVALID), (dict(vc=A[3] + 4096), INVALID), (dict(summary=A[4] + 64), INVALID),
+    # interleaved caches: not by whole halves, by less than a head, of other strides, with the summary or the rows inside
+    (dict(kcs=S(4096, 1024, 64), vc=A[3] + 2048, vcs=S(4096, 1024, 64)), INVALID),
+    (dict(kcs=S(4096, 128, 256), vc=A[3] + 64, vcs=S(4096, 128, 256)), INVALID),
+    (dict(kcs=S(4096, 1024, 64), vc=A[3] + 4096, vcs=S(4096, 64, 128)), INVALID),
+    (dict(kcs=S(4096, 1024, 64), vc=A[3], vcs=S(4096, 1024, 64)), INVALID),
+    (dict(kcs=S(6144, 1024, 64), vc=A[3] + 4096, vcs=S(6144, 1024, 64), summary=A[3] + 8192), INVALID),
+    (dict(kcs=S(6144, 1024, 64), vc=A[3] + 4096, vcs=S(6144, 1024, 64), k=A[3] + 8192), INVALID),
     (dict(kc=A[0] + 512), INVALID), (dict(vc=A[2]), INVALID), (dict(H=1 << 20, n_pages=1 << 30), INVALID)])
 def test_write_validation(lib, kw, status):
     assert write(lib, **kw) == status

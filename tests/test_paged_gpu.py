@@ -183,6 +183,35 @@ def test_write(H, D, P, order, old, new, spare, with_summary):
     check_write(len(slots), H, D, P, order, slots, n_pages, with_summary)
 
 
+@pytest.mark.parametrize("shape,dims,keys", [
+    ((2, 9, 3, 32, 64), (0, 1, 2, 3, 4), 0), ((9, 2, 3, 32, 64), (1, 0, 2, 3, 4), 0),
+    ((9, 2, 3, 32, 64), (1, 0, 2, 3, 4), 1), ((9, 32, 2, 3, 64), (2, 0, 3, 1, 4), 0),
+    ((9, 32, 3, 2, 64), (3, 0, 2, 1, 4), 1), ((9, 3, 2, 32, 64), (2, 0, 1, 3, 4), 0),
+    ((9, 3, 32, 2, 64), (3, 0, 1, 2, 4), 0)])
+def test_keys_and_values_in_one_allocation(shape, dims, keys):
+    """Pages, heads or rows of keys and values in turn: written and attended to as in two allocations."""
+    both = rand(*shape, seed=1)
+    pair = both.permute(*dims)  # [2, n_pages, H, P, D]
+    k, v = pair[keys], pair[1 - keys]
+    n_pages, H, P, D = k.shape
+    apart = [x.clone(memory_format=torch.contiguous_format) for x in (k, v)]
+    lens = [50, 0, 32, 97]
+    table, _ = tables(lens, P, extra_pages=n_pages - 7)
+    slots = np.concatenate([table[b, np.arange(n) // P] * P + np.arange(n) % P for b, n in enumerate(lens)])
+    new = rand(len(slots), 2 * H, D, seed=2)
+    q, td, sl = rand(len(lens), 2 * H, D, seed=3), dev(table), dev(lens)
+    res = []
+    for kc, vc in ((k, v), apart):
+        summary = torch.zeros(n_pages, H, 2, D, device=DEV, dtype=torch.bfloat16)
+        da.paged_kv_write(new[:, :H], new[:, H:], dev(slots, torch.int64), kc, vc, summary=summary)
+        sel = da.paged_select(q, summary, td, sl, P, 2)
+        res.append((kc, vc, summary, sel, *da.paged_attn_fwd(q, kc, vc, td, sl),
+                    *da.paged_attn_fwd(q, kc, vc, td, sl, selected=sel)))
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+    check_attn(*res[0][4:6], po.attend(q, k, v, td, sl, D ** -0.5))
+
+
 def test_write_skips_and_nan():
     """Slots outside the pool are skipped wherever they stand (a page's run goes on behind them, as a
     run of its own rows), and a NaN key shows in its page's summary."""
