@@ -91,15 +91,22 @@ __device__ __forceinline__ int pages_now(const SelectLaunch& a, int b) {
   return pages_of(min(max(0, a.seq_lens[b]), a.max_pages * a.page_size), a.page_size);
 }
 
-// A warp scores 16 pages of one (request, key/value head), the n table columns' from 16 chunk on:
-// store(i, key) gets each one's, by one lane.  Returns the largest sum |q| |k|.
+// A lane's table entry of a warp's chunk.  It is read before the request's length is known, or while
+// the chunk before is scored: one latency less in the chain (any entry of the row may be read).
+__device__ __forceinline__ int entry_of(const SelectLaunch& a, int b, long long chunk) {
+  const long long i = chunk * kChunk + (threadIdx.x & 31);
+  return (threadIdx.x & 31) < kChunk && i < a.max_pages ? a.table[b * a.table_stride + i] : -1;
+}
+
+// A warp scores 16 pages of one (request, key/value head), the n table columns' from 16 chunk on, of
+// whose entries every lane brings its own: store(i, key) gets each one's, by one lane.  Returns the
+// largest sum |q| |k|.
 template <int D, typename Store>
-__device__ __forceinline__ float score_pages(const SelectLaunch& a, int b, int g, int n, int chunk, Store store) {
+__device__ __forceinline__ float score_pages(const SelectLaunch& a, int b, int g, int n, int chunk, int entry,
+                                             Store store) {
   constexpr int kLoads = 2 * D / 32;  // 64-byte pieces of a page's [lo | hi]
   const int lane = threadIdx.x & 31, j = lane & 3, i0 = chunk * kChunk;
-  int page = -1;
-  if (lane < kChunk && i0 + lane < n) page = a.table[b * a.table_stride + i0 + lane];
-  if (page >= a.n_pages) page = -1;
+  const int page = i0 + lane < n && entry < a.n_pages ? entry : -1;
   const int p0 = __shfl_sync(~0u, page, lane >> 2), p1 = __shfl_sync(~0u, page, (lane >> 2) + 8);
   uint4 x0[kLoads], x1[kLoads];
   const uint4* s0 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.summary) +
@@ -166,12 +173,17 @@ __global__ void __launch_bounds__(kScoreWarps * 32) paged_score_kernel(const __g
   const int bg = blockIdx.y + blockIdx.z * gridDim.y;
   if (bg >= a.batch * a.h_kv) return;
   const int b = bg / a.h_kv, g = bg - b * a.h_kv;
+  int chunk = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
+  int entry = entry_of(a, b, chunk);
   const int n = pages_now(a, b);
   if (n <= a.top_k) return;  // nothing to choose
   uint32_t* keys = p.keys + static_cast<long long>(bg) * a.max_pages;
-  for (int chunk = blockIdx.x * kScoreWarps + (threadIdx.x >> 5); chunk * kChunk < n; chunk += gridDim.x * kScoreWarps) {
-    const float mag = score_pages<D>(a, b, g, n, chunk, [&](int i, uint32_t key) { keys[i] = key; });
+  while (chunk * kChunk < n) {
+    const int next = chunk + gridDim.x * kScoreWarps, entry2 = entry_of(a, b, next);
+    const float mag = score_pages<D>(a, b, g, n, chunk, entry, [&](int i, uint32_t key) { keys[i] = key; });
     if ((threadIdx.x & 31) == 0) p.bounds[static_cast<long long>(bg) * p.chunks + chunk] = mag;
+    chunk = next;
+    entry = entry2;
   }
 }
 
@@ -207,10 +219,11 @@ __device__ __forceinline__ int block_below(int x, int* sm, int& all) {
 }
 
 // The 64-bit score of table column i, over heads h_first .. h_end - 1 of the group, as an integer of
-// the same order, by one warp: a lane takes two channels in every 64.  Sums are 64-bit integers in units of 1 / unit (a power of two for
-// which sum |q| |k| of every page stays below 2^62): each product, exact in 32 bits, is rounded
-// once, to 2^-61 of the largest page's sum or finer, so that the sum is exact but for that, in
-// any order, and far cheaper than in fp64, of which this GPU does two operations a clock and SM.
+// the same order, by one warp: a lane takes two channels in every 64.  Sums are 64-bit integers in
+// units of 1 / unit (a power of two for which sum |q| |k| of every page stays below 2^62): each
+// product, exact in 32 bits, is rounded once, to 2^-61 of the largest page's sum or finer, so that the
+// sum is exact but for that, in any order, and far cheaper than in fp64, of which this GPU does two
+// operations a clock and SM.
 // unit = 0 (some score is not finite in 32 bits, or all are near its underflow): fp64 after all.
 __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, float unit, int h_first, int h_end) {
   const int lane = threadIdx.x & 31;
@@ -480,6 +493,8 @@ __global__ void __launch_bounds__(kPickThreads) paged_select_few_kernel(const __
   const SelectLaunch& a = p.a;
   const int bg = blockIdx.x / kSelectCluster, rank = blockIdx.x % kSelectCluster;
   const int b = bg / a.h_kv, g = bg - b * a.h_kv, warp = threadIdx.x >> 5;
+  int chunk = warp * kSelectCluster + rank;
+  int entry = entry_of(a, b, chunk);
   const int n = pages_now(a, b);
   int* out = a.selected + static_cast<long long>(bg) * a.top_k;
   if (n <= a.top_k || a.top_k == 1) {
@@ -488,9 +503,12 @@ __global__ void __launch_bounds__(kPickThreads) paged_select_few_kernel(const __
   }
   uint32_t* keys = cluster.map_shared_rank(sm.cache, 0);
   float mag = 0.f;
-  for (int chunk = warp * kSelectCluster + rank; chunk * kChunk < n; chunk += kSelectCluster * kPickWarps) {
-    const float x = score_pages<D>(a, b, g, n, chunk, [&](int i, uint32_t key) { keys[i] = key; });
+  while (chunk * kChunk < n) {
+    const int next = chunk + kSelectCluster * kPickWarps, entry2 = entry_of(a, b, next);
+    const float x = score_pages<D>(a, b, g, n, chunk, entry, [&](int i, uint32_t key) { keys[i] = key; });
     mag = x > mag || x != x ? x : mag;
+    chunk = next;
+    entry = entry2;
   }
   if ((threadIdx.x & 31) == 0) cluster.map_shared_rank(mags, 0)[rank * kPickWarps + warp] = __float_as_uint(mag);
   cluster.sync();
@@ -503,7 +521,8 @@ size_t mask_words(int max_pages) { return (static_cast<size_t>(max_pages) + 31) 
 
 // One block of 512 threads and their registers fits an SM: clusters for all rows at once, or none.
 // Against two launches (in a graph; each launch also costs the host 2 us): 8 rows of 500 pages 7.4
-// and 8.7 us, of 1705 pages 10.8 and 12.3, of 4725 pages 15.9 and 15.7, of 8000 pages 21.3 and 20.2.
+// and 8.7 us, of 1705 pages 10.8 and 12.3, of 3000 pages 12.7 and 12.4, of 4725 pages 15.4 and 13.8;
+// 16 rows of 3000 pages 15.8 and 14.9, of 4725 pages 23.9 and 19.7.
 bool few_rows(size_t rows, int max_pages) {
   return rows * kSelectCluster <= static_cast<size_t>(host::sm_count()) && max_pages <= kFewPages;
 }
