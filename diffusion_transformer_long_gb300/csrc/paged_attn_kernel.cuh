@@ -147,7 +147,7 @@ struct Item {
 };
 __device__ __forceinline__ Item item_of(const PagedParams& p, int b) {
   Item x;
-  x.len = min(max(0, __ldg(p.seq_lens + b)), p.max_len);
+  x.len = min(max(0, p.seq_lens[b]), p.max_len);
   x.pages = pages_of(x.len, p.page_size);
   x.tiles = p.selected ? min(x.pages, p.n_selected) * p.page_tiles : pages_of(x.len, kTile);
   x.units = max(1, (x.tiles + kUnitTiles - 1) / kUnitTiles);
@@ -219,9 +219,9 @@ struct Producer {
     if (lane < x.n) {
       int col = t / p.page_tiles;
       const int row = (t - col * p.page_tiles) * kTile;
-      if (p.selected) col = __ldg(p.selected + (static_cast<long long>(w.b) * p.h_kv + x.head) * p.n_selected + col);
+      if (p.selected) col = p.selected[(static_cast<long long>(w.b) * p.h_kv + x.head) * p.n_selected + col];
       if (col >= 0 && col < w.it.pages) {
-        x.page = __ldg(p.table + w.b * p.table_stride + col);
+        x.page = p.table[w.b * p.table_stride + col];
         const int keys = min(kTile, w.it.len - col * p.page_size - row);
         if (keys > 0) x.spot = row | keys << 16;
       }
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     ptx::fence_mbar_init();
   }
   __syncwarp();
-  wait_for_inputs();
+  wait_for_inputs_and_copies();
   const long long c = blockIdx.x;
   long long total = 0, blocks = 0, run0 = 0;  // blocks with a run, and where this one's begins
   long long share = 0, extra = 0;             // runs: share + 1 each for the first `extra`, share for the others
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
           p.q + w.b * p.q_b + static_cast<long long>(hk * p.group + h) * p.q_h + (lane & 3) * 2);
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        const uint2 x = h < p.group ? make_uint2(__ldg(q + k * 8), __ldg(q + k * 8 + 4)) : make_uint2(0, 0);
+        const uint2 x = h < p.group ? make_uint2(q[k * 8], q[k * 8 + 4]) : make_uint2(0, 0);
         if constexpr (kQShared) {
           q_sm[(nb * kSteps + k) * 32 + lane] = x;
         } else {

@@ -116,8 +116,8 @@ __device__ __forceinline__ float score_pages(const SelectLaunch& a, int b, int g
   const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    x0[i] = p0 >= 0 ? __ldg(s0 + 4 * i) : none;
-    x1[i] = p1 >= 0 ? __ldg(s1 + 4 * i) : none;
+    x0[i] = p0 >= 0 ? s0[4 * i] : none;
+    x1[i] = p1 >= 0 ? s1[4 * i] : none;
   }
   const int group = a.h_q / a.h_kv;
   float best0 = -INFINITY, best1 = -INFINITY, mag = 0.f;
@@ -131,7 +131,7 @@ __device__ __forceinline__ float score_pages(const SelectLaunch& a, int b, int g
     for (int i = 0; i < kLoads; ++i) {
       // lane j's words of piece i: channels 8 j .. 8 j + 7 of 32, two products of 16
       const bool hi = i >= kLoads / 2;
-      uint4 y = __ldg(q + 4 * (i % (kLoads / 2)));
+      uint4 y = q[4 * (i % (kLoads / 2))];
       y.x = half_of(y.x, hi);
       y.y = half_of(y.y, hi);
       y.z = half_of(y.z, hi);
@@ -242,7 +242,7 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
     long long best = static_cast<long long>(1ull << 63);  // below every sum
 #pragma unroll 4
     for (int h = h_first; h < h_end; ++h) {
-      const uint32_t q0 = __ldg(qh + h * q_step), q1 = parts > 1 ? __ldg(qh + h * q_step + 32) : 0;
+      const uint32_t q0 = qh[h * q_step], q1 = parts > 1 ? qh[h * q_step + 32] : 0;
       long long s = term(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
                     term(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
                     term(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +
@@ -259,7 +259,7 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
   };
   double best = -INFINITY;
   for (int h = h_first; h < h_end; ++h) {
-    const uint32_t q0 = __ldg(qh + h * q_step), q1 = parts > 1 ? __ldg(qh + h * q_step + 32) : 0;
+    const uint32_t q0 = qh[h * q_step], q1 = parts > 1 ? qh[h * q_step + 32] : 0;
     double s = larger(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
                larger(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
                larger(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +

@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_rows(const __grid_c
   const long long slot = p.slots[t];
   if (slot < 0 || slot >= p.n_slots) return;
   const long long page = slot / p.page_size, r = slot - page * p.page_size;
-  const uint4 k = __ldcs(reinterpret_cast<const uint4*>(p.k_new + t * p.kn_n + h * p.kn_h + vec));
-  const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p.v_new + t * p.vn_n + h * p.vn_h + vec));
+  const uint4 k = load_once(p.k_new + t * p.kn_n + h * p.kn_h + vec);
+  const uint4 v = load_once(p.v_new + t * p.vn_n + h * p.vn_h + vec);
   *reinterpret_cast<uint4*>(p.k_cache + page * p.ks_p + h * p.ks_h + r * p.ks_r + vec) = k;
   *reinterpret_cast<uint4*>(p.v_cache + page * p.vs_p + h * p.vs_h + r * p.vs_r + vec) = v;
 }
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_runs(const __grid_c
       memcpy(e.lo, &a, 16);
       memcpy(e.hi, &b, 16);
     } else {
-      e.take(__ldcs(reinterpret_cast<const uint4*>(k_src + t * p.kn_n)), true);
+      e.take(load_once(k_src + t * p.kn_n), true);
     }
     const long long first = p.slots[t] - t;  // slot - token along the run
     const int most = min(p.page_size - at.row, p.tokens - t);
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_runs(const __grid_c
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (i < m) {
-          k[i] = __ldcs(reinterpret_cast<const uint4*>(k_src + (t + i) * p.kn_n));
-          v[i] = __ldcs(reinterpret_cast<const uint4*>(v_src + (t + i) * p.vn_n));
+          k[i] = load_once(k_src + (t + i) * p.kn_n);
+          v[i] = load_once(v_src + (t + i) * p.vn_n);
         }
       }
 #pragma unroll
