@@ -19,6 +19,12 @@ def pytest_collection_modifyitems(config, items):
     except Exception:  # pragma: no cover
         has_gpu = False
     if has_gpu:
+        # Calls on made-up device addresses.  Some are refused for want of a workspace, which the same
+        # sizes do not need on a real GPU: there they would be launched and fault.
+        skip = pytest.mark.skip(reason="made-up device addresses: run where there is no GPU")
+        for item in items:
+            if item.path.name == "test_paged_abi.py" and item.originalname.endswith("_validation"):
+                item.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA device")
     for item in items:
