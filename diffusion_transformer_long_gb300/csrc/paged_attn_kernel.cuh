@@ -651,8 +651,10 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
     pos = next_pos;
   }
   if constexpr (kClusters) {
-    // Every block's sums against their common maximum; block r joins the heads r, r + 8, ..
-    if (seg.u0 == seg.u1 && threadIdx.x < R) mine_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    // Every block's sums against their common maximum; block r joins the heads r, r + 8, ..  A maximum of
+    // -inf does not mean that there is nothing to join: the fmaxf of scores that are all NaN leaves it there, and
+    // the sums are NaN.  A block without units, whose sums were never written, has the sum -1.
+    if (seg.u0 == seg.u1 && threadIdx.x < R) mine_ml[threadIdx.x] = make_float2(-INFINITY, -1.f);
     const auto cluster = cooperative_groups::this_cluster();
     cluster.sync();
     const int hk = seg.j / p.head_blocks, h0 = (seg.j - hk * p.head_blocks) * R;
@@ -668,10 +670,11 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
         x[r] = cluster.map_shared_rank(mine, r)[head * D + d];
         M = fmaxf(M, y[r].x);
       }
+      const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll
       for (int r = 0; r < kCluster; ++r) {
-        if (y[r].x == -INFINITY) continue;  // no keys: its sums were never written
-        const float f = ptx::ex2_approx(y[r].x - M);
+        if (y[r].y < 0.f) continue;
+        const float f = ptx::ex2_approx(y[r].x - base);
         L = fmaf(f, y[r].y, L);
         sum = fmaf(f, x[r], sum);
       }
@@ -714,9 +717,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, L = 0.f;
   auto add = [&](float m, float l, const float4& y) {
-    const float top = fmaxf(M, m);
-    if (top == -INFINITY) return;
-    const float f = ptx::ex2_approx(M - top), w = ptx::ex2_approx(m - top);
+    // a part with the maximum -inf weighs nothing, but NaN sums (all its scores were NaN) have to show
+    const float top = fmaxf(M, m), base = top == -INFINITY ? 0.f : top;
+    const float f = ptx::ex2_approx(M - base), w = ptx::ex2_approx(m - base);
     M = top;
     L = fmaf(w, l, L * f);
     acc.x = fmaf(w, y.x, acc.x * f);

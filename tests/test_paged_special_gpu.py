@@ -1,0 +1,60 @@
+"""The paged attention where scores or values are no ordinary numbers: what the definition makes of them, whatever
+launch, grid and split of the keys a call gets."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_oracle as po
+from diffusion_transformer_long_gb300 import ditattn as da
+from test_paged_gpu import check_attn, make_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=[0, 1000, 1, 3, 50], ids=lambda g: f"grid {g}")
+def grid(request):
+    """The launch that the sizes choose (0), the one for many items, and that on capped grids."""
+    da.set_grid_limit(request.param)
+    yield request.param
+    da.set_grid_limit(0)
+
+
+def check_with_nan(o, lse, ref):
+    """NaN where the 64-bit form has it (whole rows: a score is NaN), its values elsewhere."""
+    o_ref, lse_ref, (mag, pv) = ref
+    none = np.isnan(lse_ref)
+    assert np.array_equal(np.isnan(lse.cpu().numpy()), none)
+    assert o.isnan().cpu().numpy()[none].all() and not o.isnan().cpu().numpy()[~none].any()
+    o, lse = o.masked_fill(torch.as_tensor(none, device=o.device)[..., None], 0), lse.nan_to_num(0, math.inf, -math.inf)
+    for x in (o_ref, lse_ref, mag, pv):
+        x[none] = 0
+    check_attn(o, lse, ref)
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("what", ["query", "key", "page", "first part", "last part", "all keys"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,P", [([1, 40, 0], 4, 2, 64, 16), ([4000, 300, 17], 6, 2, 128, 16),
+                                             ([9000], 3, 1, 64, 64), ([700, 90], 24, 1, 128, 32)])
+def test_nan_scores_show(lens, Hq, Hkv, D, P, what, selected, grid):
+    q, k, v, table, sl = make_case(lens, Hq, Hkv, D, P, seed=len(lens))
+    n = -(-lens[0] // P)  # request 0's pages
+    pages = table[0, :n].long()
+    if what == "query":
+        q[0, 1, 3] = float("nan")
+        q[-1, Hq - 1, D - 1] = float("nan")  # (in a request without keys: not seen)
+    elif what == "key":
+        k[pages[n // 2], 0, 0, 5] = float("nan")
+    else:
+        part = dict(page=pages[n // 2:n // 2 + 1])
+        part.update({"first part": pages[:(n + 2) // 3], "last part": pages[n // 3:], "all keys": pages})
+        k[part[what], Hkv - 1, :, 7] = float("nan")
+    sel = None
+    if selected:
+        m = table.shape[1]
+        sel = torch.arange(m, device=q.device, dtype=torch.int32).expand(len(lens), Hkv, m).contiguous()
+    with np.errstate(invalid="ignore"):
+        ref = po.attend(q, k, v, table, sl, D ** -0.5, selected=sel)
+    assert np.isnan(ref[1][0]).any()
+    check_with_nan(*da.paged_attn_fwd(q, k, v, table, sl, selected=sel), ref)
