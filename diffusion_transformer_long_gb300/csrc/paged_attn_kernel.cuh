@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kThreadsPaged, 2) paged_attn_kernel(const __gr
           } else if (!whole) {
             *reinterpret_cast<float4*>(p.part_o + part * D + d0 + i) = x;
           } else if (h < p.group) {
+            if (L == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // (sums of weights 0 and values that are not finite)
             OT* dst = static_cast<OT*>(p.out) + row * D + d0 + i;
             if constexpr (sizeof(OT) == 4)
               *reinterpret_cast<float4*>(dst) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
@@ -749,6 +750,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   if (slice != 0) return;
   for (int s = 1; s < min(n, kSlices); ++s) add(ml_sm[s].x, ml_sm[s].y, acc_sm[s][quad]);
   const float inv = L == 0.f ? 0.f : 1.f / L;
+  if (L == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);  // (sums of weights 0 and values that are not finite)
   const long long row = static_cast<long long>(note.x) * p.h_q + hk * p.group + h;
   OT* dst = static_cast<OT*>(p.out) + row * D + quad * 4;
   if constexpr (sizeof(OT) == 4)

@@ -375,8 +375,9 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
  * request b, with key/value head h / (H_q / H_kv),
  *   s_j = scale * q_bh . k_j;  out_bh = sum_j softmax_j(s_j) v_j;  lse_bh = ln sum_j exp(s_j)
  * over the seq_lens[b] first tokens (the new token's own key among them, once written).
- * A request without keys, or without one that scores above -inf, gets out = 0, lse = -inf.  The
- * keys' length is split over the GPU
+ * A request without keys, or without one that scores above -inf, gets out = 0, lse = -inf.  A NaN
+ * score makes its row NaN; a value that is not finite makes its channel of every other row that sees
+ * it infinite or NaN (a weight of 0 does not hide it).  The keys' length is split over the GPU
  * and the parts are joined exactly (the dit_attn_lse_merge combination), in an order that
  * the lengths alone fix: equal calls give equal bits.
  *   q           : device bf16 [B, H_q, D] view (s.b, s.h; s.n is not used); NULL strides:

@@ -58,3 +58,32 @@ def test_nan_scores_show(lens, Hq, Hkv, D, P, what, selected, grid):
         ref = po.attend(q, k, v, table, sl, D ** -0.5, selected=sel)
     assert np.isnan(ref[1][0]).any()
     check_with_nan(*da.paged_attn_fwd(q, k, v, table, sl, selected=sel), ref)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,P", [([40, 1], 4, 2, 64, 16), ([4000, 300], 6, 2, 128, 16), ([9000], 3, 1, 64, 64)])
+def test_values_behind_scores_of_minus_infinity(lens, Hq, Hkv, D, P, bad, grid):
+    """A request none of whose keys scores above -inf has no output, whatever its values hold; where another key
+    counts, 0 times such a value shows in its channel."""
+    q, k, v, table, sl = make_case(lens, Hq, Hkv, D, P, seed=3)
+    q[:, :, 0] = 1.0
+    n = -(-lens[0] // P)
+    pages = table[0, :n].long()
+    k[pages, :, :, 0] = -float("inf")
+    v[pages, 0, :, 5] = bad
+    o, lse = da.paged_attn_fwd(q, k, v, table, sl)
+    cut = table.clone()
+    cut[0] = -1
+    check_attn(o, lse, po.attend(q, k.nan_to_num(neginf=0), v.nan_to_num(0, 0, 0), cut, sl, D ** -0.5))
+    assert (o[0] == 0).all() and (lse[0] == -math.inf).all()
+    # one page of keys that count, the last
+    k[pages[-1], :, :, 0] = 0
+    v[pages[-1], 0, :, 5] = 0
+    cut[0, n - 1] = table[0, n - 1]
+    o, lse = da.paged_attn_fwd(q, k, v, table, sl)
+    if n > 1:
+        assert o[0, :Hq // Hkv, 5].isnan().all()
+        o[0, :Hq // Hkv, 5] = 0
+    kept = v.nan_to_num(0, 0, 0)
+    kept[pages, 0, :, 5] = 0
+    check_attn(o, lse, po.attend(q, k.nan_to_num(neginf=0), kept, cut, sl, D ** -0.5))
