@@ -218,14 +218,26 @@ __device__ __forceinline__ int block_below(int x, int* sm, int& all) {
   return up - x + (warp > 0 ? before : 0);
 }
 
+// Sum * 2^(e - 54), |sum| < 2^62, rounded to fp64 and as an integer of the same order, by integer
+// arithmetic (an fp64 instruction costs a block 16 clocks a warp).
+__device__ __forceinline__ unsigned long long key_of(long long sum, int e) {
+  if (sum == 0) return 1ull << 63;
+  unsigned long long m = static_cast<unsigned long long>(sum < 0 ? -sum : sum);
+  const int top = 63 - __clzll(m), down = top - 52;
+  if (down > 0) m = (m + (1ull << (down - 1)) - 1 + (m >> down & 1)) >> down;  // to nearest, ties to even
+  else m <<= -down;
+  const unsigned long long bits = (static_cast<unsigned long long>(1023 + top + e - 54) << 52) + (m - (1ull << 52));
+  return sum < 0 ? ~(bits | 1ull << 63) : bits | 1ull << 63;
+}
+
 // The 64-bit score of table column i, over heads h_first .. h_end - 1 of the group, as an integer of
-// the same order, by one warp: a lane takes two channels in every 64.  Sums are 64-bit integers in
-// units of 1 / unit (a power of two for which sum |q| |k| of every page stays below 2^62): each
-// product, exact in 32 bits, is rounded once, to 2^-61 of the largest page's sum or finer, so that the
-// sum is exact but for that, in any order, and far cheaper than in fp64, of which this GPU does two
-// operations a clock and SM.
-// unit = 0 (some score is not finite in 32 bits, or all are near its underflow): fp64 after all.
-__device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, float unit, int h_first, int h_end) {
+// the same order, by one warp: a lane takes two channels in every 64.  A head's sum is of 64-bit
+// integers in units of 2^(e - 54), 2^e the power of two in its own largest term (the pages' scales may be far apart):
+// each of the up to 128 terms, products exact in 32 bits, is rounded once, to 2^-55 of the largest, so that the
+// sum is as good as one in fp64, in any order, and far cheaper: this GPU does two fp64 operations a clock
+// and SM.  A term that is not finite in 32 bits, or all of them below 2^-72 (near the underflow
+// of the products): fp64 after all.
+__device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, int h_first, int h_end) {
   const int lane = threadIdx.x & 31;
   const int page = a.table[b * a.table_stride + i];
   if (page < 0 || page >= a.n_pages) return 0;
@@ -237,38 +249,45 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + static_cast<long long>(g) * (a.h_q / a.h_kv) * a.q_h;
   const uint32_t* qh = reinterpret_cast<const uint32_t*>(q) + lane;
   const long long q_step = a.q_h / 2;
-  if (unit > 0.f) {
-    auto term = [&](float x, float l, float h) { return __float2ll_rn(fmaxf(x * l, x * h) * unit); };
-    long long best = static_cast<long long>(1ull << 63);  // below every sum
-#pragma unroll 4
-    for (int h = h_first; h < h_end; ++h) {
-      const uint32_t q0 = qh[h * q_step], q1 = parts > 1 ? qh[h * q_step + 32] : 0;
-      long long s = term(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
-                    term(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
-                    term(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +
-                    term(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      best = max(best, s);
-    }
-    return static_cast<unsigned long long>(best) ^ 1ull << 63;
-  }
   auto larger = [](float x, float l, float h) {  // NaN in either product is NaN
     const double u = static_cast<double>(x) * l, v = static_cast<double>(x) * h;
     return u != u ? u : v != v ? v : fmax(u, v);
   };
-  double best = -INFINITY;
+  unsigned long long best = 0;  // below every score
+#pragma unroll 4
   for (int h = h_first; h < h_end; ++h) {
     const uint32_t q0 = qh[h * q_step], q1 = parts > 1 ? qh[h * q_step + 32] : 0;
-    double s = larger(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
-               larger(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
-               larger(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +
-               larger(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1));
+    float odd = 0.f;  // NaN where a product is not finite
+    auto term = [&](float x, float l, float h) {
+      const float u = x * l, v = x * h;
+      odd += (u - u) + (v - v);
+      return fmaxf(u, v);
+    };
+    const float t[4] = {term(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)),
+                        term(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)),
+                        term(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)),
+                        term(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1))};
+    const float most = fmaxf(fmaxf(fabsf(t[0]), fabsf(t[1])), fmaxf(fabsf(t[2]), fabsf(t[3])));
+    const int e = static_cast<int>(__reduce_max_sync(~0u, odd == 0.f ? __float_as_uint(most) : 0x7f800000u) >> 23) - 127;
+    if (e >= -72 && e < 128) {
+      const float unit = __uint_as_float(static_cast<uint32_t>(54 - e + 127) << 23);
+      long long s = 0;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    best = fmax(best, s != s ? static_cast<double>(INFINITY) : s);
+      for (int k = 0; k < 4; ++k) s += __float2ll_rn(t[k] * unit);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      best = max(best, key_of(s, e));
+    } else {
+      double s = larger(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
+                 larger(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
+                 larger(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +
+                 larger(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+      best = max(best, key_of(s != s ? static_cast<double>(INFINITY) : s));
+    }
   }
-  return key_of(best);
+  return best;
 }
 
 struct PickSmem {
@@ -332,9 +351,6 @@ __device__ __forceinline__ void pick_pages(const PickParams& p, PickSmem& sm, in
   // range), rounded up; in 32 bits, since every fp64 instruction costs a block 16 clocks a warp
   const float wide = __fmul_ru(2.002f, __fmaf_ru(kErr, mag, 0x1p-110f));
   const bool unknown = hi >= kInfKey || !(mag < INFINITY);
-  // at least 2^60 units in mag, and every page's magnitudes (mag may be short by kErr of itself)
-  // below 2^62; sums from 2^-40 up keep the products that count far from 2^-126
-  const float unit = !unknown && mag >= 0x1p-40f ? scalbnf(1.f, 60 - ilogbf(mag)) : 0.f;
   uint32_t from = 0, to = ~0u;  // pages whose key is above `to` are in, below `from` out
   int above = 0;                // pages above the range [lo, hi]
   int sure;                     // pages above `to`
@@ -397,7 +413,7 @@ __device__ __forceinline__ void pick_pages(const PickParams& p, PickSmem& sm, in
       __syncthreads();
       for (long long x = warp; x < static_cast<long long>(mids) * group; x += kPickWarps) {
         const int i = static_cast<int>(x / group), h = static_cast<int>(x - static_cast<long long>(i) * group);
-        const unsigned long long k = exact_key(a, b, g, between[i], unit, h, h + 1);
+        const unsigned long long k = exact_key(a, b, g, between[i], h, h + 1);
         if (lane == 0) atomicMax(ranked + i, k);
       }
       __syncthreads();
@@ -420,7 +436,7 @@ __device__ __forceinline__ void pick_pages(const PickParams& p, PickSmem& sm, in
                                       : p.exact + static_cast<long long>(bg) * a.max_pages;
     for (int i = warp; i < others; i += kPickWarps) {
       if (keys[i] - from > to - from) continue;
-      const unsigned long long k = exact_key(a, b, g, i, unit, 0, a.h_q / a.h_kv);
+      const unsigned long long k = exact_key(a, b, g, i, 0, a.h_q / a.h_kv);
       if (lane == 0) exact[i] = k;
     }
     __syncthreads();

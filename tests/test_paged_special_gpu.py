@@ -1,5 +1,5 @@
-"""The paged attention where scores or values are no ordinary numbers: what the definition makes of them, whatever
-launch, grid and split of the keys a call gets."""
+"""The paged attention and selection where scores or values are no ordinary numbers, or of very different sizes: what
+the definition makes of them, whatever launch, grid and split of the keys a call gets."""
 import math
 
 import numpy as np
@@ -8,7 +8,7 @@ import torch
 
 import paged_oracle as po
 from diffusion_transformer_long_gb300 import ditattn as da
-from test_paged_gpu import check_attn, make_case
+from test_paged_gpu import check_attn, dev, launch, make_case, rand, tables, widened  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,38 @@ def test_values_behind_scores_of_minus_infinity(lens, Hq, Hkv, D, P, bad, grid):
     kept = v.nan_to_num(0, 0, 0)
     kept[pages, 0, :, 5] = 0
     check_attn(o, lse, po.attend(q, k.nan_to_num(neginf=0), kept, cut, sl, D ** -0.5))
+
+
+# ------------------------------------------------------------------ selection
+
+
+@pytest.mark.parametrize("n", [40, 700, 2047, 9001])
+@pytest.mark.parametrize("kind", ["both", "positive", "negative", "newest", "unused", "every page"])
+@pytest.mark.parametrize("e", [20, 40, 70, 100])
+def test_select_beside_pages_of_another_scale(n, kind, e, launch):
+    """One page far larger than the others (or each page of its own size): the others keep their order."""
+    P, Hq, Hkv, D = 16, 3, 1, 64 if n % 2 else 128
+    lens = [n * P, n * P - 5]
+    table, n_pages = tables(lens, P, seed=n)
+    q = rand(2, Hq, D, seed=1)
+    a, b = rand(n_pages, Hkv, 1, D, seed=2), rand(n_pages, Hkv, 1, D, seed=3)
+    summary = torch.cat((torch.minimum(a, b), torch.maximum(a, b)), 2)
+    at = table[0, n - 1 if kind == "newest" else n // 3]
+    if kind in ("both", "newest"):
+        summary[at] *= 2.0 ** e
+    elif kind == "positive":
+        summary[at] = (q[0, 0] * 2.0 ** e).expand(Hkv, 2, D)
+    elif kind == "negative":
+        summary[at] = (q[0, 0] * -2.0 ** e).expand(Hkv, 2, D)
+    elif kind == "unused":  # minima that no product of a positive query takes
+        q = q.abs()
+        summary[at, :, 0] = -2.0 ** e
+    else:
+        g = torch.Generator(device="cuda").manual_seed(5)
+        x = torch.randint(-e // 2, e // 2 + 1, (n_pages, 1, 1, 1), generator=g, device="cuda")
+        summary *= torch.exp2(x.float()).to(torch.bfloat16)
+    t = dev(table)
+    t, sl = (widened(t, launch) if n < 2100 else t), dev(lens)
+    for top_k in (2, n // 3, n - 2):
+        got = da.paged_select(q, summary, t, sl, P, top_k)
+        assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
