@@ -240,7 +240,7 @@ __device__ __forceinline__ unsigned long long key_of(long long sum, int e) {
 __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, int h_first, int h_end) {
   const int lane = threadIdx.x & 31;
   const int page = a.table[b * a.table_stride + i];
-  if (page < 0 || page >= a.n_pages) return 0;
+  if (page < 0 || page >= a.n_pages) return key_of(-static_cast<double>(INFINITY));  // as a page that scores -inf
   const uint32_t* lo = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.summary) +
                                                          (static_cast<long long>(page) * a.h_kv + g) * 2 * a.d) + lane;
   const uint32_t* hi = lo + a.d / 2;

@@ -122,3 +122,20 @@ def test_select_beside_pages_of_another_scale(n, kind, e, launch):
     for top_k in (2, n // 3, n - 2):
         got = da.paged_select(q, summary, t, sl, P, top_k)
         assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
+
+
+@pytest.mark.parametrize("n", [100, 1500, 9001])
+def test_select_pages_without_keys_tie_with_scores_of_minus_infinity(n, launch):
+    """Both score -inf: the lower index first, whichever it is."""
+    P, Hq, Hkv, D = 16, 2, 1, 64
+    table, n_pages = tables([n * P], P, seed=n, extra_cols=0)
+    q = rand(1, Hq, D, seed=1).abs()
+    summary = rand(n_pages, Hkv, 1, D, seed=2).repeat(1, 1, 2, 1)
+    kind = np.random.default_rng(3).integers(0, 4, n)
+    summary[dev(table[0, :n][kind == 1], torch.int64), :, :, 0] = -float("inf")
+    table[0, :n][kind == 2] = -1
+    t = dev(table)
+    t, sl = (widened(t, launch) if n < 2100 else t), dev([n * P])
+    for top_k in (n // 4, n // 2, n * 5 // 8, n * 3 // 4, n - 1):
+        got = da.paged_select(q, summary, t, sl, P, top_k)
+        assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
