@@ -17,6 +17,7 @@ namespace {
 using namespace ditattn::api;
 
 constexpr long long kMaxSpan = 1LL << 60;  // elements a view may reach, far inside 64-bit bytes
+constexpr int kMaxTokens = 1 << 30;        // of a step: token indexes and what is added to them stay in 32 bits
 
 // Sizes of the page pool and of a request's table row.
 dit_status check_pages(int page_size, int n_pages, int max_pages) {
@@ -95,7 +96,7 @@ dit_status dit_paged_plan(const int* new_lens, const int* seq_lens, int* block_t
                           int* seq_lens_out, int* n_free_out, int* cu_new, long long* slots, int B,
                           int max_pages, int page_size, int n_pages, int pool_capacity,
                           int max_tokens, dit_stream stream) {
-  if (B < 1 || max_tokens < 1 || max_tokens > (1 << 30) || pool_capacity < 0)
+  if (B < 1 || max_tokens < 1 || max_tokens > kMaxTokens || pool_capacity < 0)
     return DIT_ERR_INVALID_ARG;
   const dit_status s = check_pages(page_size, n_pages, max_pages);
   if (s != DIT_OK) return s;
@@ -136,6 +137,7 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
                               int page_size, int n_pages, dit_stream stream) {
   dit_status s = check_dims(1, H, T, D);
   if (s != DIT_OK) return s;
+  if (T > kMaxTokens) return DIT_ERR_INVALID_ARG;
   s = check_pages(page_size, n_pages, 1);
   if (s != DIT_OK) return s;
   auto rows = [&](const dit_strides* p) {

@@ -359,6 +359,7 @@ dit_status dit_paged_plan(const int* new_lens, const int* seq_lens, int* block_t
  *                   and channel the minimum (index 0) and maximum (1) of its keys.  A page
  *                   whose row 0 is written starts anew from the rows of this call; any
  *                   other touched page is widened by them.  NaN keys make it NaN.
+ *   T             : 1 .. 2^30
  * Slots are distinct, and with a summary the tokens of one page follow each other in
  * ascending slots, as dit_paged_plan lays them out.  (Repeated slots or scattered rows of
  * a page leave either row, and the page's summary, unspecified; nothing else.)

@@ -78,6 +78,14 @@ def test_write_validation(lib, kw, status):
     assert write(lib, **kw) == status
 
 
+@pytest.mark.parametrize("T", [(1 << 30) + 1, (1 << 31) - 1])
+def test_write_token_count_validation(lib, T):
+    """Past 2^30 tokens their indexes would pass 32 bits inside a launch."""
+    few = dict(ks=S(64, 64, 8), vs=S(64, 64, 8), H=1, summary=None)  # rows that overlap: they fit a GPU's memory
+    assert write(lib, T=T, **few) == INVALID
+    assert write(lib, T=1 << 30, **few) != INVALID  # (no GPU here: the launch fails)
+
+
 NEED = 1 << 30
 
 
