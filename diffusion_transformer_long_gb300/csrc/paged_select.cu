@@ -577,8 +577,10 @@ cudaError_t launch_paged_select(const SelectLaunch& a, cudaStream_t st) {
   const size_t needed = (static_cast<size_t>(p.chunks) + kScoreWarps - 1) / kScoreWarps;
   const dim3 grid(static_cast<unsigned>(std::min(needed, most)), rows_y,
                   static_cast<unsigned>((rows + rows_y - 1) / rows_y));
-  const cudaError_t e = a.d == 64 ? launch_after(paged_score_kernel<64>, grid, dim3(kScoreWarps * 32), 0, st, p)
-                                  : launch_after(paged_score_kernel<128>, grid, dim3(kScoreWarps * 32), 0, st, p);
+  cudaError_t e = cudaSuccess;
+  if (a.top_k > 1)  // (else the newest page alone is listed, whatever the scores)
+    e = a.d == 64 ? launch_after(paged_score_kernel<64>, grid, dim3(kScoreWarps * 32), 0, st, p)
+                  : launch_after(paged_score_kernel<128>, grid, dim3(kScoreWarps * 32), 0, st, p);
   return e != cudaSuccess ? e : launch_after(paged_pick_kernel, dim3(static_cast<unsigned>(rows)), dim3(kPickThreads), 0, st, p);
 }
 

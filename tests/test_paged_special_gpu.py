@@ -139,3 +139,16 @@ def test_select_pages_without_keys_tie_with_scores_of_minus_infinity(n, launch):
     for top_k in (n // 4, n // 2, n * 5 // 8, n * 3 // 4, n - 1):
         got = da.paged_select(q, summary, t, sl, P, top_k)
         assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
+
+
+def test_select_of_the_newest_page_scores_nothing():
+    """top_k = 1: nothing goes through the workspace."""
+    lens, P, Hq, Hkv, D = [40000, 0, 17], 16, 4, 2, 64
+    table, n_pages = tables(lens, P)
+    q, summary = rand(3, Hq, D, seed=1), rand(n_pages, Hkv, 2, D, seed=2)
+    need = da.lib().dit_paged_select_workspace_bytes(3, Hkv, table.shape[1])
+    ws = torch.full((need,), 0x5A, dtype=torch.uint8, device="cuda")
+    assert need > 0
+    got = da.paged_select(q, summary, dev(table), dev(lens), P, 1, workspace=ws)
+    assert got.flatten().tolist() == [2499] * Hkv + [-1] * Hkv + [1] * Hkv
+    assert (ws == 0x5A).all()
