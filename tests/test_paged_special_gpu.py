@@ -34,7 +34,7 @@ def check_with_nan(o, lse, ref):
 
 
 @pytest.mark.parametrize("selected", [False, True])
-@pytest.mark.parametrize("what", ["query", "key", "page", "first part", "last part", "all keys"])
+@pytest.mark.parametrize("what", ["query", "key", "page", "first part", "last part", "all keys", "infinite"])
 @pytest.mark.parametrize("lens,Hq,Hkv,D,P", [([1, 40, 0], 4, 2, 64, 16), ([4000, 300, 17], 6, 2, 128, 16),
                                              ([9000], 3, 1, 64, 64), ([700, 90], 24, 1, 128, 32)])
 def test_nan_scores_show(lens, Hq, Hkv, D, P, what, selected, grid):
@@ -46,6 +46,9 @@ def test_nan_scores_show(lens, Hq, Hkv, D, P, what, selected, grid):
         q[-1, Hq - 1, D - 1] = float("nan")  # (in a request without keys: not seen)
     elif what == "key":
         k[pages[n // 2], 0, 0, 5] = float("nan")
+    elif what == "infinite":  # a score of +inf: inf - inf
+        q[0, :, 5] = 1.0
+        k[pages[n // 2], 0, 0, 5] = float("inf")
     else:
         part = dict(page=pages[n // 2:n // 2 + 1])
         part.update({"first part": pages[:(n + 2) // 3], "last part": pages[n // 3:], "all keys": pages})
@@ -87,6 +90,18 @@ def test_values_behind_scores_of_minus_infinity(lens, Hq, Hkv, D, P, bad, grid):
     kept = v.nan_to_num(0, 0, 0)
     kept[pages, 0, :, 5] = 0
     check_attn(o, lse, po.attend(q, k.nan_to_num(neginf=0), kept, cut, sl, D ** -0.5))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,P", [([4000, 300, 17], 6, 2, 128, 16), ([9000], 3, 1, 64, 64),
+                                             ([700, 90], 24, 1, 128, 32), ([64], 2, 2, 64, 16), ([1500], 40, 1, 128, 16)])
+def test_float_output_keeps_all_parts_of_the_weights(lens, Hq, Hkv, D, P, launch):
+    """fp32 output, flat scores: the 2-norm of the error is that of 32-bit weights.  Their relative errors, of random sign
+    from key to key, are the exponential's (at most 2^-22) and a few roundings (2^-24 each): below 8e-7 together.
+    Weights in two bf16 parts would be off by up to 2^-18 evenly, 2^-18 / sqrt(3) = 2.2e-6 in the mean."""
+    q, k, v, table, sl = make_case(lens, Hq, Hkv, D, P, seed=1, q_scale=0.25)
+    o = da.paged_attn_fwd(q, k, v, table, sl)[0].double().cpu().numpy()
+    want = po.attend(q, k, v, table, sl, D ** -0.5)[0]
+    assert np.linalg.norm(o - want) <= 8e-7 * np.linalg.norm(want)
 
 
 # ------------------------------------------------------------------ selection
