@@ -288,12 +288,13 @@ dit_status dit_layout_copy(const void* src, const dit_strides* src_strides, void
 
 /* ---------------------------------------------------------------------------
  * Paged key/value caches: requests of different and growing lengths in pages of
- * one pool, for generation with cached keys (text encoders and captioners of the
- * pages' pipelines, autoregressive video blocks).  One step of a batch is
+ * one pool, for generation with cached keys, a token at a time (text encoders and
+ * captioners of the pages' pipelines).  One step of a batch is
  *   dit_paged_plan      pages and slots for the step's new tokens, from lengths
  *   dit_paged_kv_write  their keys and values into the slots, page summaries
  *   dit_paged_select    (sparse attention only) the best pages for each query
  *   dit_paged_attn_fwd  one query token of each request against its pages
+ * A prompt can be planned and written, but not attended from: its causal attention is not here.
  * All lengths, tables and slots live on the device, so that a step can be captured
  * into a graph once and replayed as the lengths grow.
  *
@@ -361,8 +362,9 @@ dit_status dit_paged_plan(const int* new_lens, const int* seq_lens, int* block_t
  *                   other touched page is widened by them.  NaN keys make it NaN.
  *   T             : 1 .. 2^30
  * Slots are distinct, and with a summary the tokens of one page follow each other in
- * ascending slots, as dit_paged_plan lays them out.  (Repeated slots or scattered rows of
- * a page leave either row, and the page's summary, unspecified; nothing else.)
+ * ascending slots, as dit_paged_plan lays them out.  (A slot that is repeated is
+ * left with any mix of its tokens' 16-byte pieces, keys and values apart; it, and scattered rows of a page, leave
+ * the page's summary unspecified.  Nothing else is touched.)
  */
 dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_strides,
                               const void* v_new, const dit_strides* v_new_strides,
@@ -376,11 +378,13 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
  * request b, with key/value head h / (H_q / H_kv),
  *   s_j = scale * q_bh . k_j;  out_bh = sum_j softmax_j(s_j) v_j;  lse_bh = ln sum_j exp(s_j)
  * over the seq_lens[b] first tokens (the new token's own key among them, once written).
- * A request without keys, or without one that scores above -inf, gets out = 0, lse = -inf.  A NaN
- * score makes its row NaN; a value that is not finite makes its channel of every other row that sees
- * it infinite or NaN (a weight of 0 does not hide it).  The keys' length is split over the GPU
- * and the parts are joined exactly (the dit_attn_lse_merge combination), in an order that
- * the lengths alone fix: equal calls give equal bits.
+ * A request without keys, or without one that scores above -inf, gets out = 0, lse = -inf.  A score
+ * that is NaN or +inf in 32 bits makes its row NaN; a value that is not finite makes its channel of every
+ * other row that sees it infinite or NaN (a weight of 0 does not hide it).  Sums of weights, up to 2^8 each,
+ * times values are held in fp32 before the division: values past 2^120 / seq_lens[b] may overflow
+ * there.  The keys' length is split over the GPU and the parts are joined exactly (the
+ * dit_attn_lse_merge combination), in an order that the sizes and lengths alone fix: equal calls give
+ * equal bits.
  *   q           : device bf16 [B, H_q, D] view (s.b, s.h; s.n is not used); NULL strides:
  *                 contiguous
  *   k_cache, v_cache, block_table, seq_lens : as above (read).  Rows past a request's
@@ -406,7 +410,7 @@ dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const
                               dit_stream stream);
 
 /* Workspace bytes of a dit_paged_attn_fwd call with these sizes on the current device: 0 for
- * few requests of few keys, which need none, and when a size is not positive. */
+ * few requests with room for few keys (pages * page_size), which need none, and when a size is not positive. */
 size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D, int page_size, int pages);
 
 /*
@@ -433,7 +437,7 @@ dit_status dit_paged_select(const void* q, const dit_strides* q_strides, const v
                             size_t workspace_bytes, dit_stream stream);
 
 /* Workspace bytes of a dit_paged_select call with these sizes on the current device: 0 for few
- * requests of few pages, which need none, and when a size is not positive. */
+ * requests with room for few pages, which need none, and when a size is not positive. */
 size_t dit_paged_select_workspace_bytes(int B, int H_kv, int max_pages);
 
 /*
