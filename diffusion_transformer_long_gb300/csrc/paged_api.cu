@@ -221,7 +221,8 @@ dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const
       !aligned(selected, 4) || !out || !aligned(out, 16) || !aligned(lse, 4))
     return DIT_ERR_INVALID_ARG;
   if (selected && (n_selected < 1 || n_selected > max_pages)) return DIT_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale) || !valid_dtype(out_dtype)) return DIT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f) || !valid_dtype(out_dtype))  // (used in base 2)
+    return DIT_ERR_INVALID_ARG;
   const size_t need = dit_paged_attn_workspace_bytes(B, H_q, H_kv, D, page_size, selected ? n_selected : max_pages);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return DIT_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(B) * H_q;

@@ -397,6 +397,7 @@ dit_status dit_paged_kv_write(const void* k_new, const dit_strides* k_new_stride
  *   out         : device [B, H_q, D] of out_dtype, contiguous, 16-byte aligned (written)
  *   lse         : device fp32 [B, H_q] (written), or NULL
  *   H_q         : a multiple of H_kv
+ *   scale       : > 0, and finite times log2 e in 32 bits
  *   workspace   : at least dit_paged_attn_workspace_bytes(B, H_q, H_kv, D, page_size, pages) bytes,
  *                 pages = n_selected with `selected`, else max_pages; NULL where that is 0
  */

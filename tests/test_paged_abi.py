@@ -112,6 +112,12 @@ def test_attn_validation(lib, kw, status):
     assert attn(lib, **kw) == status
 
 
+def test_attn_scale_validation(lib):
+    """Scores are held in base 2: a scale that is finite only without that factor would make them all infinite."""
+    assert attn(lib, scale=2.4e38) == INVALID and attn(lib, scale=math.inf) == INVALID
+    assert attn(lib, scale=2.3e38) != INVALID  # (no GPU here: the launch fails)
+
+
 def select(lib, **kw):
     a = dict(q=A[0], qs=None, summary=A[1], table=A[2], stride=10, lens=A[3], sel=A[4], B=3, Hq=8, Hkv=2, D=128, P=16,
              n_pages=9, max_pages=10, top_k=4, ws=A[5], ws_bytes=NEED)
