@@ -3,7 +3,7 @@
 // over the query heads h of a key/value head's group; listed are the newest page and the
 // top_k - 1 others with the highest scores, ties to the lower index, by the scores in 64 bits.
 //
-// Scoring.  max(q lo, q hi) = max(q, 0) hi + min(q, 0) lo, so the scores of 16 pages against 8
+// Scoring.  max(q lo, q hi) = max(q, 0) hi + min(q, 0) lo for lo <= hi, so the scores of 16 pages against 8
 // heads are a matrix product over 2 D channels, on mma.sync straight from the summaries in
 // global memory: a lane's 16-byte loads hold its operands once the channels are renumbered (the
 // order of a sum's terms is free).  4 D bytes per page and head: bound by HBM, or by latency.
@@ -87,6 +87,21 @@ __device__ __forceinline__ uint32_t half_of(uint32_t w, bool positive) {
   return w;
 }
 
+__device__ __forceinline__ void sort_pair(uint32_t& lo, uint32_t& hi) {
+  __nv_bfloat162 x, y;
+  memcpy(&x, &lo, 4);
+  memcpy(&y, &hi, 4);
+  const __nv_bfloat162 least = __hmin2_nan(x, y), most = __hmax2_nan(x, y);
+  memcpy(&lo, &least, 4);
+  memcpy(&hi, &most, 4);
+}
+__device__ __forceinline__ void sort_pair(uint4& lo, uint4& hi) {
+  sort_pair(lo.x, hi.x);
+  sort_pair(lo.y, hi.y);
+  sort_pair(lo.z, hi.z);
+  sort_pair(lo.w, hi.w);
+}
+
 __device__ __forceinline__ int pages_now(const SelectLaunch& a, int b) {
   return pages_of(min(max(0, a.seq_lens[b]), a.max_pages * a.page_size), a.page_size);
 }
@@ -118,6 +133,12 @@ __device__ __forceinline__ float score_pages(const SelectLaunch& a, int b, int g
   for (int i = 0; i < kLoads; ++i) {
     x0[i] = p0 >= 0 ? s0[4 * i] : none;
     x1[i] = p1 >= 0 ? s1[4 * i] : none;
+  }
+  // the smaller value first, whichever half holds it (NaN: both), so that the product below is max(q lo, q hi)
+#pragma unroll
+  for (int i = 0; i < kLoads / 2; ++i) {
+    sort_pair(x0[i], x0[i + kLoads / 2]);
+    sort_pair(x1[i], x1[i + kLoads / 2]);
   }
   const int group = a.h_q / a.h_kv;
   float best0 = -INFINITY, best1 = -INFINITY, mag = 0.f;

@@ -156,6 +156,23 @@ def test_select_pages_without_keys_tie_with_scores_of_minus_infinity(n, launch):
         assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
 
 
+@pytest.mark.parametrize("kind", ["some", "empty"])
+@pytest.mark.parametrize("n", [100, 1500, 4000])
+def test_select_takes_either_order_of_the_extremes(n, kind, launch):
+    """Summaries of which some have the larger value first, or are those of no key at all (+inf, -inf)."""
+    P, Hq, Hkv, D = 16, 6, 2, 128
+    table, n_pages = tables([n * P, n * P - 5], P, seed=n)
+    q, summary = rand(2, Hq, D, seed=1), rand(n_pages, Hkv, 2, D, seed=2)
+    if kind == "empty":
+        some = torch.as_tensor(np.random.default_rng(3).random(n_pages) < 0.1)
+        summary[some, :, 0], summary[some, :, 1] = float("inf"), -float("inf")
+    t = dev(table)
+    t, sl = (widened(t, launch) if n < 2100 else t), dev([n * P, n * P - 5])
+    for top_k in (2, n // 20, n // 3):
+        got = da.paged_select(q, summary, t, sl, P, top_k)
+        assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
+
+
 def test_select_of_the_newest_page_scores_nothing():
     """top_k = 1: nothing goes through the workspace."""
     lens, P, Hq, Hkv, D = [40000, 0, 17], 16, 4, 2, 64
