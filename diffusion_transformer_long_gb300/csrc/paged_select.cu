@@ -239,16 +239,38 @@ __device__ __forceinline__ int block_below(int x, int* sm, int& all) {
   return up - x + (warp > 0 ? before : 0);
 }
 
-// Sum * 2^(e - 54), |sum| < 2^62, rounded to fp64 and as an integer of the same order, by integer
-// arithmetic (an fp64 instruction costs a block 16 clocks a warp).
+// Sum * 2^(e - 54), |sum| < 2^62, rounded to fp64's 53 bits (halves away from zero) and as an integer
+// of the same order as the fp64 numbers, by integer arithmetic: an fp64 instruction costs a block 16 clocks a warp.
 __device__ __forceinline__ unsigned long long key_of(long long sum, int e) {
-  if (sum == 0) return 1ull << 63;
-  unsigned long long m = static_cast<unsigned long long>(sum < 0 ? -sum : sum);
-  const int top = 63 - __clzll(m), down = top - 52;
-  if (down > 0) m = (m + (1ull << (down - 1)) - 1 + (m >> down & 1)) >> down;  // to nearest, ties to even
-  else m <<= -down;
-  const unsigned long long bits = (static_cast<unsigned long long>(1023 + top + e - 54) << 52) + (m - (1ull << 52));
-  return sum < 0 ? ~(bits | 1ull << 63) : bits | 1ull << 63;
+  const unsigned long long sign = static_cast<unsigned long long>(sum >> 63);
+  const unsigned long long m = (static_cast<unsigned long long>(sum) ^ sign) - sign;
+  const int lead = __clzll(m);
+  const unsigned long long top = m << (lead & 63);  // its highest bit is bit 63: what goes over is the exponent's last 1
+  const unsigned long long bits =
+      (static_cast<unsigned long long>(1023 - 54 + 63 - 1 + e - lead) << 52) + (top >> 11) + (top >> 10 & 1);
+  return sum == 0 ? 1ull << 63 : bits ^ sign ^ 1ull << 63;
+}
+
+// The warp's sum of the lanes' four terms, |t| < 2^(e + 1), -72 <= e < 128, each rounded to a whole number of units of
+// 2^(e - 54): in three pieces of 18 bits, whose sums stay in 32.  Adding 1.5 * 2^23 rounds to a whole number (a
+// conversion to 64 bits costs as much as an fp64 instruction).
+__device__ __forceinline__ long long warp_sum(const float (&t)[4], int e) {
+  constexpr float kRound = 12582912.f;
+  const float unit = __uint_as_float(static_cast<uint32_t>(18 - e + 127) << 23);
+  int p[3] = {0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float y = t[k] * unit;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const float z = y + kRound;
+      p[i] += __float_as_int(z) - __float_as_int(kRound);
+      y = (y - (z - kRound)) * 262144.f;  // the rest, exactly
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i) p[i] = __reduce_add_sync(~0u, p[i]);
+  return static_cast<long long>(p[0]) * (1ll << 36) + static_cast<long long>(p[1]) * (1ll << 18) + p[2];
 }
 
 // The 64-bit score of table column i, over heads h_first .. h_end - 1 of the group, as an integer of
@@ -256,7 +278,7 @@ __device__ __forceinline__ unsigned long long key_of(long long sum, int e) {
 // integers in units of 2^(e - 54), 2^e the power of two in its own largest term (the pages' scales may be far apart):
 // each of the up to 128 terms, products exact in 32 bits, is rounded once, to 2^-55 of the largest, so that the
 // sum is as good as one in fp64, in any order, and far cheaper: this GPU does two fp64 operations a clock
-// and SM.  A term that is not finite in 32 bits, or all of them below 2^-72 (near the underflow
+// and SM.  A term that is not finite in 32 bits, or all of them below 2^-72 but not 0 (near the underflow
 // of the products): fp64 after all.
 __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int i, int h_first, int h_end) {
   const int lane = threadIdx.x & 31;
@@ -267,6 +289,8 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
   const uint32_t* hi = lo + a.d / 2;
   const int parts = a.d / 64;
   const uint32_t lo0 = lo[0], hi0 = hi[0], lo1 = parts > 1 ? lo[32] : 0, hi1 = parts > 1 ? hi[32] : 0;
+  const float l[4] = {ptx::bf16lo(lo0), ptx::bf16hi(lo0), ptx::bf16lo(lo1), ptx::bf16hi(lo1)};
+  const float r[4] = {ptx::bf16lo(hi0), ptx::bf16hi(hi0), ptx::bf16lo(hi1), ptx::bf16hi(hi1)};
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + b * a.q_b + static_cast<long long>(g) * (a.h_q / a.h_kv) * a.q_h;
   const uint32_t* qh = reinterpret_cast<const uint32_t*>(q) + lane;
   const long long q_step = a.q_h / 2;
@@ -278,35 +302,35 @@ __device__ unsigned long long exact_key(const SelectLaunch& a, int b, int g, int
 #pragma unroll 4
   for (int h = h_first; h < h_end; ++h) {
     const uint32_t q0 = qh[h * q_step], q1 = parts > 1 ? qh[h * q_step + 32] : 0;
-    float odd = 0.f;  // NaN where a product is not finite
-    auto term = [&](float x, float l, float h) {
-      const float u = x * l, v = x * h;
-      odd += (u - u) + (v - v);
-      return fmaxf(u, v);
-    };
-    const float t[4] = {term(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)),
-                        term(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)),
-                        term(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)),
-                        term(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1))};
-    const float most = fmaxf(fmaxf(fabsf(t[0]), fabsf(t[1])), fmaxf(fabsf(t[2]), fabsf(t[3])));
+    const float x[4] = {ptx::bf16lo(q0), ptx::bf16hi(q0), ptx::bf16lo(q1), ptx::bf16hi(q1)};
+    float t[4], most = 0.f, odd = 0.f;  // odd: NaN where a product is not finite
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float u = x[k] * l[k], v = x[k] * r[k];
+      odd = fmaf(u, 0.f, fmaf(v, 0.f, odd));
+      t[k] = fmaxf(u, v);
+      most = fmaxf(most, fabsf(t[k]));
+    }
     const int e = static_cast<int>(__reduce_max_sync(~0u, odd == 0.f ? __float_as_uint(most) : 0x7f800000u) >> 23) - 127;
     if (e >= -72 && e < 128) {
-      const float unit = __uint_as_float(static_cast<uint32_t>(54 - e + 127) << 23);
-      long long s = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) s += __float2ll_rn(t[k] * unit);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      best = max(best, key_of(s, e));
-    } else {
-      double s = larger(ptx::bf16lo(q0), ptx::bf16lo(lo0), ptx::bf16lo(hi0)) +
-                 larger(ptx::bf16hi(q0), ptx::bf16hi(lo0), ptx::bf16hi(hi0)) +
-                 larger(ptx::bf16lo(q1), ptx::bf16lo(lo1), ptx::bf16lo(hi1)) +
-                 larger(ptx::bf16hi(q1), ptx::bf16hi(lo1), ptx::bf16hi(hi1));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-      best = max(best, key_of(s != s ? static_cast<double>(INFINITY) : s));
+      best = max(best, key_of(warp_sum(t, e), e));
+      continue;
     }
+    // all terms 0, none of them a product that underflowed: zeroed keys, or a query of zeros
+    bool none = odd == 0.f && most == 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      none &= x[k] == 0.f || ((l[k] == 0.f || x[k] * l[k] != 0.f) && (r[k] == 0.f || x[k] * r[k] != 0.f));
+    if (__all_sync(~0u, none)) {
+      best = max(best, 1ull << 63);
+      continue;
+    }
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s += larger(x[k], l[k], r[k]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
+    best = max(best, key_of(s != s ? static_cast<double>(INFINITY) : s));
   }
   return best;
 }

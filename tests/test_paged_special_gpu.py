@@ -173,6 +173,25 @@ def test_select_takes_either_order_of_the_extremes(n, kind, launch):
         assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
 
 
+@pytest.mark.parametrize("n", [100, 1500, 9001])
+@pytest.mark.parametrize("e", [-30, -60, -90, -120])
+def test_select_zeros_among_scores_that_underflow(n, e, launch):
+    """Pages of zeros tie with each other only: products that vanish in 32 bits still have their order in 64."""
+    P, Hq, Hkv, D = 16, 2, 1, 64 if n % 2 else 128
+    table, n_pages = tables([n * P], P, seed=n, extra_cols=0)
+    q = rand(1, Hq, D, seed=1) * 2.0 ** e
+    a, b = rand(n_pages, Hkv, 1, D, seed=2), rand(n_pages, Hkv, 1, D, seed=3)
+    summary = torch.cat((torch.minimum(a, b), torch.maximum(a, b)), 2) * 2.0 ** e
+    kind = torch.as_tensor(np.random.default_rng(3).integers(0, 4, n_pages))
+    summary[kind == 1] = 0
+    summary[kind == 2] *= -1  # minima above maxima: scores below 0
+    t = dev(table)
+    t, sl = (widened(t, launch) if n < 2100 else t), dev([n * P])
+    for top_k in (n // 4, n // 2, n * 5 // 8, n * 3 // 4, n - 1):
+        got = da.paged_select(q, summary, t, sl, P, top_k)
+        assert np.array_equal(got.cpu().numpy(), po.select(q, summary, t, sl, P, top_k)), top_k
+
+
 def test_select_of_the_newest_page_scores_nothing():
     """top_k = 1: nothing goes through the workspace."""
     lens, P, Hq, Hkv, D = [40000, 0, 17], 16, 4, 2, 64
