@@ -67,6 +67,29 @@ cudaError_t launch_paged_attn(const PagedAttnLaunch& a, cudaStream_t st);
 // Workspace bytes on the current device; `keys`: the most that a request can attend to.
 size_t paged_attn_workspace(int batch, int h_q, int h_kv, int d, long long keys);
 
+struct PrefillLaunch {
+  const void* q;
+  long long q_n, q_h;  // token and head strides (elements)
+  const void* k_cache;
+  const void* v_cache;
+  Strides ks, vs;
+  const int* table;
+  long long table_stride;
+  const int* seq_lens;
+  const int* cu_new;
+  const int* start_lens;  // may be null
+  void* out;
+  float* lse;  // may be null
+  bool out_f32, causal;
+  int tokens, batch, h_q, h_kv, d, page_size, n_pages, max_pages;
+  float scale;
+  void* workspace;
+  int* status;
+};
+cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st);
+// Workspace bytes on the current device; `keys`: the most that a request can hold.
+size_t paged_prefill_workspace(int d, long long keys);
+
 struct SelectLaunch {
   const void* q;
   long long q_b, q_h;

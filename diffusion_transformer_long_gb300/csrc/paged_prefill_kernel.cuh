@@ -1,0 +1,1172 @@
+// Attention of a step's new tokens over a paged key/value cache, and the join of its parts.
+//
+// Query token i of request b, at position p = start_b + i, with key/value head h of its group of
+// G = H_q / H_kv query heads:
+//   s_j = scale q . k_j over the cached keys j < seq_lens[b] (causal: j <= p too),
+//   o = sum_j softmax_j(s_j) v_j,  lse = ln sum_j exp(s_j)
+//
+// An item is (request, key/value head, block of tokens): two Q tiles of 128 rows, row r of a tile being
+// token r / G, head r % G of the group, so that a group's heads share one pass over the keys whatever G is
+// and a few tokens still fill a tile.  One TMA box of (64 channels, G heads, 128 / G tokens) a tile and
+// channel block lays the rows out that way.  The pipeline is that of the dense kernel (attn_kernel.cuh:
+// scores and products on tcgen05 with both accumulators in tensor memory, the softmax's online maximum
+// raised only when it falls behind by 2^8, weights rounded to bf16 and normalised by the sum of the rounded
+// ones, the lse from the unrounded sum), with four differences:
+//
+// - Keys and values come page by page: the producer warp's lanes look a batch of table entries up (one
+//   batch ahead), and each copies its own run of at most 128 rows of one page (the largest power of two
+//   that divides the page size) to its place in the 128-byte-swizzled tile.  An entry outside the pool
+//   becomes a copy from past the pool's end, which reads as zeros, and a bit in the tile's mask.
+// - Each row has its own last key, and each Q tile its own last tile, so that a tile that no row of one Q
+//   tile sees is not multiplied for it.  Values behind the request's last key are zeroed in shared memory.
+//   Values that some rows of a tile must not see are looked through for infinities and NaN, which a weight
+//   of 0 would not hide: they are taken out and given to the rows that see them at the end.
+// - Work is dealt out by cost.  A run of the batch's keys (each item's last row's, and a fixed cost an
+//   item), in the order request, head, tokens, goes to each block, whatever it belongs to: causal items are of
+//   very different lengths, and a few tokens on a long cache are few items.  A run that ends inside an item
+//   leaves fp32 parts in the workspace, at most two a block, joined in the blocks' order by a second
+//   launch: equal calls give equal bits.  Where the table has no room for long items they stay whole
+//   and there is no second launch.
+// - One warp works the segments of the block's run out, from the lengths on the device, into a ring that the
+//   other roles read: they agree by construction and hold none of the arithmetic in registers.
+//
+// Bound by the tensor pipe and the softmax's chain for chunks of tokens, by HBM for a few tokens a request.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_kernel.cuh"
+#include "paged_device.cuh"
+#include "paged_launch.h"
+#include "sm103_ptx.cuh"
+
+namespace ditattn {
+namespace prefill {
+
+constexpr int kSchedWarp = 11;
+constexpr int kSegs = 4;               // segments in the ring
+constexpr int kSegWords = 16;
+constexpr int kMaskRing = 8;           // key tiles whose masks are held (the producer runs at most 3 ahead)
+constexpr int kHeldWords = 16;         // per segment: 3 tiles x 128 keys, then a flag
+constexpr int kItemCost = 256;         // what an item costs beside its keys, in keys
+constexpr int kMinRun = 512;           // a block's smallest run, in keys
+constexpr int kItemRows = 2 * kBlockM;
+constexpr int kConsumers = 3 + 8 + 4;  // of a segment: producer, two issuers, softmax and epilogue warps
+
+struct PrefillParams {
+  CUtensorMap tm_q;        // (D, head of the group, token, key/value head)
+  CUtensorMap tm_k, tm_v;  // (D, row, head, page)
+  const __nv_bfloat16* v_cache;
+  Strides vs;
+  const int* table;
+  long long table_stride;
+  const int* seq_lens;
+  const int* cu_new;
+  const int* start_lens;  // or null: a request's new tokens are its last
+  void* out;
+  int out_align32;
+  float* lse;       // may be null
+  float* part_o;    // [blocks][2][256][D]
+  float* part_lse;  // [blocks][2][256], base 2
+  int4* meta;       // [blocks]: (first row of the item's tokens, tokens, key/value head, parts; 0: nothing to join)
+  int batch, tokens, h_q, h_kv, group, tile_tokens;  // tile_tokens: of a Q tile, 128 / group
+  int page_size, n_pages, max_len;
+  int box_rows;   // rows of one copy
+  int div_group;  // 2^16 / group, rounded up: r / group for r < 128 is r * div_group >> 16
+  int causal;
+  int split;  // 0: items stay whole
+  float scale_log2;
+  int* status;
+  long long wait_limit;
+  int stall;
+};
+
+template <int D>
+struct Smem {
+  using A = AttnSmem<D>;
+  static constexpr int bSegFull = A::kNumBars;  // + slot
+  static constexpr int bSegEmpty = bSegFull + kSegs;
+  static constexpr int bHeld = bSegEmpty + kSegs;  // + tile: what a segment's O_t lacks is known
+  static constexpr int kNumBars = bHeld + 2;
+  static constexpr uint32_t kBars = A::kBars;
+  static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
+  static constexpr uint32_t kAbort = kTmemSlot + 4;
+  static constexpr uint32_t kMasks = kAbort + 4;
+  static constexpr uint32_t kSeg = (kMasks + kMaskRing * 4 + 15) & ~15u;
+  static constexpr uint32_t kHeld = kSeg + kSegs * kSegWords * 4;
+  static constexpr uint32_t kInvLp = kHeld + kSegs * kHeldWords * 4;
+  static constexpr uint32_t kUsed = kInvLp + 2 * kBlockM * 4;
+  static constexpr uint32_t kBytes = kUsed + 1024;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+// One request of the step, from the lengths on the device.
+struct Request {
+  int row0, n;      // first row of its new tokens, how many
+  int len;          // cached keys
+  long long start;  // position of the first new token
+  __device__ __forceinline__ void load(const PrefillParams& p, int b) {
+    row0 = min(max(p.cu_new[b], 0), p.tokens);
+    n = max(0, min(max(p.cu_new[b + 1], 0), p.tokens) - row0);
+    len = min(max(p.seq_lens[b], 0), p.max_len);
+    start = p.start_lens ? p.start_lens[b] : static_cast<long long>(len) - n;
+  }
+  __device__ __forceinline__ int items(const PrefillParams& p) const {
+    return (n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+  }
+  // Keys that the first `upto` tokens see at most.
+  __device__ __forceinline__ int seen(const PrefillParams& p, long long upto) const {
+    if (!p.causal) return len;
+    return static_cast<int>(min(max(start + upto, 0LL), static_cast<long long>(len)));
+  }
+  __device__ __forceinline__ int item_keys(const PrefillParams& p, int i) const {
+    return seen(p, min(static_cast<long long>(n), static_cast<long long>(i + 1) * 2 * p.tile_tokens));
+  }
+  // Cost of the first i items of one head: i kItemCost + sum of item_keys.  All but the request's last
+  // item end at start + (u + 1) tb, clipped to [0, len].
+  __device__ __forceinline__ long long cost(const PrefillParams& p, int i) const {
+    long long sum = static_cast<long long>(i) * kItemCost;
+    if (!p.causal) return sum + static_cast<long long>(i) * len;
+    if (i > 0 && i == items(p)) sum += item_keys(p, --i);
+    const long long tb = 2 * p.tile_tokens;
+    const long long lo = start < 0 ? min(static_cast<long long>(i), -start / tb) : 0;
+    long long hi = len > start ? (len - start + tb - 1) / tb - 1 : 0;  // items that end before len
+    hi = min(max(hi, lo), static_cast<long long>(i));
+    const long long m = hi - lo;
+    sum += m * start + tb * (m * (lo + hi + 1) / 2);
+    return sum + (i - hi) * len;
+  }
+  // The item of one head in which cost x lies.
+  __device__ __forceinline__ int find(const PrefillParams& p, long long x) const {
+    int lo = 0, hi = items(p) - 1;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (cost(p, mid) <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+struct Segment {
+  int b, h;        // request (below 0: no more), key/value head
+  int row0, ntok;  // first row of the item's tokens, how many
+  int pos0;        // position of the first, at most len
+  int len;
+  int k0, e0, e1;  // key tiles [k0, e_t) of Q tile t
+  int kind;        // 0: the whole item, 1: a later part (slot 0), 2: its first part (slot 1)
+  __device__ __forceinline__ int end(int t) const { return t ? e1 : e0; }
+  __device__ __forceinline__ int last() const { return max(e0, e1); }
+  __device__ __forceinline__ bool present(const PrefillParams& p, int t) const {
+    return t == 0 || ntok > p.tile_tokens;
+  }
+  // Keys that row r of Q tile t sees.  Rows without a token see what the tile's last token does.
+  __device__ __forceinline__ int limit(const PrefillParams& p, int t, int r) const {
+    if (!p.causal) return len;
+    const int tok = min(t * p.tile_tokens + ((r * p.div_group) >> 16), min(ntok, (t + 1) * p.tile_tokens) - 1);
+    return static_cast<int>(min(max(static_cast<long long>(pos0) + tok + 1, 0LL), static_cast<long long>(len)));
+  }
+  // Keys that every row sees.
+  __device__ __forceinline__ int seen_by_all(const PrefillParams& p) const { return limit(p, 0, 0); }
+  __device__ __forceinline__ bool has_token(const PrefillParams& p, int t, int r, int& tok) const {
+    const int i = (r * p.div_group) >> 16;
+    tok = t * p.tile_tokens + i;
+    return i < p.tile_tokens && tok < ntok;
+  }
+};
+
+using detail::Descs;
+using detail::k_item;  // K/V ring items of a segment in consumption order, as in the dense kernel
+using detail::v_item;
+using detail::wait_or_abort;
+
+__device__ __forceinline__ void raise_abort(const PrefillParams& p, volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(p.status, kStatusTimeout);
+}
+
+// The ring of segments as a role sees it.
+template <int D>
+struct Segments {
+  uint32_t sbase;
+  int n = 0;  // taken so far
+  __device__ __forceinline__ explicit Segments(uint32_t s) : sbase(s) {}
+  __device__ __forceinline__ uint32_t bar(int i) const { return sbase + Smem<D>::kBars + 8u * i; }
+  __device__ __forceinline__ uint32_t slot() const { return sbase + Smem<D>::kSeg + (n % kSegs) * kSegWords * 4; }
+  __device__ __forceinline__ uint32_t held() const { return sbase + Smem<D>::kHeld + (n % kSegs) * kHeldWords * 4; }
+  __device__ __forceinline__ bool wait(const PrefillParams& p, const volatile int* abort_flag) const {
+    return wait_or_abort(bar(Smem<D>::bSegFull + n % kSegs), (n / kSegs) & 1, abort_flag, p.wait_limit);
+  }
+  __device__ __forceinline__ Segment read() const {
+    int w[12];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(slot() + 16 * i)
+                   : "memory");
+    return {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7], w[8], w[9]};
+  }
+  // One lane of the role's warp: the segment's words are no longer needed.
+  __device__ __forceinline__ void release() const { ptx::mbar_arrive(bar(Smem<D>::bSegEmpty + n % kSegs)); }
+};
+
+// The block's run, segment by segment (one warp).
+template <int D>
+__device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase, int lane, volatile int* abort_flag) {
+  using S = Smem<D>;
+  const int c = blockIdx.x;
+  Request rq;
+  long long total = 0;
+  for (int b = lane; b < p.batch; b += 32) {
+    rq.load(p, b);
+    total += rq.cost(p, rq.items(p));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  total *= p.h_kv;
+  const long long blocks = min(static_cast<long long>(gridDim.x), max(1LL, total / kMinRun));
+  const long long run0 = c < blocks ? total * c / blocks : total, run1 = c < blocks ? total * (c + 1) / blocks : total;
+  int4 meta = make_int4(0, 0, 0, 0);
+  int n = 0;  // segments written
+  bool ok = true;
+  auto emit = [&](const Segment& s) {
+    const int slot = n % kSegs;
+    if (n >= kSegs) {
+      ok = wait_or_abort(sbase + S::kBars + 8u * (S::bSegEmpty + slot), (n / kSegs - 1) & 1, abort_flag, p.wait_limit);
+      ok = __all_sync(~0u, ok);
+      if (!ok) return;
+    }
+    if (lane == 0) {
+      const uint32_t at = sbase + S::kSeg + slot * kSegWords * 4;
+      const int w[12] = {s.b, s.h, s.row0, s.ntok, s.pos0, s.len, s.k0, s.e0, s.e1, s.kind, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16 * i), "r"(w[4 * i]), "r"(w[4 * i + 1]),
+                     "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                     : "memory");
+      ptx::mbar_arrive(sbase + S::kBars + 8u * (S::bSegFull + slot));
+    }
+    ++n;
+  };
+  if (run0 < run1) {
+    // The request in which the run begins, 32 at a time.
+    int b = 0;
+    long long base = 0;  // cost of the requests before b
+    for (;; b += 32) {
+      long long mine = 0;
+      if (b + lane < p.batch) {
+        rq.load(p, b + lane);
+        mine = rq.cost(p, rq.items(p)) * p.h_kv;
+      }
+      long long upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const unsigned past = __ballot_sync(~0u, base + upto > run0);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        base += __shfl_sync(~0u, upto - mine, l);
+        b += l;
+        break;
+      }
+      base += __shfl_sync(~0u, upto, 31);
+    }
+    rq.load(p, b);
+    int nb = rq.items(p);
+    const long long per_head = rq.cost(p, nb);
+    int h = static_cast<int>((run0 - base) / per_head);
+    long long x0 = run0 - base - h * per_head;
+    int i = rq.find(p, x0);
+    x0 -= rq.cost(p, i);
+    long long at = run0;  // x0's place in the whole
+    while (ok) {
+      const int keys = rq.item_keys(p, i);
+      const long long cost = static_cast<long long>(keys) + kItemCost, take = min(cost - x0, run1 - at);
+      const int ntiles = (keys + kBlockN - 1) / kBlockN;
+      auto cut = [&](long long x) { return x >= keys ? ntiles : static_cast<int>((x + kBlockN - 1) / kBlockN); };
+      int a = cut(x0), e = cut(x0 + take);
+      bool any = a < e || (ntiles == 0 && x0 == 0);
+      if (!p.split) {  // an item goes to the block in whose run it begins
+        any = x0 == 0;
+        a = 0;
+        e = ntiles;
+      }
+      if (any) {
+        Segment s;
+        s.b = b;
+        s.h = h;
+        const int t0 = i * 2 * p.tile_tokens;
+        s.row0 = rq.row0 + t0;
+        s.ntok = min(rq.n - t0, 2 * p.tile_tokens);
+        s.len = rq.len;
+        s.pos0 = static_cast<int>(max(min(rq.start + t0, static_cast<long long>(rq.len)), -(1LL << 30)));
+        s.k0 = a;
+        const int f0 = (rq.seen(p, t0 + min(s.ntok, p.tile_tokens)) + kBlockN - 1) / kBlockN;
+        s.e0 = max(a, min(f0, e));
+        s.e1 = s.ntok > p.tile_tokens ? e : a;
+        s.kind = a == 0 && e == ntiles ? 0 : a == 0 ? 2 : 1;
+        if (s.kind == 2) {
+          // The item's last part is in the first block whose run ends behind the item's last tile's start.
+          const long long x = at - x0 + static_cast<long long>(ntiles - 1) * kBlockN;
+          const long long last = ((x + 1) * blocks + total - 1) / total - 1;
+          meta = make_int4(s.row0, s.ntok, h, static_cast<int>(last) - c + 1);
+        }
+        emit(s);
+      }
+      at += take;
+      if (at >= run1) break;
+      x0 = 0;
+      if (++i == nb) {
+        i = 0;
+        if (++h == p.h_kv) {
+          h = 0;
+          // The next request with new tokens.
+          for (++b; b < p.batch; b += 32) {
+            bool has = false;
+            if (b + lane < p.batch) {
+              rq.load(p, b + lane);
+              has = rq.n > 0;
+            }
+            const unsigned some = __ballot_sync(~0u, has);
+            if (some) {
+              b += __ffs(some) - 1;
+              break;
+            }
+          }
+          if (b >= p.batch) break;  // (not reached: the run would have ended)
+          rq.load(p, b);
+          nb = rq.items(p);
+        }
+      }
+    }
+  }
+  if (ok) {
+    Segment s{};
+    s.b = -1;
+    emit(s);
+  }
+  if (p.split && lane == 0) p.meta[c] = meta;
+  if (!ok) raise_abort(p, abort_flag);
+}
+
+// Copies: Q of each segment, then its key and value tiles (one warp; each lane its own rows of a tile).
+template <int D>
+__device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase, int lane, volatile int* abort_flag) {
+  using L = AttnSmem<D>;
+  using S = Smem<D>;
+  constexpr int kRegions = D / 64;
+  auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
+  auto wait = [&](int b, uint32_t parity) {
+    return __all_sync(~0u, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
+  };
+  const int boxes = kBlockN / p.box_rows;  // of a tile: 1, 2, 4 or 8
+  const int per_batch = 32 / boxes;        // tiles looked up at once
+  const int box = lane % boxes;            // the lane's box of a tile
+  const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * 128 * kRegions;
+
+  uint32_t kpar = 0, vpar = 0;  // bit s: parity of the next K_FULL[s] / V_FULL[s] phase
+  int last_bar[kStages];        // barrier and parity of the newest copy into each slot
+  uint32_t last_par[kStages];
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    last_bar[s] = -1;
+    last_par[s] = 0;
+  }
+  int q_loads = 0, it = 0, tiles = 0;  // Q loads, ring index, key tiles so far
+  bool ok = true;
+  Segments<D> segs(sbase);
+  for (;; ++segs.n) {
+    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    const Segment sg = segs.read();
+    __syncwarp();
+    if (lane == 0) segs.release();
+    if (sg.b < 0) break;
+    const int kend = sg.last();
+    if (kend == sg.k0) continue;  // no keys
+    // Q_t is free once the previous segment's last S MMAs have completed.
+    if (!(ok = wait(L::bQEmpty, (q_loads & 1) ^ 1))) break;
+    if (lane == 0) {
+      ptx::mbar_arrive_expect_tx(bar(L::bQFull), q_bytes * ((sg.e0 > sg.k0) + (sg.e1 > sg.k0)));
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (sg.end(t) > sg.k0)
+#pragma unroll
+          for (int r = 0; r < kRegions; ++r)
+            ptx::tma_load_4d(sbase + (t ? L::kQ1 : L::kQ0) + r * L::kRegion, &p.tm_q, bar(L::bQFull), r * 64, 0,
+                             sg.row0 + t * p.tile_tokens, sg.h);
+    }
+    ++q_loads;
+    if (p.stall) return;  // test only: the consumers' first K wait will expire
+
+    const int pages = pages_of(sg.len, p.page_size);
+    const int* const row = p.table + sg.b * p.table_stride;
+    // The lane's box of tile j0 + lane / boxes: page (-1: none, -2: behind the keys), first row in it.
+    auto look_up = [&](int j0, int& page, int& first) {
+      const unsigned key = static_cast<unsigned>(j0 + lane / boxes) * kBlockN + box * p.box_rows;
+      const int col = static_cast<int>(key / static_cast<unsigned>(p.page_size));
+      first = static_cast<int>(key - static_cast<unsigned>(col) * p.page_size);
+      page = -2;
+      if (j0 + lane / boxes < kend && col < pages) {
+        page = row[col];
+        if (page < 0 || page >= p.n_pages) page = -1;
+      }
+    };
+    int page_a, first_a, page_b, first_b;  // the batch in use and the one ahead
+    int base = sg.k0;
+    look_up(base, page_a, first_a);
+    look_up(base + per_batch, page_b, first_b);
+    int kpage = -2, kfirst = 0, vpage = -2, vfirst = 0;  // of the lane's box in the newest key tile, and in the one before
+    auto take = [&](int j) {
+      if (j - base == per_batch) {
+        base = j;
+        page_a = page_b;
+        first_a = first_b;
+        look_up(base + per_batch, page_b, first_b);
+      }
+      const int from = (j - base) * boxes + box;
+      vpage = kpage;
+      vfirst = kfirst;
+      kpage = __shfl_sync(~0u, page_a, from);
+      kfirst = __shfl_sync(~0u, first_a, from);
+    };
+    auto load = [&](bool is_v, int page, int first) {
+      const int s = it % kStages;
+      if (!wait(L::bKVEmpty + s, ((it / kStages) & 1) ^ 1)) return false;
+      const int fb = (is_v ? L::bVFull : L::bKFull) + s;
+      const uint32_t par = ((is_v ? vpar : kpar) >> s) & 1;
+      if (is_v) vpar ^= 1u << s; else kpar ^= 1u << s;
+      if (!is_v) {
+        // A bit for every 16 keys: without a page.
+        const unsigned none = __ballot_sync(~0u, page == -1) & ((1u << boxes) - 1);
+        unsigned mask = 0;
+        if (none)
+          for (int q = 0; q < 8; ++q)
+            if ((none >> (q * boxes / 8)) & 1) mask |= 1u << q;
+        if (lane == 0)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + S::kMasks + 4 * (tiles % kMaskRing)), "r"(mask)
+                       : "memory");
+        ++tiles;
+      }
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar(fb), L::kTile);
+      __syncwarp();
+      if (lane < boxes * kRegions) {
+        const int r = lane / boxes;  // channel block (the lane's box is lane % boxes)
+        ptx::tma_load_4d(sbase + L::kKV + s * L::kTile + r * L::kRegion + box * p.box_rows * 128,
+                         is_v ? &p.tm_v : &p.tm_k, bar(fb), r * 64, first, sg.h, page < 0 ? p.n_pages : page);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kStages; ++q)
+        if (q == s) {
+          last_bar[q] = fb;
+          last_par[q] = par;
+        }
+      ++it;
+      return true;
+    };
+    take(sg.k0);
+    if (!(ok = load(false, kpage, kfirst))) break;
+    for (int j = sg.k0; j < kend; ++j) {
+      if (j + 1 < kend) {
+        take(j + 1);
+        if (!(ok = load(false, kpage, kfirst))) break;
+        ok = load(true, vpage, vfirst);
+      } else {
+        ok = load(true, kpage, kfirst);
+      }
+      if (!ok) break;
+    }
+    if (!ok) break;
+  }
+  if (!ok) {
+    if (lane == 0) raise_abort(p, abort_flag);
+    // Let every copy this warp started land before the block can exit.
+    if (q_loads > 0) ptx::mbar_wait(bar(L::bQFull), (q_loads - 1) & 1, p.wait_limit);
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+      if (last_bar[s] >= 0) ptx::mbar_wait(bar(last_bar[s]), last_par[s], p.wait_limit);
+  }
+}
+
+// S_t = Q_t K^T (one thread).
+template <int D>
+__device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem,
+                                         volatile int* abort_flag) {
+  using L = AttnSmem<D>;
+  auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
+  constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBlockM, kBlockN, false, false);
+  const Descs<D> ds(sbase);
+  auto issue = [&](int t, int slot) {
+    const uint32_t kb = Descs<D>::pick(ds.k, slot);
+    const uint32_t qa = ds.q[t];
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = ((k / 4) * L::kRegion + (k % 4) * 32) >> 4;
+      ptx::mma_bf16_ss(tmem + t * kBlockN, Descs<D>::full(qa + off), Descs<D>::full(kb + off), kIdesc, k > 0 ? 1u : 0u);
+    }
+  };
+  auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, abort_flag, p.wait_limit); };
+
+  uint32_t kpar = 0;
+  int g[2] = {0, 0};  // S tiles issued for each Q tile
+  int loads = 0, ring0 = 0;
+  bool ok = true;
+  Segments<D> segs(sbase);
+  for (; ok; ++segs.n) {
+    if (!(ok = segs.wait(p, abort_flag))) break;
+    const Segment sg = segs.read();
+    segs.release();
+    if (sg.b < 0) break;
+    const int nt = sg.last() - sg.k0;
+    if (nt == 0) continue;
+    if (!(ok = wait(L::bQFull, loads & 1))) break;
+    ++loads;
+    for (int j = 0; j < nt; ++j) {
+      const int sK = (ring0 + k_item(j)) % kStages;
+      ok = wait(L::bKFull + sK, (kpar >> sK) & 1);
+      kpar ^= 1u << sK;
+      if (!ok) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || sg.k0 + j >= sg.end(t)) continue;
+        // S_t is overwritten: softmax t must have loaded the last one.
+        if (g[t] > 0 && !(ok = wait(L::bSEmpty + t, (g[t] - 1) & 1))) continue;
+        ptx::tc_fence_after();
+        issue(t, sK);
+        ptx::mma_commit(bar(L::bSFull + t));
+        ++g[t];
+      }
+      if (!ok) break;
+      ptx::mma_commit(bar(L::bKVEmpty + sK));
+    }
+    if (ok) ptx::mma_commit(bar(L::bQEmpty));
+    ring0 += 2 * nt;
+  }
+  if (!ok) {
+    raise_abort(p, abort_flag);
+    ptx::mma_commit(bar(L::bDrainS));
+    ptx::mbar_wait(bar(L::bDrainS), 0, p.wait_limit);
+  }
+}
+
+// A bit in each half of w whose bf16 is infinite or NaN: bits 15 and 31.
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// Row i, 16-byte piece ch (whole rows are gone through, so the swizzle does not matter) of a value tile.
+template <int D>
+__device__ __forceinline__ uint32_t v_piece(uint32_t tile, int i, int ch) {
+  return tile + (ch / 8) * AttnSmem<D>::kRegion + i * 128 + (ch % 8) * 16;
+}
+
+// Rows [valid, 128) of a value tile become zeros: a weight of 0 does not hide what a page holds behind
+// the request's last key.  (One warp.)
+template <int D>
+__device__ __forceinline__ void clear_rows(uint32_t tile, int valid, int lane) {
+  for (int x = lane; x < (kBlockN - valid) * (D / 8); x += 32)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v_piece<D>(tile, valid + x / (D / 8), x % (D / 8))),
+                 "r"(0)
+                 : "memory");
+}
+
+// Infinities and NaN in the first `valid` rows of a value tile become 0; four words of the rows that
+// had one (bit l of word i: row 32 i + l) go to `words`.  Returns whether any had.  (One warp, a row a lane.)
+template <int D>
+__device__ __forceinline__ bool take_out(uint32_t tile, int valid, uint32_t words, int lane) {
+  bool any = false;
+  for (int i = 0; i < 4; ++i) {
+    const int row = 32 * i + lane;
+    uint32_t bad = 0;
+    if (row < valid) {
+#pragma unroll 4
+      for (int ch = 0; ch < D / 8; ++ch) {
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(v_piece<D>(tile, row, (ch & 8) | ((ch + lane) & 7)))
+                     : "memory");
+        bad |= non_finite(w[0]) | non_finite(w[1]) | non_finite(w[2]) | non_finite(w[3]);
+      }
+    }
+    const unsigned rows = __ballot_sync(~0u, bad != 0);
+    if (rows == 0) continue;
+    any = true;
+    if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(words + 4 * i), "r"(rows) : "memory");
+    if (bad) {
+      for (int x = 0; x < D / 2; ++x) {
+        const uint32_t at = v_piece<D>(tile, row, x / 4) + (x % 4) * 4;
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+        const uint32_t f = non_finite(w);
+        const uint32_t keep = ~(((f >> 15) & 1) * 0xffffu | (f >> 31) * 0xffff0000u);
+        if (f) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w & keep) : "memory");
+      }
+    }
+  }
+  return any;
+}
+
+// O_t += P_t V (one warp; lane 0 issues).
+template <int D>
+__device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int lane,
+                                          volatile int* abort_flag) {
+  using L = AttnSmem<D>;
+  using S = Smem<D>;
+  auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
+  constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBlockM, D, false, true);
+  const Descs<D> ds(sbase);
+  auto issue = [&](int t, int slot, bool acc, int half) {
+    const uint32_t vb = Descs<D>::pick(ds.v, slot);
+    const uint32_t pa = ds.pp[t];
+#pragma unroll
+    for (int k = half * 4; k < half * 4 + 4; ++k) {
+      const uint32_t aoff = ((k / 4) * L::kRegion + (k % 4) * 32) >> 4;
+      ptx::mma_bf16_ss(tmem + 2 * kBlockN + t * D, Descs<D>::full(pa + aoff), Descs<D>::full(vb + k * 128), kIdesc,
+                       (acc || k > 0) ? 1u : 0u);
+    }
+  };
+  auto wait = [&](int b, uint32_t parity) {
+    return __all_sync(~0u, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
+  };
+
+  uint32_t vpar = 0;
+  int g[2] = {0, 0};     // PV tiles issued for each Q tile
+  int used[2] = {0, 0};  // segments in which O_t was written
+  int ring0 = 0;
+  bool ok = true;
+  Segments<D> segs(sbase);
+  for (; ok; ++segs.n) {
+    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    const Segment sg = segs.read();
+    if (sg.b < 0) break;
+    const uint32_t held = segs.held();
+    if (lane < kHeldWords) asm volatile("st.shared.b32 [%0], %1;" ::"r"(held + 4 * lane), "r"(0) : "memory");
+    __syncwarp();
+    const int nt = sg.last() - sg.k0;
+    const int seen = sg.seen_by_all(p);
+    for (int j = 0; j < nt; ++j) {
+      const int sV = (ring0 + v_item(j, nt)) % kStages;
+      ok = wait(L::bVFull + sV, (vpar >> sV) & 1);
+      vpar ^= 1u << sV;
+      if (!ok) break;
+      const int key0 = (sg.k0 + j) * kBlockN, valid = min(sg.len - key0, kBlockN);
+      if (valid < kBlockN || key0 + valid > seen) {
+        const uint32_t tile = sbase + L::kKV + sV * L::kTile;
+        if (valid < kBlockN) clear_rows<D>(tile, valid, lane);
+        if (key0 + valid > seen) {
+          if (take_out<D>(tile, valid, held + (key0 / kBlockN - seen / kBlockN) * 16, lane) && lane == 0)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(held + 4 * (kHeldWords - 1)), "r"(1) : "memory");
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || sg.k0 + j >= sg.end(t)) continue;
+        if (!(ok = wait(L::bPLo + t, g[t] & 1))) continue;
+        // The first PV of a segment overwrites O_t: the last one's epilogue must have read it.
+        if (j == 0) {
+          if (used[t] > 0 && !(ok = wait(L::bOEmpty + t, (used[t] - 1) & 1))) continue;
+          ++used[t];
+        }
+        if (lane == 0) {
+          ptx::tc_fence_after();
+          issue(t, sV, j > 0, 0);
+        }
+        if (!(ok = wait(L::bPFull + t, g[t] & 1))) continue;
+        if (lane == 0) {
+          ptx::tc_fence_after();
+          issue(t, sV, j > 0, 1);
+          ptx::mma_commit(bar(L::bPVDone + t));
+          if (sg.k0 + j + 1 == sg.end(t)) ptx::mbar_arrive(bar(S::bHeld + t));
+        }
+        __syncwarp();
+        ++g[t];
+      }
+      if (!ok) break;
+      if (lane == 0) ptx::mma_commit(bar(L::bKVEmpty + sV));
+    }
+    ring0 += 2 * nt;
+    if (!ok) break;
+    __syncwarp();
+    if (lane == 0) segs.release();
+  }
+  if (!ok && lane == 0) {
+    raise_abort(p, abort_flag);
+    ptx::mma_commit(bar(L::bDrainPV));
+    ptx::mbar_wait(bar(L::bDrainPV), 0, p.wait_limit);
+  }
+}
+
+// Softmax of Q tile t (four warps, a row a thread).
+template <int D>
+__device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int t, int warp,
+                                           int lane, volatile int* abort_flag) {
+  using L = AttnSmem<D>;
+  using S = Smem<D>;
+  auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;  // row in the Q tile == TMEM lane
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t tS = tmem + t * kBlockN + lane_off;
+  const uint32_t tO = tmem + 2 * kBlockN + t * D + lane_off;
+  const uint32_t sP = sbase + (t ? L::kP1 : L::kP0);
+  const uint32_t sw = static_cast<uint32_t>(r & 7);
+  const float c = p.scale_log2;
+  auto wait = [&](int b, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
+  };
+
+  int g = 0;      // tiles processed by this warpgroup
+  int tiles = 0;  // key tiles of the block so far, for their masks
+  int li = 0;     // segments handed to the epilogue
+  bool ok = true;
+  Segments<D> segs(sbase);
+  for (; ok; ++segs.n) {
+    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    int nt, left;  // the Q tile's key tiles; the row's keys from the first of them on
+    {
+      const Segment sg = segs.read();
+      if (sg.b < 0) break;
+      if (!sg.present(p, t)) {
+        tiles += sg.last() - sg.k0;
+        __syncwarp();
+        if (lane == 0) segs.release();
+        continue;
+      }
+      nt = sg.end(t) - sg.k0;
+      left = sg.limit(p, t, r) - sg.k0 * kBlockN;
+    }
+    float m = -INFINITY;  // running max of scale*log2e*s (possibly stale by < 2^8)
+    float l = 0.f;        // running sum of 2^(c*s - m), for the LSE
+    float lp = 0.f;       // running sum of the bf16-rounded P the PV GEMM sees, for O
+    for (int j = 0; j < nt; ++j, ++g) {
+      if (!(ok = wait(L::bSFull + t, g & 1))) break;
+      ptx::tc_fence_after();
+      float s[kBlockN];
+      float cmax[kBlockN / 32];
+#pragma unroll
+      for (int cc = 0; cc < kBlockN / 32; ++cc) {
+        uint32_t u[32];
+        ptx::tmem_ld32_max(tS + cc * 32, u, cmax[cc]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[cc * 32 + i] = __uint_as_float(u[i]);
+      }
+      uint32_t none;  // 16-key pieces without a page
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(none)
+                   : "r"(sbase + S::kMasks + 4 * ((tiles + j) % kMaskRing))
+                   : "memory");
+      ptx::tmem_wait_ld();
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(bar(L::bSEmpty + t));
+
+      float mx = ptx::fmax3(cmax[0], cmax[1], fmaxf(cmax[2], cmax[3]));
+      const int valid = left - j * kBlockN;
+      if (valid < kBlockN || none) {
+        // Keys that the row does not see are masked to -inf, so their P is exactly 0, and the max is
+        // taken over the others only.
+#pragma unroll
+        for (int i = 0; i < kBlockN; ++i)
+          if (i >= valid || ((none >> (i / 16)) & 1)) s[i] = -INFINITY;
+        float a[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          a[q] = ptx::fmax3(s[16 * q], s[16 * q + 1], s[16 * q + 2]);
+#pragma unroll
+          for (int i = 3; i < 15; i += 2) a[q] = ptx::fmax3(a[q], s[16 * q + i], s[16 * q + i + 1]);
+          a[q] = fmaxf(a[q], s[16 * q + 15]);
+        }
+        mx = ptx::fmax3(ptx::fmax3(a[0], a[1], a[2]), ptx::fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+      }
+      const float m_tile = mx * c;
+      const bool raise = m_tile > m + kRescaleLog2;
+      float alpha = 1.f;
+      if (raise) {
+        alpha = ptx::ex2_approx(m - m_tile);  // 0 where m = -inf
+        m = m_tile;
+      }
+      l *= alpha;
+      lp *= alpha;
+      bool pv_prev_done = (g == 0);
+      if (j > 0 && __any_sync(0xffffffffu, raise)) {
+        if (!(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
+        pv_prev_done = true;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t u[16];
+          ptx::tmem_ld16(tO + cc * 16, u);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+          ptx::tmem_st16(tO + cc * 16, u);
+        }
+        ptx::tmem_wait_st();
+      }
+
+      // P = 2^(c*s - m); a row that has seen nothing yet keeps m = -inf, and takes 0 in its place.
+      const float mm = m == -INFINITY ? 0.f : m;
+      const uint64_t c2 = ptx::f2pack(c, c);
+      const uint64_t nm2 = ptx::f2pack(-mm, -mm);
+      uint64_t acc_l[4];
+      float acc_lp[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc_l[q] = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc_lp[q] = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = half * 64; i < half * 64 + 64; i += 2) {
+          float x0, x1;
+          ptx::f2unpack(ptx::ffma2(ptx::f2pack(s[i], s[i + 1]), c2, nm2), x0, x1);
+          s[i] = ptx::ex2_approx(x0);
+          s[i + 1] = ptx::ex2_approx(x1);
+        }
+        // The P_t buffer is free once the last PV has read it.
+        if (half == 0 && !pv_prev_done && !(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
+#pragma unroll
+        for (int ch = half * 8; ch < half * 8 + 8; ++ch) {
+          uint32_t wv[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float p0 = s[8 * ch + 2 * q], p1 = s[8 * ch + 2 * q + 1];
+            wv[q] = ptx::pack_bf16x2(p0, p1);
+            acc_l[q] = ptx::fadd2(acc_l[q], ptx::f2pack(p0, p1));
+            detail::add_bf16x2(acc_lp[2 * q], acc_lp[2 * q + 1], wv[q]);
+          }
+          const uint32_t addr = sP + half * L::kRegion + r * 128 + ((static_cast<uint32_t>(ch % 8) ^ sw) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(wv[0]), "r"(wv[1]), "r"(wv[2]),
+                       "r"(wv[3])
+                       : "memory");
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(half == 0 ? L::bPLo + t : L::bPFull + t));
+      }
+      if (!ok) break;
+      const uint64_t sl = ptx::fadd2(ptx::fadd2(acc_l[0], acc_l[1]), ptx::fadd2(acc_l[2], acc_l[3]));
+      float a0, a1;
+      ptx::f2unpack(sl, a0, a1);
+      l += a0 + a1;
+      lp += ((acc_lp[0] + acc_lp[1]) + (acc_lp[2] + acc_lp[3])) + ((acc_lp[4] + acc_lp[5]) + (acc_lp[6] + acc_lp[7]));
+    }
+    if (!ok) break;
+
+    // 1 / sum to the epilogue (0: no key scored above -inf), the LSE to where it goes.
+    const Segment sg = segs.read();
+    tiles += sg.last() - sg.k0;
+    const float lse2 = m + log2f(l);
+    if (li > 0 && !(ok = wait(L::bEpiTaken + t, (li - 1) & 1))) break;
+    reinterpret_cast<float*>(__cvta_shared_to_generic(sbase + S::kInvLp))[t * kBlockM + r] = lp == 0.f ? 0.f : 1.f / lp;
+    ptx::mbar_arrive(bar(L::bEpiReady + t));
+    ++li;
+    int tok;
+    if (sg.has_token(p, t, r, tok)) {
+      const int head = r - ((r * p.div_group) >> 16) * p.group;
+      if (sg.kind)
+        p.part_lse[(static_cast<size_t>(blockIdx.x) * 2 + (sg.kind - 1)) * kItemRows + t * kBlockM + r] = lse2;
+      else if (p.lse)
+        p.lse[static_cast<size_t>(sg.row0 + tok) * p.h_q + sg.h * p.group + head] = lse2 * 0.69314718055994530942f;
+    }
+    __syncwarp();
+    if (lane == 0) segs.release();
+  }
+  if (!ok) raise_abort(p, abort_flag);
+}
+
+// What the PV products left out: the infinities and NaN among the values that some rows of the item do not
+// see, added to the stored output `dst` (D channels) of a row that sees `limit` keys.
+template <int D, typename T>
+__device__ __forceinline__ void give_back(const PrefillParams& p, const Segment& sg, uint32_t held, int limit, T* dst) {
+  const int tile0 = sg.seen_by_all(p) / kBlockN;
+  for (int w = 0; w < kHeldWords - 1; ++w) {
+    uint32_t rows;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(rows) : "r"(held + 4 * w) : "memory");
+    for (; rows; rows &= rows - 1) {
+      const int key = (tile0 + w / 4) * kBlockN + (w % 4) * 32 + __ffs(rows) - 1;
+      if (key >= limit) continue;
+      const int page = p.table[sg.b * p.table_stride + key / p.page_size];
+      if (page < 0 || page >= p.n_pages) continue;
+      const __nv_bfloat16* v = p.v_cache + page * p.vs.b_ + sg.h * p.vs.h_ + (key % p.page_size) * p.vs.n_;
+      for (int i = 0; i < D; ++i) {
+        const float f = __bfloat162float(v[i]);
+        if (isfinite(f)) continue;
+        if constexpr (sizeof(T) == 4)
+          dst[i] += f;
+        else
+          dst[i] = __float2bfloat16(__bfloat162float(dst[i]) + f);
+      }
+    }
+  }
+}
+
+// O_t out of tensor memory, normalised, to the output or to the block's parts (four warps).  The stores are
+// the dense kernel's: fp32 rows through two butterfly stages (8 rows x 128 bytes a store), bf16 rows as they are.
+template <int D, bool kOutF32>
+__device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int warp, int lane,
+                                            volatile int* abort_flag) {
+  using L = AttnSmem<D>;
+  using S = Smem<D>;
+  auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const float* hand = reinterpret_cast<const float*>(__cvta_shared_to_generic(sbase + S::kInvLp));
+  const int r_lo = lane & 7, cgrp = lane >> 3;  // fp32 store layout after the transpose
+  auto wait = [&](int b, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
+  };
+
+  int li0 = 0, li1 = 0;      // segments of each Q tile
+  int used0 = 0, used1 = 0;  // those of them with keys
+  int g0 = 0, g1 = 0;        // key tiles of each Q tile
+  bool ok = true;
+  Segments<D> segs(sbase);
+  for (; ok; ++segs.n) {
+    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    const Segment sg = segs.read();
+    if (sg.b < 0) break;
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {
+      if (!sg.present(p, t)) continue;
+      const int nt = sg.end(t) - sg.k0;
+      const int li = t ? li1++ : li0++, used = t ? used1 : used0;
+      const int g = t ? (g1 += nt) : (g0 += nt);
+      if (nt > 0) ++(t ? used1 : used0);
+      if (!(ok = wait(L::bEpiReady + t, li & 1))) break;
+      const float inv_l = hand[t * kBlockM + r];
+      ptx::mbar_arrive(bar(L::bEpiTaken + t));
+      const bool none = inv_l == 0.f;  // the row has no key above -inf: its output is 0 whatever O_t holds
+      bool missing = false;
+      if (nt > 0) {
+        if (!(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
+        if (!(ok = wait(S::bHeld + t, used & 1))) break;
+        uint32_t flag;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(flag) : "r"(segs.held() + 4 * (kHeldWords - 1)) : "memory");
+        missing = flag != 0;
+      }
+      ptx::tc_fence_after();
+      const uint32_t tO = tmem + 2 * kBlockN + t * D + lane_off;
+      auto release_if = [&](bool last) {
+        if (last && nt > 0) {  // O_t has been read: the PV issuer may start the next segment's
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(L::bOEmpty + t));
+        }
+      };
+      // Row x of the tile (tokens and heads in turn) to its place in the output, or below 0.
+      auto place = [&](int x) -> long long {
+        int tok;
+        if (!sg.has_token(p, t, x, tok)) return -1;
+        if (sg.kind)
+          return ((static_cast<long long>(blockIdx.x) * 2 + (sg.kind - 1)) * kItemRows + t * kBlockM + x) * D;
+        const int head = x - ((x * p.div_group) >> 16) * p.group;
+        return (static_cast<long long>(sg.row0 + tok) * p.h_q + sg.h * p.group + head) * D;
+      };
+      if (kOutF32 || sg.kind) {
+        float* const base = sg.kind ? p.part_o : static_cast<float*>(p.out);
+        const bool align32 = sg.kind || p.out_align32;
+        long long at[4];
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) at[rr] = place(quarter * 32 + rr * 8 + r_lo);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          ptx::tmem_ld32(tO + c * 32, x);
+          ptx::tmem_wait_ld();
+          release_if(c == D / 32 - 1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = none ? 0u : __float_as_uint(__uint_as_float(x[i]) * inv_l);
+          detail::swap_lane_reg_bit<4, 4>(x, lane);
+          detail::swap_lane_reg_bit<3, 3>(x, lane);
+          // x[8*rr + i] = (row 32*quarter + 8*rr + r_lo, column 32*c + 8*cgrp + i)
+#pragma unroll
+          for (int rr = 0; rr < 4; ++rr)
+            if (at[rr] >= 0) detail::st_global_32B(base + at[rr] + c * 32 + cgrp * 8, align32, &x[rr * 8]);
+        }
+        if (missing) {
+          __syncwarp();
+          const long long mine = place(r);
+          if (mine >= 0 && !none) give_back<D>(p, sg, segs.held(), sg.limit(p, t, r), base + mine);
+        }
+      } else if constexpr (!kOutF32) {
+        const long long mine = place(r);
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(p.out) + mine;
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          uint32_t wd[32];  // 64 columns of this thread's row as bf16 pairs
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t a[32];
+            ptx::tmem_ld32(tO + half * 64 + c * 32, a);
+            ptx::tmem_wait_ld();
+            release_if(half == D / 64 - 1 && c == 1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              wd[c * 16 + i] = none ? 0u
+                                    : ptx::pack_bf16x2(__uint_as_float(a[2 * i]) * inv_l,
+                                                       __uint_as_float(a[2 * i + 1]) * inv_l);
+          }
+          if (mine >= 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) detail::st_global_32B(dst + half * 64 + 2 * i, p.out_align32, &wd[i]);
+          }
+        }
+        if (missing && mine >= 0 && !none) give_back<D>(p, sg, segs.held(), sg.limit(p, t, r), dst);
+      }
+    }
+    if (!ok) break;
+    __syncwarp();
+    if (lane == 0) segs.release();
+  }
+  if (!ok) raise_abort(p, abort_flag);
+}
+
+template <int D, bool kOutF32>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
+  using L = AttnSmem<D>;
+  using S = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = ptx::smem_addr(smem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kAbort);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
+    ptx::mbar_init(bar(L::bQFull), 1);
+    ptx::mbar_init(bar(L::bQEmpty), 1);
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(bar(L::bKFull + s), 1);
+      ptx::mbar_init(bar(L::bVFull + s), 1);
+      ptx::mbar_init(bar(L::bKVEmpty + s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(bar(L::bSFull + t), 1);
+      ptx::mbar_init(bar(L::bSEmpty + t), kBlockM);
+      ptx::mbar_init(bar(L::bPFull + t), kBlockM);
+      ptx::mbar_init(bar(L::bPLo + t), kBlockM);
+      ptx::mbar_init(bar(L::bPVDone + t), 1);
+      ptx::mbar_init(bar(L::bOEmpty + t), kBlockM);
+      ptx::mbar_init(bar(L::bEpiReady + t), kBlockM);
+      ptx::mbar_init(bar(L::bEpiTaken + t), kBlockM);
+      ptx::mbar_init(bar(S::bHeld + t), 1);
+    }
+    for (int s = 0; s < kSegs; ++s) {
+      ptx::mbar_init(bar(S::bSegFull + s), 1);
+      ptx::mbar_init(bar(S::bSegEmpty + s), kConsumers);
+    }
+    ptx::mbar_init(bar(L::bDrainS), 1);
+    ptx::mbar_init(bar(L::bDrainPV), 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    ptx::tma_prefetch_desc(&p.tm_q);
+    ptx::tma_prefetch_desc(&p.tm_k);
+    ptx::tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(sbase + S::kTmemSlot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kTmemSlot);
+  wait_for_inputs_and_copies();
+
+  using Regs = RegSplit<false>;
+  if (warp < kLoadWarp) {
+    ptx::setmaxnreg_inc<Regs::kSoftmax>();
+    softmax_wg<D>(p, sbase, tmem, warp >> 2, warp, lane, abort_flag);
+  } else if (warp < kEpiWarp0) {
+    ptx::setmaxnreg_dec<Regs::kIssue>();
+    if (warp == kLoadWarp) {
+      producer<D>(p, sbase, lane, abort_flag);
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) s_issuer<D>(p, sbase, tmem, abort_flag);
+    } else if (warp == kPvWarp) {
+      pv_issuer<D>(p, sbase, tmem, lane, abort_flag);
+    } else {
+      scheduler<D>(p, sbase, lane, abort_flag);
+    }
+    __syncwarp();
+  } else {
+    ptx::setmaxnreg_dec<Regs::kEpilogue>();
+    epilogue_wg<D, kOutF32>(p, sbase, tmem, warp, lane, abort_flag);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int kJoinRows = 8;  // rows (warps) of a join block
+
+// The items that more than one block worked on: a row's parts, each normalised with its lse, in the order of
+// the blocks, weighted by 2^(lse - max).
+template <int D, bool kOutF32>
+__global__ void __launch_bounds__(kJoinRows * 32) join_kernel(const __grid_constant__ PrefillParams p) {
+  wait_for_inputs();
+  const int4 m = p.meta[blockIdx.x];
+  if (m.w == 0) return;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int t = row / kBlockM, r = row % kBlockM;
+  const int i = (r * p.div_group) >> 16, tok = t * p.tile_tokens + i;
+  if (i >= p.tile_tokens || tok >= m.y) return;
+  // Part 0 is the first block's slot 1, part n the n-th next block's slot 0.
+  auto part = [&](int n) { return (static_cast<size_t>(blockIdx.x + n) * 2 + (n == 0)) * kItemRows + row; };
+  constexpr int kV = D / 32;
+  float top = -INFINITY;
+  for (int n = lane; n < m.w; n += 32) top = fmaxf(top, p.part_lse[part(n)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if (top == -INFINITY) top = 0.f;  // (no part has a key, or all are NaN, which their weights show)
+  float acc[kV] = {}, sum = 0.f;
+  for (int n0 = 0; n0 < m.w; n0 += 32) {
+    const int mine = n0 + lane;
+    // Below 0: the part has no key above -inf for this row, and counts for nothing.  (A weight that rounds to
+    // 0 still shows what is not finite.)
+    float w = mine < m.w ? p.part_lse[part(mine)] : -INFINITY;
+    w = w == -INFINITY ? -1.f : exp2f(w - top);
+    const int end = min(32, m.w - n0);
+#pragma unroll 4
+    for (int n = 0; n < end; ++n) {
+      const float wn = __shfl_sync(~0u, w, n);
+      const float* o = p.part_o + part(n0 + n) * D + lane * kV;
+      float x[kV];
+#pragma unroll
+      for (int q = 0; q < kV; ++q) x[q] = o[q];
+      if (wn < 0.f) continue;
+      sum += wn;
+#pragma unroll
+      for (int q = 0; q < kV; ++q) acc[q] = fmaf(wn, x[q], acc[q]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const size_t at = static_cast<size_t>(m.x + tok) * p.h_q + m.z * p.group + (r - i * p.group);
+  if (p.lse && lane == 0) p.lse[at] = (top + log2f(sum)) * 0.69314718055994530942f;
+  if constexpr (kOutF32) {
+    float* dst = static_cast<float*>(p.out) + at * D + lane * kV;
+#pragma unroll
+    for (int q = 0; q < kV; ++q) dst[q] = acc[q] * inv;
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at * D + lane * kV);
+#pragma unroll
+    for (int q = 0; q < kV; q += 2) dst[q / 2] = ptx::pack_bf16x2(acc[q] * inv, acc[q + 1] * inv);
+  }
+}
+
+}  // namespace prefill
+}  // namespace ditattn

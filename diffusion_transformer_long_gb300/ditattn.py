@@ -26,7 +26,8 @@ EXPORTED_SYMBOLS = ("dit_attn_fwd", "dit_attn_fwd_strided", "dit_attn_chunk_fwd"
                     "dit_attn_splitkv_workspace_bytes", "dit_attn_splitkv_suggest",
                     "dit_attn_chunk_fwd_splitkv_noalloc",
                     "dit_paged_plan", "dit_paged_kv_write", "dit_paged_attn_fwd",
-                    "dit_paged_attn_workspace_bytes", "dit_paged_select",
+                    "dit_paged_attn_workspace_bytes", "dit_paged_prefill_fwd",
+                    "dit_paged_prefill_workspace_bytes", "dit_paged_select",
                     "dit_paged_select_workspace_bytes", "dit_attn_check", "dit_test_inject_stall", "dit_test_set_grid_limit",
                     "dit_status_string", "dit_version")
 
@@ -96,6 +97,11 @@ def lib() -> ctypes.CDLL:
                                          I, F, I, P, ctypes.c_size_t, P]
         L.dit_paged_attn_workspace_bytes.restype = ctypes.c_size_t
         L.dit_paged_attn_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        L.dit_paged_prefill_fwd.restype = I
+        L.dit_paged_prefill_fwd.argtypes = [P, SP, P, SP, P, SP, P, LL, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I,
+                                            P, ctypes.c_size_t, P]
+        L.dit_paged_prefill_workspace_bytes.restype = ctypes.c_size_t
+        L.dit_paged_prefill_workspace_bytes.argtypes = [I, I, I]
         L.dit_paged_select.restype = I
         L.dit_paged_select.argtypes = [P, SP, P, P, LL, P, P, I, I, I, I, I, I, I, I, P,
                                        ctypes.c_size_t, P]
@@ -824,6 +830,12 @@ def _select_need(index, B, Hkv, max_pages):
     return lib().dit_paged_select_workspace_bytes(B, Hkv, max_pages)
 
 
+@functools.lru_cache(maxsize=4096)
+def _prefill_need(index, D, page_size, max_pages):
+    """dit_paged_prefill_workspace_bytes on the current device, number `index`."""
+    return lib().dit_paged_prefill_workspace_bytes(D, page_size, max_pages)
+
+
 def _workspace(workspace, need, device):
     """(buffer or None, its address or None, bytes) of a call's workspace: the caller's, or a new one."""
     if need == 0:
@@ -958,6 +970,58 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, selected=None, ou
         torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_paged_attn_fwd")
+    return out, lse
+
+
+def _batch_of(seq_lens):
+    """The number of requests, from their lengths."""
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be a CUDA tensor of one dimension")
+    return seq_lens.shape[0]
+
+
+def paged_prefill_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_new, start_lens=None, causal=True, out=None,
+                      lse=None, scale=None, out_dtype=torch.float32, workspace=None, stream=None, with_lse=True):
+    """dit_paged_prefill_fwd: the step's new tokens, q bf16 [T, H_q, D] (a view with contiguous D) packed in
+    request order (cu_new int32 [B + 1], paged_plan's), over the requests' seq_lens[b] cached tokens, their own
+    among them; `causal` False: every token sees all of them.  start_lens (int32 [B]): the position of each
+    request's first new token, by default such that they are its last.  Rows of no request are left as
+    they are.  The workspace is allocated with torch unless given.
+
+    Returns (out [T, H_q, D] of out_dtype, lse fp32 [T, H_q]); with_lse=False returns (out, None)."""
+    dev, index = _check_rows(q, "q", 3)
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_prefill_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_new, start_lens, causal, out, lse,
+                                     scale, out_dtype, workspace, None, with_lse)
+    T, Hq, D = q.shape
+    n_pages, Hkv, P, Dc = _check_caches(k_cache, v_cache, index)
+    if Dc != D:
+        raise ValueError(f"the caches hold heads of {Dc}, q of {D}")
+    B = _batch_of(seq_lens)
+    max_pages, stride = _check_table(block_table, seq_lens, B, index)
+    _check_tensor(cu_new, "cu_new", torch.int32, (B + 1,), index)
+    if start_lens is not None:
+        _check_tensor(start_lens, "start_lens", torch.int32, (B,), index)
+    if out is not None or lse is not None:
+        _check_out(out, lse, (T, Hq, D), dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), device=dev, dtype=out_dtype)
+    if not with_lse:
+        lse = None
+    elif lse is None:
+        lse = torch.empty((T, Hq), device=dev, dtype=torch.float32)
+    workspace, ws, size = _workspace(workspace, _prefill_need(index, D, P, max_pages), dev)
+    qn, qh, _ = q.stride()
+    st = lib().dit_paged_prefill_fwd(
+        q.data_ptr(), Strides(D, qh, qn), k_cache.data_ptr(), Strides(*k_cache.stride()[:3]), v_cache.data_ptr(),
+        Strides(*v_cache.stride()[:3]), block_table.data_ptr(), stride, seq_lens.data_ptr(), cu_new.data_ptr(),
+        None if start_lens is None else start_lens.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        T, B, Hq, Hkv, D, P, n_pages, max_pages, 1 if causal else 0, 1.0 / math.sqrt(D) if scale is None else float(scale),
+        _dt(out.dtype), ws, size, torch._C._cuda_getCurrentRawStream(index))
+    if st != DIT_OK:
+        raise DitError(st, "dit_paged_prefill_fwd")
     return out, lse
 
 

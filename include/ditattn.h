@@ -415,6 +415,54 @@ dit_status dit_paged_attn_fwd(const void* q, const dit_strides* q_strides, const
 size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D, int page_size, int pages);
 
 /*
+ * Attention of a step's new tokens over the cache: prompts, chunks of prompts, a block of video
+ * tokens behind the blocks before it, a few candidate tokens of each request.  The step's tokens are
+ * packed as dit_paged_plan packs them: request b's are the n_b rows cu_new[b] .. cu_new[b + 1] - 1 of q and
+ * out, at the positions start_b, start_b + 1 ..., their own keys and values in the cache already.  For
+ * query head h at position p, with key/value head h / (H_q / H_kv),
+ *   s_j = scale * q . k_j;  out = sum_j softmax_j(s_j) v_j;  lse = ln sum_j exp(s_j)
+ * over the cached keys j < seq_lens[b], with `causal` those j <= p.  A row that sees no key, or none that
+ * scores above -inf, gets out = 0, lse = -inf.  A score that is NaN or +inf in 32 bits makes its row NaN; a
+ * value that is not finite makes its channel of the rows that see it infinite or NaN (a weight of 0 does
+ * not hide it), and of no other row.  Weights are rounded to bf16 (off by at most 2^-8 of each, and normalised
+ * by the sum of the rounded ones), in fp32 output too; the lse is that of the unrounded ones.  Sums of weights,
+ * up to 2^8 each, times values are held in fp32 before the division: values past 2^120 / seq_lens[b] may
+ * overflow there.
+ * Rows of q in front of cu_new[0] and from cu_new[B] on have no request: their rows of out and lse are left
+ * as they are.  Work is split by the lengths on the device and joined in a fixed order: equal calls
+ * give equal bits.
+ *   q           : device bf16 view [T, H_q, D] (read); token t, head h starts t * s.n + h * s.h elements from
+ *                 the base (s.b is not used).  NULL strides: contiguous.
+ *   k_cache, v_cache, block_table, seq_lens : as above (read).  Rows past a request's length may hold
+ *                 anything, NaN included.
+ *   cu_new      : device int32 [B + 1], as dit_paged_plan writes it (read).  Entries count as within [0, T], and
+ *                 a request whose entries descend has no tokens; rows that two requests claim are left with
+ *                 either's values.
+ *   start_lens  : device int32 [B] (read), or NULL: start_b = seq_lens[b] - n_b, the request's last tokens.
+ *                 Give the lengths before the step where a request may have run out of pages: its tokens
+ *                 without a slot then keep their positions and see the keys that were stored.
+ *   out         : device [T, H_q, D] of out_dtype, contiguous, 16-byte aligned (written)
+ *   lse         : device fp32 [T, H_q] (written), or NULL
+ *   T           : 1 .. 2^30;  B : 1 .. 2^31 - 2;  H_q : a multiple of H_kv, at most 128 H_kv (above:
+ *                 DIT_ERR_UNSUPPORTED)
+ *   causal      : 0 or 1
+ *   scale       : > 0, and finite times log2 e in 32 bits
+ *   workspace   : at least dit_paged_prefill_workspace_bytes(D, page_size, max_pages) bytes; NULL where that is 0
+ */
+dit_status dit_paged_prefill_fwd(const void* q, const dit_strides* q_strides, const void* k_cache,
+                                 const dit_strides* k_strides, const void* v_cache,
+                                 const dit_strides* v_strides, const int* block_table,
+                                 long long table_stride, const int* seq_lens, const int* cu_new,
+                                 const int* start_lens, void* out, float* lse, int T, int B, int H_q,
+                                 int H_kv, int D, int page_size, int n_pages, int max_pages, int causal,
+                                 float scale, dit_dtype out_dtype, void* workspace,
+                                 size_t workspace_bytes, dit_stream stream);
+
+/* Workspace bytes of a dit_paged_prefill_fwd call with these sizes on the current device: 0 for
+ * requests with room for few keys (max_pages * page_size), which need none, and when a size is not positive. */
+size_t dit_paged_prefill_workspace_bytes(int D, int page_size, int max_pages);
+
+/*
  * The pages whose keys can score highest, for attention over those alone.  For request b
  * and key/value head g the score of page i is
  *   max over the query heads h of the group of  sum_d max(q_hd * lo_d, q_hd * hi_d)

@@ -1,0 +1,67 @@
+"""Plain 64-bit forms of the operators for prompts over the paged cache, for the tests.
+
+Written from the definitions in include/ditattn.h; shares no code with the library.
+"""
+import math
+
+import numpy as np
+import torch
+
+
+def requests(cu_new, seq_lens, T, max_len, start_lens=None):
+    """(first row, new tokens, cached keys, position of the first new token) of each request."""
+    res = []
+    for b in range(len(seq_lens)):
+        lo, hi = (min(max(int(x), 0), T) for x in (cu_new[b], cu_new[b + 1]))
+        n, length = max(0, hi - lo), min(max(int(seq_lens[b]), 0), max_len)
+        res.append((lo, n, length, length - n if start_lens is None else int(start_lens[b])))
+    return res
+
+
+def places(table, b, length, P, n_pages):
+    """(pages, rows) of the keys of request b by position; page -1: none."""
+    j = np.arange(length)
+    page = table[b, j // P] if length else np.zeros(0, np.int64)
+    return np.where((page >= 0) & (page < n_pages), page, -1), j % P
+
+
+def attend(q, k_cache, v_cache, table, seq_lens, cu_new, scale, causal=True, start_lens=None, device="cpu"):
+    """(out, lse, owned, (mag, pv)) in fp64: owned [T] tells the rows of a request; mag [T, Hq] is
+    scale max_j sum_d |q_d k_jd| over the keys that a row sees, pv [T, Hq, D] sum_j p_j |v_j|."""
+    q, k_cache, v_cache = (x.detach().to(device).double() for x in (q, k_cache, v_cache))
+    table = np.asarray(table.cpu()).astype(np.int64)
+    host = lambda x: None if x is None else [int(y) for y in x.cpu()]  # noqa: E731
+    T, Hq, D = q.shape
+    n_pages, Hkv, P = k_cache.shape[:3]
+    G = Hq // Hkv
+    o, pv = (torch.zeros(T, Hq, D, dtype=torch.float64, device=device) for _ in range(2))
+    lse = torch.full((T, Hq), -math.inf, dtype=torch.float64, device=device)
+    mag = torch.zeros(T, Hq, dtype=torch.float64, device=device)
+    owned = torch.zeros(T, dtype=torch.bool)
+    for b, (row, n, length, start) in enumerate(requests(host(cu_new), host(seq_lens), T, table.shape[1] * P,
+                                                         host(start_lens))):
+        owned[row:row + n] = True
+        if n == 0 or length == 0:
+            continue
+        page, at = places(table, b, length, P, n_pages)
+        have = torch.as_tensor(page >= 0, device=device)
+        page, at = (torch.as_tensor(np.maximum(x, 0), device=device) for x in (page, at))
+        see = have[None, :].expand(n, -1)
+        if causal:
+            pos = torch.arange(n, device=device)[:, None] + start
+            see = see & (torch.arange(length, device=device)[None, :] <= pos)
+        for h in range(Hq):
+            k, v = k_cache[page, h // G, at], v_cache[page, h // G, at]
+            x = q[row:row + n, h]
+            s = scale * (x @ k.T)
+            s = torch.where(see, s, -math.inf)
+            m = s.amax(1, keepdim=True)
+            e = torch.exp(s - torch.where(m == -math.inf, 0.0, m))
+            z = e.sum(1, keepdim=True)
+            p = e / torch.where(z > 0, z, 1.0)
+            o[row:row + n, h] = p @ v
+            pv[row:row + n, h] = p @ v.abs()
+            lse[row:row + n, h] = (m + torch.log(z))[:, 0]
+            a = torch.where(see, x.abs() @ k.abs().T, 0.0)
+            mag[row:row + n, h] = scale * a.amax(1)
+    return o.cpu(), lse.cpu(), owned, (mag.cpu(), pv.cpu())
