@@ -362,12 +362,18 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
   using S = Smem<D>;
   constexpr int kRegions = D / 64;
   auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
+  // Lane 0 waits for all.
   auto wait = [&](int b, uint32_t parity) {
-    return __all_sync(~0u, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
+    bool done = true;
+    if (lane == 0) done = wait_or_abort(bar(b), parity, abort_flag, p.wait_limit);
+    return __shfl_sync(~0u, done, 0) != 0;
   };
   const int boxes = kBlockN / p.box_rows;  // of a tile: 1, 2, 4 or 8
   const int per_batch = 32 / boxes;        // tiles looked up at once
   const int box = lane % boxes;            // the lane's box of a tile
+  // The lane copies channel block lane / boxes of its box, if there are that many.
+  const int copy_col = lane / boxes * 64;
+  const uint32_t copy_dst = sbase + L::kKV + lane / boxes * L::kRegion + box * p.box_rows * 128;
   const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * 128 * kRegions;
 
   uint32_t kpar = 0, vpar = 0;  // bit s: parity of the next K_FULL[s] / V_FULL[s] phase
@@ -435,9 +441,11 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
       kpage = __shfl_sync(~0u, page_a, from);
       kfirst = __shfl_sync(~0u, first_a, from);
     };
+    // The slot's turn comes late (three slots, two tiles in use), so that all but the copies themselves
+    // stands before the wait for it.  (The copies may complete before the bytes are expected: the phase
+    // still waits for lane 0's arrival.)
     auto load = [&](bool is_v, int page, int first) {
       const int s = it % kStages;
-      if (!wait(L::bKVEmpty + s, ((it / kStages) & 1) ^ 1)) return false;
       const int fb = (is_v ? L::bVFull : L::bKFull) + s;
       const uint32_t par = ((is_v ? vpar : kpar) >> s) & 1;
       if (is_v) vpar ^= 1u << s; else kpar ^= 1u << s;
@@ -453,14 +461,12 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
                        : "memory");
         ++tiles;
       }
+      const uint32_t dst = copy_dst + s * L::kTile;
+      const CUtensorMap* const tm = is_v ? &p.tm_v : &p.tm_k;
+      if (page < 0) page = p.n_pages;
+      if (!wait(L::bKVEmpty + s, ((it / kStages) & 1) ^ 1)) return false;
       if (lane == 0) ptx::mbar_arrive_expect_tx(bar(fb), L::kTile);
-      __syncwarp();
-      if (lane < boxes * kRegions) {
-        const int r = lane / boxes;  // channel block (the lane's box is lane % boxes)
-        ptx::tma_load_4d(sbase + L::kKV + s * L::kTile + r * L::kRegion + box * p.box_rows * 128,
-                         is_v ? &p.tm_v : &p.tm_k, bar(fb), r * 64, first, sg.h, page < 0 ? p.n_pages : page);
-      }
-      __syncwarp();
+      if (lane < boxes * kRegions) ptx::tma_load_4d(dst, tm, bar(fb), copy_col, first, sg.h, page);
 #pragma unroll
       for (int q = 0; q < kStages; ++q)
         if (q == s) {
@@ -630,10 +636,9 @@ __device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase
                        (acc || k > 0) ? 1u : 0u);
     }
   };
-  auto wait = [&](int b, uint32_t parity) {
-    return __all_sync(~0u, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
-  };
+  auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, abort_flag, p.wait_limit); };
 
+  // (lane 0's)
   uint32_t vpar = 0;
   int g[2] = {0, 0};     // PV tiles issued for each Q tile
   int used[2] = {0, 0};  // segments in which O_t was written
@@ -641,7 +646,8 @@ __device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase
   bool ok = true;
   Segments<D> segs(sbase);
   for (; ok; ++segs.n) {
-    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    if (lane == 0) ok = segs.wait(p, abort_flag);
+    if (!(ok = __shfl_sync(~0u, ok, 0) != 0)) break;
     const Segment sg = segs.read();
     if (sg.b < 0) break;
     const uint32_t held = segs.held();
@@ -649,51 +655,62 @@ __device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase
     __syncwarp();
     const int nt = sg.last() - sg.k0;
     const int seen = sg.seen_by_all(p);
-    for (int j = 0; j < nt; ++j) {
-      const int sV = (ring0 + v_item(j, nt)) % kStages;
-      ok = wait(L::bVFull + sV, (vpar >> sV) & 1);
-      vpar ^= 1u << sV;
-      if (!ok) break;
-      const int key0 = (sg.k0 + j) * kBlockN, valid = min(sg.len - key0, kBlockN);
-      if (valid < kBlockN || key0 + valid > seen) {
-        const uint32_t tile = sbase + L::kKV + sV * L::kTile;
-        if (valid < kBlockN) clear_rows<D>(tile, valid, lane);
-        if (key0 + valid > seen) {
-          if (take_out<D>(tile, valid, held + (key0 / kBlockN - seen / kBlockN) * 16, lane) && lane == 0)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(held + 4 * (kHeldWords - 1)), "r"(1) : "memory");
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-      }
+    // The tiles from `edge` on hold keys that some row does not see, or the request's last key; before them lane 0
+    // works alone, and the others wait for it without taking issue slots.
+    const int edge = max(0, min(nt, min(seen, sg.len) / kBlockN - sg.k0));
+    auto multiply = [&](int j, int sV) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!ok || sg.k0 + j >= sg.end(t)) continue;
-        if (!(ok = wait(L::bPLo + t, g[t] & 1))) continue;
+        if (sg.k0 + j >= sg.end(t)) continue;
+        if (!wait(L::bPLo + t, g[t] & 1)) return false;
         // The first PV of a segment overwrites O_t: the last one's epilogue must have read it.
         if (j == 0) {
-          if (used[t] > 0 && !(ok = wait(L::bOEmpty + t, (used[t] - 1) & 1))) continue;
+          if (used[t] > 0 && !wait(L::bOEmpty + t, (used[t] - 1) & 1)) return false;
           ++used[t];
         }
-        if (lane == 0) {
-          ptx::tc_fence_after();
-          issue(t, sV, j > 0, 0);
-        }
-        if (!(ok = wait(L::bPFull + t, g[t] & 1))) continue;
-        if (lane == 0) {
-          ptx::tc_fence_after();
-          issue(t, sV, j > 0, 1);
-          ptx::mma_commit(bar(L::bPVDone + t));
-          if (sg.k0 + j + 1 == sg.end(t)) ptx::mbar_arrive(bar(S::bHeld + t));
-        }
-        __syncwarp();
+        ptx::tc_fence_after();
+        issue(t, sV, j > 0, 0);
+        if (!wait(L::bPFull + t, g[t] & 1)) return false;
+        ptx::tc_fence_after();
+        issue(t, sV, j > 0, 1);
+        ptx::mma_commit(bar(L::bPVDone + t));
+        if (sg.k0 + j + 1 == sg.end(t)) ptx::mbar_arrive(bar(S::bHeld + t));
         ++g[t];
       }
+      ptx::mma_commit(bar(L::bKVEmpty + sV));
+      return true;
+    };
+    auto await_v = [&](int sV) {
+      const bool done = wait(L::bVFull + sV, (vpar >> sV) & 1);
+      vpar ^= 1u << sV;
+      return done;
+    };
+    if (lane == 0) {
+      for (int j = 0; ok && j < edge; ++j) {
+        const int sV = (ring0 + v_item(j, nt)) % kStages;
+        ok = await_v(sV) && multiply(j, sV);
+      }
+    }
+    ok = __shfl_sync(~0u, ok, 0) != 0;
+    for (int j = edge; ok && j < nt; ++j) {
+      const int sV = (ring0 + v_item(j, nt)) % kStages;
+      if (lane == 0) ok = await_v(sV);
+      ok = __shfl_sync(~0u, ok, 0) != 0;
       if (!ok) break;
-      if (lane == 0) ptx::mma_commit(bar(L::bKVEmpty + sV));
+      const int key0 = (sg.k0 + j) * kBlockN, valid = min(sg.len - key0, kBlockN);
+      const uint32_t tile = sbase + L::kKV + sV * L::kTile;
+      if (valid < kBlockN) clear_rows<D>(tile, valid, lane);
+      if (key0 + valid > seen) {
+        if (take_out<D>(tile, valid, held + (key0 / kBlockN - seen / kBlockN) * 16, lane) && lane == 0)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(held + 4 * (kHeldWords - 1)), "r"(1) : "memory");
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ok = multiply(j, sV);
+      ok = __shfl_sync(~0u, ok, 0) != 0;
     }
     ring0 += 2 * nt;
     if (!ok) break;
-    __syncwarp();
     if (lane == 0) segs.release();
   }
   if (!ok && lane == 0) {
@@ -768,7 +785,7 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
 
       float mx = ptx::fmax3(cmax[0], cmax[1], fmaxf(cmax[2], cmax[3]));
       const int valid = left - j * kBlockN;
-      if (valid < kBlockN || none) {
+      if (__any_sync(0xffffffffu, valid < kBlockN || none)) {
         // Keys that the row does not see are masked to -inf, so their P is exactly 0, and the max is
         // taken over the others only.
 #pragma unroll
