@@ -14,8 +14,6 @@ using namespace prefill;
 
 namespace {
 
-constexpr int kMaxBlocks = 256;  // largest grid the workspace serves
-
 // Requests with room for at most this many keys keep their items whole: one launch and no workspace.
 constexpr long long kWholeKeys = 1024;
 
@@ -70,18 +68,18 @@ cudaError_t launch(const PrefillParams& p, int blocks, cudaStream_t st) {
 }
 
 int grid_blocks() {
-  const int blocks = std::min(kMaxBlocks, host::sm_count());
+  const int blocks = std::min(kMaxGrid, host::sm_count());
   return grid_limit() > 0 ? std::min(blocks, grid_limit()) : blocks;
 }
 
 // Rows of the parts that the workspace holds: two items a block.
-size_t part_rows() { return static_cast<size_t>(std::min(kMaxBlocks, host::sm_count())) * 2 * kItemRows; }
+size_t part_rows() { return static_cast<size_t>(std::min(kMaxGrid, host::sm_count())) * 2 * kItemRows; }
 
 }  // namespace
 
 size_t paged_prefill_workspace(int d, long long keys) {
   if (keys <= kWholeKeys) return 0;
-  return part_rows() * (d + 1) * 4 + kMaxBlocks * sizeof(int4);
+  return part_rows() * (d + 1) * 4 + kMaxGrid * sizeof(int4);
 }
 
 cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {

@@ -21,12 +21,12 @@
 //   tile sees is not multiplied for it.  Values behind the request's last key are zeroed in shared memory.
 //   Values that some rows of a tile must not see are looked through for infinities and NaN, which a weight
 //   of 0 would not hide: they are taken out and given to the rows that see them at the end.
-// - Work is dealt out by cost.  A run of the batch's keys (each item's last row's, and a fixed cost an
-//   item), in the order request, head, tokens, goes to each block, whatever it belongs to: causal items are of
-//   very different lengths, and a few tokens on a long cache are few items.  A run that ends inside an item
-//   leaves fp32 parts in the workspace, at most two a block, joined in the blocks' order by a second
-//   launch: equal calls give equal bits.  Where the table has no room for long items they stay whole
-//   and there is no second launch.
+// - Work is dealt out by cost (an item's keys, and a fixed cost beside them): whole items in waves over the
+//   blocks while there are many, and the rest in runs of key tiles, whatever they belong to, such that all
+//   blocks' costs end up alike: causal items are of very different lengths, and a few tokens on a long
+//   cache are few items.  A run that ends inside an item leaves fp32 parts in the workspace, at most two a
+//   block, joined in the blocks' order by a second launch: equal calls give equal bits.  Where the table has no
+//   room for long items they stay whole and there is no second launch.
 // - One warp works the segments of the block's run out, from the lengths on the device, into a ring that the
 //   other roles read: they agree by construction and hold none of the arithmetic in registers.
 //
@@ -51,10 +51,11 @@ constexpr int kSchedWarp = 11;
 constexpr int kSegs = 4;               // segments in the ring
 constexpr int kSegWords = 16;
 constexpr int kMaskRing = 8;           // key tiles whose masks are held (the producer runs at most 3 ahead)
-constexpr int kHeldWords = 16;         // per segment: 3 tiles x 128 keys, then a flag
+constexpr int kHeldWords = 16;         // per segment: 3 tiles x 128 keys, then a flag of each epilogue warp
 constexpr int kItemCost = 256;         // what an item costs beside its keys, in keys
 constexpr int kMinRun = 512;           // a block's smallest run, in keys
 constexpr int kItemRows = 2 * kBlockM;
+constexpr int kMaxGrid = 256;          // largest grid
 constexpr int kConsumers = 3 + 8 + 4;  // of a segment: producer, two issuers, softmax and epilogue warps
 
 struct PrefillParams {
@@ -90,8 +91,9 @@ struct Smem {
   using A = AttnSmem<D>;
   static constexpr int bSegFull = A::kNumBars;  // + slot
   static constexpr int bSegEmpty = bSegFull + kSegs;
-  static constexpr int bHeld = bSegEmpty + kSegs;  // + tile: what a segment's O_t lacks is known
-  static constexpr int kNumBars = bHeld + 2;
+  static constexpr int bVEdge = bSegEmpty + kSegs;  // a value tile that some row must not see whole has landed
+  static constexpr int bVFixed = bVEdge + 1;        // ... and is ready for the product (128)
+  static constexpr int kNumBars = bVFixed + 1;
   static constexpr uint32_t kBars = A::kBars;
   static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 4;
@@ -140,15 +142,6 @@ struct Request {
     sum += m * start + tb * (m * (lo + hi + 1) / 2);
     return sum + (i - hi) * len;
   }
-  // The item of one head in which cost x lies.
-  __device__ __forceinline__ int find(const PrefillParams& p, long long x) const {
-    int lo = 0, hi = items(p) - 1;
-    while (lo < hi) {
-      const int mid = lo + (hi - lo + 1) / 2;
-      if (cost(p, mid) <= x) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  }
 };
 
 struct Segment {
@@ -171,6 +164,11 @@ struct Segment {
   }
   // Keys that every row sees.
   __device__ __forceinline__ int seen_by_all(const PrefillParams& p) const { return limit(p, 0, 0); }
+  // The segment's key tiles from this one on (counted from k0) hold keys that some row does not see, or the
+  // request's last key.
+  __device__ __forceinline__ int edge(const PrefillParams& p) const {
+    return max(0, min(last(), seen_by_all(p) / kBlockN) - k0);
+  }
   __device__ __forceinline__ bool has_token(const PrefillParams& p, int t, int r, int& tok) const {
     const int i = (r * p.div_group) >> 16;
     tok = t * p.tile_tokens + i;
@@ -181,10 +179,20 @@ struct Segment {
 using detail::Descs;
 using detail::k_item;  // K/V ring items of a segment in consumption order, as in the dense kernel
 using detail::v_item;
-using detail::wait_or_abort;
 
-__device__ __forceinline__ void raise_abort(const PrefillParams& p, volatile int* abort_flag) {
-  *abort_flag = 1;
+// The dense kernel's bounded wait and abort, by shared address (a generic pointer costs the softmax two registers).
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint32_t abort_flag, long long limit) {
+  if (ptx::mbar_test_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    int stop;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
+    if (stop || clock64() - t0 > limit) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ void raise_abort(const PrefillParams& p, uint32_t abort_flag) {
+  asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
   atomicOr(p.status, kStatusTimeout);
 }
 
@@ -197,8 +205,8 @@ struct Segments {
   __device__ __forceinline__ uint32_t bar(int i) const { return sbase + Smem<D>::kBars + 8u * i; }
   __device__ __forceinline__ uint32_t slot() const { return sbase + Smem<D>::kSeg + (n % kSegs) * kSegWords * 4; }
   __device__ __forceinline__ uint32_t held() const { return sbase + Smem<D>::kHeld + (n % kSegs) * kHeldWords * 4; }
-  __device__ __forceinline__ bool wait(const PrefillParams& p, const volatile int* abort_flag) const {
-    return wait_or_abort(bar(Smem<D>::bSegFull + n % kSegs), (n / kSegs) & 1, abort_flag, p.wait_limit);
+  __device__ __forceinline__ bool wait(const PrefillParams& p) const {
+    return wait_or_abort(bar(Smem<D>::bSegFull + n % kSegs), (n / kSegs) & 1, sbase + Smem<D>::kAbort, p.wait_limit);
   }
   __device__ __forceinline__ Segment read() const {
     int w[12];
@@ -214,30 +222,52 @@ struct Segments {
   __device__ __forceinline__ void release() const { ptx::mbar_arrive(bar(Smem<D>::bSegEmpty + n % kSegs)); }
 };
 
-// The block's run, segment by segment (one warp).
+// The block's segments (one warp).  Items count in the order request, block of tokens, head, so that the blocks of
+// a wave work on neighbouring items, side by side through the same keys (with the heads outermost and a run of items to
+// each block, 152 places of all heads' keys were read at once: 27280 keys, 24 heads, 25 % of the reads hit L2).
+// Waves of whole items go over the blocks, to and fro, for as long as no block has more than its share of the cost;
+// what is left is dealt out so that all blocks' costs end up alike.
 template <int D>
-__device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase, int lane, volatile int* abort_flag) {
+__device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase, int lane) {
   using S = Smem<D>;
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, grid = gridDim.x;
   Request rq;
-  long long total = 0;
+  long long total = 0, items = 0;
+  int least = 0x7fffffff, most = -1;  // keys of the shortest and the longest item
   for (int b = lane; b < p.batch; b += 32) {
     rq.load(p, b);
-    total += rq.cost(p, rq.items(p));
+    const int nb = rq.items(p);
+    total += rq.cost(p, nb);
+    items += nb;
+    if (nb > 0) {  // (item_keys does not fall with the item)
+      least = min(least, rq.item_keys(p, 0));
+      most = max(most, rq.item_keys(p, nb - 1));
+    }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  for (int o = 16; o; o >>= 1) {
+    total += __shfl_xor_sync(~0u, total, o);
+    items += __shfl_xor_sync(~0u, items, o);
+  }
   total *= p.h_kv;
-  const long long blocks = min(static_cast<long long>(gridDim.x), max(1LL, total / kMinRun));
-  const long long run0 = c < blocks ? total * c / blocks : total, run1 = c < blocks ? total * (c + 1) / blocks : total;
+  items *= p.h_kv;
+  least = __reduce_min_sync(~0u, least);
+  most = __reduce_max_sync(~0u, most);
+  const bool even = least == most;
+  const long long share = total / grid;
+  // Waves that are safe without looking at the blocks' loads.
+  long long waves = p.split ? items / grid : (items + grid - 1) / grid;
+  if (p.split && !even) waves = min(waves, min(2LL, share / (most + kItemCost)));
+
   int4 meta = make_int4(0, 0, 0, 0);
   int n = 0;  // segments written
   bool ok = true;
   auto emit = [&](const Segment& s) {
     const int slot = n % kSegs;
     if (n >= kSegs) {
-      ok = wait_or_abort(sbase + S::kBars + 8u * (S::bSegEmpty + slot), (n / kSegs - 1) & 1, abort_flag, p.wait_limit);
-      ok = __all_sync(~0u, ok);
+      if (lane == 0)
+        ok = wait_or_abort(sbase + S::kBars + 8u * (S::bSegEmpty + slot), (n / kSegs - 1) & 1, sbase + Smem<D>::kAbort, p.wait_limit);
+      ok = __shfl_sync(~0u, ok, 0) != 0;
       if (!ok) return;
     }
     if (lane == 0) {
@@ -252,96 +282,208 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
     }
     ++n;
   };
-  if (run0 < run1) {
-    // The request in which the run begins, 32 at a time.
-    int b = 0;
-    long long base = 0;  // cost of the requests before b
-    for (;; b += 32) {
+  // Key tiles [a, e) of item i of request b, for head h.
+  auto emit_item = [&](int b, int i, int h, int a, int e, int ntiles) {
+    Segment s;
+    s.b = b;
+    s.h = h;
+    const int t0 = i * 2 * p.tile_tokens;
+    s.row0 = rq.row0 + t0;
+    s.ntok = min(rq.n - t0, 2 * p.tile_tokens);
+    s.len = rq.len;
+    s.pos0 = static_cast<int>(max(min(rq.start + t0, static_cast<long long>(rq.len)), -(1LL << 30)));
+    s.k0 = a;
+    const int f0 = (rq.seen(p, t0 + min(s.ntok, p.tile_tokens)) + kBlockN - 1) / kBlockN;
+    s.e0 = max(a, min(f0, e));
+    s.e1 = s.ntok > p.tile_tokens ? e : a;
+    s.kind = a == 0 && e == ntiles ? 0 : a == 0 ? 2 : 1;
+    emit(s);
+  };
+  // The first request, from b on, up to which `value` (of a request, in rq) adds up to more than x - base; base becomes
+  // the sum before it.  b = batch: there is none.
+  auto seek = [&](int& b, long long& base, long long x, auto value) {
+    for (; b < p.batch; b += 32) {
       long long mine = 0;
       if (b + lane < p.batch) {
         rq.load(p, b + lane);
-        mine = rq.cost(p, rq.items(p)) * p.h_kv;
+        mine = value();
       }
       long long upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += x;
+        const long long y = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += y;
       }
-      const unsigned past = __ballot_sync(~0u, base + upto > run0);
+      const unsigned past = __ballot_sync(~0u, base + upto > x);
       if (past) {
         const int l = __ffs(past) - 1;
         base += __shfl_sync(~0u, upto - mine, l);
         b += l;
-        break;
+        rq.load(p, b);
+        return;
       }
       base += __shfl_sync(~0u, upto, 31);
     }
-    rq.load(p, b);
-    int nb = rq.items(p);
-    const long long per_head = rq.cost(p, nb);
-    int h = static_cast<int>((run0 - base) / per_head);
-    long long x0 = run0 - base - h * per_head;
-    int i = rq.find(p, x0);
-    x0 -= rq.cost(p, i);
-    long long at = run0;  // x0's place in the whole
-    while (ok) {
-      const int keys = rq.item_keys(p, i);
-      const long long cost = static_cast<long long>(keys) + kItemCost, take = min(cost - x0, run1 - at);
-      const int ntiles = (keys + kBlockN - 1) / kBlockN;
-      auto cut = [&](long long x) { return x >= keys ? ntiles : static_cast<int>((x + kBlockN - 1) / kBlockN); };
-      int a = cut(x0), e = cut(x0 + take);
-      bool any = a < e || (ntiles == 0 && x0 == 0);
-      if (!p.split) {  // an item goes to the block in whose run it begins
-        any = x0 == 0;
-        a = 0;
-        e = ntiles;
-      }
-      if (any) {
-        Segment s;
-        s.b = b;
-        s.h = h;
-        const int t0 = i * 2 * p.tile_tokens;
-        s.row0 = rq.row0 + t0;
-        s.ntok = min(rq.n - t0, 2 * p.tile_tokens);
-        s.len = rq.len;
-        s.pos0 = static_cast<int>(max(min(rq.start + t0, static_cast<long long>(rq.len)), -(1LL << 30)));
-        s.k0 = a;
-        const int f0 = (rq.seen(p, t0 + min(s.ntok, p.tile_tokens)) + kBlockN - 1) / kBlockN;
-        s.e0 = max(a, min(f0, e));
-        s.e1 = s.ntok > p.tile_tokens ? e : a;
-        s.kind = a == 0 && e == ntiles ? 0 : a == 0 ? 2 : 1;
-        if (s.kind == 2) {
-          // The item's last part is in the first block whose run ends behind the item's last tile's start.
-          const long long x = at - x0 + static_cast<long long>(ntiles - 1) * kBlockN;
-          const long long last = ((x + 1) * blocks + total - 1) / total - 1;
-          meta = make_int4(s.row0, s.ntok, h, static_cast<int>(last) - c + 1);
+  };
+
+  int wave_b = 0;
+  long long wave_base = 0, wave_have = 0;  // items before request wave_b, and its own
+  auto emit_waves = [&](long long k0, long long k1) {
+    for (long long k = k0; ok && k < k1; ++k) {
+      const long long w = k * grid + (k & 1 ? grid - 1 - c : c);
+      if (w >= items) continue;
+      if (w >= wave_base + wave_have)
+        seek(wave_b, wave_base, w, [&] { return static_cast<long long>(rq.items(p)) * p.h_kv; });
+      else
+        rq.load(p, wave_b);
+      wave_have = static_cast<long long>(rq.items(p)) * p.h_kv;
+      const int i = static_cast<int>((w - wave_base) / p.h_kv);
+      const int h = static_cast<int>(w - wave_base - static_cast<long long>(i) * p.h_kv);
+      const int ntiles = (rq.item_keys(p, i) + kBlockN - 1) / kBlockN;
+      emit_item(wave_b, i, h, 0, ntiles, ntiles);
+    }
+  };
+  emit_waves(0, waves);
+
+  if (ok && p.split && waves * grid < items) {
+    // Each lane holds the loads of kOwn blocks in a row, then their shares of the rest, then where their runs end.
+    constexpr int kOwn = kMaxGrid / 32;
+    long long end[kOwn];
+    long long before = 0;  // cost of what the waves took
+    if (even) {
+      before = total / items * (waves * grid);
+    } else if (waves > 0) {
+#pragma unroll
+      for (int q = 0; q < kOwn; ++q) end[q] = 0;
+      int b = 0;
+      long long base = 0, have = 0;
+      rq.load(p, 0);
+      have = static_cast<long long>(rq.items(p)) * p.h_kv;
+      const long long sure = waves, most_waves = items / grid;
+      for (long long k = 0; k < most_waves; ++k) {
+        int cost[kOwn];
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q) {
+          // In the order of the items: of block lane kOwn + q, or on the way back of lane kOwn + kOwn - 1 - q.
+          const int x = lane * kOwn + (k & 1 ? kOwn - 1 - q : q);
+          cost[q] = 0;
+          if (x >= grid) continue;
+          const long long w = k * grid + (k & 1 ? grid - 1 - x : x);
+          while (w >= base + have) {
+            base += have;
+            rq.load(p, ++b);
+            have = static_cast<long long>(rq.items(p)) * p.h_kv;
+          }
+          cost[q] = rq.item_keys(p, static_cast<int>((w - base) / p.h_kv)) + kItemCost;
         }
-        emit(s);
+        bool over = false;
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q) over |= end[q] + (k & 1 ? cost[kOwn - 1 - q] : cost[q]) > share;
+        if (k >= sure && __any_sync(~0u, over)) break;
+#pragma unroll
+        for (int q = 0; q < kOwn; ++q) end[q] += k & 1 ? cost[kOwn - 1 - q] : cost[q];
+        waves = k + 1;
       }
-      at += take;
-      if (at >= run1) break;
-      x0 = 0;
-      if (++i == nb) {
-        i = 0;
+      emit_waves(sure, waves);
+#pragma unroll
+      for (int q = 0; q < kOwn; ++q) before += end[q];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(~0u, before, o);
+    }
+    if (even || waves == 0 || total - before < static_cast<long long>(grid) * kMinRun) {
+      const long long blocks = min(static_cast<long long>(grid), max(1LL, (total - before) / kMinRun));
+#pragma unroll
+      for (int q = 0; q < kOwn; ++q) end[q] = lane * kOwn + q < blocks ? 1 : 0;
+    } else {
+#pragma unroll
+      for (int q = 0; q < kOwn; ++q) {
+        const long long rest = share - end[q];
+        end[q] = lane * kOwn + q < grid && rest > 0 ? rest : 0;
+      }
+    }
+    long long mine = 0;
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) mine = end[q] += mine;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const long long all = __shfl_sync(~0u, upto, 31);
+    const double unit = static_cast<double>(total - before) / static_cast<double>(max(1LL, all));
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) {
+      const long long x = upto - mine + end[q];  // of `all` (none: the first block's)
+      end[q] = x == all ? total : before + static_cast<long long>(static_cast<double>(x) * unit);
+    }
+    // This block's run: [run0, run1).
+    long long run0 = before, run1 = before;
+    {
+      long long x0 = 0, x1 = 0;
+#pragma unroll
+      for (int q = 0; q < kOwn; ++q) {
+        if (q == (c + kOwn - 1) % kOwn) x0 = end[q];
+        if (q == c % kOwn) x1 = end[q];
+      }
+      x0 = __shfl_sync(~0u, x0, ((c + kOwn - 1) / kOwn - 1) & 31);
+      run1 = __shfl_sync(~0u, x1, c / kOwn);
+      if (c > 0) run0 = x0;
+    }
+    if (ok && run0 < total) {
+      int b = 0;
+      long long base = 0;
+      seek(b, base, run0, [&] { return rq.cost(p, rq.items(p)) * p.h_kv; });
+      int nb = rq.items(p);
+      // Item i, head h, and how far into its cost.
+      int i, h;
+      long long x0;
+      {
+        int lo = 0, hi = nb - 1;
+        while (lo < hi) {
+          const int mid = lo + (hi - lo + 1) / 2;
+          if (rq.cost(p, mid) * p.h_kv <= run0 - base) lo = mid; else hi = mid - 1;
+        }
+        i = lo;
+        x0 = run0 - base - rq.cost(p, i) * p.h_kv;
+        const long long each = static_cast<long long>(rq.item_keys(p, i)) + kItemCost;
+        h = static_cast<int>(x0 / each);
+        x0 -= h * each;
+      }
+      long long at = run0;  // x0's place in the whole
+      while (ok) {
+        const int keys = rq.item_keys(p, i);
+        const long long cost = static_cast<long long>(keys) + kItemCost, take = min(cost - x0, run1 - at);
+        const int ntiles = (keys + kBlockN - 1) / kBlockN;
+        auto cut = [&](long long x) { return x >= keys ? ntiles : static_cast<int>((x + kBlockN - 1) / kBlockN); };
+        const int a = cut(x0), e = cut(x0 + take);
+        // A run that meets an item begun before has a part of it, if an empty one, unless its tiles are all done.
+        if (a < e || (ntiles == 0 && x0 == 0 && take > 0) || (x0 > 0 && a < ntiles)) {
+          if (a == 0 && e < ntiles) {
+            // The item's last part is in the first block whose run ends behind the item's last tile's start.
+            const long long x = at - x0 + static_cast<long long>(ntiles - 1) * kBlockN;
+            int last = 0;
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q) last += lane * kOwn + q < grid && end[q] <= x;
+            last = __reduce_add_sync(~0u, last);
+            const int t0 = i * 2 * p.tile_tokens;
+            meta = make_int4(rq.row0 + t0, min(rq.n - t0, 2 * p.tile_tokens), h, last - c + 1);
+          }
+          emit_item(b, i, h, a, e, ntiles);
+        }
+        at += take;
+        if (at >= run1) break;
+        x0 = 0;
         if (++h == p.h_kv) {
           h = 0;
-          // The next request with new tokens.
-          for (++b; b < p.batch; b += 32) {
-            bool has = false;
-            if (b + lane < p.batch) {
-              rq.load(p, b + lane);
-              has = rq.n > 0;
-            }
-            const unsigned some = __ballot_sync(~0u, has);
-            if (some) {
-              b += __ffs(some) - 1;
-              break;
-            }
+          if (++i == nb) {
+            i = 0;
+            ++b;
+            long long none = 0;
+            seek(b, none, 0, [&] { return static_cast<long long>(rq.n); });  // the next with new tokens
+            if (b >= p.batch) break;  // (not reached: the run would have ended)
+            nb = rq.items(p);
           }
-          if (b >= p.batch) break;  // (not reached: the run would have ended)
-          rq.load(p, b);
-          nb = rq.items(p);
         }
       }
     }
@@ -352,12 +494,12 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
     emit(s);
   }
   if (p.split && lane == 0) p.meta[c] = meta;
-  if (!ok) raise_abort(p, abort_flag);
+  if (!ok) raise_abort(p, sbase + Smem<D>::kAbort);
 }
 
 // Copies: Q of each segment, then its key and value tiles (one warp; each lane its own rows of a tile).
 template <int D>
-__device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase, int lane, volatile int* abort_flag) {
+__device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase, int lane) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
   constexpr int kRegions = D / 64;
@@ -365,7 +507,7 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
   // Lane 0 waits for all.
   auto wait = [&](int b, uint32_t parity) {
     bool done = true;
-    if (lane == 0) done = wait_or_abort(bar(b), parity, abort_flag, p.wait_limit);
+    if (lane == 0) done = wait_or_abort(bar(b), parity, sbase + Smem<D>::kAbort, p.wait_limit);
     return __shfl_sync(~0u, done, 0) != 0;
   };
   const int boxes = kBlockN / p.box_rows;  // of a tile: 1, 2, 4 or 8
@@ -388,7 +530,7 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
   bool ok = true;
   Segments<D> segs(sbase);
   for (;; ++segs.n) {
-    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    if (!(ok = __all_sync(~0u, segs.wait(p)))) break;
     const Segment sg = segs.read();
     __syncwarp();
     if (lane == 0) segs.release();
@@ -491,7 +633,7 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
     if (!ok) break;
   }
   if (!ok) {
-    if (lane == 0) raise_abort(p, abort_flag);
+    if (lane == 0) raise_abort(p, sbase + Smem<D>::kAbort);
     // Let every copy this warp started land before the block can exit.
     if (q_loads > 0) ptx::mbar_wait(bar(L::bQFull), (q_loads - 1) & 1, p.wait_limit);
 #pragma unroll
@@ -502,8 +644,7 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
 
 // S_t = Q_t K^T (one thread).
 template <int D>
-__device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem,
-                                         volatile int* abort_flag) {
+__device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem) {
   using L = AttnSmem<D>;
   auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
   constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBlockM, kBlockN, false, false);
@@ -517,7 +658,7 @@ __device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase,
       ptx::mma_bf16_ss(tmem + t * kBlockN, Descs<D>::full(qa + off), Descs<D>::full(kb + off), kIdesc, k > 0 ? 1u : 0u);
     }
   };
-  auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, abort_flag, p.wait_limit); };
+  auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, sbase + Smem<D>::kAbort, p.wait_limit); };
 
   uint32_t kpar = 0;
   int g[2] = {0, 0};  // S tiles issued for each Q tile
@@ -525,7 +666,7 @@ __device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase,
   bool ok = true;
   Segments<D> segs(sbase);
   for (; ok; ++segs.n) {
-    if (!(ok = segs.wait(p, abort_flag))) break;
+    if (!(ok = segs.wait(p))) break;
     const Segment sg = segs.read();
     segs.release();
     if (sg.b < 0) break;
@@ -555,7 +696,7 @@ __device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase,
     ring0 += 2 * nt;
   }
   if (!ok) {
-    raise_abort(p, abort_flag);
+    raise_abort(p, sbase + Smem<D>::kAbort);
     ptx::mma_commit(bar(L::bDrainS));
     ptx::mbar_wait(bar(L::bDrainS), 0, p.wait_limit);
   }
@@ -564,63 +705,44 @@ __device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase,
 // A bit in each half of w whose bf16 is infinite or NaN: bits 15 and 31.
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
-// Row i, 16-byte piece ch (whole rows are gone through, so the swizzle does not matter) of a value tile.
+// Row `row` of a value tile, before the products: zeros if it is not one of the first `valid` (a weight of 0 does not
+// hide what a page holds behind the request's last key), and else, where `look`, without its infinities and NaN;
+// true: it had some.  (The epilogue's threads, a row each; whole rows are gone through, in an order that spreads the
+// banks, so the swizzle does not matter.)
 template <int D>
-__device__ __forceinline__ uint32_t v_piece(uint32_t tile, int i, int ch) {
-  return tile + (ch / 8) * AttnSmem<D>::kRegion + i * 128 + (ch % 8) * 16;
-}
-
-// Rows [valid, 128) of a value tile become zeros: a weight of 0 does not hide what a page holds behind
-// the request's last key.  (One warp.)
-template <int D>
-__device__ __forceinline__ void clear_rows(uint32_t tile, int valid, int lane) {
-  for (int x = lane; x < (kBlockN - valid) * (D / 8); x += 32)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v_piece<D>(tile, valid + x / (D / 8), x % (D / 8))),
-                 "r"(0)
-                 : "memory");
-}
-
-// Infinities and NaN in the first `valid` rows of a value tile become 0; four words of the rows that
-// had one (bit l of word i: row 32 i + l) go to `words`.  Returns whether any had.  (One warp, a row a lane.)
-template <int D>
-__device__ __forceinline__ bool take_out(uint32_t tile, int valid, uint32_t words, int lane) {
-  bool any = false;
-  for (int i = 0; i < 4; ++i) {
-    const int row = 32 * i + lane;
-    uint32_t bad = 0;
-    if (row < valid) {
-#pragma unroll 4
-      for (int ch = 0; ch < D / 8; ++ch) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(v_piece<D>(tile, row, (ch & 8) | ((ch + lane) & 7)))
+__device__ __forceinline__ bool fix_row(uint32_t tile, int row, int valid, bool look) {
+  const uint32_t at = tile + row * 128;
+  uint32_t bad = 0;
+#pragma unroll 1
+  for (int ch = 0; ch < D / 8; ++ch) {
+    const uint32_t piece = at + (ch / 8) * AttnSmem<D>::kRegion + ((ch + row) & 7) * 16;
+    if (row >= valid) {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece), "r"(0) : "memory");
+    } else if (look) {
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(piece)
+                   : "memory");
+      uint32_t here = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t f = non_finite(w[i]);
+        here |= f;
+        w[i] &= ~(((f >> 15) & 1) * 0xffffu | (f >> 31) * 0xffff0000u);
+      }
+      if (here)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                      : "memory");
-        bad |= non_finite(w[0]) | non_finite(w[1]) | non_finite(w[2]) | non_finite(w[3]);
-      }
-    }
-    const unsigned rows = __ballot_sync(~0u, bad != 0);
-    if (rows == 0) continue;
-    any = true;
-    if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(words + 4 * i), "r"(rows) : "memory");
-    if (bad) {
-      for (int x = 0; x < D / 2; ++x) {
-        const uint32_t at = v_piece<D>(tile, row, x / 4) + (x % 4) * 4;
-        uint32_t w;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-        const uint32_t f = non_finite(w);
-        const uint32_t keep = ~(((f >> 15) & 1) * 0xffffu | (f >> 31) * 0xffff0000u);
-        if (f) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w & keep) : "memory");
-      }
+      bad |= here;
     }
   }
-  return any;
+  return bad != 0;
 }
 
-// O_t += P_t V (one warp; lane 0 issues).
+// O_t += P_t V (one thread: what lanes wait for one another costs here, each product waits for).
 template <int D>
-__device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int lane,
-                                          volatile int* abort_flag) {
+__device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
   auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
@@ -636,85 +758,60 @@ __device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase
                        (acc || k > 0) ? 1u : 0u);
     }
   };
-  auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, abort_flag, p.wait_limit); };
+  auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, sbase + S::kAbort, p.wait_limit); };
 
-  // (lane 0's)
-  uint32_t vpar = 0;
-  int g[2] = {0, 0};     // PV tiles issued for each Q tile
-  int used[2] = {0, 0};  // segments in which O_t was written
+  uint32_t vpar = 0, fixed = 0;
+  int g[2] = {0, 0};           // PV tiles issued for each Q tile
+  uint32_t used[2] = {1, 1};   // parity of O_EMPTY for the last segment that wrote O_t
   int ring0 = 0;
   bool ok = true;
   Segments<D> segs(sbase);
   for (; ok; ++segs.n) {
-    if (lane == 0) ok = segs.wait(p, abort_flag);
-    if (!(ok = __shfl_sync(~0u, ok, 0) != 0)) break;
-    const Segment sg = segs.read();
-    if (sg.b < 0) break;
-    const uint32_t held = segs.held();
-    if (lane < kHeldWords) asm volatile("st.shared.b32 [%0], %1;" ::"r"(held + 4 * lane), "r"(0) : "memory");
-    __syncwarp();
-    const int nt = sg.last() - sg.k0;
-    const int seen = sg.seen_by_all(p);
-    // The tiles from `edge` on hold keys that some row does not see, or the request's last key; before them lane 0
-    // works alone, and the others wait for it without taking issue slots.
-    const int edge = max(0, min(nt, min(seen, sg.len) / kBlockN - sg.k0));
-    auto multiply = [&](int j, int sV) {
+    if (!(ok = segs.wait(p))) break;
+    int nt0, nt1, edge;
+    {
+      const Segment sg = segs.read();
+      if (sg.b < 0) break;
+      nt0 = sg.e0 - sg.k0;
+      nt1 = sg.e1 - sg.k0;
+      edge = sg.edge(p);
+    }
+    segs.release();
+    const int nt = max(nt0, nt1);
+    for (int j = 0; j < nt; ++j) {
+      const int sV = (ring0 + v_item(j, nt)) % kStages;
+      ok = wait(L::bVFull + sV, (vpar >> sV) & 1);
+      vpar ^= 1u << sV;
+      if (!ok) break;
+      if (j >= edge) {
+        ptx::mbar_arrive(bar(S::bVEdge));
+        if (!(ok = wait(S::bVFixed, fixed))) break;
+        fixed ^= 1;
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (sg.k0 + j >= sg.end(t)) continue;
-        if (!wait(L::bPLo + t, g[t] & 1)) return false;
+        if (!ok || j >= (t ? nt1 : nt0)) continue;
+        if (!(ok = wait(L::bPLo + t, g[t] & 1))) continue;
         // The first PV of a segment overwrites O_t: the last one's epilogue must have read it.
         if (j == 0) {
-          if (used[t] > 0 && !wait(L::bOEmpty + t, (used[t] - 1) & 1)) return false;
-          ++used[t];
+          if (!(ok = wait(L::bOEmpty + t, used[t]))) continue;  // (nothing to wait for the first time)
+          used[t] ^= 1;
         }
         ptx::tc_fence_after();
         issue(t, sV, j > 0, 0);
-        if (!wait(L::bPFull + t, g[t] & 1)) return false;
+        if (!(ok = wait(L::bPFull + t, g[t] & 1))) continue;
         ptx::tc_fence_after();
         issue(t, sV, j > 0, 1);
         ptx::mma_commit(bar(L::bPVDone + t));
-        if (sg.k0 + j + 1 == sg.end(t)) ptx::mbar_arrive(bar(S::bHeld + t));
         ++g[t];
       }
-      ptx::mma_commit(bar(L::bKVEmpty + sV));
-      return true;
-    };
-    auto await_v = [&](int sV) {
-      const bool done = wait(L::bVFull + sV, (vpar >> sV) & 1);
-      vpar ^= 1u << sV;
-      return done;
-    };
-    if (lane == 0) {
-      for (int j = 0; ok && j < edge; ++j) {
-        const int sV = (ring0 + v_item(j, nt)) % kStages;
-        ok = await_v(sV) && multiply(j, sV);
-      }
-    }
-    ok = __shfl_sync(~0u, ok, 0) != 0;
-    for (int j = edge; ok && j < nt; ++j) {
-      const int sV = (ring0 + v_item(j, nt)) % kStages;
-      if (lane == 0) ok = await_v(sV);
-      ok = __shfl_sync(~0u, ok, 0) != 0;
       if (!ok) break;
-      const int key0 = (sg.k0 + j) * kBlockN, valid = min(sg.len - key0, kBlockN);
-      const uint32_t tile = sbase + L::kKV + sV * L::kTile;
-      if (valid < kBlockN) clear_rows<D>(tile, valid, lane);
-      if (key0 + valid > seen) {
-        if (take_out<D>(tile, valid, held + (key0 / kBlockN - seen / kBlockN) * 16, lane) && lane == 0)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(held + 4 * (kHeldWords - 1)), "r"(1) : "memory");
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ok = multiply(j, sV);
-      ok = __shfl_sync(~0u, ok, 0) != 0;
+      ptx::mma_commit(bar(L::bKVEmpty + sV));
     }
     ring0 += 2 * nt;
-    if (!ok) break;
-    if (lane == 0) segs.release();
   }
-  if (!ok && lane == 0) {
-    raise_abort(p, abort_flag);
+  if (!ok) {
+    raise_abort(p, sbase + S::kAbort);
     ptx::mma_commit(bar(L::bDrainPV));
     ptx::mbar_wait(bar(L::bDrainPV), 0, p.wait_limit);
   }
@@ -723,7 +820,7 @@ __device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase
 // Softmax of Q tile t (four warps, a row a thread).
 template <int D>
 __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int t, int warp,
-                                           int lane, volatile int* abort_flag) {
+                                           int lane) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
   auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
@@ -736,16 +833,16 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
   const uint32_t sw = static_cast<uint32_t>(r & 7);
   const float c = p.scale_log2;
   auto wait = [&](int b, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
+    return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, sbase + Smem<D>::kAbort, p.wait_limit));
   };
 
   int g = 0;      // tiles processed by this warpgroup
   int tiles = 0;  // key tiles of the block so far, for their masks
-  int li = 0;     // segments handed to the epilogue
+  uint32_t taken = 1;  // parity of EPI_TAKEN for the last segment
   bool ok = true;
   Segments<D> segs(sbase);
   for (; ok; ++segs.n) {
-    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    if (!(ok = __all_sync(~0u, segs.wait(p)))) break;
     int nt, left;  // the Q tile's key tiles; the row's keys from the first of them on
     {
       const Segment sg = segs.read();
@@ -762,7 +859,8 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
     float m = -INFINITY;  // running max of scale*log2e*s (possibly stale by < 2^8)
     float l = 0.f;        // running sum of 2^(c*s - m), for the LSE
     float lp = 0.f;       // running sum of the bf16-rounded P the PV GEMM sees, for O
-    for (int j = 0; j < nt; ++j, ++g) {
+    bool first = true;
+    for (; nt > 0; --nt, ++g, ++tiles, left -= kBlockN, first = false) {
       if (!(ok = wait(L::bSFull + t, g & 1))) break;
       ptx::tc_fence_after();
       float s[kBlockN];
@@ -777,20 +875,26 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
       uint32_t none;  // 16-key pieces without a page
       asm volatile("ld.shared.b32 %0, [%1];"
                    : "=r"(none)
-                   : "r"(sbase + S::kMasks + 4 * ((tiles + j) % kMaskRing))
+                   : "r"(sbase + S::kMasks + 4 * (tiles % kMaskRing))
                    : "memory");
       ptx::tmem_wait_ld();
       ptx::tc_fence_before();
       ptx::mbar_arrive(bar(L::bSEmpty + t));
 
       float mx = ptx::fmax3(cmax[0], cmax[1], fmaxf(cmax[2], cmax[3]));
-      const int valid = left - j * kBlockN;
-      if (__any_sync(0xffffffffu, valid < kBlockN || none)) {
+      // (The branches that few tiles take are marked, so that their code stands apart: in the loop's midst it
+      // starved the warps of instructions.)
+      if (__builtin_expect(__any_sync(0xffffffffu, left < kBlockN || none), 0)) {
         // Keys that the row does not see are masked to -inf, so their P is exactly 0, and the max is
         // taken over the others only.
 #pragma unroll
         for (int i = 0; i < kBlockN; ++i)
-          if (i >= valid || ((none >> (i / 16)) & 1)) s[i] = -INFINITY;
+          if (i >= left) s[i] = -INFINITY;
+        if (__builtin_expect(none != 0, 0)) {
+#pragma unroll
+          for (int i = 0; i < kBlockN; ++i)
+            if ((none >> (i / 16)) & 1) s[i] = -INFINITY;
+        }
         float a[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -811,7 +915,7 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
       l *= alpha;
       lp *= alpha;
       bool pv_prev_done = (g == 0);
-      if (j > 0 && __any_sync(0xffffffffu, raise)) {
+      if (__builtin_expect(!first && __any_sync(0xffffffffu, raise), 0)) {
         if (!(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
         pv_prev_done = true;
         ptx::tc_fence_after();
@@ -878,24 +982,24 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
 
     // 1 / sum to the epilogue (0: no key scored above -inf), the LSE to where it goes.
     const Segment sg = segs.read();
-    tiles += sg.last() - sg.k0;
+    tiles += sg.last() - sg.end(t);
     const float lse2 = m + log2f(l);
-    if (li > 0 && !(ok = wait(L::bEpiTaken + t, (li - 1) & 1))) break;
+    if (!(ok = wait(L::bEpiTaken + t, taken))) break;  // (the first time there is nothing to wait for)
+    taken ^= 1;
     reinterpret_cast<float*>(__cvta_shared_to_generic(sbase + S::kInvLp))[t * kBlockM + r] = lp == 0.f ? 0.f : 1.f / lp;
     ptx::mbar_arrive(bar(L::bEpiReady + t));
-    ++li;
     int tok;
     if (sg.has_token(p, t, r, tok)) {
       const int head = r - ((r * p.div_group) >> 16) * p.group;
       if (sg.kind)
-        p.part_lse[(static_cast<size_t>(blockIdx.x) * 2 + (sg.kind - 1)) * kItemRows + t * kBlockM + r] = lse2;
+        p.part_lse[(static_cast<int>(blockIdx.x) * 2 + sg.kind - 1) * kItemRows + t * kBlockM + r] = lse2;
       else if (p.lse)
-        p.lse[static_cast<size_t>(sg.row0 + tok) * p.h_q + sg.h * p.group + head] = lse2 * 0.69314718055994530942f;
+        p.lse[(sg.row0 + tok) * p.h_q + sg.h * p.group + head] = lse2 * 0.69314718055994530942f;
     }
     __syncwarp();
     if (lane == 0) segs.release();
   }
-  if (!ok) raise_abort(p, abort_flag);
+  if (!ok) raise_abort(p, sbase + Smem<D>::kAbort);
 }
 
 // What the PV products left out: the infinities and NaN among the values that some rows of the item do not
@@ -903,7 +1007,8 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
 template <int D, typename T>
 __device__ __forceinline__ void give_back(const PrefillParams& p, const Segment& sg, uint32_t held, int limit, T* dst) {
   const int tile0 = sg.seen_by_all(p) / kBlockN;
-  for (int w = 0; w < kHeldWords - 1; ++w) {
+  #pragma unroll 1
+  for (int w = 0; w < 12; ++w) {
     uint32_t rows;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(rows) : "r"(held + 4 * w) : "memory");
     for (; rows; rows &= rows - 1) {
@@ -912,6 +1017,7 @@ __device__ __forceinline__ void give_back(const PrefillParams& p, const Segment&
       const int page = p.table[sg.b * p.table_stride + key / p.page_size];
       if (page < 0 || page >= p.n_pages) continue;
       const __nv_bfloat16* v = p.v_cache + page * p.vs.b_ + sg.h * p.vs.h_ + (key % p.page_size) * p.vs.n_;
+#pragma unroll 1
       for (int i = 0; i < D; ++i) {
         const float f = __bfloat162float(v[i]);
         if (isfinite(f)) continue;
@@ -927,8 +1033,7 @@ __device__ __forceinline__ void give_back(const PrefillParams& p, const Segment&
 // O_t out of tensor memory, normalised, to the output or to the block's parts (four warps).  The stores are
 // the dense kernel's: fp32 rows through two butterfly stages (8 rows x 128 bytes a store), bf16 rows as they are.
 template <int D, bool kOutF32>
-__device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int warp, int lane,
-                                            volatile int* abort_flag) {
+__device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int warp, int lane) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
   auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
@@ -938,37 +1043,71 @@ __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sba
   const float* hand = reinterpret_cast<const float*>(__cvta_shared_to_generic(sbase + S::kInvLp));
   const int r_lo = lane & 7, cgrp = lane >> 3;  // fp32 store layout after the transpose
   auto wait = [&](int b, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, abort_flag, p.wait_limit));
+    return __all_sync(0xffffffffu, wait_or_abort(bar(b), parity, sbase + Smem<D>::kAbort, p.wait_limit));
   };
 
-  int li0 = 0, li1 = 0;      // segments of each Q tile
-  int used0 = 0, used1 = 0;  // those of them with keys
-  int g0 = 0, g1 = 0;        // key tiles of each Q tile
+  int li0 = 0, li1 = 0;  // segments of each Q tile
+  int g0 = 0, g1 = 0;    // key tiles of each Q tile
+  int ring0 = 0;         // ring index of the segment's first tile
+  uint32_t fixed = 0;    // parity of V_EDGE and V_FIXED
   bool ok = true;
   Segments<D> segs(sbase);
   for (; ok; ++segs.n) {
-    if (!(ok = __all_sync(~0u, segs.wait(p, abort_flag)))) break;
+    if (!(ok = __all_sync(~0u, segs.wait(p)))) break;
     const Segment sg = segs.read();
     if (sg.b < 0) break;
+    // Between segments' outputs these warps are idle: the value tiles at the request's end, or that some rows must
+    // not see, pass through their hands.
+    uint32_t held = 0;  // whether something was taken out of a tile
+    {
+      const int n = sg.last() - sg.k0, seen = sg.seen_by_all(p);
+      if (n > sg.edge(p)) {
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(segs.held() + 4 * (12 + quarter)), "r"(0) : "memory");
+        if (lane < 3)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(segs.held() + 4 * (4 * lane + quarter)), "r"(0) : "memory");
+        __syncwarp();
+      }
+      for (int j = sg.edge(p); j < n; ++j) {
+        // (The PV issuer tells when it has landed: of V_FULL's phases these warps see few, and by its parity
+        // they could not tell which.)
+        if (!(ok = wait(S::bVEdge, fixed))) break;
+        const int s = (ring0 + v_item(j, n)) % kStages;
+        const int key0 = (sg.k0 + j) * kBlockN, valid = min(sg.len - key0, kBlockN);
+        const unsigned rows =
+            __ballot_sync(~0u, fix_row<D>(sbase + L::kKV + s * L::kTile, r, valid, key0 + valid > seen));
+        if (rows && lane == 0) {
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(segs.held() + 4 * (4 * (key0 / kBlockN - seen / kBlockN) + quarter)),
+                       "r"(rows)
+                       : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(segs.held() + 4 * (12 + quarter)), "r"(1) : "memory");
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(bar(S::bVFixed));
+        if (!(ok = wait(S::bVFixed, fixed))) break;  // (for the other warps' flags)
+        fixed ^= 1;
+      }
+      if (!ok) break;
+      if (n > sg.edge(p)) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t flag;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(flag) : "r"(segs.held() + 4 * (12 + q)) : "memory");
+          held |= flag;
+        }
+      }
+      ring0 = (ring0 + 2 * n) % kStages;
+    }
 #pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       if (!sg.present(p, t)) continue;
       const int nt = sg.end(t) - sg.k0;
-      const int li = t ? li1++ : li0++, used = t ? used1 : used0;
+      const int li = t ? li1++ : li0++;
       const int g = t ? (g1 += nt) : (g0 += nt);
-      if (nt > 0) ++(t ? used1 : used0);
       if (!(ok = wait(L::bEpiReady + t, li & 1))) break;
       const float inv_l = hand[t * kBlockM + r];
       ptx::mbar_arrive(bar(L::bEpiTaken + t));
       const bool none = inv_l == 0.f;  // the row has no key above -inf: its output is 0 whatever O_t holds
-      bool missing = false;
-      if (nt > 0) {
-        if (!(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
-        if (!(ok = wait(S::bHeld + t, used & 1))) break;
-        uint32_t flag;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(flag) : "r"(segs.held() + 4 * (kHeldWords - 1)) : "memory");
-        missing = flag != 0;
-      }
+      if (nt > 0 && !(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
       ptx::tc_fence_after();
       const uint32_t tO = tmem + 2 * kBlockN + t * D + lane_off;
       auto release_if = [&](bool last) {
@@ -977,19 +1116,18 @@ __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sba
           ptx::mbar_arrive(bar(L::bOEmpty + t));
         }
       };
-      // Row x of the tile (tokens and heads in turn) to its place in the output, or below 0.
-      auto place = [&](int x) -> long long {
+      // Row x of the tile (tokens and heads in turn) to its row in the output or the parts, or below 0.
+      auto place = [&](int x) {
         int tok;
         if (!sg.has_token(p, t, x, tok)) return -1;
-        if (sg.kind)
-          return ((static_cast<long long>(blockIdx.x) * 2 + (sg.kind - 1)) * kItemRows + t * kBlockM + x) * D;
+        if (sg.kind) return (static_cast<int>(blockIdx.x) * 2 + sg.kind - 1) * kItemRows + t * kBlockM + x;
         const int head = x - ((x * p.div_group) >> 16) * p.group;
-        return (static_cast<long long>(sg.row0 + tok) * p.h_q + sg.h * p.group + head) * D;
+        return (sg.row0 + tok) * p.h_q + sg.h * p.group + head;  // (tokens * h_q < 2^31)
       };
       if (kOutF32 || sg.kind) {
         float* const base = sg.kind ? p.part_o : static_cast<float*>(p.out);
         const bool align32 = sg.kind || p.out_align32;
-        long long at[4];
+        int at[4];
 #pragma unroll
         for (int rr = 0; rr < 4; ++rr) at[rr] = place(quarter * 32 + rr * 8 + r_lo);
 #pragma unroll
@@ -1005,44 +1143,41 @@ __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sba
           // x[8*rr + i] = (row 32*quarter + 8*rr + r_lo, column 32*c + 8*cgrp + i)
 #pragma unroll
           for (int rr = 0; rr < 4; ++rr)
-            if (at[rr] >= 0) detail::st_global_32B(base + at[rr] + c * 32 + cgrp * 8, align32, &x[rr * 8]);
+            if (at[rr] >= 0)
+              detail::st_global_32B(base + static_cast<size_t>(at[rr]) * D + c * 32 + cgrp * 8, align32, &x[rr * 8]);
         }
-        if (missing) {
+        if (held) {
           __syncwarp();
-          const long long mine = place(r);
-          if (mine >= 0 && !none) give_back<D>(p, sg, segs.held(), sg.limit(p, t, r), base + mine);
+          const int mine = place(r);
+          if (mine >= 0 && !none)
+            give_back<D>(p, sg, segs.held(), sg.limit(p, t, r), base + static_cast<size_t>(mine) * D);
         }
       } else if constexpr (!kOutF32) {
-        const long long mine = place(r);
-        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(p.out) + mine;
+        const int mine = place(r);
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(mine) * D;
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          uint32_t wd[32];  // 64 columns of this thread's row as bf16 pairs
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t a[32];
+          ptx::tmem_ld32(tO + c * 32, a);
+          ptx::tmem_wait_ld();
+          release_if(c == D / 32 - 1);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t a[32];
-            ptx::tmem_ld32(tO + half * 64 + c * 32, a);
-            ptx::tmem_wait_ld();
-            release_if(half == D / 64 - 1 && c == 1);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              wd[c * 16 + i] = none ? 0u
-                                    : ptx::pack_bf16x2(__uint_as_float(a[2 * i]) * inv_l,
-                                                       __uint_as_float(a[2 * i + 1]) * inv_l);
-          }
+          for (int i = 0; i < 16; ++i)
+            a[i] = none ? 0u
+                        : ptx::pack_bf16x2(__uint_as_float(a[2 * i]) * inv_l, __uint_as_float(a[2 * i + 1]) * inv_l);
           if (mine >= 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) detail::st_global_32B(dst + half * 64 + 2 * i, p.out_align32, &wd[i]);
+            detail::st_global_32B(dst + c * 32, p.out_align32, &a[0]);
+            detail::st_global_32B(dst + c * 32 + 16, p.out_align32, &a[8]);
           }
         }
-        if (missing && mine >= 0 && !none) give_back<D>(p, sg, segs.held(), sg.limit(p, t, r), dst);
+        if (held && mine >= 0 && !none) give_back<D>(p, sg, segs.held(), sg.limit(p, t, r), dst);
       }
     }
     if (!ok) break;
     __syncwarp();
     if (lane == 0) segs.release();
   }
-  if (!ok) raise_abort(p, abort_flag);
+  if (!ok) raise_abort(p, sbase + Smem<D>::kAbort);
 }
 
 template <int D, bool kOutF32>
@@ -1053,7 +1188,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = ptx::smem_addr(smem);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kAbort);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
@@ -1074,15 +1208,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       ptx::mbar_init(bar(L::bOEmpty + t), kBlockM);
       ptx::mbar_init(bar(L::bEpiReady + t), kBlockM);
       ptx::mbar_init(bar(L::bEpiTaken + t), kBlockM);
-      ptx::mbar_init(bar(S::bHeld + t), 1);
     }
     for (int s = 0; s < kSegs; ++s) {
       ptx::mbar_init(bar(S::bSegFull + s), 1);
       ptx::mbar_init(bar(S::bSegEmpty + s), kConsumers);
     }
+    ptx::mbar_init(bar(S::bVEdge), 1);
+    ptx::mbar_init(bar(S::bVFixed), kBlockM);
     ptx::mbar_init(bar(L::bDrainS), 1);
     ptx::mbar_init(bar(L::bDrainPV), 1);
-    *abort_flag = 0;
+    *reinterpret_cast<volatile int*>(smem + S::kAbort) = 0;
     ptx::fence_mbar_init();
   }
   if (warp == kLoadWarp && lane == 0) {
@@ -1103,22 +1238,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   using Regs = RegSplit<false>;
   if (warp < kLoadWarp) {
     ptx::setmaxnreg_inc<Regs::kSoftmax>();
-    softmax_wg<D>(p, sbase, tmem, warp >> 2, warp, lane, abort_flag);
+    softmax_wg<D>(p, sbase, tmem, warp >> 2, warp, lane);
   } else if (warp < kEpiWarp0) {
     ptx::setmaxnreg_dec<Regs::kIssue>();
     if (warp == kLoadWarp) {
-      producer<D>(p, sbase, lane, abort_flag);
+      producer<D>(p, sbase, lane);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) s_issuer<D>(p, sbase, tmem, abort_flag);
+      if (lane == 0) s_issuer<D>(p, sbase, tmem);
     } else if (warp == kPvWarp) {
-      pv_issuer<D>(p, sbase, tmem, lane, abort_flag);
+      if (lane == 0) pv_issuer<D>(p, sbase, tmem);
     } else {
-      scheduler<D>(p, sbase, lane, abort_flag);
+      scheduler<D>(p, sbase, lane);
     }
     __syncwarp();
   } else {
     ptx::setmaxnreg_dec<Regs::kEpilogue>();
-    epilogue_wg<D, kOutF32>(p, sbase, tmem, warp, lane, abort_flag);
+    epilogue_wg<D, kOutF32>(p, sbase, tmem, warp, lane);
   }
 
   ptx::tc_fence_before();
