@@ -17,29 +17,53 @@ namespace {
 // Requests with room for at most this many keys keep their items whole: one launch and no workspace.
 constexpr long long kWholeKeys = 1024;
 
-bool encode(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[4], const long long (&strides)[3],
-            int box1, int box2) {
+// A map of bf16 elements: extents, strides (elements) of all dimensions but the first, box.
+template <int N>
+bool encode(CUtensorMap* m, const void* base, const long long (&dims)[N], const long long (&strides)[N - 1],
+            const int (&boxes)[N]) {
   EncodeTiledFn fn = tensor_map_encoder();
   if (!fn) return false;
-  cuuint64_t st[3];
-  for (int i = 0; i < 3; ++i) st[i] = static_cast<cuuint64_t>(strides[i]) * 2;
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box1), static_cast<cuuint32_t>(box2), 1};
-  const cuuint32_t elem[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, st, box, elem,
+  cuuint64_t d[N], st[N - 1];
+  cuuint32_t box[N], elem[N];
+  for (int i = 0; i < N; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    box[i] = static_cast<cuuint32_t>(boxes[i]);
+    elem[i] = 1;
+    if (i) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
+  }
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, const_cast<void*>(base), d, st, box, elem,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// (D, row, head, page) of a paged cache: boxes of `rows` rows x 64 channels.
-bool encode_cache(CUtensorMap* m, const void* base, const Strides& s, int d, int page_size, int heads, int n_pages,
+// A paged cache's map of fused copies of `rows` rows (see KvTile); false: the strides do not allow one.
+bool encode_fused(CUtensorMap* m, KvPlace* kv, const void* base, const Strides& s, int d, int page_size, int heads,
+                  int n_pages, int rows) {
+  constexpr long long kMost = 1LL << 31;  // coordinates, and steps between them, are 32-bit numbers
+  const int groups = page_size / 8;
+  if (d != 128) return false;
+  long long apart = s.b_ / s.h_;
+  if (s.b_ % s.h_ == 0 && apart >= heads && apart * n_pages + heads < kMost) {
+    *kv = {1, static_cast<int>(apart)};
+    if (encode<5>(m, base, {64, 8, d / 64, groups, (n_pages - 1) * apart + heads}, {s.n_, 64, 8 * s.n_, s.h_},
+                  {64, 8, d / 64, rows / 8, 1}))
+      return true;
+  }
+  apart = s.b_ / (8 * s.n_);
+  if (s.b_ % (8 * s.n_) != 0 || apart < groups || apart * n_pages + groups >= kMost) return false;
+  *kv = {0, static_cast<int>(apart)};
+  return encode<5>(m, base, {64, 8, d / 64, (n_pages - 1) * apart + groups, heads}, {s.n_, 64, 8 * s.n_, s.h_},
+                   {64, 8, d / 64, rows / 8, 1});
+}
+
+// One of copies of `rows` rows of one channel block: (D, row, head, page).
+bool encode_plain(CUtensorMap* m, const void* base, const Strides& s, int d, int page_size, int heads, int n_pages,
                   int rows) {
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
-                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n_pages)};
-  return encode(m, base, dims, {s.n_, s.h_, s.b_}, rows, 1);
+  return encode<4>(m, base, {d, page_size, heads, n_pages}, {s.n_, s.h_, s.b_}, {64, rows, 1, 1});
 }
 
 // Sets the shared-memory opt-in once per device and instantiation.
-template <int D, bool kF32>
+template <int D, bool kF32, bool kFused>
 cudaError_t prepare() {
   static std::mutex mu;
   static bool done[64] = {};
@@ -49,18 +73,18 @@ cudaError_t prepare() {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(prefill_kernel<D, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    e = cudaFuncSetAttribute(prefill_kernel<D, kF32, kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   return cudaSuccess;
 }
 
-template <int D, bool kF32>
+template <int D, bool kF32, bool kFused>
 cudaError_t launch(const PrefillParams& p, int blocks, cudaStream_t st) {
-  cudaError_t e = prepare<D, kF32>();
+  cudaError_t e = prepare<D, kF32, kFused>();
   if (e != cudaSuccess) return e;
-  e = launch_after(prefill_kernel<D, kF32>, dim3(blocks), dim3(kThreads), Smem<D>::kBytes, st, p);
+  e = launch_after(prefill_kernel<D, kF32, kFused>, dim3(blocks), dim3(kThreads), Smem<D>::kBytes, st, p);
   if (e != cudaSuccess || !p.split) return e;
   const int rows = p.tokens <= p.tile_tokens ? p.tokens * p.group : kItemRows;
   return launch_after(join_kernel<D, kF32>, dim3(blocks, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * 32), 0,
@@ -88,11 +112,17 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   p.tile_tokens = kBlockM / p.group;
   p.box_rows = 16;
   while (p.box_rows < kBlockN && a.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
-  const cuuint64_t qdims[4] = {static_cast<cuuint64_t>(a.d), static_cast<cuuint64_t>(p.group),
-                               static_cast<cuuint64_t>(a.tokens), static_cast<cuuint64_t>(a.h_kv)};
-  if (!encode(&p.tm_q, a.q, qdims, {a.q_h, a.q_n, a.q_h * p.group}, p.group, p.tile_tokens) ||
-      !encode_cache(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows) ||
-      !encode_cache(&p.tm_v, a.v_cache, a.vs, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows))
+  if (!encode<4>(&p.tm_q, a.q, {a.d, p.group, a.tokens, a.h_kv}, {a.q_h, a.q_n, a.q_h * p.group},
+                 {64, p.group, p.tile_tokens, 1}))
+    return cudaErrorInvalidValue;
+  // Copies of 16 rows are fused in pages of long requests: the copies' number bounds them (54560 keys, one head: 970
+  // and 1197 us; 4 x 9024, 24 heads on 8: 387 and 415).  For short ones a fused copy's longer way counts (16 x 2512: 309
+  // and 296; 8 x 5024: 463 and 465), and of larger runs there are few enough (runs of 128: 1032 and 927 us).
+  const bool fused = p.box_rows == 16 && static_cast<long long>(a.max_pages) * a.page_size > 5120 &&
+      encode_fused(&p.tm_k, &p.kv[0], a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows) &&
+      encode_fused(&p.tm_v, &p.kv[1], a.v_cache, a.vs, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows);
+  if (!fused && (!encode_plain(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows) ||
+                 !encode_plain(&p.tm_v, a.v_cache, a.vs, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows)))
     return cudaErrorInvalidValue;
   p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
   p.vs = a.vs;
@@ -121,8 +151,9 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   p.part_lse = p.part_o + part_rows() * a.d;
   p.meta = reinterpret_cast<int4*>(p.part_lse + part_rows());
   const int blocks = grid_blocks();
-  if (a.d == 64) return a.out_f32 ? launch<64, true>(p, blocks, st) : launch<64, false>(p, blocks, st);
-  return a.out_f32 ? launch<128, true>(p, blocks, st) : launch<128, false>(p, blocks, st);
+  if (a.d == 64) return a.out_f32 ? launch<64, true, false>(p, blocks, st) : launch<64, false, false>(p, blocks, st);
+  if (fused) return a.out_f32 ? launch<128, true, true>(p, blocks, st) : launch<128, false, true>(p, blocks, st);
+  return a.out_f32 ? launch<128, true, false>(p, blocks, st) : launch<128, false, false>(p, blocks, st);
 }
 
 }  // namespace ditattn

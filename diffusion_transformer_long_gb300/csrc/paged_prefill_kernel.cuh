@@ -58,9 +58,27 @@ constexpr int kItemRows = 2 * kBlockM;
 constexpr int kMaxGrid = 256;          // largest grid
 constexpr int kConsumers = 3 + 8 + 4;  // of a segment: producer, two issuers, softmax and epilogue warps
 
+// How a cache's rows reach a tile.  A tile of D = 128 holds two blocks of 64 channels, 128 bytes a row.  A copy brings
+// a run of rows of one block, and the blocks are 16 KB apart; or (fused) both blocks of the run, as a 5-D box (64
+// channels, 8 rows, channel blocks, groups of 8 rows, ..): groups of 8 rows follow each other, the blocks in turn in
+// each.  That takes one of the four dimensions row-in-group, group, head, page out of the map, which the strides allow
+// where pages are whole numbers of heads apart (by_head), or of groups of rows.
+// (The layout is a template's: an issuer that works descriptors out between the products starves the tensor pipe,
+// 1640 -> 1360 TFLOP/s on 54560 keys in pages of 128.)
+struct KvPlace {
+  int by_head;  // fused: page * apart + head is the last coordinate, else page * apart + group the last but one
+  int apart;
+};
+template <int D, bool kFused>
+struct KvTile {
+  static_assert(D == 128 || !kFused, "one channel block needs no fusing");
+  static constexpr uint32_t kGroup = kFused ? 2048 : 1024;                // bytes from one group of 8 rows to the next
+  static constexpr uint32_t kBlock = kFused ? 1024 : AttnSmem<D>::kRegion;  // from one channel block to the next
+};
+
 struct PrefillParams {
   CUtensorMap tm_q;        // (D, head of the group, token, key/value head)
-  CUtensorMap tm_k, tm_v;  // (D, row, head, page)
+  CUtensorMap tm_k, tm_v;  // paged_prefill.cu: encode_cache
   const __nv_bfloat16* v_cache;
   Strides vs;
   const int* table;
@@ -77,6 +95,7 @@ struct PrefillParams {
   int batch, tokens, h_q, h_kv, group, tile_tokens;  // tile_tokens: of a Q tile, 128 / group
   int page_size, n_pages, max_len;
   int box_rows;   // rows of one copy
+  KvPlace kv[2];  // of K and V, fused
   int div_group;  // 2^16 / group, rounded up: r / group for r < 128 is r * div_group >> 16
   int causal;
   int split;  // 0: items stay whole
@@ -176,7 +195,6 @@ struct Segment {
   }
 };
 
-using detail::Descs;
 using detail::k_item;  // K/V ring items of a segment in consumption order, as in the dense kernel
 using detail::v_item;
 
@@ -194,6 +212,23 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uin
 __device__ __forceinline__ void raise_abort(const PrefillParams& p, uint32_t abort_flag) {
   asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
   atomicOr(p.status, kStatusTimeout);
+}
+
+// Shared-memory matrix descriptors, as the dense kernel's: the high word holds the stride byte offset (from one
+// group of 8 rows to the next), the version and the 128-byte swizzle, the low word the address and the leading
+// byte offset.
+__device__ constexpr uint32_t desc_hi(uint32_t group) { return (group >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc(uint32_t hi, uint32_t lo) {
+  return (static_cast<uint64_t>(hi) << 32) | static_cast<uint64_t>(lo);
+}
+
+__device__ __forceinline__ uint32_t pick(const uint32_t (&a)[kStages], int slot) {
+  uint32_t r = a[0];
+#pragma unroll
+  for (int s = 1; s < kStages; ++s)
+    if (slot == s) r = a[s];
+  return r;
 }
 
 // The ring of segments as a role sees it.
@@ -497,8 +532,17 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
   if (!ok) raise_abort(p, sbase + Smem<D>::kAbort);
 }
 
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 // Copies: Q of each segment, then its key and value tiles (one warp; each lane its own rows of a tile).
-template <int D>
+template <int D, bool kFused>
 __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase, int lane) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
@@ -513,9 +557,10 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
   const int boxes = kBlockN / p.box_rows;  // of a tile: 1, 2, 4 or 8
   const int per_batch = 32 / boxes;        // tiles looked up at once
   const int box = lane % boxes;            // the lane's box of a tile
-  // The lane copies channel block lane / boxes of its box, if there are that many.
-  const int copy_col = lane / boxes * 64;
-  const uint32_t copy_dst = sbase + L::kKV + lane / boxes * L::kRegion + box * p.box_rows * 128;
+  // The lane copies its box, or channel block lane / boxes of it where those are copied apart.
+  const int copy_block = kFused ? 0 : lane / boxes;
+  const uint32_t copy_dst = sbase + L::kKV + box * (p.box_rows / 8) * KvTile<D, kFused>::kGroup +
+                            copy_block * KvTile<D, kFused>::kBlock;
   const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * 128 * kRegions;
 
   uint32_t kpar = 0, vpar = 0;  // bit s: parity of the next K_FULL[s] / V_FULL[s] phase
@@ -603,12 +648,22 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
                        : "memory");
         ++tiles;
       }
-      const uint32_t dst = copy_dst + s * L::kTile;
       const CUtensorMap* const tm = is_v ? &p.tm_v : &p.tm_k;
-      if (page < 0) page = p.n_pages;
+      const KvPlace kv = p.kv[is_v];
+      const uint32_t dst = copy_dst + s * L::kTile;
+      if (page < 0) page = p.n_pages;  // (past the pool: zeros)
+      int c2 = sg.h, c3 = page;
+      if constexpr (kFused) {
+        c2 = first / 8 + (kv.by_head ? 0 : page * kv.apart);
+        c3 = sg.h + (kv.by_head ? page * kv.apart : 0);
+      }
       if (!wait(L::bKVEmpty + s, ((it / kStages) & 1) ^ 1)) return false;
       if (lane == 0) ptx::mbar_arrive_expect_tx(bar(fb), L::kTile);
-      if (lane < boxes * kRegions) ptx::tma_load_4d(dst, tm, bar(fb), copy_col, first, sg.h, page);
+      if constexpr (kFused) {
+        if (lane < boxes) tma_load_5d(dst, tm, bar(fb), 0, 0, 0, c2, c3);
+      } else if (lane < boxes * kRegions) {
+        ptx::tma_load_4d(dst, tm, bar(fb), copy_block * 64, first, c2, c3);
+      }
 #pragma unroll
       for (int q = 0; q < kStages; ++q)
         if (q == s) {
@@ -643,19 +698,25 @@ __device__ __forceinline__ void producer(const PrefillParams& p, uint32_t sbase,
 }
 
 // S_t = Q_t K^T (one thread).
-template <int D>
+template <int D, bool kFused>
 __device__ __forceinline__ void s_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem) {
   using L = AttnSmem<D>;
   auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
   constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBlockM, kBlockN, false, false);
-  const Descs<D> ds(sbase);
+  constexpr uint32_t qhi = desc_hi(1024), khi = desc_hi(KvTile<D, kFused>::kGroup);
+  constexpr uint32_t kblock = KvTile<D, kFused>::kBlock >> 4;
+  uint32_t ks[kStages];
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) ks[s] = desc_lo(sbase + L::kKV + s * L::kTile, 16);
+  const uint32_t qs[2] = {desc_lo(sbase + L::kQ0, 16), desc_lo(sbase + L::kQ1, 16)};
+  // Both K-major: a step of 16 channels advances 32 bytes inside a channel block, then goes to the next.
   auto issue = [&](int t, int slot) {
-    const uint32_t kb = Descs<D>::pick(ds.k, slot);
-    const uint32_t qa = ds.q[t];
+    const uint32_t kb = pick(ks, slot), qa = qs[t];
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = ((k / 4) * L::kRegion + (k % 4) * 32) >> 4;
-      ptx::mma_bf16_ss(tmem + t * kBlockN, Descs<D>::full(qa + off), Descs<D>::full(kb + off), kIdesc, k > 0 ? 1u : 0u);
+      const uint32_t step = (k % 4) * 2;
+      ptx::mma_bf16_ss(tmem + t * kBlockN, desc(qhi, qa + (k / 4) * (L::kRegion >> 4) + step),
+                       desc(khi, kb + (k / 4) * kblock + step), kIdesc, k > 0 ? 1u : 0u);
     }
   };
   auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, sbase + Smem<D>::kAbort, p.wait_limit); };
@@ -709,13 +770,13 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) { return ((w & 0x7f80
 // hide what a page holds behind the request's last key), and else, where `look`, without its infinities and NaN;
 // true: it had some.  (The epilogue's threads, a row each; whole rows are gone through, in an order that spreads the
 // banks, so the swizzle does not matter.)
-template <int D>
+template <int D, bool kFused>
 __device__ __forceinline__ bool fix_row(uint32_t tile, int row, int valid, bool look) {
-  const uint32_t at = tile + row * 128;
+  const uint32_t at = tile + (row / 8) * KvTile<D, kFused>::kGroup + (row % 8) * 128;
   uint32_t bad = 0;
 #pragma unroll 1
   for (int ch = 0; ch < D / 8; ++ch) {
-    const uint32_t piece = at + (ch / 8) * AttnSmem<D>::kRegion + ((ch + row) & 7) * 16;
+    const uint32_t piece = at + (ch / 8) * KvTile<D, kFused>::kBlock + ((ch + row) & 7) * 16;
     if (row >= valid) {
       asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(piece), "r"(0) : "memory");
     } else if (look) {
@@ -741,22 +802,25 @@ __device__ __forceinline__ bool fix_row(uint32_t tile, int row, int valid, bool 
 }
 
 // O_t += P_t V (one thread: what lanes wait for one another costs here, each product waits for).
-template <int D>
+template <int D, bool kFused>
 __device__ __forceinline__ void pv_issuer(const PrefillParams& p, uint32_t sbase, uint32_t tmem) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
   auto bar = [&](int i) { return sbase + L::kBars + 8u * i; };
   constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kBlockM, D, false, true);
-  const Descs<D> ds(sbase);
-  auto issue = [&](int t, int slot, bool acc, int half) {
-    const uint32_t vb = Descs<D>::pick(ds.v, slot);
-    const uint32_t pa = ds.pp[t];
+  constexpr uint32_t phi = desc_hi(1024), vhi = desc_hi(KvTile<D, kFused>::kGroup);
+  constexpr uint32_t vgroups = KvTile<D, kFused>::kGroup >> 3;
+  uint32_t vs[kStages];
 #pragma unroll
-    for (int k = half * 4; k < half * 4 + 4; ++k) {
-      const uint32_t aoff = ((k / 4) * L::kRegion + (k % 4) * 32) >> 4;
-      ptx::mma_bf16_ss(tmem + 2 * kBlockN + t * D, Descs<D>::full(pa + aoff), Descs<D>::full(vb + k * 128), kIdesc,
-                       (acc || k > 0) ? 1u : 0u);
-    }
+  for (int s = 0; s < kStages; ++s) vs[s] = desc_lo(sbase + L::kKV + s * L::kTile, KvTile<D, kFused>::kBlock);
+  const uint32_t ps[2] = {desc_lo(sbase + L::kP0, 16), desc_lo(sbase + L::kP1, 16)};
+  // P K-major; V with the channels contiguous, 16 keys (two groups of rows) a step.
+  auto issue = [&](int t, int slot, bool acc, int half) {
+    const uint32_t vb = pick(vs, slot), pa = ps[t];
+#pragma unroll
+    for (int k = half * 4; k < half * 4 + 4; ++k)
+      ptx::mma_bf16_ss(tmem + 2 * kBlockN + t * D, desc(phi, pa + (k / 4) * (L::kRegion >> 4) + (k % 4) * 2),
+                       desc(vhi, vb + k * vgroups), kIdesc, (acc || k > 0) ? 1u : 0u);
   };
   auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar(b), parity, sbase + S::kAbort, p.wait_limit); };
 
@@ -1032,7 +1096,7 @@ __device__ __forceinline__ void give_back(const PrefillParams& p, const Segment&
 
 // O_t out of tensor memory, normalised, to the output or to the block's parts (four warps).  The stores are
 // the dense kernel's: fp32 rows through two butterfly stages (8 rows x 128 bytes a store), bf16 rows as they are.
-template <int D, bool kOutF32>
+template <int D, bool kOutF32, bool kFused>
 __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sbase, uint32_t tmem, int warp, int lane) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
@@ -1074,7 +1138,7 @@ __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sba
         const int s = (ring0 + v_item(j, n)) % kStages;
         const int key0 = (sg.k0 + j) * kBlockN, valid = min(sg.len - key0, kBlockN);
         const unsigned rows =
-            __ballot_sync(~0u, fix_row<D>(sbase + L::kKV + s * L::kTile, r, valid, key0 + valid > seen));
+            __ballot_sync(~0u, fix_row<D, kFused>(sbase + L::kKV + s * L::kTile, r, valid, key0 + valid > seen));
         if (rows && lane == 0) {
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(segs.held() + 4 * (4 * (key0 / kBlockN - seen / kBlockN) + quarter)),
                        "r"(rows)
@@ -1180,7 +1244,7 @@ __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sba
   if (!ok) raise_abort(p, sbase + Smem<D>::kAbort);
 }
 
-template <int D, bool kOutF32>
+template <int D, bool kOutF32, bool kFused>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
   using L = AttnSmem<D>;
   using S = Smem<D>;
@@ -1242,18 +1306,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   } else if (warp < kEpiWarp0) {
     ptx::setmaxnreg_dec<Regs::kIssue>();
     if (warp == kLoadWarp) {
-      producer<D>(p, sbase, lane);
+      producer<D, kFused>(p, sbase, lane);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) s_issuer<D>(p, sbase, tmem);
+      if (lane == 0) s_issuer<D, kFused>(p, sbase, tmem);
     } else if (warp == kPvWarp) {
-      if (lane == 0) pv_issuer<D>(p, sbase, tmem);
+      if (lane == 0) pv_issuer<D, kFused>(p, sbase, tmem);
     } else {
       scheduler<D>(p, sbase, lane);
     }
     __syncwarp();
   } else {
     ptx::setmaxnreg_dec<Regs::kEpilogue>();
-    epilogue_wg<D, kOutF32>(p, sbase, tmem, warp, lane);
+    epilogue_wg<D, kOutF32, kFused>(p, sbase, tmem, warp, lane);
   }
 
   ptx::tc_fence_before();

@@ -139,6 +139,41 @@ def test_many_requests(room):
         s.check(True, torch.bfloat16)
 
 
+@pytest.mark.parametrize("order", ["hnd", "nhd", "part", "kv in one", "rows of both"])
+@pytest.mark.parametrize("P", [16, 48])
+def test_copies_of_both_channel_blocks(P, order):
+    """Wide tables of small pages: one copy brings both channel blocks of 16 rows, where the strides allow it."""
+    for Hq, Hkv in ((6, 2), (4, 1), (3, 3)):
+        s = Step([0, 700, 77], [200, 90, 1], Hq, Hkv, 128, P, "part" if order == "part" else "hnd", room=9000, seed=P)
+        n = s.n_pages
+        if order == "nhd":
+            s.k, s.v = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (s.k, s.v))
+        elif order == "kv in one":
+            both = torch.stack((s.k, s.v), 1)
+            s.k, s.v = both[:, 0], both[:, 1]
+        elif order == "rows of both":
+            both = torch.stack((s.k.transpose(1, 2), s.v.transpose(1, 2)), 2).contiguous()
+            s.k, s.v = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+        s.table[1, 4], s.table[0, 1] = n + 5, -1
+        s.check(True)
+        s.check(False)
+        page, row = int(s.table[1, (789 - 30) // P]), (789 - 30) % P  # a value that the first 59 tokens do not see
+        s.v[page, :, row, 65] = math.inf
+        got, _ = s.run()
+        first = int(s.cu[1])
+        assert got[first:first + 59].isfinite().all() and not got[first + 59:first + 90, :, 65].isfinite().any()
+
+
+def test_one_page():
+    for P in (16, 128):
+        for Hq, Hkv in ((2, 1), (4, 2)):
+            s = Step([0], [P], Hq, Hkv, 128, P, room=9000)
+            k, v = s.k[int(s.table[0, 0])][None].clone(), s.v[int(s.table[0, 0])][None].clone()
+            s.table[0, 0] = 0
+            s.k, s.v, s.n_pages = k, v, 1
+            s.check()
+
+
 def test_no_tokens_and_no_keys():
     for room in (0, 2048):
         s = Step([0, 40, 0], [0, 0, 0], 2, 1, 64, 16, spare=5, room=room)
