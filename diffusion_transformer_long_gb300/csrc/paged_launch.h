@@ -67,6 +67,26 @@ cudaError_t launch_paged_attn(const PagedAttnLaunch& a, cudaStream_t st);
 // Workspace bytes on the current device; `keys`: the most that a request can attend to.
 size_t paged_attn_workspace(int batch, int h_q, int h_kv, int d, long long keys);
 
+struct RopeLaunch {  // queries, keys (heads 0: none)
+  const void* in[2];
+  void* out[2];
+  Strides is[2], os[2];
+  const void* weight[2];  // may be null
+  int heads[2];
+  bool weight_f32, norm, interleaved;
+  float eps, rot_scale;
+  const int* positions;  // or cu_new, start_lens
+  long long pos_b, pos_axis;
+  const int* cu_new;
+  const int* start_lens;
+  int requests;
+  const float* freqs;
+  int pairs, axes;  // 0 pairs: no rotation
+  int axis_pairs[4];
+  int batch, n, d;
+};
+cudaError_t launch_qk_norm_rope(const RopeLaunch& a, cudaStream_t st);
+
 struct PrefillLaunch {
   const void* q;
   long long q_n, q_h;  // token and head strides (elements)

@@ -1,4 +1,4 @@
-// C entry points of prompts over the paged key/value cache (declared in include/ditattn.h): argument
+// C entry points of norms with rotary positions and of prompts over the paged key/value cache (declared in include/ditattn.h): argument
 // validation and dispatch.  Validation makes no CUDA call but the workspace sizes' look at the device's
 // SM count.
 #include <cuda_runtime.h>
@@ -28,9 +28,134 @@ bool valid_tokens(const void* p, const dit_strides& s, int T, int H) {
   return p && aligned(p, 16) && valid_strides(s) && s.n <= kMaxSpan / T && s.h <= kMaxSpan / H;
 }
 
+// A [B, H, N, D] view's strides; a size-1 dimension's addresses nothing.
+dit_strides row_strides(const dit_strides* s, int B, int H, int N, int D) {
+  dit_strides x = s ? *s : contiguous(H, N, D);
+  if (B == 1) x.b = D;
+  if (H == 1) x.h = D;
+  if (N == 1) x.n = D;
+  return x;
+}
+
+struct View {
+  const void* p;
+  dit_strides s;
+  int H;
+  bool valid(int B, int N) const {
+    return p && aligned(p, 16) && valid_strides(s) && s.b <= kMaxSpan / B && s.h <= kMaxSpan / H && s.n <= kMaxSpan / N;
+  }
+  Range range(int B, int N, int D) const { return span(p, view_span(s, B, H, N, D, 2)); }
+  bool same(const View& v) const {
+    return p == v.p && H == v.H && s.b == v.s.b && s.h == v.s.h && s.n == v.s.n;
+  }
+};
+
+// True if the two views share no element: apart, or the heads of one beside those of the other in the rows of one
+// allocation (slices of a fused projection), which the rows that hold both show.
+bool views_apart(const View& a, const View& b, int B, int N, int D) {
+  if (!overlap(a.range(B, N, D), b.range(B, N, D))) return true;
+  if (a.s.b != b.s.b || a.s.n != b.s.n) return false;
+  const bool swap = reinterpret_cast<uintptr_t>(b.p) < reinterpret_cast<uintptr_t>(a.p);
+  const View &lo = swap ? b : a, &hi = swap ? a : b;
+  const long long gap = static_cast<long long>((reinterpret_cast<uintptr_t>(hi.p) - reinterpret_cast<uintptr_t>(lo.p)) / 2);
+  const long long lo_row = (lo.H - 1) * lo.s.h + D, both = gap + (hi.H - 1) * hi.s.h + D;
+  if (gap < lo_row) return false;
+  return no_self_overlap({a.s.b, both, a.s.n}, B, 1, N, both);
+}
+
 }  // namespace
 
 extern "C" {
+
+dit_status dit_qk_norm_rope(const void* q, const dit_strides* q_strides, void* q_out,
+                            const dit_strides* q_out_strides, int H_q, const void* k,
+                            const dit_strides* k_strides, void* k_out, const dit_strides* k_out_strides,
+                            int H_k, int norm, float eps, const void* q_weight, const void* k_weight,
+                            dit_dtype weight_dtype, const float* freqs, const int* axis_pairs, int axes,
+                            int interleaved, float rot_scale, const int* positions, long long pos_b,
+                            long long pos_axis, const int* cu_new, const int* start_lens, int requests, int B,
+                            int N, int D, dit_stream stream) {
+  dit_status s = check_dims(B, H_q, N, D);
+  if (s != DIT_OK) return s;
+  if (H_k < 0 || (H_k > 0) != (k != nullptr) || (!k && (k_out || k_weight))) return DIT_ERR_INVALID_ARG;
+  if (k && (s = check_dims(B, H_k, N, D)) != DIT_OK) return s;
+  if (static_cast<long long>(B) * N > kMaxTokens) return DIT_ERR_INVALID_ARG;
+  const int sides = k ? 2 : 1;
+  const View in[2] = {{q, row_strides(q_strides, B, H_q, N, D), H_q}, {k, row_strides(k_strides, B, H_k, N, D), H_k}};
+  const View out[2] = {{q_out, row_strides(q_out_strides, B, H_q, N, D), H_q},
+                       {k_out, row_strides(k_out_strides, B, H_k, N, D), H_k}};
+  const void* weight[2] = {q_weight, k_weight};
+  if ((norm != 0 && norm != 1) || (!norm && (q_weight || k_weight)) || (norm && !(eps >= 0.f && std::isfinite(eps))) ||
+      !valid_dtype(weight_dtype))
+    return DIT_ERR_INVALID_ARG;
+  const int wsize = dtype_bytes(weight_dtype);
+  // The rotation: frequencies of all pairs, and positions given, or packed requests.
+  if ((axes > 0) != (freqs != nullptr) || axes < 0 || (!norm && !freqs)) return DIT_ERR_INVALID_ARG;
+  if (axes > 4) return DIT_ERR_UNSUPPORTED;
+  long long pairs = 0;
+  if (freqs) {
+    if (!axis_pairs || !aligned(freqs, 4) || (interleaved != 0 && interleaved != 1) || !std::isfinite(rot_scale))
+      return DIT_ERR_INVALID_ARG;
+    for (int a = 0; a < axes; ++a) {
+      if (axis_pairs[a] < 0) return DIT_ERR_INVALID_ARG;
+      pairs += axis_pairs[a];
+    }
+    if (pairs < 1 || 2 * pairs > D) return DIT_ERR_INVALID_ARG;
+    if (pairs % 8 != 0) return DIT_ERR_UNSUPPORTED;
+    const bool packed = !positions;
+    if (!aligned(positions, 4) || !aligned(cu_new, 4) || !aligned(start_lens, 4)) return DIT_ERR_INVALID_ARG;
+    if (packed && (!cu_new || !start_lens || requests < 1 || requests == INT_MAX || B != 1 || axes != 1))
+      return DIT_ERR_INVALID_ARG;
+    if (!packed && (cu_new || start_lens || pos_b < 0 || pos_axis < 0 || pos_b > kMaxSpan / B || pos_axis > kMaxSpan / 4))
+      return DIT_ERR_INVALID_ARG;
+  } else if (positions || cu_new || start_lens) {
+    return DIT_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < sides; ++i) {
+    if (!in[i].valid(B, N) || !out[i].valid(B, N) || !aligned(weight[i], wsize)) return DIT_ERR_INVALID_ARG;
+    if (!no_self_overlap(out[i].s, B, out[i].H, N, D)) return DIT_ERR_INVALID_ARG;
+  }
+  const long long pos_span = positions ? ((B - 1) * pos_b + (axes - 1) * pos_axis + N) * 4 : 0;
+  const Range reads[] = {span(q_weight, q_weight ? D * wsize : 0), span(k_weight, k_weight ? D * wsize : 0),
+                         span(freqs, freqs ? pairs * 4 : 0), span(positions, pos_span),
+                         span(cu_new, cu_new ? 4LL * (requests + 1LL) : 0), span(start_lens, start_lens ? 4LL * requests : 0)};
+  for (int i = 0; i < sides; ++i) {
+    for (const Range& r : reads)
+      if (overlap(out[i].range(B, N, D), r)) return DIT_ERR_INVALID_ARG;
+    // In place, or apart.
+    for (int j = 0; j < sides; ++j)
+      if (!(i == j && out[i].same(in[j])) && !views_apart(out[i], in[j], B, N, D)) return DIT_ERR_INVALID_ARG;
+  }
+  if (sides == 2 && !views_apart(out[0], out[1], B, N, D)) return DIT_ERR_INVALID_ARG;
+  ditattn::RopeLaunch a{};
+  for (int i = 0; i < sides; ++i) {
+    a.in[i] = in[i].p;
+    a.out[i] = const_cast<void*>(out[i].p);
+    a.is[i] = {in[i].s.b, in[i].s.h, in[i].s.n};
+    a.os[i] = {out[i].s.b, out[i].s.h, out[i].s.n};
+    a.weight[i] = weight[i];
+    a.heads[i] = in[i].H;
+  }
+  a.weight_f32 = weight_dtype == DIT_F32;
+  a.norm = norm != 0;
+  a.interleaved = interleaved != 0;
+  a.eps = eps;
+  a.rot_scale = rot_scale;
+  a.positions = positions;
+  a.pos_b = pos_b;
+  a.pos_axis = pos_axis;
+  a.cu_new = cu_new;
+  a.start_lens = start_lens;
+  a.requests = requests;
+  a.freqs = freqs;
+  a.pairs = static_cast<int>(pairs);
+  a.axes = axes;
+  for (int i = 0; i < axes; ++i) a.axis_pairs[i] = axis_pairs[i];
+  a.batch = B;
+  a.n = N;
+  a.d = D;
+  return done(ditattn::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+}
 
 size_t dit_paged_prefill_workspace_bytes(int D, int page_size, int max_pages) {
   if (D < 1 || page_size < 1 || max_pages < 1) return 0;

@@ -25,7 +25,7 @@ EXPORTED_SYMBOLS = ("dit_attn_fwd", "dit_attn_fwd_strided", "dit_attn_chunk_fwd"
                     "dit_attn_stale_kv_fwd", "dit_attn_chunk_fwd_splitkv",
                     "dit_attn_splitkv_workspace_bytes", "dit_attn_splitkv_suggest",
                     "dit_attn_chunk_fwd_splitkv_noalloc",
-                    "dit_paged_plan", "dit_paged_kv_write", "dit_paged_attn_fwd",
+                    "dit_qk_norm_rope", "dit_paged_plan", "dit_paged_kv_write", "dit_paged_attn_fwd",
                     "dit_paged_attn_workspace_bytes", "dit_paged_prefill_fwd",
                     "dit_paged_prefill_workspace_bytes", "dit_paged_select",
                     "dit_paged_select_workspace_bytes", "dit_attn_check", "dit_test_inject_stall", "dit_test_set_grid_limit",
@@ -88,6 +88,9 @@ def lib() -> ctypes.CDLL:
         L.dit_attn_chunk_fwd_accumulate.argtypes = [P, P, P, P, P, I, I, I, I, I, LL, F, P]
         L.dit_attn_lse_merge.restype = I
         L.dit_attn_lse_merge.argtypes = [P, P, I, P, P, I, I, I, I, I, I, P]
+        L.dit_qk_norm_rope.restype = I
+        L.dit_qk_norm_rope.argtypes = [P, SP, P, SP, I, P, SP, P, SP, I, I, F, P, P, I, P, ctypes.POINTER(I), I, I, F, P, LL,
+                                       LL, P, P, I, I, I, I, P]
         L.dit_paged_plan.restype = I
         L.dit_paged_plan.argtypes = [P, P, P, LL, P, P, P, P, P, P, I, I, I, I, I, I, P]
         L.dit_paged_kv_write.restype = I
@@ -724,6 +727,128 @@ def attention(q, k, v, scale=None, chunks=None, out_dtype=torch.float32,
         out, lse = chunk_attention(q, k, v, chunks, scale=scale, out_dtype=out_dtype,
                                    partial_dtype=partial_dtype)
     return out, lse
+
+
+# ------------------------------------------------------------------ norms and rotary positions
+
+
+def rope_freqs(rot, theta=10000.0, scaling=None, factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0,
+               device="cuda"):
+    """The frequencies of qk_norm_rope for `rot` rotated channels, f_i = theta^(-2 i / rot): (freqs fp32 [n], axis_pairs,
+    rot_scale).  `rot` is a number, or the channels of each position axis (a video's frame, row and column: 44, 42, 42 of
+    128), each with frequencies of its own.  For contexts `factor` times as long as original_len, `scaling`:
+      None      as they are
+      "linear"  every position divided by factor
+      "ntk"     a larger base, theta * factor^(rot / (rot - 2)): the slowest pair stretched by factor, the fastest not
+      "yarn"    pairs that turn less than beta_slow times in original_len positions divided by factor, those that
+                turn more than beta_fast times left, in between in proportion; rot_scale = 0.1 ln(factor) + 1
+    Computed in 64 bits on the host."""
+    dims = [int(rot)] if isinstance(rot, int) else [int(r) for r in rot]
+    if any(r < 2 or r % 2 for r in dims) or not dims:
+        raise ValueError("each axis has a positive, even number of channels")
+    if scaling not in (None, "linear", "ntk", "yarn") or not factor >= 1 or not theta > 0:
+        raise ValueError("scaling is None, 'linear', 'ntk' or 'yarn', factor at least 1, theta positive")
+    out = []
+    for r in dims:
+        i = torch.arange(r // 2, dtype=torch.float64)
+        base = theta * factor ** (r / (r - 2)) if scaling == "ntk" and r > 2 else theta
+        f = base ** (-2 * i / r)
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            turns = original_len * f / (2 * math.pi)
+            keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+            f = f * (keep + (1 - keep) / factor)
+        out.append(f)
+    return (torch.cat(out).float().to(device), [r // 2 for r in dims],
+            0.1 * math.log(factor) + 1 if scaling == "yarn" else 1.0)
+
+
+def _rope_view(t, name, index):
+    """(B, H, N, D) and strides (b, h, n) of a [B, H, N, D] or a packed [T, H, D] bf16 view."""
+    if t.dim() == 3:
+        _check_tensor(t, name, torch.bfloat16, (None,) * 3, index, rows=True)
+        return (1, t.shape[1], t.shape[0], t.shape[2]), Strides(t.shape[2], t.stride(1), t.stride(0))
+    _check_tensor(t, name, torch.bfloat16, (None,) * 4, index, rows=True)
+    return tuple(t.shape), Strides(*t.stride()[:3])
+
+
+def qk_norm_rope(q, k=None, positions=None, freqs=None, axis_pairs=None, interleaved=False, rot_scale=1.0, eps=None,
+                 q_weight=None, k_weight=None, cu_new=None, start_lens=None, q_out=None, k_out=None, stream=None):
+    """dit_qk_norm_rope: RMS norms of each head of q and k (eps None: none; weights [D], bf16 or fp32, or None) and rotary
+    positions (freqs None: none), in one pass.  q, k: bf16 views [B, H, N, D], or [T, H, D] of packed tokens.
+
+    freqs (fp32 [n]), axis_pairs and rot_scale are rope_freqs'; axis_pairs None: one axis.  Positions, int32: [N] or
+    [axes, N] for all of the batch, or [axes, B, N]; or, of packed requests, cu_new [R + 1] (paged_plan's) and
+    start_lens [R], the position of each request's first token: tokens of no request are then left as they are.
+
+    Returns (q_out, k_out or None), contiguous in the inputs' shapes unless given; in place: q_out=q, k_out=k."""
+    dev, index = _check_rows(q, "q", q.dim() if isinstance(q, torch.Tensor) and q.dim() in (3, 4) else 4)
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return qk_norm_rope(q, k, positions, freqs, axis_pairs, interleaved, rot_scale, eps, q_weight, k_weight, cu_new,
+                                start_lens, q_out, k_out)
+    (B, Hq, N, D), qs = _rope_view(q, "q", index)
+    Hk, ks, kos = 0, None, None
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+            raise ValueError("k must have as many dimensions as q")
+        (Bk, Hk, Nk, Dk), ks = _rope_view(k, "k", index)
+        if (Bk, Nk, Dk) != (B, N, D):
+            raise ValueError("q and k must be of the same tokens and head size")
+        if k_out is None:
+            k_out = torch.empty(k.shape, device=dev, dtype=torch.bfloat16)
+        else:
+            _check_tensor(k_out, "k_out", torch.bfloat16, k.shape, index, rows=True)
+        kos = _rope_view(k_out, "k_out", index)[1]
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    if q_out is None:
+        q_out = torch.empty(q.shape, device=dev, dtype=torch.bfloat16)
+    else:
+        _check_tensor(q_out, "q_out", torch.bfloat16, q.shape, index, rows=True)
+    qos = _rope_view(q_out, "q_out", index)[1]
+    wdt = torch.bfloat16
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    if given:
+        wdt = given[0].dtype
+        for w in given:
+            _check_tensor(w, "weights", wdt, (D,), index)
+    axes, pairs, pos_b, pos_axis, requests = 0, None, 0, 0, 0
+    if freqs is None:
+        if positions is not None or cu_new is not None or start_lens is not None:
+            raise ValueError("positions need freqs")
+    else:
+        _check_tensor(freqs, "freqs", torch.float32, (None,), index)
+        pairs = [freqs.shape[0]] if axis_pairs is None else [int(x) for x in axis_pairs]
+        axes = len(pairs)
+        if sum(pairs) != freqs.shape[0]:
+            raise ValueError(f"axis_pairs must add up to the {freqs.shape[0]} frequencies")
+        if positions is not None:
+            if cu_new is not None or start_lens is not None:
+                raise ValueError("positions, or cu_new and start_lens")
+            shape = {1: (N,), 2: (axes, N), 3: (axes, B, N)}.get(getattr(positions, "dim", int)(), (axes, B, N))
+            if len(shape) == 1 and axes != 1:
+                raise ValueError(f"positions must have shape [{axes}, {N}]")
+            _check_tensor(positions, "positions", torch.int32, shape, index)
+            pos_b, pos_axis = (N if len(shape) == 3 else 0), (B * N if len(shape) == 3 else N)
+        else:
+            if cu_new is None or start_lens is None or not isinstance(start_lens, torch.Tensor) or start_lens.dim() != 1:
+                raise ValueError("freqs need positions, or cu_new and start_lens")
+            requests = start_lens.shape[0]
+            _check_tensor(start_lens, "start_lens", torch.int32, (requests,), index)
+            _check_tensor(cu_new, "cu_new", torch.int32, (requests + 1,), index)
+        pairs = (ctypes.c_int * axes)(*pairs)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    st = lib().dit_qk_norm_rope(
+        q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, ptr(k), ks, ptr(k_out), kos, Hk, 0 if eps is None else 1,
+        0.0 if eps is None else float(eps), ptr(q_weight), ptr(k_weight), _dt(wdt), ptr(freqs), pairs, axes,
+        1 if interleaved else 0, float(rot_scale), ptr(positions), pos_b, pos_axis, ptr(cu_new), ptr(start_lens), requests,
+        B, N, D, torch._C._cuda_getCurrentRawStream(index))
+    if st != DIT_OK:
+        raise DitError(st, "dit_qk_norm_rope")
+    return q_out, k_out
 
 
 # ------------------------------------------------------------------ paged key/value caches

@@ -286,6 +286,43 @@ dit_status dit_layout_copy(const void* src, const dit_strides* src_strides, void
                            const dit_strides* dst_strides, int B, int H, int N, int D,
                            dit_dtype dtype, dit_stream stream);
 
+/*
+ * Norms of queries and keys for each head and rotary positions, in one pass, before the attention or
+ * before the cache (arganzheng.life multi-GPU diffusion parallelism, section 4.1 Ulysses: RoPE sliced with the
+ * tokens; valdrada.cn Wan2.2, TP section: QK norms).  For every head x of every token,
+ *   z = w x / sqrt(mean_d x_d^2 + eps)                                            (norm; else z = x)
+ * and pair i of the first 2 n channels, n the sum of axis_pairs, (2 i, 2 i + 1) where `interleaved`, else
+ * (i, i + n), at the angle t = pos_a(i) * freqs[i],
+ *   y_first = s (z_first cos t - z_second sin t),  y_second = s (z_first sin t + z_second cos t)
+ * with s = rot_scale; the channels behind them are y = z.  In 32 bits, rounded to bf16 once; the angle
+ * is taken modulo a turn exactly, whatever the position.  A sum of squares that overflows 32 bits makes its head 0 or NaN.
+ *   q, k          : device bf16 [B, H, N, D] views (read); NULL strides: contiguous.  A packed step's [T, H, D] is
+ *                   B = 1, N = T.  k may be NULL (H_k = 0, no k_out, no k_weight): queries alone.
+ *   q_out, k_out  : device bf16 views of the same shapes (written), of any layout (token-major in, head-major out):
+ *                   each may be its input in place (the same view), and shares no element with anything else.
+ *   norm          : 0 or 1; eps >= 0 (read with norm alone)
+ *   q_weight, k_weight : device [D] of weight_dtype (read), or NULL (1); NULL without norm
+ *   freqs         : device fp32 [n] (read): the angle of each pair per position, so that stretched and
+ *                   scaled positions are a matter of the table; NULL (axes = 0): no rotation
+ *   axis_pairs    : host int [axes]: pair i turns with the position axis a(i) in which it falls (a video's frame,
+ *                   row and column); 1 axis: a token's index.  n a multiple of 8, 2 n <= D; axes <= 4
+ *                   (more, or other n: DIT_ERR_UNSUPPORTED).
+ *   positions     : device int32 (read): token (b, n) is at positions[b * pos_b + a * pos_axis + n] on axis a (pos_b = 0:
+ *                   the same for every b); any value.  NULL: packed requests (B = 1, one axis),
+ *   cu_new, start_lens, requests : device int32 [requests + 1], [requests] (read): token n of request r (dit_paged_plan's
+ *                   cu_new) is at start_lens[r] + n - cu_new[r].  Tokens of no request are left as they are.
+ *                   cu_new ascends (else its tokens' positions are unspecified).
+ *   B * N         : at most 2^30
+ */
+dit_status dit_qk_norm_rope(const void* q, const dit_strides* q_strides, void* q_out,
+                            const dit_strides* q_out_strides, int H_q, const void* k,
+                            const dit_strides* k_strides, void* k_out, const dit_strides* k_out_strides,
+                            int H_k, int norm, float eps, const void* q_weight, const void* k_weight,
+                            dit_dtype weight_dtype, const float* freqs, const int* axis_pairs, int axes,
+                            int interleaved, float rot_scale, const int* positions, long long pos_b,
+                            long long pos_axis, const int* cu_new, const int* start_lens, int requests, int B,
+                            int N, int D, dit_stream stream);
+
 /* ---------------------------------------------------------------------------
  * Paged key/value caches: requests of different and growing lengths in pages of
  * one pool, for generation with cached keys, a token at a time (text encoders and

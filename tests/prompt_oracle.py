@@ -65,3 +65,25 @@ def attend(q, k_cache, v_cache, table, seq_lens, cu_new, scale, causal=True, sta
             a = torch.where(see, x.abs() @ k.abs().T, 0.0)
             mag[row:row + n, h] = scale * a.amax(1)
     return o.cpu(), lse.cpu(), owned, (mag.cpu(), pv.cpu())
+
+
+def norm_rope(x, weight, eps, freqs, axis_pairs, positions, interleaved, rot_scale):
+    """(y, size) in fp64 of x [B, H, N, D]: norms (eps None: none), then the rotation (freqs None: none) at positions
+    [axes, B, N]; size is |z_first| + |z_second| of each channel's pair, what y's errors are relative to."""
+    z = x.detach().cpu().double()
+    if eps is not None:
+        z = z / torch.sqrt((z * z).mean(-1, keepdim=True) + eps)
+        if weight is not None:
+            z = z * weight.cpu().double()
+    if freqs is None:
+        return z, z.abs()
+    f = freqs.cpu().double()
+    axis = np.repeat(np.arange(len(axis_pairs)), axis_pairs)
+    t = positions.cpu().double()[axis].permute(1, 2, 0)[:, None] * f  # [B, 1, N, n]
+    c, s, n = torch.cos(t) * rot_scale, torch.sin(t) * rot_scale, len(f)
+    i, j = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+    y, size = z.clone(), z.abs()
+    y[..., i], y[..., j] = z[..., i] * c - z[..., j] * s, z[..., i] * s + z[..., j] * c
+    both = (z[..., i].abs() + z[..., j].abs()) * abs(rot_scale)
+    size[..., i], size[..., j] = both, both
+    return y, size
