@@ -4,14 +4,16 @@
 //   pair i of the first 2 n channels, (2 i, 2 i + 1) or (i, i + n), at angle t_i = pos_a(i) f_i:
 //     y_first = s (z_first cos t_i - z_second sin t_i),  y_second = s (z_first sin t_i + z_second cos t_i)
 // Each value is read and written once: bound by HBM (75600 tokens, 40 + 40 heads of 128, token-major to
-// head-major: %s us, %s TB/s; one token of each of 64 requests, 24 + 8 heads: %s us in a graph).
+// head-major: 505 us, 6.1 TB/s; half-and-half pairs in place of interleaved ones 487 us, 6.4; a copy's rate is 6.8).
 //
-// A lane holds 8 neighbouring channels of a head, 16 bytes, so that a warp takes two heads of 128 or four of 64 at
-// a step.  Every warp walks over tokens by itself, with kIters steps' loads in flight (the next token's first ones
-// before its angles), and no barrier holds it up: with a block's warps on one token and its angles shared behind
-// a barrier, 75600 tokens took 1370 us.  It works the token's cosines and sines out into shared memory, and folds them
-// with the weights into two factors a channel, y = r (A x + B x'), with x' the pair's other channel: the lane's own, or
-// that of the lane n / 8 away.  Where there are few tokens several warps take one, a part of its heads each.
+// A lane holds two 16-byte pieces of a head, of 8 channels each, so that a warp takes four heads of 128 or eight of 64 at
+// a step (queries, then keys), and a pair's channels are in one lane: neighbours in a piece, or the pieces i and
+// i + n / 8.  Every warp walks over tokens by itself, the loads of kIters steps ahead of its arithmetic (the next
+// token's first ones before its angles), and no barrier holds it up: with a block's warps on one token and its angles
+// shared behind a barrier, 75600 tokens took 1370 us; with one piece a lane and the other of a pair by a shuffle,
+// 600 us, bound by the instructions.  It works the token's cosines and sines out into shared memory, and folds them with
+// the weights into two factors a channel, y = r (A x + B x'), with x' the pair's other channel.  Where there are few
+// tokens several warps take one, a part of its heads each.
 //
 // The angle is exact whatever the position: a position is a whole number, so that f_i in turns need only be
 // known modulo 1, and as a 64-bit fraction its product with the position wraps by itself.  The phase is then off by
@@ -26,13 +28,14 @@
 #include "attn_host.cuh"
 #include "paged_device.cuh"
 #include "paged_launch.h"
+#include "sm103_ptx.cuh"
 
 namespace ditattn {
 namespace {
 
 constexpr int kIters = 4;   // steps of a warp whose loads are in flight at once
 constexpr int kWarps = 8;   // of a block
-constexpr int kBlocks = 4;  // of an SM
+constexpr int kBlocks = 2;  // of an SM
 
 struct Side {
   const __nv_bfloat16* in;
@@ -92,21 +95,22 @@ __device__ __forceinline__ int request_of(const RopeParams& p, int n, int lane) 
   return n < p.cu_new[lo + 1] ? lo : -1;
 }
 
-template <int D, bool kInterleaved>
+// kWhole: all channels turn.
+template <int D, bool kInterleaved, bool kWhole>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;  // lanes of a head, heads of a warp's step
-  __shared__ uint64_t step_turns[64];                  // the pairs' turns a position
-  __shared__ float size[64];                           // their scale (NaN where the frequency is not finite)
-  __shared__ float2 turn[kWarps][64];                  // (cos, sin) of the pairs at each warp's token, scaled
+  constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes of a head, heads of a warp's step
+  __shared__ uint64_t step_turns[64];                   // the pairs' turns a position
+  __shared__ float size[64];                            // their scale (NaN where the frequency is not finite)
+  __shared__ float2 turn[kWarps][64];                   // (cos, sin) of the pairs at each warp's token, scaled
   __shared__ float weights[2][D];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int chan = lane % kLanes * 8, sub = lane / kLanes;
-  const bool rotated = chan < 2 * p.pairs;
-  const bool second = !kInterleaved && chan >= p.pairs;  // the lane's channels are the pairs' second ones
-  const int from = !rotated || kInterleaved ? lane : second ? lane - p.pairs / 8 : lane + p.pairs / 8;
-  // Steps: kHeads query heads, or key heads, at a time.
-  const int q_steps = (p.side[0].heads + kHeads - 1) / kHeads;
-  const int steps = q_steps + (p.side[1].heads + kHeads - 1) / kHeads;
+  const int l = lane % kLanes, sub = lane / kLanes;
+  const int turning = p.pairs / 8;  // pieces of first channels
+  // The lane's pieces: the two of its pairs (not interleaved), or any two.
+  const int piece0 = kInterleaved || l < turning ? l : 2 * l;
+  const int piece1 = kInterleaved ? l + kLanes : l < turning ? l + turning : 2 * l + 1;
+  const bool rotated[2] = {piece0 < 2 * turning, piece1 < 2 * turning};
+  const int heads = p.side[0].heads + p.side[1].heads, steps = (heads + kHeads - 1) / kHeads;
   const unsigned units = static_cast<unsigned>(p.batch) * p.n * p.parts, stride = gridDim.x * kWarps;
   unsigned unit = blockIdx.x * kWarps + warp;
   int b, n, part;  // of the unit
@@ -116,16 +120,40 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(cons
     b = p.batch == 1 ? 0 : static_cast<int>(token / p.n);
     n = static_cast<int>(token - static_cast<unsigned>(b) * p.n);
   };
-  uint4 x[kIters];
-  auto load = [&](int base) {
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int step = base + i * p.parts, side = step >= q_steps;
-      const Side& s = p.side[side];
-      const int head = (step - (side ? q_steps : 0)) * kHeads + sub;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (step < steps && head < s.heads) x[i] = load_once(s.in + b * s.is.b_ + head * s.is.h_ + n * s.is.n_ + chan);
+  // The lane's walk over its heads at the token (all queries' before the keys'), for loads or for stores.
+  struct Walk {
+    int head;       // of both
+    int side;
+    char* at;       // the head's first channel
+    int64_t apart;  // bytes to the next head
+  };
+  auto place = [&](Walk& w, bool out) {
+    w.side = w.head >= p.side[0].heads;
+    const Side& s = p.side[w.side];
+    const Strides& st = out ? s.os : s.is;
+    const int h = w.head - (w.side ? p.side[0].heads : 0);
+    w.at = reinterpret_cast<char*>(out ? s.out : const_cast<__nv_bfloat16*>(s.in)) + 2 * (b * st.b_ + n * st.n_ + h * st.h_);
+    w.apart = 2 * p.parts * kHeads * st.h_;
+  };
+  auto advance = [&](Walk& w, bool out) {
+    w.head += p.parts * kHeads;
+    w.at += w.apart;
+    if (w.side == 0 && w.head >= p.side[0].heads && w.head < heads) place(w, out);
+  };
+  Walk ld = {}, sd = {};
+  uint4 x[kIters][2];
+  auto load = [&](uint4 (&y)[2]) {
+    if (ld.head < heads) {
+      y[0] = load_once(ld.at + 16 * piece0);
+      y[1] = load_once(ld.at + 16 * piece1);
+      advance(ld, false);
     }
+  };
+  auto load_first = [&]() {
+    ld.head = part * kHeads + sub;
+    if (ld.head < heads) place(ld, false);
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) load(x[i]);
   };
   // Lane a: the token's position on axis a; packed: each lane's is that of the one axis.
   auto position = [&](bool& live) -> long long {
@@ -145,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(cons
   long long at = 0;
   if (unit < units) {
     split(unit);
-    load(part);
+    load_first();
     at = position(live);
   }
   if (threadIdx.x < p.pairs) {
@@ -177,66 +205,80 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(cons
         }
       }
       __syncwarp();
-      float fa[8], fb[8];
-      int now = -1;  // whose factors they are
-      for (int base = part; base < steps; base += kIters * p.parts) {
-        if (base != part) load(base);
+      float fa[2][8], fb[2][8];
+      int now = -1;  // whose factors the lane has
+      sd.head = part * kHeads + sub;
+      if (sd.head < heads) place(sd, true);
+      int step = part;
+      while (step < steps) {
 #pragma unroll
         for (int i = 0; i < kIters; ++i) {
-          const int step = base + i * p.parts, side = step >= q_steps;
           if (step >= steps) break;
-          const Side& s = p.side[side];
-          const int head = (step - (side ? q_steps : 0)) * kHeads + sub;
-          if (side != now) {
-            now = side;
+          if (__any_sync(~0u, sd.side != now)) {
+            now = sd.side;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int c = chan + j;
-              fa[j] = weights[side][c];
-              fb[j] = 0.f;
-              if (rotated) {
-                const int pair = kInterleaved ? c / 2 : second ? c - p.pairs : c;
-                const int other = kInterleaved ? c ^ 1 : second ? c - p.pairs : c + p.pairs;
-                const float2 t = turn[warp][pair];
-                fa[j] *= t.x;
-                fb[j] = weights[side][other] * ((kInterleaved ? c & 1 : second) ? t.y : -t.y);
+            for (int h = 0; h < 2; ++h) {
+              const int c0 = 8 * (h ? piece1 : piece0);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                fa[h][j] = weights[now][c0 + j];
+                fb[h][j] = 0.f;
+                if (rotated[h]) {
+                  const float2 t = turn[warp][kInterleaved ? (c0 + j) / 2 : 8 * piece0 + j];
+                  fa[h][j] *= t.x;
+                  const float other = weights[now][kInterleaved ? (c0 + j) ^ 1 : 8 * (h ? piece0 : piece1) + j];
+                  fb[h][j] = other * ((kInterleaved ? j & 1 : h) ? t.y : -t.y);
+                }
               }
             }
           }
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          float v[8];
+          float v[2][8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[h][2 * j] = ptx::bf16lo(w[j]);
+              v[h][2 * j + 1] = ptx::bf16hi(w[j]);
+            }
           }
+          load(x[i]);
           float r = 1.f;
           if (p.norm) {
-            float sum = 0.f;
+            float sum = 0.f, more = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+            for (int j = 0; j < 8; ++j) {
+              sum = fmaf(v[0][j], v[0][j], sum);
+              more = fmaf(v[1][j], v[1][j], more);
+            }
+            sum += more;
 #pragma unroll
             for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
             r = rsqrtf(sum * (1.f / D) + p.eps);
           }
-          uint32_t z[4];
+          uint4 z[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float o0 = v[2 * j + 1], o1 = v[2 * j];  // the pairs' other channels
-            if (!kInterleaved && p.pairs) {
-              const uint32_t o = __shfl_sync(~0u, w[j], from);
-              o0 = __uint_as_float(o << 16);
-              o1 = __uint_as_float(o & 0xffff0000u);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float o = fb[h][j + e] * (kInterleaved ? v[h][j + 1 - e] : v[1 - h][j + e]);
+                if constexpr (!kWhole) o = rotated[h] ? o : 0.f;  // (0 times what is not finite)
+                y[e] = fmaf(fa[h][j + e], v[h][j + e], o) * r;
+              }
+              w[j / 2] = ptx::pack_bf16x2(y[0], y[1]);
             }
-            // (0 times what is not finite: channels that are not turned take no other)
-            const float y0 = fmaf(fa[2 * j], v[2 * j], rotated ? fb[2 * j] * o0 : 0.f) * r;
-            const float y1 = fmaf(fa[2 * j + 1], v[2 * j + 1], rotated ? fb[2 * j + 1] * o1 : 0.f) * r;
-            const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-            z[j] = *reinterpret_cast<const uint32_t*>(&h);
+            z[h] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (head < s.heads)
-            *reinterpret_cast<uint4*>(s.out + b * s.os.b_ + head * s.os.h_ + n * s.os.n_ + chan) =
-                make_uint4(z[0], z[1], z[2], z[3]);
+          if (sd.head < heads) {
+            *reinterpret_cast<uint4*>(sd.at + 16 * piece0) = z[0];
+            *reinterpret_cast<uint4*>(sd.at + 16 * piece1) = z[1];
+            advance(sd, true);
+          }
+          step += p.parts;
         }
       }
       __syncwarp();
@@ -244,7 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(cons
     unit += stride;
     if (unit >= units) break;
     split(unit);
-    load(part);
+    load_first();
     at = position(live);
   }
 }
@@ -271,19 +313,23 @@ cudaError_t launch_qk_norm_rope(const RopeLaunch& a, cudaStream_t st) {
   p.rot_scale = a.rot_scale;
   p.batch = a.batch;
   p.n = a.n;
-  const int heads = 256 / a.d;  // of a warp's step
-  const int steps = (a.heads[0] + heads - 1) / heads + (a.heads[1] + heads - 1) / heads;
+  const int heads = 512 / a.d;  // of a warp's step
+  const int steps = (a.heads[0] + a.heads[1] + heads - 1) / heads;
   const long long tokens = static_cast<long long>(a.batch) * a.n;
-  // A warp a token, or, of fewer tokens than the GPU's warps, several.
+  // A warp a token, or, of fewer tokens than the GPU's warps, several.  (Of a few tokens a warp, splitting them too so
+  // that the last round is shorter costs more angles than it saves: 4608 tokens, 24 + 24 heads, 29 and 34 us.)
   const long long warps = static_cast<long long>(host::sm_count()) * kBlocks * kWarps;
   p.parts = static_cast<int>(std::min<long long>(steps, std::max(1LL, warps / tokens)));
   const long long blocks = std::min(warps, tokens * p.parts + kWarps - 1) / kWarps;
   const dim3 grid(static_cast<unsigned>(blocks)), block(32 * kWarps);
-  if (a.d == 64)
-    return a.interleaved ? launch_after(qk_norm_rope_kernel<64, true>, grid, block, 0, st, p)
-                         : launch_after(qk_norm_rope_kernel<64, false>, grid, block, 0, st, p);
-  return a.interleaved ? launch_after(qk_norm_rope_kernel<128, true>, grid, block, 0, st, p)
-                       : launch_after(qk_norm_rope_kernel<128, false>, grid, block, 0, st, p);
+  auto run = [&](auto kernel) { return launch_after(kernel, grid, block, 0, st, p); };
+  const bool whole = 2 * p.pairs == a.d;
+  if (a.d == 64) {
+    if (a.interleaved) return whole ? run(qk_norm_rope_kernel<64, true, true>) : run(qk_norm_rope_kernel<64, true, false>);
+    return whole ? run(qk_norm_rope_kernel<64, false, true>) : run(qk_norm_rope_kernel<64, false, false>);
+  }
+  if (a.interleaved) return whole ? run(qk_norm_rope_kernel<128, true, true>) : run(qk_norm_rope_kernel<128, true, false>);
+  return whole ? run(qk_norm_rope_kernel<128, false, true>) : run(qk_norm_rope_kernel<128, false, false>);
 }
 
 }  // namespace ditattn
