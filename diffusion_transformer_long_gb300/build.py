@@ -18,7 +18,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libditattn.so")
 SOURCES = ["attn_fwd.cu", "attn_fwd_short.cu", "lse_merge.cu", "layout_copy.cu", "noalloc.cu", "ditattn_api.cu",
            "paged_api.cu", "paged_plan.cu", "paged_write.cu", "paged_attn.cu", "paged_attn_few.cu",
-           "paged_select.cu", "prompt_api.cu", "paged_prefill.cu", "qk_norm_rope.cu"]
+           "paged_select.cu", "prompt_api.cu", "paged_prefill.cu", "qk_norm_rope.cu",
+           "paged_mass.cu", "paged_evict.cu"]
 HEADERS = ["attn_kernel.cuh", "attn_host.cuh", "merge_math.cuh", "sm103_ptx.cuh", "launch.h", "api_checks.h",
            "paged_launch.h", "paged_device.cuh", "paged_attn_kernel.cuh", "paged_checks.h",
            "paged_prefill_kernel.cuh"]

@@ -110,6 +110,42 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st);
 // Workspace bytes on the current device; `keys`: the most that a request can hold.
 size_t paged_prefill_workspace(int d, long long keys);
 
+struct MassLaunch {
+  const void* q;
+  long long q_n, q_h;
+  const float* lse;
+  const void* k_cache;
+  Strides ks;
+  const int* table;
+  long long table_stride;
+  const int* seq_lens;
+  const int* cu_new;      // null: one token a request
+  const int* start_lens;  // may be null
+  const float* mass;
+  float* mass_out;
+  int tokens, batch, h_q, h_kv, d, page_size, n_pages, max_pages, window;
+  float scale;
+};
+cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st);
+
+struct EvictLaunch {
+  const float* mass;
+  const int* table;
+  long long table_stride;
+  int* table_out;
+  long long out_stride;
+  const int* seq_lens;
+  int* lens_out;
+  int* stack;
+  const int* n_free;
+  int* n_free_out;
+  int batch, h_kv, page_size, n_pages, max_pages, capacity, keep, recent;
+  void* workspace;
+};
+constexpr int kEvictMaxBatch = 8192;
+cudaError_t launch_paged_evict(const EvictLaunch& a, cudaStream_t st);
+size_t paged_evict_workspace(int batch, int max_pages);
+
 struct SelectLaunch {
   const void* q;
   long long q_b, q_h;

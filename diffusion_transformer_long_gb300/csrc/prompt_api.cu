@@ -237,4 +237,101 @@ dit_status dit_paged_prefill_fwd(const void* q, const dit_strides* q_strides, co
   return done(ditattn::launch_paged_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 
+dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, const float* lse, const void* k_cache,
+                               const dit_strides* k_strides, const int* block_table, long long table_stride,
+                               const int* seq_lens, const int* cu_new, const int* start_lens, const float* mass,
+                               float* mass_out, int T, int B, int H_q, int H_kv, int D, int page_size,
+                               int n_pages, int max_pages, int window, float scale, dit_stream stream) {
+  if (T < 1 || T > kMaxTokens || B < 1 || B == INT_MAX || window < 0) return DIT_ERR_INVALID_ARG;
+  if (!cu_new && (T != B || start_lens)) return DIT_ERR_INVALID_ARG;
+  dit_status s = check_heads(T, H_q, H_kv, D);
+  if (s != DIT_OK) return s;
+  s = check_pages(page_size, n_pages, max_pages);
+  if (s != DIT_OK) return s;
+  const dit_strides qs = token_strides(q_strides, T, H_q, D);
+  const dit_strides ks = cache_strides(k_strides, n_pages, H_kv, page_size, D);
+  if (!valid_tokens(q, qs, T, H_q) || !valid_cache(k_cache, ks, n_pages, H_kv) || !lse || !aligned(lse, 4) ||
+      !valid_table(block_table, table_stride, B, max_pages) || !seq_lens || !aligned(seq_lens, 4) ||
+      !aligned(cu_new, 4) || !aligned(start_lens, 4) || !mass || !aligned(mass, 4) || !mass_out || !aligned(mass_out, 4))
+    return DIT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return DIT_ERR_INVALID_ARG;
+  const Range out = span(mass_out, 4LL * n_pages * H_kv);
+  const Range ins[] = {span(q, view_span(qs, 1, H_q, T, D, 2)), span(lse, 4LL * T * H_q),
+                       cache_range(k_cache, ks, n_pages, H_kv, page_size, D),
+                       span(block_table, table_bytes(B, max_pages, table_stride)), span(seq_lens, 4LL * B),
+                       span(cu_new, cu_new ? 4LL * (B + 1LL) : 0), span(start_lens, start_lens ? 4LL * B : 0)};
+  for (const Range& in : ins)
+    if (overlap(out, in)) return DIT_ERR_INVALID_ARG;
+  if (mass != mass_out && overlap(out, span(mass, 4LL * n_pages * H_kv))) return DIT_ERR_INVALID_ARG;
+  ditattn::MassLaunch a;
+  a.q = q;
+  a.q_n = qs.n;
+  a.q_h = qs.h;
+  a.lse = lse;
+  a.k_cache = k_cache;
+  a.ks = {ks.b, ks.h, ks.n};
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.seq_lens = seq_lens;
+  a.cu_new = cu_new;
+  a.start_lens = start_lens;
+  a.mass = mass;
+  a.mass_out = mass_out;
+  a.tokens = T;
+  a.batch = B;
+  a.h_q = H_q;
+  a.h_kv = H_kv;
+  a.d = D;
+  a.page_size = page_size;
+  a.n_pages = n_pages;
+  a.max_pages = max_pages;
+  a.window = window;
+  a.scale = scale;
+  return done(ditattn::launch_paged_mass(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dit_paged_evict_workspace_bytes(int B, int max_pages) {
+  if (B < 1 || max_pages < 1) return 0;
+  return ditattn::paged_evict_workspace(B, max_pages);
+}
+
+dit_status dit_paged_evict(const float* mass, const int* block_table, long long table_stride, int* table_out,
+                           long long table_out_stride, const int* seq_lens, int* seq_lens_out, int* free_pages,
+                           const int* n_free, int* n_free_out, int B, int H_kv, int page_size, int n_pages,
+                           int max_pages, int pool_capacity, int keep, int recent, void* workspace,
+                           size_t workspace_bytes, dit_stream stream) {
+  if (B < 1 || H_kv < 1 || pool_capacity < 0 || keep < 1 || recent < 1 || recent > keep) return DIT_ERR_INVALID_ARG;
+  const dit_status s = check_pages(page_size, n_pages, max_pages);
+  if (s != DIT_OK) return s;
+  if (B > ditattn::kEvictMaxBatch) return DIT_ERR_UNSUPPORTED;
+  if (!mass || !seq_lens || !seq_lens_out || !n_free || !n_free_out || (!free_pages && pool_capacity > 0))
+    return DIT_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(mass), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(seq_lens_out), static_cast<const void*>(free_pages),
+                        static_cast<const void*>(n_free), static_cast<const void*>(n_free_out)})
+    if (!aligned(p, 4)) return DIT_ERR_INVALID_ARG;
+  if (!valid_table(block_table, table_stride, B, max_pages) || !valid_table(table_out, table_out_stride, B, max_pages))
+    return DIT_ERR_INVALID_ARG;
+  const bool in_place = table_out == block_table && (B == 1 || table_out_stride == table_stride);
+  const size_t need = dit_paged_evict_workspace_bytes(B, max_pages);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return DIT_ERR_INVALID_ARG;
+  const Range table = span(block_table, table_bytes(B, max_pages, table_stride));
+  const Range outs[] = {span(table_out, table_bytes(B, max_pages, table_out_stride)), span(seq_lens_out, 4LL * B),
+                        span(free_pages, 4LL * pool_capacity), span(n_free_out, 4),
+                        span(workspace, static_cast<long long>(need))};
+  const Range ins[] = {table, span(seq_lens, 4LL * B), span(mass, 4LL * n_pages * H_kv), span(n_free, 4)};
+  const bool same[5] = {in_place, seq_lens_out == seq_lens, false, n_free_out == n_free, false};
+  const int of[5] = {0, 1, -1, 3, -1};  // the input that an output may be
+  for (int i = 0; i < 5; ++i) {
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(outs[i], outs[j])) return DIT_ERR_INVALID_ARG;
+    for (int j = 0; j < 4; ++j)
+      if (!(same[i] && j == of[i]) && overlap(outs[i], ins[j])) return DIT_ERR_INVALID_ARG;
+  }
+  ditattn::EvictLaunch a{mass,   block_table, table_stride, table_out, table_out_stride, seq_lens,  seq_lens_out, free_pages,
+                         n_free, n_free_out,  B,            H_kv,      page_size,        n_pages,   max_pages,    pool_capacity,
+                         keep,   recent,      workspace};
+  return done(ditattn::launch_paged_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

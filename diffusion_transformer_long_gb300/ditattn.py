@@ -27,7 +27,8 @@ EXPORTED_SYMBOLS = ("dit_attn_fwd", "dit_attn_fwd_strided", "dit_attn_chunk_fwd"
                     "dit_attn_chunk_fwd_splitkv_noalloc",
                     "dit_qk_norm_rope", "dit_paged_plan", "dit_paged_kv_write", "dit_paged_attn_fwd",
                     "dit_paged_attn_workspace_bytes", "dit_paged_prefill_fwd",
-                    "dit_paged_prefill_workspace_bytes", "dit_paged_select",
+                    "dit_paged_prefill_workspace_bytes", "dit_paged_page_mass", "dit_paged_evict",
+                    "dit_paged_evict_workspace_bytes", "dit_paged_select",
                     "dit_paged_select_workspace_bytes", "dit_attn_check", "dit_test_inject_stall", "dit_test_set_grid_limit",
                     "dit_status_string", "dit_version")
 
@@ -105,6 +106,12 @@ def lib() -> ctypes.CDLL:
                                             P, ctypes.c_size_t, P]
         L.dit_paged_prefill_workspace_bytes.restype = ctypes.c_size_t
         L.dit_paged_prefill_workspace_bytes.argtypes = [I, I, I]
+        L.dit_paged_page_mass.restype = I
+        L.dit_paged_page_mass.argtypes = [P, SP, P, P, SP, P, LL, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, P]
+        L.dit_paged_evict.restype = I
+        L.dit_paged_evict.argtypes = [P, P, LL, P, LL, P, P, P, P, P, I, I, I, I, I, I, I, I, P, ctypes.c_size_t, P]
+        L.dit_paged_evict_workspace_bytes.restype = ctypes.c_size_t
+        L.dit_paged_evict_workspace_bytes.argtypes = [I, I]
         L.dit_paged_select.restype = I
         L.dit_paged_select.argtypes = [P, SP, P, P, LL, P, P, I, I, I, I, I, I, I, I, P,
                                        ctypes.c_size_t, P]
@@ -1148,6 +1155,94 @@ def paged_prefill_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_new, start_
     if st != DIT_OK:
         raise DitError(st, "dit_paged_prefill_fwd")
     return out, lse
+
+
+def paged_page_mass(q, lse, k_cache, block_table, seq_lens, mass, cu_new=None, start_lens=None, window=0, mass_out=None,
+                    scale=None, stream=None):
+    """dit_paged_page_mass: adds to each page's drawn weight, mass fp32 [n_pages, H_kv], what the step's queries
+    q bf16 [T, H_q, D] gave it, from their attention's lse fp32 [T, H_q]; pages whose first key is new start from
+    nothing.  cu_new (int32 [B + 1]): packed new tokens, of which the last `window` (0: all) of each request count;
+    None: one token of each request (T = B).  In place unless mass_out is given, of which only the pages of requests
+    with new tokens are written.  Returns mass_out."""
+    dev, index = _check_rows(q, "q", 3)
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_page_mass(q, lse, k_cache, block_table, seq_lens, mass, cu_new, start_lens, window, mass_out, scale)
+    T, Hq, D = q.shape
+    n_pages, Hkv, P, Dc = _check_caches(k_cache, k_cache, index)
+    if Dc != D:
+        raise ValueError(f"the cache holds heads of {Dc}, q of {D}")
+    B = _batch_of(seq_lens)
+    max_pages, stride = _check_table(block_table, seq_lens, B, index)
+    _check_tensor(lse, "lse", torch.float32, (T, Hq), index)
+    _check_tensor(mass, "mass", torch.float32, (n_pages, Hkv), index)
+    if mass_out is None:
+        mass_out = mass
+    else:
+        _check_tensor(mass_out, "mass_out", torch.float32, (n_pages, Hkv), index)
+    if cu_new is not None:
+        _check_tensor(cu_new, "cu_new", torch.int32, (B + 1,), index)
+    if start_lens is not None:
+        _check_tensor(start_lens, "start_lens", torch.int32, (B,), index)
+    qn, qh, _ = q.stride()
+    st = lib().dit_paged_page_mass(
+        q.data_ptr(), Strides(D, qh, qn), lse.data_ptr(), k_cache.data_ptr(), Strides(*k_cache.stride()[:3]),
+        block_table.data_ptr(), stride, seq_lens.data_ptr(), None if cu_new is None else cu_new.data_ptr(),
+        None if start_lens is None else start_lens.data_ptr(), mass.data_ptr(), mass_out.data_ptr(), T, B, Hq, Hkv, D, P,
+        n_pages, max_pages, int(window), 1.0 / math.sqrt(D) if scale is None else float(scale),
+        torch._C._cuda_getCurrentRawStream(index))
+    if st != DIT_OK:
+        raise DitError(st, "dit_paged_page_mass")
+    return mass_out
+
+
+def paged_evict(mass, block_table, seq_lens, free_pages, n_free, page_size, keep, recent=1, table_out=None,
+                seq_lens_out=None, n_free_out=None, workspace=None, stream=None):
+    """dit_paged_evict: requests of more than `keep` pages keep the newest `recent` and, of the others, those that drew
+    most weight (mass fp32 [n_pages, H_kv], paged_page_mass's); the others' numbers go onto the stack free_pages.  The table
+    changes in place unless table_out [B, max_pages] is given.  The workspace is allocated with torch unless given.
+
+    Returns (seq_lens_out [B], n_free_out [1]); they may be seq_lens and n_free (updated in place)."""
+    if not isinstance(mass, torch.Tensor) or not mass.is_cuda:
+        raise ValueError("mass must be a CUDA tensor")
+    dev, index = mass.device, mass.get_device()
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_evict(mass, block_table, seq_lens, free_pages, n_free, page_size, keep, recent, table_out,
+                               seq_lens_out, n_free_out, workspace)
+    i32 = torch.int32
+    _check_tensor(mass, "mass", torch.float32, (None, None), index)
+    n_pages, Hkv = mass.shape
+    B = _batch_of(seq_lens)
+    max_pages, stride = _check_table(block_table, seq_lens, B, index)
+    if table_out is None:
+        table_out, out_stride = block_table, stride
+    else:
+        _check_tensor(table_out, "table_out", i32, (B, max_pages), index, rows=True)
+        out_stride = table_out.stride(0) if B > 1 else max_pages
+    if not isinstance(free_pages, torch.Tensor):
+        raise ValueError("free_pages must be a CUDA tensor")
+    _check_tensor(free_pages, "free_pages", i32, free_pages.shape[:1] or (None,), index)
+    _check_tensor(n_free, "n_free", i32, (1,), index)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(B, dtype=i32, device=dev)
+    else:
+        _check_tensor(seq_lens_out, "seq_lens_out", i32, (B,), index)
+    if n_free_out is None:
+        n_free_out = torch.empty(1, dtype=i32, device=dev)
+    else:
+        _check_tensor(n_free_out, "n_free_out", i32, (1,), index)
+    need = lib().dit_paged_evict_workspace_bytes(B, max_pages)
+    workspace, ws, size = _workspace(workspace, need, dev)
+    st = lib().dit_paged_evict(mass.data_ptr(), block_table.data_ptr(), stride, table_out.data_ptr(), out_stride,
+                               seq_lens.data_ptr(), seq_lens_out.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
+                               n_free_out.data_ptr(), B, Hkv, page_size, n_pages, max_pages, free_pages.shape[0],
+                               int(keep), int(recent), ws, size, torch._C._cuda_getCurrentRawStream(index))
+    if st != DIT_OK:
+        raise DitError(st, "dit_paged_evict")
+    return seq_lens_out, n_free_out
 
 
 def paged_select(q, summary, block_table, seq_lens, page_size, top_k, selected=None, workspace=None,

@@ -500,6 +500,57 @@ dit_status dit_paged_prefill_fwd(const void* q, const dit_strides* q_strides, co
 size_t dit_paged_prefill_workspace_bytes(int D, int page_size, int max_pages);
 
 /*
+ * The attention weight that each page has drawn, brought up to date by a step's queries: for every page of a
+ * request with new tokens, and key/value head g,
+ *   mass_out[page, g] = (0 where the page's first key is new, else mass[page, g])
+ *                       + sum over the page's keys j, the observing tokens t that see them, the query heads h of g's
+ *                         group: exp(scale * q_th . k_j - lse_th)
+ * Observing are the last `window` new tokens of each request (0: all); they see keys as with `causal` in
+ * dit_paged_prefill_fwd, whose lse this takes (dit_paged_attn_fwd's, of single tokens).  A row whose lse is -inf
+ * adds nothing; a NaN lse, or score, makes the pages that the row sees NaN.  Rows of no request are not
+ * looked at.  Sums are in 32 bits, in an order that the sizes and lengths alone fix: equal calls give equal bits.
+ *   q, k_cache, block_table, seq_lens, start_lens : as dit_paged_prefill_fwd (read)
+ *   lse       : device fp32 [T, H_q] (read)
+ *   cu_new    : device int32 [B + 1] (read), or NULL: one token of each request, its last (T = B; no start_lens)
+ *   mass      : device fp32 [n_pages, H_kv], contiguous (read)
+ *   mass_out  : device fp32 [n_pages, H_kv] (written: the pages of requests with new tokens alone); may be mass
+ *               itself.  A page that is in the table more than once is left with any of its sums.
+ *   window    : >= 0;  T : 1 .. 2^30;  scale : > 0, and finite times log2 e in 32 bits
+ */
+dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, const float* lse, const void* k_cache,
+                               const dit_strides* k_strides, const int* block_table, long long table_stride,
+                               const int* seq_lens, const int* cu_new, const int* start_lens, const float* mass,
+                               float* mass_out, int T, int B, int H_q, int H_kv, int D, int page_size,
+                               int n_pages, int max_pages, int window, float scale, dit_stream stream);
+
+/*
+ * Eviction: a request of n > keep pages, n = ceil(seq_lens[b] / page_size), keeps its newest `recent` pages and,
+ * of the others, the keep - recent that drew most weight over all heads (sum_g mass[page, g] in 64 bits; equal ones:
+ * the lower index; NaN above every number, an entry outside the pool below).  The kept ones close up in order, so that
+ * keys keep their order and the newest page stays the last; entries keep .. n - 1 of the table row become -1 and those
+ * behind are as they were; the length falls by (n - keep) * page_size.  The freed pages go onto the stack of free pages by
+ * request and column; what does not fit into it is dropped.  Other requests keep theirs.  Positions that keys were
+ * turned by (dit_qk_norm_rope) stay: a program counts them apart from the lengths (its start_lens).
+ * Every page is in one request's row, once: one that others hold too would go to the stack while they use it.
+ *   mass        : device fp32 [n_pages, H_kv], contiguous (read)
+ *   block_table : device int32 (read); table_out: device int32 [B, max_pages], rows table_out_stride apart
+ *                 (written), may be block_table itself (the same stride)
+ *   seq_lens, n_free, seq_lens_out, n_free_out : as dit_paged_plan
+ *   free_pages  : device int32 [pool_capacity] (entries from n_free on are written)
+ *   keep        : >= 1;  recent : 1 .. keep;  B : 1 .. 8192 (above: DIT_ERR_UNSUPPORTED)
+ *   workspace   : at least dit_paged_evict_workspace_bytes(B, max_pages) bytes
+ * Outputs must not overlap each other or the inputs, but for the three pairs named.
+ */
+dit_status dit_paged_evict(const float* mass, const int* block_table, long long table_stride, int* table_out,
+                           long long table_out_stride, const int* seq_lens, int* seq_lens_out, int* free_pages,
+                           const int* n_free, int* n_free_out, int B, int H_kv, int page_size, int n_pages,
+                           int max_pages, int pool_capacity, int keep, int recent, void* workspace,
+                           size_t workspace_bytes, dit_stream stream);
+
+/* Workspace bytes of a dit_paged_evict call with these sizes; 0 when a size is not positive. */
+size_t dit_paged_evict_workspace_bytes(int B, int max_pages);
+
+/*
  * The pages whose keys can score highest, for attention over those alone.  For request b
  * and key/value head g the score of page i is
  *   max over the query heads h of the group of  sum_d max(q_hd * lo_d, q_hd * hi_d)

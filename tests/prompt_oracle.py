@@ -87,3 +87,68 @@ def norm_rope(x, weight, eps, freqs, axis_pairs, positions, interleaved, rot_sca
     both = (z[..., i].abs() + z[..., j].abs()) * abs(rot_scale)
     size[..., i], size[..., j] = both, both
     return y, size
+
+
+def page_mass(q, lse, k_cache, table, seq_lens, mass, scale, cu_new=None, start_lens=None, window=0):
+    """(mass_out, size) in fp64: size [n_pages, Hkv] is sum of weights times (1 + scale max |q||k|) of what was added."""
+    q, lse, k_cache, out = (x.detach().cpu().double() for x in (q, lse, k_cache, mass))
+    table = np.asarray(table.cpu()).astype(np.int64)
+    T, Hq, D = q.shape
+    n_pages, Hkv, P = k_cache.shape[:3]
+    B, G = table.shape[0], Hq // Hkv
+    host = lambda x: [int(y) for y in x.cpu()]  # noqa: E731
+    cu = list(range(B + 1)) if cu_new is None else host(cu_new)
+    size = torch.zeros_like(out)
+    for b, (row, n, length, start) in enumerate(requests(cu, host(seq_lens), T, table.shape[1] * P,
+                                                         None if start_lens is None else host(start_lens))):
+        if n == 0 or length == 0:
+            continue
+        page, at = places(table, b, length, P, n_pages)
+        w = min(n, window) if window > 0 else n
+        for c in range(-(-length // P)):
+            if page[c * P] >= 0 and c * P >= start:
+                out[page[c * P]] = 0
+        see = torch.arange(length)[None, :] <= (torch.arange(n - w, n) + start)[:, None]
+        safe = np.maximum(page, 0)
+        for h in range(Hq):
+            k, x, m = k_cache[safe, h // G, at], q[row + n - w:row + n, h], lse[row + n - w:row + n, h]
+            s = scale * (x @ k.T)
+            e = torch.where(see & (m > -math.inf)[:, None] | (see & m.isnan()[:, None]), torch.exp(s - m[:, None]), 0.0)
+            e = e * torch.as_tensor(page >= 0)
+            big = 1 + scale * (x.abs() @ k.abs().T)
+            add = torch.where(e > 0, e * big, 0.0).sum(0)
+            ok = torch.as_tensor(page >= 0)
+            out[:, h // G].index_add_(0, torch.as_tensor(page)[ok], e.sum(0)[ok])
+            size[:, h // G].index_add_(0, torch.as_tensor(page)[ok], add[ok])
+    return out, size
+
+
+def evict(mass, table, seq_lens, free_pages, n_free, P, keep, recent):
+    """(table, lens, stack, n_free) after the eviction; Python numbers throughout."""
+    mass, table, stack = mass.detach().cpu().double().numpy(), table.cpu().numpy().copy(), free_pages.cpu().numpy().copy()
+    n_pages = mass.shape[0]
+    free, lens = min(max(0, int(n_free)), len(stack)), []
+    for b in range(len(table)):
+        length = min(max(0, int(seq_lens[b])), table.shape[1] * P)
+        n = -(-length // P)
+        if n > keep:
+            def weight(i):
+                page = int(table[b, i])
+                if not 0 <= page < n_pages:
+                    return (0, 0.0)  # below every number
+                with np.errstate(invalid="ignore"):
+                    x = float(sum(mass[page]))
+                return (2, 0.0) if math.isnan(x) else (1, x)
+            order = sorted(range(n - recent), key=lambda i: tuple(-y for y in weight(i)) + (i,))
+            stay = set(order[:keep - recent]) | set(range(n - recent, n))
+            kept = [int(table[b, i]) for i in range(n) if i in stay]
+            for i in range(n):
+                page = int(table[b, i])
+                if i not in stay and 0 <= page < n_pages:
+                    if free < len(stack):
+                        stack[free] = page
+                    free += 1
+            table[b, :n] = kept + [-1] * (n - keep)
+            length -= (n - keep) * P
+        lens.append(length)
+    return table, np.array(lens), stack, min(free, len(stack))
