@@ -773,11 +773,22 @@ def rope_freqs(rot, theta=10000.0, scaling=None, factor=1.0, original_len=4096, 
 
 def _rope_view(t, name, index):
     """(B, H, N, D) and strides (b, h, n) of a [B, H, N, D] or a packed [T, H, D] bf16 view."""
-    if t.dim() == 3:
-        _check_tensor(t, name, torch.bfloat16, (None,) * 3, index, rows=True)
-        return (1, t.shape[1], t.shape[0], t.shape[2]), Strides(t.shape[2], t.stride(1), t.stride(0))
-    _check_tensor(t, name, torch.bfloat16, (None,) * 4, index, rows=True)
-    return tuple(t.shape), Strides(*t.stride()[:3])
+    try:  # the usual case, as in _check_tensor
+        shape, stride = t.shape, t.stride()
+        usual = t.dtype is torch.bfloat16 and stride[-1] == 1 and t.get_device() == index
+    except (AttributeError, IndexError):
+        usual, shape = False, (None,) * 4
+    if not usual or len(shape) not in (3, 4):
+        _check_tensor(t, name, torch.bfloat16, (None,) * (3 if len(shape) == 3 else 4), index, rows=True)
+    if len(shape) == 3:
+        return (1, shape[1], shape[0], shape[2]), Strides(shape[2], stride[1], stride[0])
+    return shape, Strides(*stride[:3])
+
+
+@functools.lru_cache(maxsize=64)
+def _int_array(values):
+    """The values as a C array (read by the library alone)."""
+    return (ctypes.c_int * len(values))(*values)
 
 
 def qk_norm_rope(q, k=None, positions=None, freqs=None, axis_pairs=None, interleaved=False, rot_scale=1.0, eps=None,
@@ -806,32 +817,33 @@ def qk_norm_rope(q, k=None, positions=None, freqs=None, axis_pairs=None, interle
             raise ValueError("q and k must be of the same tokens and head size")
         if k_out is None:
             k_out = torch.empty(k.shape, device=dev, dtype=torch.bfloat16)
-        else:
+        elif k_out is not k:
             _check_tensor(k_out, "k_out", torch.bfloat16, k.shape, index, rows=True)
-        kos = _rope_view(k_out, "k_out", index)[1]
+        kos = ks if k_out is k else _rope_view(k_out, "k_out", index)[1]
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
     if q_out is None:
         q_out = torch.empty(q.shape, device=dev, dtype=torch.bfloat16)
-    else:
+    elif q_out is not q:
         _check_tensor(q_out, "q_out", torch.bfloat16, q.shape, index, rows=True)
-    qos = _rope_view(q_out, "q_out", index)[1]
+    qos = qs if q_out is q else _rope_view(q_out, "q_out", index)[1]
     wdt = torch.bfloat16
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    if given:
-        wdt = given[0].dtype
-        for w in given:
-            _check_tensor(w, "weights", wdt, (D,), index)
+    if q_weight is not None or k_weight is not None:
+        wdt = getattr(k_weight if q_weight is None else q_weight, "dtype", None)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _check_tensor(w, name, wdt, (D,), index)
     axes, pairs, pos_b, pos_axis, requests = 0, None, 0, 0, 0
     if freqs is None:
         if positions is not None or cu_new is not None or start_lens is not None:
             raise ValueError("positions need freqs")
     else:
         _check_tensor(freqs, "freqs", torch.float32, (None,), index)
-        pairs = [freqs.shape[0]] if axis_pairs is None else [int(x) for x in axis_pairs]
+        n = freqs.shape[0]
+        pairs = (n,) if axis_pairs is None else tuple(int(x) for x in axis_pairs)
         axes = len(pairs)
-        if sum(pairs) != freqs.shape[0]:
-            raise ValueError(f"axis_pairs must add up to the {freqs.shape[0]} frequencies")
+        if sum(pairs) != n:
+            raise ValueError(f"axis_pairs must add up to the {n} frequencies")
         if positions is not None:
             if cu_new is not None or start_lens is not None:
                 raise ValueError("positions, or cu_new and start_lens")
@@ -846,13 +858,15 @@ def qk_norm_rope(q, k=None, positions=None, freqs=None, axis_pairs=None, interle
             requests = start_lens.shape[0]
             _check_tensor(start_lens, "start_lens", torch.int32, (requests,), index)
             _check_tensor(cu_new, "cu_new", torch.int32, (requests + 1,), index)
-        pairs = (ctypes.c_int * axes)(*pairs)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        pairs = _int_array(pairs)
     st = lib().dit_qk_norm_rope(
-        q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, ptr(k), ks, ptr(k_out), kos, Hk, 0 if eps is None else 1,
-        0.0 if eps is None else float(eps), ptr(q_weight), ptr(k_weight), _dt(wdt), ptr(freqs), pairs, axes,
-        1 if interleaved else 0, float(rot_scale), ptr(positions), pos_b, pos_axis, ptr(cu_new), ptr(start_lens), requests,
-        B, N, D, torch._C._cuda_getCurrentRawStream(index))
+        q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, None if k is None else k.data_ptr(), ks,
+        None if k is None else k_out.data_ptr(), kos, Hk, 0 if eps is None else 1, 0.0 if eps is None else float(eps),
+        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), _dt(wdt),
+        None if freqs is None else freqs.data_ptr(), pairs, axes, 1 if interleaved else 0, float(rot_scale),
+        None if positions is None else positions.data_ptr(), pos_b, pos_axis, None if cu_new is None else cu_new.data_ptr(),
+        None if start_lens is None else start_lens.data_ptr(), requests, B, N, D,
+        torch._C._cuda_getCurrentRawStream(index))
     if st != DIT_OK:
         raise DitError(st, "dit_qk_norm_rope")
     return q_out, k_out
@@ -960,6 +974,12 @@ def _attn_need(index, B, Hq, Hkv, D, page_size, pages):
 def _select_need(index, B, Hkv, max_pages):
     """dit_paged_select_workspace_bytes on the current device, number `index`."""
     return lib().dit_paged_select_workspace_bytes(B, Hkv, max_pages)
+
+
+@functools.lru_cache(maxsize=4096)
+def _evict_need(B, max_pages):
+    """dit_paged_evict_workspace_bytes."""
+    return lib().dit_paged_evict_workspace_bytes(B, max_pages)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1234,8 +1254,7 @@ def paged_evict(mass, block_table, seq_lens, free_pages, n_free, page_size, keep
         n_free_out = torch.empty(1, dtype=i32, device=dev)
     else:
         _check_tensor(n_free_out, "n_free_out", i32, (1,), index)
-    need = lib().dit_paged_evict_workspace_bytes(B, max_pages)
-    workspace, ws, size = _workspace(workspace, need, dev)
+    workspace, ws, size = _workspace(workspace, _evict_need(B, max_pages), dev)
     st = lib().dit_paged_evict(mass.data_ptr(), block_table.data_ptr(), stride, table_out.data_ptr(), out_stride,
                                seq_lens.data_ptr(), seq_lens_out.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
                                n_free_out.data_ptr(), B, Hkv, page_size, n_pages, max_pages, free_pages.shape[0],
