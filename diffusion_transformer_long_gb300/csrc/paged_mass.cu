@@ -33,7 +33,9 @@ constexpr int kTile = 16;       // keys of a product
 constexpr int kTiles = 2;       // whose loads a warp has in flight
 constexpr int kRows = 128;      // (token, head) rows in shared memory at once
 constexpr int kSums = 128;      // sums of a run: pages x warps of a page
-constexpr int kFewRows = 16;    // up to so many rows, runs are short
+constexpr int kFewRows = 16;    // up to so many rows a warp takes a run by itself
+constexpr int kFewKeys = 256;   // keys of such a run (or a page's)
+constexpr int kManyKeys = 1024;  // keys of a block's run
 
 struct MassParams {
   const __nv_bfloat16* q;
@@ -82,6 +84,32 @@ struct Request {
   }
 };
 
+// The request that holds run `run`, from request b on, before which there are `base` runs; b = batch: none does.
+__device__ __forceinline__ void seek(const MassParams& p, long long run, int& b, long long& base, int lane) {
+  Request rq;
+  for (; b < p.batch; b += 32) {
+    long long mine = 0;
+    if (b + lane < p.batch) {
+      rq.load(p, b + lane);
+      mine = static_cast<long long>(rq.runs(p)) * p.h_kv;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned past = __ballot_sync(~0u, base + upto > run);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      base += __shfl_sync(~0u, upto - mine, l);
+      b += l;
+      return;
+    }
+    base += __shfl_sync(~0u, upto, 31);
+  }
+}
+
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -91,6 +119,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The sum of a lane's four weights of a tile's keys (first, at rows g and g + 8) and two (token, head) rows, whose base-2
+// lse and limits are given; `all`: keys that every row sees.
+__device__ __forceinline__ float weights(const float (&d)[4], float scale, float2 lse, int first, int g, int all,
+                                         const int* limit) {
+  float e[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) e[c] = ptx::ex2_approx(fmaf(d[c], scale, c & 1 ? -lse.y : -lse.x));
+  if (first + kTile > all) {
+    const int2 lim = *reinterpret_cast<const int2*>(limit);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (first + g + (c & 2 ? 8 : 0) >= (c & 1 ? lim.y : lim.x)) e[c] = 0.f;
+  }
+  return (e[0] + e[1]) + (e[2] + e[3]);
+}
+
+// Many rows: a block for each run.
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 2) paged_mass_kernel(const __grid_constant__ MassParams p) {
   using S = Smem<D>;
@@ -108,29 +153,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_mass_kernel(const __grid
   int b = 0;
   long long base = 0;  // runs of the requests before b
   for (long long run = blockIdx.x;; run += gridDim.x) {
-    // The request of the run, 32 at a time.
     Request rq;
-    for (; b < p.batch; b += 32) {
-      long long mine = 0;
-      if (b + lane < p.batch) {
-        rq.load(p, b + lane);
-        mine = static_cast<long long>(rq.runs(p)) * p.h_kv;
-      }
-      long long upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const unsigned past = __ballot_sync(~0u, base + upto > run);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        base += __shfl_sync(~0u, upto - mine, l);
-        b += l;
-        break;
-      }
-      base += __shfl_sync(~0u, upto, 31);
-    }
+    seek(p, run, b, base, lane);
     if (b >= p.batch) return;
     rq.load(p, b);
     const int runs = rq.runs(p);
@@ -198,31 +222,24 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_mass_kernel(const __grid
                 for (int e = 0; e < 2; ++e) ka[i][s][e] = load_once(at + (tile * kTile + g + 8 * e) * p.ks.n_ + 32 * s);
             }
           }
+          // (A query row's operands serve all tiles in flight: read for each, shared memory's rate bounded the window.)
+          for (int nb = 0; nb < blocks; ++nb) {
+            float d[kTiles][4] = {};
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
-            const int tile = i0 + i * p.page_warps;
-            if (tile >= live) break;
-            const int key = key0 + tile * kTile + g;  // and key + 8
-            const bool whole = key0 + (tile + 1) * kTile <= all;
-            for (int nb = 0; nb < blocks; ++nb) {
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < kPieces; ++s) {
+              const uint4 x = qs[(nb * kPieces + s) * 32 + lane];
 #pragma unroll
-              for (int s = 0; s < kPieces; ++s) {
-                const uint4 x = qs[(nb * kPieces + s) * 32 + lane];
-                mma16816(d, ka[i][s][0].x, ka[i][s][1].x, ka[i][s][0].y, ka[i][s][1].y, x.x, x.y);
-                mma16816(d, ka[i][s][0].z, ka[i][s][1].z, ka[i][s][0].w, ka[i][s][1].w, x.z, x.w);
+              for (int i = 0; i < kTiles; ++i) {
+                mma16816(d[i], ka[i][s][0].x, ka[i][s][1].x, ka[i][s][0].y, ka[i][s][1].y, x.x, x.y);
+                mma16816(d[i], ka[i][s][0].z, ka[i][s][1].z, ka[i][s][0].w, ka[i][s][1].w, x.z, x.w);
               }
-              const float2 m = *reinterpret_cast<const float2*>(lse2 + nb * 8 + 2 * t);
-              float e[4];
+            }
+            const float2 m = *reinterpret_cast<const float2*>(lse2 + nb * 8 + 2 * t);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) e[c] = ptx::ex2_approx(fmaf(d[c], p.scale_log2, c & 1 ? -m.y : -m.x));
-              if (!whole) {
-                const int2 lim = *reinterpret_cast<const int2*>(limit + nb * 8 + 2 * t);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  if (key + (c & 2 ? 8 : 0) >= (c & 1 ? lim.y : lim.x)) e[c] = 0.f;
-              }
-              sum += (e[0] + e[1]) + (e[2] + e[3]);
+            for (int i = 0; i < kTiles; ++i) {
+              const int tile = i0 + i * p.page_warps;
+              if (tile >= live) break;
+              sum += weights(d[i], p.scale_log2, m, key0 + tile * kTile, g, all, limit + nb * 8 + 2 * t);
             }
           }
         }
@@ -242,6 +259,128 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_mass_kernel(const __grid
       p.out[at] = sum;
     }
     __syncthreads();  // the sums are free
+  }
+}
+
+// Up to 8 kNb rows (tokens x heads of a group): a warp for each run, the query rows' operands in registers, and each piece
+// of a tile's registers filled again as soon as it is used, so that a tile is always in flight.
+template <int D, int kNb>
+__global__ void __launch_bounds__(kWarps * 32, kNb == 1 ? 3 : 2) paged_mass_few_kernel(const __grid_constant__ MassParams p) {
+  constexpr int kPieces = D / 32;
+  __shared__ float lse2[kWarps][8 * kNb];
+  __shared__ int limit[kWarps][8 * kNb];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane / 4, t = lane % 4;
+  wait_for_inputs();
+  int b = 0;
+  long long base = 0;
+  for (long long run = blockIdx.x * kWarps + warp;; run += gridDim.x * kWarps) {
+    seek(p, run, b, base, lane);
+    if (b >= p.batch) return;
+    Request rq;
+    rq.load(p, b);
+    const int runs = rq.runs(p);
+    const int h = static_cast<int>((run - base) / runs);
+    const int first = static_cast<int>((run - base) - static_cast<long long>(h) * runs) * p.run_pages;
+    const int pages = min(p.run_pages, rq.pages(p) - first);  // at most 32
+    int mine = lane < pages ? p.table[b * p.table_stride + first + lane] : -1;
+    if (mine >= p.n_pages) mine = -1;
+    const int w = p.window > 0 ? min(rq.n, p.window) : rq.n, rows = w * p.group;
+    const int tiles = p.page_size / kTile;
+    const int keys = min(pages * p.page_size, rq.len - first * p.page_size);  // of the run
+    // The tile that is loaded next: tile `tile` of the run's page `pg`.
+    int pg = 0, tile = 0;
+    const __nv_bfloat16* at = nullptr;
+    auto settle = [&]() {  // on to a page that there is
+      for (;; ++pg, tile = 0) {
+        if (pg >= pages) return;
+        const int page = __shfl_sync(~0u, mine, pg);
+        if (page < 0) continue;
+        at = p.k + page * p.ks.b_ + h * p.ks.h_ + g * p.ks.n_ + 8 * t;
+        return;
+      }
+    };
+    settle();
+    uint4 ka[kPieces][2];
+    const bool any = pg < pages;
+    if (any) {
+#pragma unroll
+      for (int s = 0; s < kPieces; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ka[s][e] = load_once(at + 8 * e * p.ks.n_ + 32 * s);
+    }
+    // The rows: lane r < 8 kNb knows row r's lse and limit; lane (g, t) has row 8 nb + g's pieces.
+    int all = 0x7fffffff;
+    for (int r = lane; r < 8 * kNb; r += 32) {
+      int lim = 0;
+      float x = 0.f;
+      if (r < rows) {
+        const int tok = r / p.group;
+        x = p.lse[static_cast<long long>(rq.row0 + rq.n - w + tok) * p.h_q + h * p.group + (r - tok * p.group)] *
+            1.4426950408889634f;
+        if (x != -INFINITY)  // (else the token saw no key above -inf)
+          lim = static_cast<int>(min(max(rq.start + (rq.n - w) + tok + 1, 0LL), static_cast<long long>(rq.len)));
+      }
+      lse2[warp][r] = x;
+      limit[warp][r] = lim;
+      all = min(all, lim);
+    }
+    all = __reduce_min_sync(~0u, all);
+    uint4 q[kNb][kPieces];
+#pragma unroll
+    for (int nb = 0; nb < kNb; ++nb) {
+      const int r = 8 * nb + g, tok = r / p.group;
+#pragma unroll
+      for (int s = 0; s < kPieces; ++s)
+        q[nb][s] = r < rows ? *reinterpret_cast<const uint4*>(p.q + (rq.row0 + rq.n - w + tok) * p.q_n +
+                                                              (h * p.group + r - tok * p.group) * p.q_h + 8 * (4 * s + t))
+                            : make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+    float2 m[kNb];
+#pragma unroll
+    for (int nb = 0; nb < kNb; ++nb) m[nb] = *reinterpret_cast<const float2*>(&lse2[warp][nb * 8 + 2 * t]);
+
+    float sum = 0.f;
+    while (pg < pages) {
+      const int now = pg, first_key = pg * p.page_size + tile * kTile;  // in the run
+      // The next tile: of this page, if it has more keys, or of the next.
+      if (++tile == tiles || first_key + kTile >= keys) {
+        ++pg;
+        tile = 0;
+        settle();
+      }
+      const bool more = pg < pages;
+      const __nv_bfloat16* const next = at + static_cast<long long>(tile) * kTile * p.ks.n_;
+      float d[kNb][4] = {};
+#pragma unroll
+      for (int s = 0; s < kPieces; ++s) {
+#pragma unroll
+        for (int nb = 0; nb < kNb; ++nb) {
+          mma16816(d[nb], ka[s][0].x, ka[s][1].x, ka[s][0].y, ka[s][1].y, q[nb][s].x, q[nb][s].y);
+          mma16816(d[nb], ka[s][0].z, ka[s][1].z, ka[s][0].w, ka[s][1].w, q[nb][s].z, q[nb][s].w);
+        }
+        if (more) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ka[s][e] = load_once(next + 8 * e * p.ks.n_ + 32 * s);
+        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < kNb; ++nb)
+        sum += weights(d[nb], p.scale_log2, m[nb], first * p.page_size + first_key, g, all, &limit[warp][nb * 8 + 2 * t]);
+      if (pg != now) {  // the page's last tile
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        const int page = __shfl_sync(~0u, mine, now);
+        if (lane == 0) {
+          const long long out = static_cast<long long>(page) * p.h_kv + h;
+          const bool begun = static_cast<long long>(first + now) * p.page_size >= rq.start;
+          p.out[out] = (begun ? 0.f : p.mass[out]) + sum;
+        }
+        sum = 0.f;
+      }
+    }
+    __syncwarp();  // the rows' words are free
   }
 }
 
@@ -291,13 +430,20 @@ cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st) {
   p.max_len = a.max_pages * a.page_size;
   p.window = a.window;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  // Pages of more than 64 keys go to several warps.  A run is 512 keys where few rows look at them, so that ragged
-  // requests fill the GPU evenly, and 2048 where the rows' loads count.
+  const long long rows = std::min(a.cu_new ? a.window > 0 ? a.window : a.tokens : 1, a.tokens) * static_cast<long long>(p.group);
+  if (rows <= kFewRows) {
+    p.page_warps = 1;
+    p.run_pages = std::max(1, kFewKeys / a.page_size);
+    const dim3 block(kWarps * 32);
+    auto run = [&](auto kernel, int blocks) { return launch_after(kernel, dim3(blocks * host::sm_count()), block, 0, st, p); };
+    if (a.d == 64)
+      return rows <= 8 ? run(paged_mass_few_kernel<64, 1>, 3) : run(paged_mass_few_kernel<64, 2>, 2);
+    return rows <= 8 ? run(paged_mass_few_kernel<128, 1>, 3) : run(paged_mass_few_kernel<128, 2>, 2);
+  }
+  // Pages of more than 64 keys go to several warps.
   p.page_warps = 1;
   while (p.page_warps < kWarps && a.page_size > 64 * p.page_warps) p.page_warps *= 2;
-  const long long rows = std::min(a.cu_new ? a.window > 0 ? a.window : a.tokens : 1, a.tokens) * static_cast<long long>(p.group);
-  const int keys = rows <= kFewRows ? 512 : 2048;
-  p.run_pages = std::min(kSums / p.page_warps, std::max(kWarps / p.page_warps, keys / a.page_size));
+  p.run_pages = std::min(kSums / p.page_warps, std::max(kWarps / p.page_warps, kManyKeys / a.page_size));
   return a.d == 64 ? launch<64>(p, st) : launch<128>(p, st);
 }
 
