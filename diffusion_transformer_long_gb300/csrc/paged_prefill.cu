@@ -143,6 +143,7 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   p.max_len = a.max_pages * a.page_size;
   p.div_group = (65536 + p.group - 1) / p.group;
   p.causal = a.causal;
+  p.key_bytes = static_cast<int>(std::min<long long>(4LL * a.h_kv * a.d, 1 << 30));
   p.split = p.max_len > kWholeKeys;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;

@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_kernel.cuh"
 #include "paged_device.cuh"
@@ -56,6 +57,7 @@ constexpr int kItemCost = 256;         // what an item costs beside its keys, in
 constexpr int kMinRun = 512;           // a block's smallest run, in keys
 constexpr int kItemRows = 2 * kBlockM;
 constexpr int kMaxGrid = 256;          // largest grid
+constexpr long long kHeadBytes = 192LL << 20;  // of a request's keys and values, above which its items go head by head
 constexpr int kConsumers = 3 + 8 + 4;  // of a segment: producer, two issuers, softmax and epilogue warps
 
 // How a cache's rows reach a tile.  A tile of D = 128 holds two blocks of 64 channels, 128 bytes a row.  A copy brings
@@ -98,6 +100,7 @@ struct PrefillParams {
   KvPlace kv[2];  // of K and V, fused
   int div_group;  // 2^16 / group, rounded up: r / group for r < 128 is r * div_group >> 16
   int causal;
+  int key_bytes;  // of one key and value, all heads
   int split;  // 0: items stay whole
   float scale_log2;
   int* status;
@@ -160,6 +163,16 @@ struct Request {
     const long long m = hi - lo;
     sum += m * start + tb * (m * (lo + hi + 1) / 2);
     return sum + (i - hi) * len;
+  }
+  // Whether the request's items count head by head, or block of tokens by block of tokens.
+  __device__ __forceinline__ bool by_head(const PrefillParams& p) const {
+    return static_cast<long long>(len) * p.key_bytes > kHeadBytes;
+  }
+  // Item w of the request: block i of head h.
+  __device__ __forceinline__ void item(const PrefillParams& p, long long w, int& i, int& h) const {
+    const int n = by_head(p) ? items(p) : p.h_kv, q = static_cast<int>(w / n), r = static_cast<int>(w - static_cast<long long>(q) * n);
+    i = by_head(p) ? r : q;
+    h = by_head(p) ? q : r;
   }
 };
 
@@ -257,9 +270,12 @@ struct Segments {
   __device__ __forceinline__ void release() const { ptx::mbar_arrive(bar(Smem<D>::bSegEmpty + n % kSegs)); }
 };
 
-// The block's segments (one warp).  Items count in the order request, block of tokens, head, so that the blocks of
-// a wave work on neighbouring items, side by side through the same keys (with the heads outermost and a run of items to
-// each block, 152 places of all heads' keys were read at once: 27280 keys, 24 heads, 25 % of the reads hit L2).
+// The block's segments (one warp).  The blocks of a wave work on neighbouring items, side by side through the same
+// keys (with a run of items to each block, 152 places of all heads' keys were read at once: 27280 keys, 24 heads,
+// 25 % of the reads hit L2).  A request's items count block of tokens by block of tokens, all heads of each, so that a
+// wave's are of like lengths (one prompt of 4608, 9216 tokens, 24 heads on 8: 174, 464 us; head by head 196, 522), but
+// head by head where all heads' keys and values are too many for L2 (27280 tokens, 24 heads, 335 MB: 3.21 ms; by
+// blocks of tokens 3.37; of 112 MB, 3.53 and 3.38).
 // Waves of whole items go over the blocks, to and fro, for as long as no block has more than its share of the cost;
 // what is left is dealt out so that all blocks' costs end up alike.
 template <int D>
@@ -372,8 +388,8 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
       else
         rq.load(p, wave_b);
       wave_have = static_cast<long long>(rq.items(p)) * p.h_kv;
-      const int i = static_cast<int>((w - wave_base) / p.h_kv);
-      const int h = static_cast<int>(w - wave_base - static_cast<long long>(i) * p.h_kv);
+      int i, h;
+      rq.item(p, w - wave_base, i, h);
       const int ntiles = (rq.item_keys(p, i) + kBlockN - 1) / kBlockN;
       emit_item(wave_b, i, h, 0, ntiles, ntiles);
     }
@@ -388,7 +404,7 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
     if (even) {
       before = total / items * (waves * grid);
     } else if (waves > 0) {
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < kOwn; ++q) end[q] = 0;
       int b = 0;
       long long base = 0, have = 0;
@@ -397,7 +413,7 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
       const long long sure = waves, most_waves = items / grid;
       for (long long k = 0; k < most_waves; ++k) {
         int cost[kOwn];
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < kOwn; ++q) {
           // In the order of the items: of block lane kOwn + q, or on the way back of lane kOwn + kOwn - 1 - q.
           const int x = lane * kOwn + (k & 1 ? kOwn - 1 - q : q);
@@ -409,35 +425,37 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
             rq.load(p, ++b);
             have = static_cast<long long>(rq.items(p)) * p.h_kv;
           }
-          cost[q] = rq.item_keys(p, static_cast<int>((w - base) / p.h_kv)) + kItemCost;
+          int i, h;
+          rq.item(p, w - base, i, h);
+          cost[q] = rq.item_keys(p, i) + kItemCost;
         }
         bool over = false;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < kOwn; ++q) over |= end[q] + (k & 1 ? cost[kOwn - 1 - q] : cost[q]) > share;
         if (k >= sure && __any_sync(~0u, over)) break;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < kOwn; ++q) end[q] += k & 1 ? cost[kOwn - 1 - q] : cost[q];
         waves = k + 1;
       }
       emit_waves(sure, waves);
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < kOwn; ++q) before += end[q];
 #pragma unroll
       for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(~0u, before, o);
     }
     if (even || waves == 0 || total - before < static_cast<long long>(grid) * kMinRun) {
       const long long blocks = min(static_cast<long long>(grid), max(1LL, (total - before) / kMinRun));
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < kOwn; ++q) end[q] = lane * kOwn + q < blocks ? 1 : 0;
     } else {
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < kOwn; ++q) {
         const long long rest = share - end[q];
         end[q] = lane * kOwn + q < grid && rest > 0 ? rest : 0;
       }
     }
     long long mine = 0;
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < kOwn; ++q) mine = end[q] += mine;
     long long upto = mine;
 #pragma unroll
@@ -447,7 +465,7 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
     }
     const long long all = __shfl_sync(~0u, upto, 31);
     const double unit = static_cast<double>(total - before) / static_cast<double>(max(1LL, all));
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < kOwn; ++q) {
       const long long x = upto - mine + end[q];  // of `all` (none: the first block's)
       end[q] = x == all ? total : before + static_cast<long long>(static_cast<double>(x) * unit);
@@ -456,7 +474,7 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
     long long run0 = before, run1 = before;
     {
       long long x0 = 0, x1 = 0;
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < kOwn; ++q) {
         if (q == (c + kOwn - 1) % kOwn) x0 = end[q];
         if (q == c % kOwn) x1 = end[q];
@@ -470,20 +488,28 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
       long long base = 0;
       seek(b, base, run0, [&] { return rq.cost(p, rq.items(p)) * p.h_kv; });
       int nb = rq.items(p);
-      // Item i, head h, and how far into its cost.
-      int i, h;
-      long long x0;
+      // Head h, item i, and how far into its cost.
+      int h = 0, i;
+      long long x0 = run0 - base;
       {
+        // By blocks of tokens, all heads' items i count before any head's i + 1.
+        const long long per_head = rq.cost(p, nb), many = rq.by_head(p) ? 1 : p.h_kv;
+        if (rq.by_head(p)) {
+          h = static_cast<int>(x0 / per_head);
+          x0 -= h * per_head;
+        }
         int lo = 0, hi = nb - 1;
         while (lo < hi) {
           const int mid = lo + (hi - lo + 1) / 2;
-          if (rq.cost(p, mid) * p.h_kv <= run0 - base) lo = mid; else hi = mid - 1;
+          if (rq.cost(p, mid) * many <= x0) lo = mid; else hi = mid - 1;
         }
         i = lo;
-        x0 = run0 - base - rq.cost(p, i) * p.h_kv;
-        const long long each = static_cast<long long>(rq.item_keys(p, i)) + kItemCost;
-        h = static_cast<int>(x0 / each);
-        x0 -= h * each;
+        x0 -= rq.cost(p, i) * many;
+        if (!rq.by_head(p)) {
+          const long long each = static_cast<long long>(rq.item_keys(p, i)) + kItemCost;
+          h = static_cast<int>(x0 / each);
+          x0 -= h * each;
+        }
       }
       long long at = run0;  // x0's place in the whole
       while (ok) {
@@ -498,7 +524,7 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
             // The item's last part is in the first block whose run ends behind the item's last tile's start.
             const long long x = at - x0 + static_cast<long long>(ntiles - 1) * kBlockN;
             int last = 0;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < kOwn; ++q) last += lane * kOwn + q < grid && end[q] <= x;
             last = __reduce_add_sync(~0u, last);
             const int t0 = i * 2 * p.tile_tokens;
@@ -509,16 +535,27 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
         at += take;
         if (at >= run1) break;
         x0 = 0;
-        if (++h == p.h_kv) {
-          h = 0;
-          if (++i == nb) {
+        bool over;
+        if (rq.by_head(p)) {
+          over = ++i == nb;
+          if (over) {
             i = 0;
-            ++b;
-            long long none = 0;
-            seek(b, none, 0, [&] { return static_cast<long long>(rq.n); });  // the next with new tokens
-            if (b >= p.batch) break;  // (not reached: the run would have ended)
-            nb = rq.items(p);
+            over = ++h == p.h_kv;
           }
+        } else {
+          over = ++h == p.h_kv;
+          if (over) {
+            h = 0;
+            over = ++i == nb;
+          }
+        }
+        if (over) {
+          i = h = 0;
+          ++b;
+          long long none = 0;
+          seek(b, none, 0, [&] { return static_cast<long long>(rq.n); });  // the next with new tokens
+          if (b >= p.batch) break;  // (not reached: the run would have ended)
+          nb = rq.items(p);
         }
       }
     }
@@ -924,9 +961,9 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
     float l = 0.f;        // running sum of 2^(c*s - m), for the LSE
     float lp = 0.f;       // running sum of the bf16-rounded P the PV GEMM sees, for O
     bool first = true;
-    for (; nt > 0; --nt, ++g, ++tiles, left -= kBlockN, first = false) {
-      if (!(ok = wait(L::bSFull + t, g & 1))) break;
-      ptx::tc_fence_after();
+    uint32_t none = 0;  // the tile's 16-key pieces without a page
+    // One tile, whose scores have been waited for.  `masked`: some row does not see it whole.
+    auto tile = [&](auto masked) {
       float s[kBlockN];
       float cmax[kBlockN / 32];
 #pragma unroll
@@ -936,25 +973,18 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
 #pragma unroll
         for (int i = 0; i < 32; ++i) s[cc * 32 + i] = __uint_as_float(u[i]);
       }
-      uint32_t none;  // 16-key pieces without a page
-      asm volatile("ld.shared.b32 %0, [%1];"
-                   : "=r"(none)
-                   : "r"(sbase + S::kMasks + 4 * (tiles % kMaskRing))
-                   : "memory");
       ptx::tmem_wait_ld();
       ptx::tc_fence_before();
       ptx::mbar_arrive(bar(L::bSEmpty + t));
 
       float mx = ptx::fmax3(cmax[0], cmax[1], fmaxf(cmax[2], cmax[3]));
-      // (The branches that few tiles take are marked, so that their code stands apart: in the loop's midst it
-      // starved the warps of instructions.)
-      if (__builtin_expect(__any_sync(0xffffffffu, left < kBlockN || none), 0)) {
+      if constexpr (decltype(masked)::value) {
         // Keys that the row does not see are masked to -inf, so their P is exactly 0, and the max is
         // taken over the others only.
 #pragma unroll
         for (int i = 0; i < kBlockN; ++i)
           if (i >= left) s[i] = -INFINITY;
-        if (__builtin_expect(none != 0, 0)) {
+        if (none != 0) {
 #pragma unroll
           for (int i = 0; i < kBlockN; ++i)
             if ((none >> (i / 16)) & 1) s[i] = -INFINITY;
@@ -979,11 +1009,11 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
       l *= alpha;
       lp *= alpha;
       bool pv_prev_done = (g == 0);
-      if (__builtin_expect(!first && __any_sync(0xffffffffu, raise), 0)) {
-        if (!(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
+      if (!first && __any_sync(0xffffffffu, raise)) {
+        if (!(ok = wait(L::bPVDone + t, (g - 1) & 1))) return;
         pv_prev_done = true;
         ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 16; ++cc) {
           uint32_t u[16];
           ptx::tmem_ld16(tO + cc * 16, u);
@@ -1015,7 +1045,7 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
           s[i + 1] = ptx::ex2_approx(x1);
         }
         // The P_t buffer is free once the last PV has read it.
-        if (half == 0 && !pv_prev_done && !(ok = wait(L::bPVDone + t, (g - 1) & 1))) break;
+        if (half == 0 && !pv_prev_done && !(ok = wait(L::bPVDone + t, (g - 1) & 1))) return;
 #pragma unroll
         for (int ch = half * 8; ch < half * 8 + 8; ++ch) {
           uint32_t wv[4];
@@ -1035,12 +1065,37 @@ __device__ __forceinline__ void softmax_wg(const PrefillParams& p, uint32_t sbas
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(half == 0 ? L::bPLo + t : L::bPFull + t));
       }
-      if (!ok) break;
       const uint64_t sl = ptx::fadd2(ptx::fadd2(acc_l[0], acc_l[1]), ptx::fadd2(acc_l[2], acc_l[3]));
       float a0, a1;
       ptx::f2unpack(sl, a0, a1);
       l += a0 + a1;
       lp += ((acc_lp[0] + acc_lp[1]) + (acc_lp[2] + acc_lp[3])) + ((acc_lp[4] + acc_lp[5]) + (acc_lp[6] + acc_lp[7]));
+      --nt;
+      ++g;
+      ++tiles;
+      left -= kBlockN;
+      first = false;
+    };
+    // The next tile's scores; whether some row does not see it whole.
+    auto next = [&](bool& mask) {
+      if (!(ok = wait(L::bSFull + t, g & 1))) return false;
+      ptx::tc_fence_after();
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(none)
+                   : "r"(sbase + S::kMasks + 4 * (tiles % kMaskRing))
+                   : "memory");
+      mask = __any_sync(0xffffffffu, left < kBlockN || none);
+      return true;
+    };
+    // Two loops, so that the common tile's instructions stand together: with the masked tile's in their midst the
+    // warps waited for instructions, by up to a tenth of the time.
+    while (ok && nt > 0) {
+      bool mask = false;
+      while (nt > 0 && next(mask) && !mask) {
+        tile(std::integral_constant<bool, false>{});
+        if (!ok) break;
+      }
+      if (ok && mask) tile(std::integral_constant<bool, true>{});
     }
     if (!ok) break;
 
@@ -1194,7 +1249,7 @@ __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sba
         int at[4];
 #pragma unroll
         for (int rr = 0; rr < 4; ++rr) at[rr] = place(quarter * 32 + rr * 8 + r_lo);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t x[32];
           ptx::tmem_ld32(tO + c * 32, x);
@@ -1219,7 +1274,7 @@ __device__ __forceinline__ void epilogue_wg(const PrefillParams& p, uint32_t sba
       } else if constexpr (!kOutF32) {
         const int mine = place(r);
         __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(mine) * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t a[32];
           ptx::tmem_ld32(tO + c * 32, a);
