@@ -53,9 +53,11 @@ constexpr int kSegs = 4;               // segments in the ring
 constexpr int kSegWords = 16;
 constexpr int kMaskRing = 8;           // key tiles whose masks are held (the producer runs at most 3 ahead)
 constexpr int kHeldWords = 16;         // per segment: 3 tiles x 128 keys, then a flag of each epilogue warp
-constexpr int kItemCost = 256;         // what an item costs beside its keys, in keys
+constexpr int kItemCost = 1024;         // what an item costs beside its keys, in keys
 constexpr int kMinRun = 512;           // a block's smallest run, in keys
 constexpr int kItemRows = 2 * kBlockM;
+constexpr int kSplitCost = 2000;       // what parts and their join cost a block, in keys (about 24 us)
+constexpr int kWholeWaves = 6;         // waves up to which whole items are tried
 constexpr int kMaxGrid = 256;          // largest grid
 constexpr long long kHeadBytes = 192LL << 20;  // of a request's keys and values, above which its items go head by head
 constexpr int kConsumers = 3 + 8 + 4;  // of a segment: producer, two issuers, softmax and epilogue warps
@@ -132,12 +134,12 @@ struct Smem {
 struct Request {
   int row0, n;      // first row of its new tokens, how many
   int len;          // cached keys
-  long long start;  // position of the first new token
+  long long start;  // position of the first new token, within [-2^30, len] (a step has at most 2^30 tokens)
   __device__ __forceinline__ void load(const PrefillParams& p, int b) {
     row0 = min(max(p.cu_new[b], 0), p.tokens);
     n = max(0, min(max(p.cu_new[b + 1], 0), p.tokens) - row0);
     len = min(max(p.seq_lens[b], 0), p.max_len);
-    start = p.start_lens ? p.start_lens[b] : static_cast<long long>(len) - n;
+    start = p.start_lens ? max(min(p.start_lens[b], len), -(1 << 30)) : static_cast<long long>(len) - n;
   }
   __device__ __forceinline__ int items(const PrefillParams& p) const {
     return (n + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
@@ -156,21 +158,21 @@ struct Request {
     long long sum = static_cast<long long>(i) * kItemCost;
     if (!p.causal) return sum + static_cast<long long>(i) * len;
     if (i > 0 && i == items(p)) sum += item_keys(p, --i);
-    const long long tb = 2 * p.tile_tokens;
-    const long long lo = start < 0 ? min(static_cast<long long>(i), -start / tb) : 0;
-    long long hi = len > start ? (len - start + tb - 1) / tb - 1 : 0;  // items that end before len
+    const unsigned tb = 2 * p.tile_tokens;
+    const long long lo = start < 0 ? min(static_cast<unsigned>(i), static_cast<unsigned>(-start) / tb) : 0;
+    long long hi = len > start ? (static_cast<unsigned>(len - start) + tb - 1) / tb - 1 : 0;  // items that end before len
     hi = min(max(hi, lo), static_cast<long long>(i));
     const long long m = hi - lo;
-    sum += m * start + tb * (m * (lo + hi + 1) / 2);
+    sum += m * start + static_cast<long long>(tb) * (m * (lo + hi + 1) / 2);
     return sum + (i - hi) * len;
   }
   // Whether the request's items count head by head, or block of tokens by block of tokens.
   __device__ __forceinline__ bool by_head(const PrefillParams& p) const {
     return static_cast<long long>(len) * p.key_bytes > kHeadBytes;
   }
-  // Item w of the request: block i of head h.
+  // Item w of the request (it has fewer than 2^31): block i of head h.
   __device__ __forceinline__ void item(const PrefillParams& p, long long w, int& i, int& h) const {
-    const int n = by_head(p) ? items(p) : p.h_kv, q = static_cast<int>(w / n), r = static_cast<int>(w - static_cast<long long>(q) * n);
+    const unsigned n = by_head(p) ? items(p) : p.h_kv, q = static_cast<unsigned>(w) / n, r = static_cast<unsigned>(w) - q * n;
     i = by_head(p) ? r : q;
     h = by_head(p) ? q : r;
   }
@@ -273,11 +275,13 @@ struct Segments {
 // The block's segments (one warp).  The blocks of a wave work on neighbouring items, side by side through the same
 // keys (with a run of items to each block, 152 places of all heads' keys were read at once: 27280 keys, 24 heads,
 // 25 % of the reads hit L2).  A request's items count block of tokens by block of tokens, all heads of each, so that a
-// wave's are of like lengths (one prompt of 4608, 9216 tokens, 24 heads on 8: 174, 464 us; head by head 196, 522), but
+// wave's are of like lengths (one prompt of 4608 tokens, 24 heads on 8: 174 us; head by head 196), but
 // head by head where all heads' keys and values are too many for L2 (27280 tokens, 24 heads, 335 MB: 3.21 ms; by
 // blocks of tokens 3.37; of 112 MB, 3.53 and 3.38).
 // Waves of whole items go over the blocks, to and fro, for as long as no block has more than its share of the cost;
-// what is left is dealt out so that all blocks' costs end up alike.
+// what is left is dealt out so that all blocks' costs end up alike.  Where that would gain less than the parts cost, all
+// items stay whole (one prompt of 4608 tokens, 24 heads on 8, L2 cold: 138 us; in parts 158).
+// The code runs once, and what it costs is fetching it: loops are rolled, divisions of 32 bits where they fit.
 template <int D>
 __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase, int lane) {
   using S = Smem<D>;
@@ -379,8 +383,51 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
 
   int wave_b = 0;
   long long wave_base = 0, wave_have = 0;  // items before request wave_b, and its own
-  auto emit_waves = [&](long long k0, long long k1) {
-    for (long long k = k0; ok && k < k1; ++k) {
+  // Each lane holds the loads of kOwn blocks in a row, then their shares of the rest, then where their runs end.
+  constexpr int kOwn = kMaxGrid / 32;
+  long long end[kOwn];
+  int load_b = 0;
+  long long load_base = 0, load_have = 0;  // (a lane's own, as wave_b ..)
+  auto start_loads = [&]() {
+#pragma unroll 1
+    for (int q = 0; q < kOwn; ++q) end[q] = 0;
+    load_b = 0;
+    load_base = 0;
+    rq.load(p, 0);
+    load_have = static_cast<long long>(rq.items(p)) * p.h_kv;
+  };
+  // Wave k on top of the loads, unless (`keep`) a block's load would pass `most_load`.  Returns whether one's does.
+  auto add_wave = [&](long long k, long long most_load, bool keep) {
+    int cost[kOwn];
+    bool over = false;
+#pragma unroll 1
+    for (int i = 0; i < kOwn; ++i) {
+      // In the order of the items: of block lane kOwn + i, or on the way back of lane kOwn + kOwn - 1 - i.
+      const int q = k & 1 ? kOwn - 1 - i : i, x = lane * kOwn + q;
+      cost[q] = 0;
+      if (x >= grid) continue;
+      const long long w = k * grid + (k & 1 ? grid - 1 - x : x);
+      if (w >= items) continue;
+      while (w >= load_base + load_have) {
+        load_base += load_have;
+        rq.load(p, ++load_b);
+        load_have = static_cast<long long>(rq.items(p)) * p.h_kv;
+      }
+      int block, h;
+      rq.item(p, w - load_base, block, h);
+      cost[q] = rq.item_keys(p, block) + kItemCost;
+      over |= end[q] + cost[q] > most_load;
+    }
+    over = __any_sync(~0u, over);
+    if (over && keep) return true;
+#pragma unroll 1
+    for (int q = 0; q < kOwn; ++q) end[q] += cost[q];
+    return over;
+  };
+  const long long full = items / grid, all_waves = (items + grid - 1) / grid;
+  long long k = 0, before = 0;  // waves that are out; cost of what the waves took
+  for (bool first = true;; first = false) {
+    for (; ok && k < waves; ++k) {
       const long long w = k * grid + (k & 1 ? grid - 1 - c : c);
       if (w >= items) continue;
       if (w >= wave_base + wave_have)
@@ -393,51 +440,34 @@ __device__ __forceinline__ void scheduler(const PrefillParams& p, uint32_t sbase
       const int ntiles = (rq.item_keys(p, i) + kBlockN - 1) / kBlockN;
       emit_item(wave_b, i, h, 0, ntiles, ntiles);
     }
-  };
-  emit_waves(0, waves);
+    if (!first || !ok || !p.split || waves == all_waves) break;
+    // Of few waves: whole items all the same, if that leaves no block further behind than the parts cost.  Else waves
+    // up to the blocks' shares.  (Waves that are out are within both.)
+    const bool few = all_waves <= kWholeWaves && share + kSplitCost >= most + kItemCost;
+    if (even) {
+      if (few && all_waves * (most + kItemCost) <= share + kSplitCost) waves = all_waves;
+    } else {
+#pragma unroll 1
+      for (int whole = few; whole >= 0; --whole) {
+        if (!whole && waves == 0) break;
+        start_loads();
+        const long long sure = waves, to = whole ? all_waves : full;
+        long long n = 0;
+#pragma unroll 1
+        for (; n < to; ++n)
+          if (add_wave(n, whole ? share + kSplitCost : share, n >= sure) && n >= sure) break;
+        if (!whole || n == all_waves) {
+          waves = max(sure, n);
+          break;
+        }
+      }
+    }
+  }
 
   if (ok && p.split && waves * grid < items) {
-    // Each lane holds the loads of kOwn blocks in a row, then their shares of the rest, then where their runs end.
-    constexpr int kOwn = kMaxGrid / 32;
-    long long end[kOwn];
-    long long before = 0;  // cost of what the waves took
     if (even) {
       before = total / items * (waves * grid);
     } else if (waves > 0) {
-#pragma unroll 1
-      for (int q = 0; q < kOwn; ++q) end[q] = 0;
-      int b = 0;
-      long long base = 0, have = 0;
-      rq.load(p, 0);
-      have = static_cast<long long>(rq.items(p)) * p.h_kv;
-      const long long sure = waves, most_waves = items / grid;
-      for (long long k = 0; k < most_waves; ++k) {
-        int cost[kOwn];
-#pragma unroll 1
-        for (int q = 0; q < kOwn; ++q) {
-          // In the order of the items: of block lane kOwn + q, or on the way back of lane kOwn + kOwn - 1 - q.
-          const int x = lane * kOwn + (k & 1 ? kOwn - 1 - q : q);
-          cost[q] = 0;
-          if (x >= grid) continue;
-          const long long w = k * grid + (k & 1 ? grid - 1 - x : x);
-          while (w >= base + have) {
-            base += have;
-            rq.load(p, ++b);
-            have = static_cast<long long>(rq.items(p)) * p.h_kv;
-          }
-          int i, h;
-          rq.item(p, w - base, i, h);
-          cost[q] = rq.item_keys(p, i) + kItemCost;
-        }
-        bool over = false;
-#pragma unroll 1
-        for (int q = 0; q < kOwn; ++q) over |= end[q] + (k & 1 ? cost[kOwn - 1 - q] : cost[q]) > share;
-        if (k >= sure && __any_sync(~0u, over)) break;
-#pragma unroll 1
-        for (int q = 0; q < kOwn; ++q) end[q] += k & 1 ? cost[kOwn - 1 - q] : cost[q];
-        waves = k + 1;
-      }
-      emit_waves(sure, waves);
 #pragma unroll 1
       for (int q = 0; q < kOwn; ++q) before += end[q];
 #pragma unroll
@@ -1358,7 +1388,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   if (warp < kLoadWarp) {
     ptx::setmaxnreg_inc<Regs::kSoftmax>();
     softmax_wg<D>(p, sbase, tmem, warp >> 2, warp, lane);
-  } else if (warp < kEpiWarp0) {
+  } else if (warp >= kEpiWarp0) {
+    ptx::setmaxnreg_dec<Regs::kEpilogue>();
+    epilogue_wg<D, kOutF32, kFused>(p, sbase, tmem, warp, lane);
+  } else {
     ptx::setmaxnreg_dec<Regs::kIssue>();
     if (warp == kLoadWarp) {
       producer<D, kFused>(p, sbase, lane);
@@ -1370,9 +1403,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       scheduler<D>(p, sbase, lane);
     }
     __syncwarp();
-  } else {
-    ptx::setmaxnreg_dec<Regs::kEpilogue>();
-    epilogue_wg<D, kOutF32, kFused>(p, sbase, tmem, warp, lane);
   }
 
   ptx::tc_fence_before();
