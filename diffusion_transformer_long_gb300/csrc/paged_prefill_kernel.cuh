@@ -48,7 +48,6 @@
 namespace ditattn {
 namespace prefill {
 
-constexpr int kSchedWarp = 11;
 constexpr int kSegs = 4;               // segments in the ring
 constexpr int kSegWords = 16;
 constexpr int kMaskRing = 8;           // key tiles whose masks are held (the producer runs at most 3 ahead)
