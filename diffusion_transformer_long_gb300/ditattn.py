@@ -875,9 +875,12 @@ def qk_norm_rope(q, k=None, positions=None, freqs=None, axis_pairs=None, interle
 # ------------------------------------------------------------------ paged key/value caches
 # One step of a batch of requests whose keys and values live in pages of one pool:
 #   lens, n_free, cu, slots = paged_plan(...)         pages and slots for the step's tokens
+#   q, k = qk_norm_rope(q, k, ..., cu_new=cu, start_lens=...)    norms and positions
 #   paged_kv_write(k, v, slots, k_cache, v_cache, summary)
+#   out, lse = paged_prefill_fwd(q, k_cache, v_cache, table, lens, cu)   new tokens, or one of each request:
 #   selected = paged_select(q, summary, table, lens, ...)        (sparse attention only)
 #   out, lse = paged_attn_fwd(q, k_cache, v_cache, table, lens, selected=selected)
+#   paged_page_mass(...); paged_evict(...)            (caches with a budget) least used pages back to the pool
 # k_cache and v_cache are [n_pages, H_kv, page_size, D] views (a token-major cache
 # [n_pages, page_size, H_kv, D] is passed as x.transpose(1, 2), the halves of one that holds keys and
 # values in turn as x[:, 0] and x[:, 1]); block_table is int32

@@ -325,13 +325,16 @@ dit_status dit_qk_norm_rope(const void* q, const dit_strides* q_strides, void* q
 
 /* ---------------------------------------------------------------------------
  * Paged key/value caches: requests of different and growing lengths in pages of
- * one pool, for generation with cached keys, a token at a time (text encoders and
- * captioners of the pages' pipelines).  One step of a batch is
- *   dit_paged_plan      pages and slots for the step's new tokens, from lengths
- *   dit_paged_kv_write  their keys and values into the slots, page summaries
- *   dit_paged_select    (sparse attention only) the best pages for each query
- *   dit_paged_attn_fwd  one query token of each request against its pages
- * A prompt can be planned and written, but not attended from: its causal attention is not here.
+ * one pool, for generation with cached keys (text encoders and captioners of the pages'
+ * pipelines, video generated block by block).  One step of a batch is
+ *   dit_paged_plan         pages and slots for the step's new tokens, from lengths
+ *   dit_qk_norm_rope       norms and positions of their queries and keys
+ *   dit_paged_kv_write     their keys and values into the slots, page summaries
+ *   dit_paged_prefill_fwd  any number of new tokens of each request against its pages, or
+ *   dit_paged_select       (sparse attention only) the best pages for each query
+ *   dit_paged_attn_fwd     one query token of each request against its pages
+ *   dit_paged_page_mass    (caches with a budget) the weight that each page has drawn
+ *   dit_paged_evict        ... and the pages that drew least back to the pool
  * All lengths, tables and slots live on the device, so that a step can be captured
  * into a graph once and replayed as the lengths grow.
  *
