@@ -21,7 +21,7 @@ SOURCES = ["attn_fwd.cu", "attn_fwd_short.cu", "lse_merge.cu", "layout_copy.cu",
            "paged_select.cu", "prompt_api.cu", "paged_prefill.cu", "qk_norm_rope.cu",
            "paged_mass.cu", "paged_evict.cu"]
 HEADERS = ["attn_kernel.cuh", "attn_host.cuh", "merge_math.cuh", "sm103_ptx.cuh", "launch.h", "api_checks.h",
-           "paged_launch.h", "paged_device.cuh", "paged_attn_kernel.cuh", "paged_checks.h",
+           "paged_launch.h", "paged_device.cuh", "paged_attn_kernel.cuh", "paged_checks.h", "paged_maps.cuh",
            "paged_prefill_kernel.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

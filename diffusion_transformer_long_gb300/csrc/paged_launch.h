@@ -125,6 +125,7 @@ struct MassLaunch {
   float* mass_out;
   int tokens, batch, h_q, h_kv, d, page_size, n_pages, max_pages, window;
   float scale;
+  int* status;
 };
 cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st);
 

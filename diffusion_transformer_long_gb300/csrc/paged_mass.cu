@@ -3,16 +3,17 @@
 //   mass[page, h] = (0 where the page's first key is new, else mass[page, h])
 //                   + sum over the page's keys j, the last `window` new tokens t that see them, the heads of h's
 //                     group: exp(scale q_t . k_j - lse_t)
-// The keys are read once for all rows (tokens x heads of a group) and no values are: half the attention's bytes,
-// bound by HBM for a few rows (48 requests of 0 to 4608 keys, 24 heads on 8: %s us, %s TB/s), and towards 128 rows by the
-// instructions (2 x 75600 keys, 40 heads on 8, 16 tokens: %s us, %s TB/s).
+// The keys are read once for all rows (tokens x heads of a group) and no values are: half the attention's bytes.
 //
-// Scores are S = K Q^T on mma.sync m16n8k16, keys as rows and (token, head) rows as columns, as the decode
-// attention has them.  A product's sum over channels may take them in any order, so that a lane's operands are
-// 16 neighbouring bytes of two keys, read straight from the cache into registers, and 16 bytes of a query row, from
-// shared memory; tiles need no staging.  A block takes a run of one request's pages for one key/value head, its
-// warps a page each (or a part of one, of large pages); the lanes' sums meet by shuffles in a fixed order, and every
-// page is written by one block: no atomics, equal calls give equal bits.
+// Up to 16 rows are bound by HBM (48 requests of 0 to 4608 keys, 24 heads on 8: 44 us, 5.2 TB/s): scores S = K Q^T on
+// mma.sync m16n8k16, keys as rows.  A product's sum over channels may take them in any order, so that a lane's operands
+// are 16 neighbouring bytes of two keys, read straight from the cache into registers, and of a query row: no staging,
+// and every warp walks over runs of pages by itself.  More rows are multiplied on tcgen05 (mma.sync in blocks
+// that shared the rows: 2 x 75600 keys, 40 heads on 8, 16 tokens: 107 us, 230 TFLOP/s, near that instruction's rate; now
+// 71).
+//
+// The lanes' sums meet by shuffles in a fixed order, and a page is written by one warp or block: no atomics in a sum, equal
+// calls give equal bits.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,6 +23,7 @@
 
 #include "attn_host.cuh"
 #include "paged_device.cuh"
+#include "paged_maps.cuh"
 #include "paged_launch.h"
 #include "sm103_ptx.cuh"
 
@@ -29,15 +31,12 @@ namespace ditattn {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTile = 16;       // keys of a product
-constexpr int kTiles = 2;       // whose loads a warp has in flight
-constexpr int kRows = 128;      // (token, head) rows in shared memory at once
-constexpr int kSums = 128;      // sums of a run: pages x warps of a page
-constexpr int kFewRows = 16;    // up to so many rows a warp takes a run by itself
-constexpr int kFewKeys = 256;   // keys of such a run (or a page's)
-constexpr int kManyKeys = 1024;  // keys of a block's run
+constexpr int kTile = 16;      // keys of an mma.sync product
+constexpr int kFewRows = 16;   // up to so many rows a warp takes a run by itself
+constexpr int kFewKeys = 256;  // keys of such a run (or a page's)
 
 struct MassParams {
+  CUtensorMap tm_q, tm_k;  // many rows: boxes of chunk_tokens tokens, and of box_rows rows of a page
   const __nv_bfloat16* q;
   long long q_n, q_h;
   const float* lse;
@@ -51,17 +50,10 @@ struct MassParams {
   const float* mass;
   float* out;
   int batch, tokens, h_q, h_kv, group, page_size, n_pages, max_len, window;
-  int page_warps, run_pages;  // warps of a page, pages of a run
+  int run_pages;  // pages of a run
+  int chunk_tokens, box_rows;
+  int* status;
   float scale_log2;
-};
-
-template <int D>
-struct Smem {
-  static constexpr int kQ = 0;                        // [rows / 8][D / 32][32 lanes] 16 bytes
-  static constexpr int kLse = kQ + kRows * D * 2;     // per row: base-2 lse, then the keys that it sees
-  static constexpr int kLimit = kLse + kRows * 4;
-  static constexpr int kSum = kLimit + kRows * 4;
-  static constexpr int kBytes = kSum + kSums * 4;
 };
 
 struct Request {
@@ -133,133 +125,6 @@ __device__ __forceinline__ float weights(const float (&d)[4], float scale, float
       if (first + g + (c & 2 ? 8 : 0) >= (c & 1 ? lim.y : lim.x)) e[c] = 0.f;
   }
   return (e[0] + e[1]) + (e[2] + e[3]);
-}
-
-// Many rows: a block for each run.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 2) paged_mass_kernel(const __grid_constant__ MassParams p) {
-  using S = Smem<D>;
-  constexpr int kPieces = D / 32;  // 16-byte pieces of a lane and row
-  extern __shared__ __align__(16) unsigned char smem[];
-  uint4* const qs = reinterpret_cast<uint4*>(smem + S::kQ);
-  float* const lse2 = reinterpret_cast<float*>(smem + S::kLse);
-  int* const limit = reinterpret_cast<int*>(smem + S::kLimit);
-  float* const sums = reinterpret_cast<float*>(smem + S::kSum);
-  __shared__ int least;  // keys that all rows in shared memory see (0 where a row takes no part)
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g = lane / 4, t = lane % 4;
-  wait_for_inputs();
-
-  int b = 0;
-  long long base = 0;  // runs of the requests before b
-  for (long long run = blockIdx.x;; run += gridDim.x) {
-    Request rq;
-    seek(p, run, b, base, lane);
-    if (b >= p.batch) return;
-    rq.load(p, b);
-    const int runs = rq.runs(p);
-    const int h = static_cast<int>((run - base) / runs), first = static_cast<int>((run - base) - static_cast<long long>(h) * runs) * p.run_pages;
-    const int pages = min(p.run_pages, rq.pages(p) - first);
-    const int* const row = p.table + b * p.table_stride + first;
-    const int w = p.window > 0 ? min(rq.n, p.window) : rq.n;
-    const long long rows = static_cast<long long>(w) * p.group;
-    const int tiles = p.page_size / kTile;
-
-    // This warp's tiles: of page warp / page_warps + i (kWarps / page_warps) those of its part.
-    const int part = warp % p.page_warps;
-    for (int i = threadIdx.x; i < kSums; i += kWarps * 32) sums[i] = 0.f;
-    for (long long r0 = 0; r0 < rows; r0 += kRows) {
-      const int here = static_cast<int>(min(rows - r0, static_cast<long long>(kRows)));
-      const int blocks = (here + 7) / 8;
-      __syncthreads();  // the rows before are done with
-      if (threadIdx.x == 0) least = 0x7fffffff;
-      __syncthreads();
-      for (int i = threadIdx.x; i < blocks * 8; i += kWarps * 32) {
-        int lim = 0;
-        float x = 0.f;
-        if (i < here) {
-          const long long r = r0 + i;
-          const int tok = static_cast<int>(r / p.group), head = static_cast<int>(r - static_cast<long long>(tok) * p.group);
-          x = p.lse[static_cast<long long>(rq.row0 + rq.n - w + tok) * p.h_q + h * p.group + head] * 1.4426950408889634f;
-          // (lse = -inf: the token saw no key above -inf)
-          if (x != -INFINITY)
-            lim = static_cast<int>(min(max(rq.start + (rq.n - w) + tok + 1, 0LL), static_cast<long long>(rq.len)));
-        }
-        lse2[i] = x;
-        limit[i] = lim;
-        atomicMin(&least, lim);
-      }
-      for (int i = threadIdx.x; i < blocks * kPieces * 32; i += kWarps * 32) {
-        const int l = i % 32, piece = i / 32 % kPieces, r = i / 32 / kPieces * 8 + l / 4;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < here) {
-          const long long rr = r0 + r;
-          const int tok = static_cast<int>(rr / p.group), head = static_cast<int>(rr - static_cast<long long>(tok) * p.group);
-          x = *reinterpret_cast<const uint4*>(p.q + (rq.row0 + rq.n - w + tok) * p.q_n + (h * p.group + head) * p.q_h +
-                                              8 * (4 * piece + l % 4));
-        }
-        qs[i] = x;
-      }
-      __syncthreads();
-      const int all = least;
-
-      for (int pg = warp / p.page_warps; pg < pages; pg += kWarps / p.page_warps) {
-        const int page = row[pg];
-        if (page < 0 || page >= p.n_pages) continue;
-        const int key0 = (first + pg) * p.page_size;
-        const __nv_bfloat16* const at = p.k + page * p.ks.b_ + h * p.ks.h_ + 8 * t;
-        const int live = min(tiles, (rq.len - key0 + kTile - 1) / kTile);  // tiles with keys
-        float sum = 0.f;
-        for (int i0 = part; i0 < live; i0 += kTiles * p.page_warps) {
-          uint4 ka[kTiles][kPieces][2];
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
-            const int tile = i0 + i * p.page_warps;
-            if (tile < live) {
-#pragma unroll
-              for (int s = 0; s < kPieces; ++s)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) ka[i][s][e] = load_once(at + (tile * kTile + g + 8 * e) * p.ks.n_ + 32 * s);
-            }
-          }
-          // (A query row's operands serve all tiles in flight: read for each, shared memory's rate bounded the window.)
-          for (int nb = 0; nb < blocks; ++nb) {
-            float d[kTiles][4] = {};
-#pragma unroll
-            for (int s = 0; s < kPieces; ++s) {
-              const uint4 x = qs[(nb * kPieces + s) * 32 + lane];
-#pragma unroll
-              for (int i = 0; i < kTiles; ++i) {
-                mma16816(d[i], ka[i][s][0].x, ka[i][s][1].x, ka[i][s][0].y, ka[i][s][1].y, x.x, x.y);
-                mma16816(d[i], ka[i][s][0].z, ka[i][s][1].z, ka[i][s][0].w, ka[i][s][1].w, x.z, x.w);
-              }
-            }
-            const float2 m = *reinterpret_cast<const float2*>(lse2 + nb * 8 + 2 * t);
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-              const int tile = i0 + i * p.page_warps;
-              if (tile >= live) break;
-              sum += weights(d[i], p.scale_log2, m, key0 + tile * kTile, g, all, limit + nb * 8 + 2 * t);
-            }
-          }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        if (lane == 0) sums[pg * p.page_warps + part] += sum;
-      }
-    }
-    __syncthreads();
-    for (int pg = threadIdx.x; pg < pages; pg += kWarps * 32) {
-      const int page = row[pg];
-      if (page < 0 || page >= p.n_pages) continue;
-      const long long at = static_cast<long long>(page) * p.h_kv + h;
-      const bool begun = static_cast<long long>(first + pg) * p.page_size >= rq.start;
-      float sum = begun ? 0.f : p.mass[at];
-      for (int i = 0; i < p.page_warps; ++i) sum += sums[pg * p.page_warps + i];
-      p.out[at] = sum;
-    }
-    __syncthreads();  // the sums are free
-  }
 }
 
 // Up to 8 kNb rows (tokens x heads of a group): a warp for each run, the query rows' operands in registers, and each piece
@@ -384,8 +249,334 @@ __global__ void __launch_bounds__(kWarps * 32, kNb == 1 ? 3 : 2) paged_mass_few_
   }
 }
 
+// ---------------------------------------------------------------- many rows
+
+constexpr int kTileN = 128;      // keys of a tile: rows of the product, so that a thread has one key's scores
+constexpr int kCols = 256;       // (token, head) rows at once: its columns
+constexpr int kRing = 4;         // key tiles in shared memory
+constexpr int kManyThreads = 384;
+constexpr int kEpilogue0 = 4;    // warps 4-7 and 8-11: a tensor-memory buffer each
+constexpr int kRunTiles = 16;    // a run's tiles, at most: 128 pieces of 16 keys
+constexpr long long kWaitLimit = 4000000000LL;
+
 template <int D>
-cudaError_t launch(const MassParams& p, cudaStream_t st) {
+struct ManySmem {
+  static constexpr uint32_t kRegion = 128 * 128;             // 128 rows of one 64-channel block
+  static constexpr uint32_t kTileBytes = kTileN * D * 2;
+  static constexpr uint32_t kQRegion = kCols * 128;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + kCols * D * 2;
+  static constexpr uint32_t kBars = kK + kRing * kTileBytes;
+  static constexpr int bQFull = 0, bQEmpty = 1, bKFull = 2, bKEmpty = bKFull + kRing, bDFull = bKEmpty + kRing,
+                       bDEmpty = bDFull + 2, bBoth = bDEmpty + 2, bDrain = bBoth + 1, kNumBars = bDrain + 1;
+  static constexpr uint32_t kTmem = kBars + kNumBars * 8;
+  static constexpr uint32_t kAbort = kTmem + 4;
+  static constexpr uint32_t kLse = (kAbort + 4 + 15) & ~15u;        // [2][256] base-2 lse
+  static constexpr uint32_t kLimit = kLse + 2 * kCols * 4;          // [2][256] keys that the row sees
+  static constexpr uint32_t kPieces = kLimit + 2 * kCols * 4;       // [2][128] sums of 16 keys
+  static constexpr uint32_t kLeast = kPieces + 2 * kRunTiles * 8 * 4;  // [2]
+  static constexpr uint32_t kBytes = kLeast + 8 + 1024;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
+  if (ptx::mbar_test_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!ptx::mbar_try_wait(bar, parity)) {
+    int stop;
+    asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
+    if (stop || clock64() - t0 > kWaitLimit) return false;
+  }
+  return true;
+}
+__device__ __forceinline__ void raise_abort(const MassParams& p, uint32_t abort_flag) {
+  asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_flag), "r"(1) : "memory");
+  atomicOr(p.status, kStatusTimeout);
+}
+
+// A block's run, which every role's warps find for themselves: some pages of one request, for one key/value head.
+struct Run {
+  int b = 0;
+  long long base = 0;  // runs of the requests before b
+  Request rq;
+  int h, first, pages, keys, tiles, rows, chunks;  // first page, pages; keys in them; rows; column blocks
+  __device__ __forceinline__ bool find(const MassParams& p, long long run, int lane) {
+    seek(p, run, b, base, lane);
+    if (b >= p.batch) return false;
+    rq.load(p, b);
+    const int runs = rq.runs(p);
+    h = static_cast<int>((run - base) / runs);
+    first = static_cast<int>((run - base) - static_cast<long long>(h) * runs) * p.run_pages;
+    pages = min(p.run_pages, rq.pages(p) - first);
+    keys = min(pages * p.page_size, rq.len - first * p.page_size);
+    tiles = (keys + kTileN - 1) / kTileN;
+    const int w = p.window > 0 ? min(rq.n, p.window) : rq.n;
+    rows = w;  // tokens
+    chunks = (w + p.chunk_tokens - 1) / p.chunk_tokens;
+    return true;
+  }
+  __device__ __forceinline__ int token0() const { return rq.n - rows; }  // the first observing one
+  __device__ __forceinline__ int tokens(const MassParams& p, int chunk) const {
+    return min(p.chunk_tokens, rows - chunk * p.chunk_tokens);
+  }
+};
+
+// The weights of 16 columns for the thread's key: scores u, the columns' lse and limits in shared memory.
+__device__ __forceinline__ float sum16(const uint32_t (&u)[16], float scale, uint32_t lse, uint32_t limit, int key,
+                                       bool whole) {
+  float sum[4] = {};
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    float m[4];
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(m[0]), "=f"(m[1]), "=f"(m[2]), "=f"(m[3])
+                 : "r"(lse + 4 * c)
+                 : "memory");
+    float e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = ptx::ex2_approx(fmaf(__uint_as_float(u[c + i]), scale, -m[i]));
+    if (!whole) {
+      int lim[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(lim[0]), "=r"(lim[1]), "=r"(lim[2]), "=r"(lim[3])
+                   : "r"(limit + 4 * c)
+                   : "memory");
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (key >= lim[i]) e[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] += e[i];
+  }
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// S^T = K Q^T on tcgen05, keys as rows, so that a thread of the epilogue has a key's scores for all columns and sums
+// their weights without a word to its neighbours.  One warp copies Q and the key tiles page by page, one thread
+// multiplies, two warpgroups take the tiles in turn out of two tensor-memory buffers.
+template <int D>
+__global__ void __launch_bounds__(kManyThreads, 1) paged_mass_many_kernel(const __grid_constant__ MassParams p) {
+  using S = ManySmem<D>;
+  constexpr int kRegions = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const uint32_t abort_flag = sbase + S::kAbort;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto bar = [&](int i) { return sbase + S::kBars + 8u * i; };
+  auto wait = [&](int i, uint32_t parity) { return wait_or_abort(bar(i), parity, abort_flag); };
+  // (lane 0 waits for its warp)
+  auto wait_warp = [&](int i, uint32_t parity) {
+    bool done = true;
+    if (lane == 0) done = wait(i, parity);
+    return __shfl_sync(~0u, done, 0) != 0;
+  };
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar(S::bQFull), 1);
+    ptx::mbar_init(bar(S::bQEmpty), 1);
+    for (int s = 0; s < kRing; ++s) {
+      ptx::mbar_init(bar(S::bKFull + s), 1);
+      ptx::mbar_init(bar(S::bKEmpty + s), 1);
+    }
+    for (int e = 0; e < 2; ++e) {
+      ptx::mbar_init(bar(S::bDFull + e), 1);
+      ptx::mbar_init(bar(S::bDEmpty + e), 128);
+    }
+    ptx::mbar_init(bar(S::bBoth), 256);
+    ptx::mbar_init(bar(S::bDrain), 1);
+    *reinterpret_cast<volatile int*>(smem + S::kAbort) = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(sbase + S::kTmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kTmem);
+  wait_for_inputs_and_copies();
+
+  Run r;
+  bool ok = true;
+  if (warp == 0) {
+    const int boxes = kTileN / p.box_rows, box = lane % boxes, block = lane / boxes;
+    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.chunk_tokens) * 128 * kRegions;
+    int it = 0, loads = 0;  // tiles, Q loads
+    for (long long run = blockIdx.x; ok && r.find(p, run, lane); run += gridDim.x) {
+      const int* const row = p.table + r.b * p.table_stride + r.first;
+      for (int c = 0; ok && c < r.chunks; ++c) {
+        if (!(ok = wait_warp(S::bQEmpty, (loads & 1) ^ 1))) break;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(bar(S::bQFull), q_bytes);
+          for (int x = 0; x < kRegions; ++x)
+            ptx::tma_load_4d(sbase + S::kQ + x * S::kQRegion, &p.tm_q, bar(S::bQFull), x * 64, 0,
+                             r.rq.row0 + r.token0() + c * p.chunk_tokens, r.h);
+        }
+        ++loads;
+        // Each lane looks up the box that it copies, a tile ahead.
+        auto look_up = [&](int j, int& page, int& at) {
+          const int key = j * kTileN + box * p.box_rows, col = key / p.page_size;
+          at = key - col * p.page_size;
+          page = p.n_pages;  // past the pool: zeros
+          if (col < r.pages) {
+            const int x = row[col];
+            if (x >= 0 && x < p.n_pages) page = x;
+          }
+        };
+        int page, at, next_page, next_at;
+        look_up(0, page, at);
+        for (int j = 0; j < r.tiles; ++j, ++it) {
+          const int s = it % kRing;
+          look_up(j + 1, next_page, next_at);
+          if (!(ok = wait_warp(S::bKEmpty + s, ((it / kRing) & 1) ^ 1))) break;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(bar(S::bKFull + s), S::kTileBytes);
+          if (block < kRegions)
+            ptx::tma_load_4d(sbase + S::kK + s * S::kTileBytes + block * S::kRegion + box * p.box_rows * 128, &p.tm_k,
+                             bar(S::bKFull + s), block * 64, at, r.h, page);
+          page = next_page;
+          at = next_at;
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) raise_abort(p, abort_flag);
+      // Let every copy land before the block can exit.
+      if (loads > 0) ptx::mbar_wait(bar(S::bQFull), (loads - 1) & 1, kWaitLimit);
+      for (int s = 0; s < kRing; ++s) {
+        const int n = (it + kRing - 1 - s) / kRing;  // copies into the slot
+        if (n > 0) ptx::mbar_wait(bar(S::bKFull + s), (n - 1) & 1, kWaitLimit);
+      }
+    }
+  } else if (warp == 1) {
+    int it = 0, loads = 0;
+    for (long long run = blockIdx.x; ok && r.find(p, run, lane); run += gridDim.x) {
+      if (lane == 0) {
+        for (int c = 0; ok && c < r.chunks; ++c) {
+          const int cols = (r.tokens(p, c) * p.group + 15) / 16 * 16;
+          const uint32_t idesc = ptx::idesc_bf16_f32(kTileN, cols, false, false);
+          if (!(ok = wait(S::bQFull, loads & 1))) break;
+          ++loads;
+          for (int j = 0; j < r.tiles; ++j, ++it) {
+            const int s = it % kRing, e = it & 1;
+            if (!(ok = wait(S::bKFull + s, (it / kRing) & 1) && wait(S::bDEmpty + e, ((it / 2) & 1) ^ 1))) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+              const uint32_t a = (sbase + S::kK + s * S::kTileBytes + (k / 4) * S::kRegion + (k % 4) * 32) >> 4;
+              const uint32_t q = (sbase + S::kQ + (k / 4) * S::kQRegion + (k % 4) * 32) >> 4;
+              ptx::mma_bf16_ss(tmem + e * kCols, static_cast<uint64_t>(hi) << 32 | a | 1u << 16,
+                               static_cast<uint64_t>(hi) << 32 | q | 1u << 16, idesc, k > 0);
+            }
+            ptx::mma_commit(bar(S::bDFull + e));
+            ptx::mma_commit(bar(S::bKEmpty + s));
+          }
+          if (ok) ptx::mma_commit(bar(S::bQEmpty));
+        }
+        if (!ok) {
+          raise_abort(p, abort_flag);
+          ptx::mma_commit(bar(S::bDrain));
+          ptx::mbar_wait(bar(S::bDrain), 0, kWaitLimit);
+        }
+      }
+      ok = __shfl_sync(~0u, ok, 0) != 0;
+    }
+  } else if (warp >= kEpilogue0) {
+    const int e = (warp - kEpilogue0) / 4, quarter = warp & 3, key_row = quarter * 32 + lane;
+    const int thread = threadIdx.x - kEpilogue0 * 32;  // of both warpgroups
+    const uint32_t tD = tmem + e * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t phase = 0;
+    auto both = [&]() {  // both warpgroups meet (a bounded wait)
+      ptx::mbar_arrive(bar(S::bBoth));
+      ok = __all_sync(~0u, wait(S::bBoth, phase));
+      phase ^= 1;
+      return ok;
+    };
+    int it = 0, chunk = 0, count = 0;  // tiles, column blocks, runs
+    for (long long run = blockIdx.x; ok && r.find(p, run, lane); run += gridDim.x, ++count) {
+      float* const pieces = reinterpret_cast<float*>(smem + S::kPieces) + (count & 1) * kRunTiles * 8;
+      if (thread < kRunTiles * 8) pieces[thread] = 0.f;
+      for (int c = 0; c < r.chunks; ++c, ++chunk) {
+        // Lse and limits of the columns, in turn in two places: who writes them has seen the barrier behind which all
+        // were through with the place.
+        const uint32_t lse = sbase + S::kLse + (chunk & 1) * kCols * 4, limit = sbase + S::kLimit + (chunk & 1) * kCols * 4;
+        int* const least = reinterpret_cast<int*>(smem + S::kLeast) + (chunk & 1);
+        const int cols = r.tokens(p, c) * p.group;
+        {
+          const int tok = thread / p.group;
+          int lim = 0;
+          float x = 0.f;
+          if (thread < cols) {
+            const int t = r.token0() + c * p.chunk_tokens + tok;  // of the request's new tokens
+            x = p.lse[static_cast<long long>(r.rq.row0 + t) * p.h_q + r.h * p.group + (thread - tok * p.group)] *
+                1.4426950408889634f;
+            if (x != -INFINITY)  // (else the token saw no key above -inf)
+              lim = static_cast<int>(min(max(r.rq.start + t + 1, 0LL), static_cast<long long>(r.rq.len)));
+          }
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(lse + 4 * thread), "f"(x) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(limit + 4 * thread), "r"(lim) : "memory");
+          if (thread == 0) *least = 0x7fffffff;
+          if (!both()) break;
+          if (thread < cols) atomicMin(least, lim);
+        }
+        if (!both()) break;
+        const int all = *least;
+        for (int j = 0; j < r.tiles; ++j, ++it) {
+          if ((it & 1) != e) continue;
+          if (!(ok = __all_sync(~0u, wait(S::bDFull + e, (it / 2) & 1)))) break;
+          ptx::tc_fence_after();
+          const int first = r.first * p.page_size + j * kTileN, key = first + key_row;
+          const bool whole = first + kTileN <= min(all, r.first * p.page_size + r.keys);
+          float sum = 0.f;
+          int x = 0;
+          for (; x + 32 <= cols; x += 32) {
+            uint32_t u[2][16];
+            ptx::tmem_ld16(tD + x, u[0]);
+            ptx::tmem_ld16(tD + x + 16, u[1]);
+            ptx::tmem_wait_ld();
+            sum += sum16(u[0], p.scale_log2, lse + 4 * x, limit + 4 * x, key, whole);
+            sum += sum16(u[1], p.scale_log2, lse + 4 * x + 64, limit + 4 * x + 64, key, whole);
+          }
+          for (; x < cols; x += 16) {  // (columns without a row see no key)
+            uint32_t u[16];
+            ptx::tmem_ld16(tD + x, u);
+            ptx::tmem_wait_ld();
+            sum += sum16(u, p.scale_log2, lse + 4 * x, limit + 4 * x, key, whole && x + 16 <= cols);
+          }
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(bar(S::bDEmpty + e));
+          if (key_row + j * kTileN >= r.keys) sum = 0.f;
+#pragma unroll
+          for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+          if ((lane & 15) == 0) pieces[j * 8 + key_row / 16] += sum;
+        }
+        if (!ok) break;
+      }
+      if (!ok || !both()) break;
+      for (int i = thread; i < r.pages; i += 256) {
+        const int page = p.table[r.b * p.table_stride + r.first + i];
+        if (page < 0 || page >= p.n_pages) continue;
+        const long long out = static_cast<long long>(page) * p.h_kv + r.h;
+        float sum = static_cast<long long>(r.first + i) * p.page_size >= r.rq.start ? 0.f : p.mass[out];
+        for (int k = i * p.page_size / 16; k < (i + 1) * p.page_size / 16; ++k) sum += pieces[k];
+        p.out[out] = sum;
+      }
+    }
+    if (!ok) raise_abort(p, abort_flag);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_many(const MassParams& p, cudaStream_t st) {
   static std::mutex mu;
   static bool done[64] = {};
   int dev = 0;
@@ -395,12 +586,13 @@ cudaError_t launch(const MassParams& p, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(paged_mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+      e = cudaFuncSetAttribute(paged_mass_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               ManySmem<D>::kBytes);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
   }
-  return launch_after(paged_mass_kernel<D>, dim3(2 * host::sm_count()), dim3(kWarps * 32), Smem<D>::kBytes, st, p);
+  return launch_after(paged_mass_many_kernel<D>, dim3(host::sm_count()), dim3(kManyThreads), ManySmem<D>::kBytes, st, p);
 }
 
 }  // namespace
@@ -430,9 +622,9 @@ cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st) {
   p.max_len = a.max_pages * a.page_size;
   p.window = a.window;
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.status = a.status;
   const long long rows = std::min(a.cu_new ? a.window > 0 ? a.window : a.tokens : 1, a.tokens) * static_cast<long long>(p.group);
   if (rows <= kFewRows) {
-    p.page_warps = 1;
     p.run_pages = std::max(1, kFewKeys / a.page_size);
     const dim3 block(kWarps * 32);
     auto run = [&](auto kernel, int blocks) { return launch_after(kernel, dim3(blocks * host::sm_count()), block, 0, st, p); };
@@ -440,11 +632,17 @@ cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st) {
       return rows <= 8 ? run(paged_mass_few_kernel<64, 1>, 3) : run(paged_mass_few_kernel<64, 2>, 2);
     return rows <= 8 ? run(paged_mass_few_kernel<128, 1>, 3) : run(paged_mass_few_kernel<128, 2>, 2);
   }
-  // Pages of more than 64 keys go to several warps.
-  p.page_warps = 1;
-  while (p.page_warps < kWarps && a.page_size > 64 * p.page_warps) p.page_warps *= 2;
-  p.run_pages = std::min(kSums / p.page_warps, std::max(kWarps / p.page_warps, kManyKeys / a.page_size));
-  return a.d == 64 ? launch<64>(p, st) : launch<128>(p, st);
+  p.chunk_tokens = std::min(kCols / p.group, a.cu_new ? a.tokens : 1);
+  p.box_rows = maps::box_rows(a.page_size);
+  if (!maps::encode_queries(&p.tm_q, a.q, a.q_n, a.q_h, a.d, p.group, a.tokens, a.h_kv, p.chunk_tokens) ||
+      !maps::encode_rows(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows))
+    return cudaErrorInvalidValue;
+  // Runs of 2048 keys, or of fewer where there is not room for four runs a block.
+  const long long room = static_cast<long long>(a.batch) * a.h_kv * p.max_len;
+  int keys = kRunTiles * kTileN;
+  while (keys > 4 * kTileN && room / keys < 4LL * host::sm_count()) keys /= 2;
+  p.run_pages = std::max(1, keys / a.page_size);
+  return a.d == 64 ? launch_many<64>(p, st) : launch_many<128>(p, st);
 }
 
 }  // namespace ditattn

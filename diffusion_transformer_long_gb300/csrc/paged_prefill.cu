@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "attn_host.cuh"
+#include "paged_maps.cuh"
 #include "paged_prefill_kernel.cuh"
 
 namespace ditattn {
@@ -17,25 +18,6 @@ namespace {
 // Requests with room for at most this many keys keep their items whole: one launch and no workspace.
 constexpr long long kWholeKeys = 1024;
 
-// A map of bf16 elements: extents, strides (elements) of all dimensions but the first, box.
-template <int N>
-bool encode(CUtensorMap* m, const void* base, const long long (&dims)[N], const long long (&strides)[N - 1],
-            const int (&boxes)[N]) {
-  EncodeTiledFn fn = tensor_map_encoder();
-  if (!fn) return false;
-  cuuint64_t d[N], st[N - 1];
-  cuuint32_t box[N], elem[N];
-  for (int i = 0; i < N; ++i) {
-    d[i] = static_cast<cuuint64_t>(dims[i]);
-    box[i] = static_cast<cuuint32_t>(boxes[i]);
-    elem[i] = 1;
-    if (i) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
-  }
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, const_cast<void*>(base), d, st, box, elem,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // A paged cache's map of fused copies of `rows` rows (see KvTile); false: the strides do not allow one.
 bool encode_fused(CUtensorMap* m, KvPlace* kv, const void* base, const Strides& s, int d, int page_size, int heads,
                   int n_pages, int rows) {
@@ -45,21 +27,15 @@ bool encode_fused(CUtensorMap* m, KvPlace* kv, const void* base, const Strides& 
   long long apart = s.b_ / s.h_;
   if (s.b_ % s.h_ == 0 && apart >= heads && apart * n_pages + heads < kMost) {
     *kv = {1, static_cast<int>(apart)};
-    if (encode<5>(m, base, {64, 8, d / 64, groups, (n_pages - 1) * apart + heads}, {s.n_, 64, 8 * s.n_, s.h_},
+    if (maps::encode<5>(m, base, {64, 8, d / 64, groups, (n_pages - 1) * apart + heads}, {s.n_, 64, 8 * s.n_, s.h_},
                   {64, 8, d / 64, rows / 8, 1}))
       return true;
   }
   apart = s.b_ / (8 * s.n_);
   if (s.b_ % (8 * s.n_) != 0 || apart < groups || apart * n_pages + groups >= kMost) return false;
   *kv = {0, static_cast<int>(apart)};
-  return encode<5>(m, base, {64, 8, d / 64, (n_pages - 1) * apart + groups, heads}, {s.n_, 64, 8 * s.n_, s.h_},
+  return maps::encode<5>(m, base, {64, 8, d / 64, (n_pages - 1) * apart + groups, heads}, {s.n_, 64, 8 * s.n_, s.h_},
                    {64, 8, d / 64, rows / 8, 1});
-}
-
-// One of copies of `rows` rows of one channel block: (D, row, head, page).
-bool encode_plain(CUtensorMap* m, const void* base, const Strides& s, int d, int page_size, int heads, int n_pages,
-                  int rows) {
-  return encode<4>(m, base, {d, page_size, heads, n_pages}, {s.n_, s.h_, s.b_}, {64, rows, 1, 1});
 }
 
 // Sets the shared-memory opt-in once per device and instantiation.
@@ -110,10 +86,8 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   PrefillParams p;
   p.group = a.h_q / a.h_kv;
   p.tile_tokens = kBlockM / p.group;
-  p.box_rows = 16;
-  while (p.box_rows < kBlockN && a.page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
-  if (!encode<4>(&p.tm_q, a.q, {a.d, p.group, a.tokens, a.h_kv}, {a.q_h, a.q_n, a.q_h * p.group},
-                 {64, p.group, p.tile_tokens, 1}))
+  p.box_rows = maps::box_rows(a.page_size);
+  if (!maps::encode_queries(&p.tm_q, a.q, a.q_n, a.q_h, a.d, p.group, a.tokens, a.h_kv, p.tile_tokens))
     return cudaErrorInvalidValue;
   // Copies of 16 rows are fused in pages of long requests: the copies' number bounds them (54560 keys, one head: 970
   // and 1197 us; 4 x 9024, 24 heads on 8: 387 and 415).  For short ones a fused copy's longer way counts (16 x 2512: 309
@@ -121,8 +95,8 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   const bool fused = p.box_rows == 16 && static_cast<long long>(a.max_pages) * a.page_size > 5120 &&
       encode_fused(&p.tm_k, &p.kv[0], a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows) &&
       encode_fused(&p.tm_v, &p.kv[1], a.v_cache, a.vs, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows);
-  if (!fused && (!encode_plain(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows) ||
-                 !encode_plain(&p.tm_v, a.v_cache, a.vs, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows)))
+  if (!fused && (!maps::encode_rows(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows) ||
+                 !maps::encode_rows(&p.tm_v, a.v_cache, a.vs, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows)))
     return cudaErrorInvalidValue;
   p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
   p.vs = a.vs;

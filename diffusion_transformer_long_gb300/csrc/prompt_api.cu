@@ -248,9 +248,10 @@ dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, cons
   if (s != DIT_OK) return s;
   s = check_pages(page_size, n_pages, max_pages);
   if (s != DIT_OK) return s;
+  if (H_q / H_kv > 256) return DIT_ERR_UNSUPPORTED;  // a product's columns
   const dit_strides qs = token_strides(q_strides, T, H_q, D);
   const dit_strides ks = cache_strides(k_strides, n_pages, H_kv, page_size, D);
-  if (!valid_tokens(q, qs, T, H_q) || !valid_cache(k_cache, ks, n_pages, H_kv) || !lse || !aligned(lse, 4) ||
+  if (!valid_tokens(q, qs, T, H_q) || qs.h >= (1LL << 39) / (H_q / H_kv) || !valid_cache(k_cache, ks, n_pages, H_kv) || !lse || !aligned(lse, 4) ||
       !valid_table(block_table, table_stride, B, max_pages) || !seq_lens || !aligned(seq_lens, 4) ||
       !aligned(cu_new, 4) || !aligned(start_lens, 4) || !mass || !aligned(mass, 4) || !mass_out || !aligned(mass_out, 4))
     return DIT_ERR_INVALID_ARG;
@@ -287,6 +288,8 @@ dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, cons
   a.max_pages = max_pages;
   a.window = window;
   a.scale = scale;
+  a.status = ditattn::status_word();
+  if (!a.status) return DIT_ERR_CUDA;
   return done(ditattn::launch_paged_mass(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -518,7 +518,8 @@ size_t dit_paged_prefill_workspace_bytes(int D, int page_size, int max_pages);
  *   mass      : device fp32 [n_pages, H_kv], contiguous (read)
  *   mass_out  : device fp32 [n_pages, H_kv] (written: the pages of requests with new tokens alone); may be mass
  *               itself.  A page that is in the table more than once is left with any of its sums.
- *   window    : >= 0;  T : 1 .. 2^30;  scale : > 0, and finite times log2 e in 32 bits
+ *   window    : >= 0;  T : 1 .. 2^30;  H_q : a multiple of H_kv, at most 256 H_kv (above: DIT_ERR_UNSUPPORTED)
+ *   scale     : > 0, and finite times log2 e in 32 bits
  */
 dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, const float* lse, const void* k_cache,
                                const dit_strides* k_strides, const int* block_table, long long table_stride,
