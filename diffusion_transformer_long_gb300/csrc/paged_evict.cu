@@ -8,11 +8,13 @@
 //
 // Two launches.  The first turns weights into 64-bit keys whose order is the numbers' (NaN above all, an entry without
 // a page below all), over the whole GPU: an SM adds two numbers of 64 bits a clock.  It also counts what a request can
-// give back, and keeps the lengths and the stack's height as they were.  In the second a block a request finds the border
-// key digit by digit, eight bits a pass (and no further than tells the kept ones from the others), places what is
-// kept and what goes by scans over flags, and knows from the counts where on the stack its pages go.  Bound by
-// latency: the bytes would take 0.3 us (16 x 75600 keys in pages of 16, 8 heads) and 0.1 us (256 requests of up to 4608
-// in pages of 64, 24 heads), the two launches take %s and %s us in a graph.
+// give back, and keeps the lengths and the stack's height as they were.  In the second a block a request finds the
+// border key digit by digit, eight bits a pass (from the first bit that not all share, and no further than tells the
+// kept ones from the others), places what is kept and what goes by scans over flags, and knows from the counts where on
+// the stack its pages go.  Bound by latency: the bytes would take 0.3 us (16 x 75600 keys in pages of 16, 8 heads) and
+// 0.1 us (256 requests of up to 4608 in pages of 64, 24 heads), the two launches take 23 and 14 us in a graph
+// (28.8 and 14.7 with 512 columns placed at a time and the search begun at the top digit; chunks of 256 columns in the
+// first launch and 1024 threads in the second change nothing).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -29,6 +31,7 @@ constexpr int kScoreThreads = 256;
 constexpr int kChunk = 1024;  // table columns of a scoring block
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 4;  // table columns a thread places at a time
 constexpr int kShared = 12288;  // keys that stay in shared memory
 
 struct EvictParams {
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
   extern __shared__ __align__(8) unsigned char smem[];
   __shared__ int hist[256];
   __shared__ int warps[kWarps];
+  __shared__ unsigned spread[2];  // bits in which keys differ
   __shared__ int found[3];  // the border's digit, how many to take among those that share it, and whether that is all
   const int b = blockIdx.x;
   wait_for_inputs();
@@ -144,6 +148,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
     return;
   }
   // Where on the stack the request's pages go.
+  if (threadIdx.x < 2) spread[threadIdx.x] = 0;
   int before = 0;
   for (int i = threadIdx.x; i < b; i += kThreads) before += gives(p, i);
   int all;
@@ -160,20 +165,33 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
 
   const int old = n - p.recent, want = p.keep - p.recent;  // 0 <= want < old
   const uint64_t* key = p.keys + static_cast<long long>(b) * p.max_pages;
-  if (old <= kShared) {
-    uint64_t* const mine = reinterpret_cast<uint64_t*>(smem);
-    for (int i = threadIdx.x; i < old; i += kThreads) mine[i] = key[i];
-    key = mine;
+  const uint64_t first = key[0];
+  uint64_t differ = 0;
+  uint64_t* const mine = reinterpret_cast<uint64_t*>(smem);
+  for (int i = threadIdx.x; i < old; i += kThreads) {
+    const uint64_t x = key[i];
+    differ |= x ^ first;
+    if (old <= kShared) mine[i] = x;
   }
+  if (old <= kShared) key = mine;
+  for (int half = 0; half < 2; ++half) {
+    const unsigned x = __reduce_or_sync(~0u, static_cast<unsigned>(differ >> (32 * half)));
+    if (threadIdx.x % 32 == 0) atomicOr(&spread[half], x);
+  }
+  __syncthreads();
+  // The search starts with the first bit in which some differ: what all share would have every thread count in one
+  // place (weights of one sign and few exponents do for ten bits).
+  int rest = 64 - __clzll(static_cast<long long>(static_cast<uint64_t>(spread[1]) << 32 | spread[0]));
   // Taken are the keys above the border, and the first `left` of those equal to it.
-  uint64_t border = want > 0 ? 0 : ~0ull;
+  uint64_t border = want == 0 ? ~0ull : rest < 64 ? first & ~0ull << rest : 0;
   int left = want;
-  for (int shift = 56; want > 0 && shift >= 0; shift -= 8) {
+  while (want > 0 && rest > 0) {
     if (threadIdx.x < 256) hist[threadIdx.x] = 0;
     __syncthreads();
-    const uint64_t above = shift == 56 ? 0 : ~0ull << (shift + 8);
+    const uint64_t above = rest == 64 ? 0 : ~0ull << rest;
+    const int width = min(rest, 8), shift = rest - width;
     for (int i = threadIdx.x; i < old; i += kThreads)
-      if ((key[i] & above) == border) atomicAdd(&hist[key[i] >> shift & 255], 1);
+      if ((key[i] & above) == border) atomicAdd(&hist[key[i] >> shift & ((1 << width) - 1)], 1);
     __syncthreads();
     if (threadIdx.x < 32) {
       // Lane l: digits 255 - 8 l and the seven below it.
@@ -201,6 +219,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
     __syncthreads();
     border |= static_cast<uint64_t>(found[0]) << shift;
     left = found[1];
+    rest = shift;
     if (found[2]) {  // all that begin like this are taken: those not below it (it is not 0: some key is not taken)
       --border;
       left = 0;
@@ -209,22 +228,41 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const __grid_constant__
     __syncthreads();
   }
   __syncthreads();
-  // In chunks of the block's threads, each read before its places, which are never behind it, are written.
+  // In chunks of kPer neighbours a thread, each chunk read before its places, which are never behind it, are written.
   int kept = 0, dropped = 0, equal = 0;
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    const int page = i < n ? row[i] : -1;
-    const uint64_t x = i < old ? key[i] : 0;
-    const bool same = i < old && left > 0 && x == border;
-    int total;
-    const int rank = equal + scan(same, warps, total);
-    equal += total;
-    const bool stays = i < n && (i >= old || x > border || (same && rank < left));
-    const bool goes = i < n && !stays && page >= 0 && page < p.n_pages;
-    const int at = scan(stays | goes << 16, warps, total);
-    if (stays) out[kept + (at & 0xffff)] = page;
-    const long long top = height + dropped + (at >> 16);
-    if (goes && top < p.capacity) p.stack[top] = page;
+  for (int i0 = 0; i0 < n; i0 += kThreads * kPer) {
+    const int i = i0 + threadIdx.x * kPer;
+    int page[kPer], total;
+    unsigned same = 0, stays = 0, goes = 0;  // a bit a neighbour
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) page[j] = i + j < n ? row[i + j] : -1;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint64_t x = i + j < old ? key[i + j] : 0;
+      same |= static_cast<unsigned>(i + j < old && left > 0 && x == border) << j;
+      stays |= static_cast<unsigned>(i + j < n && (i + j >= old || x > border)) << j;
+    }
+    if (left > 0) {
+      int rank = equal + scan(__popc(same), warps, total);
+      equal += total;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (same >> j & 1 && rank++ < left) stays |= 1u << j;
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      goes |= static_cast<unsigned>(!(stays >> j & 1) && page[j] >= 0 && page[j] < p.n_pages) << j;
+    const int at = scan(__popc(stays) | __popc(goes) << 16, warps, total);
+    int place = kept + (at & 0xffff);
+    long long top = height + dropped + (at >> 16);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (stays >> j & 1) out[place++] = page[j];
+      if (goes >> j & 1) {
+        if (top < p.capacity) p.stack[top] = page[j];
+        ++top;
+      }
+    }
     kept += total & 0xffff;
     dropped += total >> 16;
   }
