@@ -15,6 +15,11 @@ using namespace ditattn::api;
 
 namespace {
 
+constexpr int kMaxRequests = 1 << 30;  // request indexes, a warp's step past the last one too, stay in 32 bits
+
+// Whether the kernels' 32-bit key indexes reach past a full table row's last tile.
+bool room_counts(int page_size, int max_pages) { return static_cast<long long>(max_pages) * page_size <= 1 << 30; }
+
 // A [T, H, D] view of a step's tokens: its strides (n, h) in the manner of cache_strides.
 dit_strides token_strides(const dit_strides* s, int T, int H, int D) {
   dit_strides x = s ? *s : dit_strides{D, D, static_cast<long long>(H) * D};
@@ -104,7 +109,7 @@ dit_status dit_qk_norm_rope(const void* q, const dit_strides* q_strides, void* q
     if (pairs % 8 != 0) return DIT_ERR_UNSUPPORTED;
     const bool packed = !positions;
     if (!aligned(positions, 4) || !aligned(cu_new, 4) || !aligned(start_lens, 4)) return DIT_ERR_INVALID_ARG;
-    if (packed && (!cu_new || !start_lens || requests < 1 || requests == INT_MAX || B != 1 || axes != 1))
+    if (packed && (!cu_new || !start_lens || requests < 1 || requests > kMaxRequests || B != 1 || axes != 1))
       return DIT_ERR_INVALID_ARG;
     if (!packed && (cu_new || start_lens || pos_b < 0 || pos_axis < 0 || pos_b > kMaxSpan / B || pos_axis > kMaxSpan / 4))
       return DIT_ERR_INVALID_ARG;
@@ -170,12 +175,12 @@ dit_status dit_paged_prefill_fwd(const void* q, const dit_strides* q_strides, co
                                  int H_kv, int D, int page_size, int n_pages, int max_pages, int causal,
                                  float scale, dit_dtype out_dtype, void* workspace,
                                  size_t workspace_bytes, dit_stream stream) {
-  if (T < 1 || T > kMaxTokens || B < 1 || B == INT_MAX) return DIT_ERR_INVALID_ARG;
+  if (T < 1 || T > kMaxTokens || B < 1 || B > kMaxRequests) return DIT_ERR_INVALID_ARG;
   dit_status s = check_heads(T, H_q, H_kv, D);
   if (s != DIT_OK) return s;
   s = check_pages(page_size, n_pages, max_pages);
   if (s != DIT_OK) return s;
-  if (H_q / H_kv > 128) return DIT_ERR_UNSUPPORTED;  // a tile's rows
+  if (H_q / H_kv > 128 /* a tile's rows */ || !room_counts(page_size, max_pages)) return DIT_ERR_UNSUPPORTED;
   const dit_strides qs = token_strides(q_strides, T, H_q, D);
   const dit_strides ks = cache_strides(k_strides, n_pages, H_kv, page_size, D);
   const dit_strides vs = cache_strides(v_strides, n_pages, H_kv, page_size, D);
@@ -242,13 +247,13 @@ dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, cons
                                const int* seq_lens, const int* cu_new, const int* start_lens, const float* mass,
                                float* mass_out, int T, int B, int H_q, int H_kv, int D, int page_size,
                                int n_pages, int max_pages, int window, float scale, dit_stream stream) {
-  if (T < 1 || T > kMaxTokens || B < 1 || B == INT_MAX || window < 0) return DIT_ERR_INVALID_ARG;
+  if (T < 1 || T > kMaxTokens || B < 1 || B > kMaxRequests || window < 0) return DIT_ERR_INVALID_ARG;
   if (!cu_new && (T != B || start_lens)) return DIT_ERR_INVALID_ARG;
   dit_status s = check_heads(T, H_q, H_kv, D);
   if (s != DIT_OK) return s;
   s = check_pages(page_size, n_pages, max_pages);
   if (s != DIT_OK) return s;
-  if (H_q / H_kv > 256) return DIT_ERR_UNSUPPORTED;  // a product's columns
+  if (H_q / H_kv > 256 /* a product's columns */ || !room_counts(page_size, max_pages)) return DIT_ERR_UNSUPPORTED;
   const dit_strides qs = token_strides(q_strides, T, H_q, D);
   const dit_strides ks = cache_strides(k_strides, n_pages, H_kv, page_size, D);
   if (!valid_tokens(q, qs, T, H_q) || qs.h >= (1LL << 39) / (H_q / H_kv) || !valid_cache(k_cache, ks, n_pages, H_kv) || !lse || !aligned(lse, 4) ||

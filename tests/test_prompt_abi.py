@@ -188,3 +188,18 @@ def test_binding_refuses_wrong_tensors():
         da.paged_page_mass(x, x, c, i[None], i, x)
     with pytest.raises(ValueError):
         da.paged_evict(torch.zeros(3, 2), i[None], i, i, i, 16, 2)
+
+
+@pytest.mark.parametrize("B", [(1 << 30) + 1, (1 << 31) - 2])
+def test_request_limit(lib, B):
+    """Request indexes stay in 32 bits in a warp's step past the last one."""
+    assert prefill(lib, B=B) == INVALID and mass(lib, B=B) == INVALID
+    assert rope(lib, pos=None, cu=A[8], start=A[9], requests=B, B=1, pairs=(16,)) == INVALID
+
+
+@pytest.mark.parametrize("call", [prefill, mass])
+def test_room_limit(lib, call):
+    """Key indexes stay in 32 bits in a full row's last tile."""
+    at = dict(B=1, T=1, cu=A[5], P=16)
+    assert call(lib, max_pages=(1 << 26) + 1, **at) == UNSUPPORTED
+    assert call(lib, max_pages=1 << 20, P=1024, **{k: v for k, v in at.items() if k != "P"}) not in (INVALID, UNSUPPORTED)
