@@ -10,7 +10,7 @@
 // are 16 neighbouring bytes of two keys, read straight from the cache into registers, and of a query row: no staging,
 // and every warp walks over runs of pages by itself.  More rows are multiplied on tcgen05 (mma.sync in blocks
 // that shared the rows: 2 x 75600 keys, 40 heads on 8, 16 tokens: 107 us, 230 TFLOP/s, near that instruction's rate; now
-// 71).
+// 63 to 73).
 //
 // The lanes' sums meet by shuffles in a fixed order, and a page is written by one warp or block: no atomics in a sum, equal
 // calls give equal bits.
@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 #include <mutex>
 
@@ -256,7 +257,8 @@ constexpr int kCols = 256;       // (token, head) rows at once: its columns
 constexpr int kRing = 4;         // key tiles in shared memory
 constexpr int kManyThreads = 384;
 constexpr int kEpilogue0 = 4;    // warps 4-7 and 8-11: a tensor-memory buffer each
-constexpr int kRunTiles = 16;    // a run's tiles, at most: 128 pieces of 16 keys
+constexpr int kRunTiles = 32;    // a run's tiles, at most: 256 pieces of 16 keys
+constexpr int kRunCost = 256;    // what a run costs beside its keys, in keys (1.5 us)
 constexpr long long kWaitLimit = 4000000000LL;
 
 template <int D>
@@ -637,11 +639,19 @@ cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st) {
   if (!maps::encode_queries(&p.tm_q, a.q, a.q_n, a.q_h, a.d, p.group, a.tokens, a.h_kv, p.chunk_tokens) ||
       !maps::encode_rows(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows))
     return cudaErrorInvalidValue;
-  // Runs of 2048 keys, or of fewer where there is not room for four runs a block.
-  const long long room = static_cast<long long>(a.batch) * a.h_kv * p.max_len;
-  int keys = kRunTiles * kTileN;
-  while (keys > 4 * kTileN && room / keys < 4LL * host::sm_count()) keys /= 2;
-  p.run_pages = std::max(1, keys / a.page_size);
+  // Runs of 512 to 4096 keys, whichever would end first if every request filled its row of the table: longer ones cost
+  // less beside their keys, and leave more blocks idle in the last round (2 x 75600 keys, 8 heads: runs of 4096, 2048,
+  // 1024, 512: 73, 77, 85, 98 us; 27280 keys, 24 heads: 61, 54, 55, 59).
+  long long best = LLONG_MAX;
+  for (int keys = 512; keys <= kRunTiles * kTileN; keys += 512) {
+    const int pages = std::max(1, keys / a.page_size);
+    const long long runs = static_cast<long long>(a.batch) * a.h_kv * ((a.max_pages + pages - 1) / pages);
+    const long long cost = (runs + host::sm_count() - 1) / host::sm_count() * (pages * a.page_size + kRunCost);
+    if (cost <= best) {
+      best = cost;
+      p.run_pages = pages;
+    }
+  }
   return a.d == 64 ? launch_many<64>(p, st) : launch_many<128>(p, st);
 }
 

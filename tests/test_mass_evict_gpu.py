@@ -74,6 +74,15 @@ def test_mass_many_requests():
         check_mass(s)
 
 
+@pytest.mark.parametrize("columns,P", [(0, 64), (2048, 64), (2500, 48), (150, 1024)])
+def test_mass_runs_of_pages(columns, P):
+    """The table's room sets how many pages a block takes at a time."""
+    s = Step([9000, 4097, 0, 2100], [33, 20, 30, 1], 6, 2, 128, P, seed=columns)
+    if columns:
+        s.table = torch.cat([s.table, torch.full((4, columns), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+    check_mass(s, 20)
+
+
 def test_mass_unusual_contents():
     """Positions anywhere, entries outside the pool, lengths below 0, rows without a key, keys that are not finite."""
     s = Step([64, 300, 10], [40, 33, 6], 6, 2, 64, 32, spare=4)
