@@ -17,6 +17,10 @@ namespace {
 
 // Requests with room for at most this many keys keep their items whole: one launch and no workspace.
 constexpr long long kWholeKeys = 1024;
+// Items are of one Q tile of 64 rows where the step's rows (tokens x heads of a group) fill at most 1 / kOneShare of a
+// whole tile a request (16 tokens, 24 heads on 8, 64 requests of 100-4096 keys: 128 us, of two tiles 145; 30 tokens, more than
+// one such item a request: 194 and 154).
+constexpr long long kOneShare = 2;
 
 // A paged cache's map of fused copies of `rows` rows (see KvTile); false: the strides do not allow one.
 bool encode_fused(CUtensorMap* m, KvPlace* kv, const void* base, const Strides& s, int d, int page_size, int heads,
@@ -39,7 +43,7 @@ bool encode_fused(CUtensorMap* m, KvPlace* kv, const void* base, const Strides& 
 }
 
 // Sets the shared-memory opt-in once per device and instantiation.
-template <int D, bool kF32, bool kFused>
+template <int D, bool kOne, bool kF32, bool kFused>
 cudaError_t prepare() {
   static std::mutex mu;
   static bool done[64] = {};
@@ -49,20 +53,20 @@ cudaError_t prepare() {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(prefill_kernel<D, kF32, kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    e = cudaFuncSetAttribute(prefill_kernel<D, kOne, kF32, kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D, kOne>::kBytes);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   return cudaSuccess;
 }
 
-template <int D, bool kF32, bool kFused>
+template <int D, bool kOne, bool kF32, bool kFused>
 cudaError_t launch(const PrefillParams& p, int blocks, cudaStream_t st) {
-  cudaError_t e = prepare<D, kF32, kFused>();
+  cudaError_t e = prepare<D, kOne, kF32, kFused>();
   if (e != cudaSuccess) return e;
-  e = launch_after(prefill_kernel<D, kF32, kFused>, dim3(blocks), dim3(kThreads), Smem<D>::kBytes, st, p);
+  e = launch_after(prefill_kernel<D, kOne, kF32, kFused>, dim3(blocks), dim3(kThreads), Smem<D, kOne>::kBytes, st, p);
   if (e != cudaSuccess || !p.split) return e;
-  const int rows = p.tokens <= p.tile_tokens ? p.tokens * p.group : kItemRows;
+  const int rows = std::min(p.tokens, p.item_tokens) <= p.tile_tokens ? std::min(p.tokens, p.tile_tokens) * p.group : kItemRows;
   return launch_after(join_kernel<D, kF32>, dim3(blocks, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinRows * 32), 0,
                       st, p);
 }
@@ -85,7 +89,10 @@ size_t paged_prefill_workspace(int d, long long keys) {
 cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   PrefillParams p;
   p.group = a.h_q / a.h_kv;
-  p.tile_tokens = kBlockM / p.group;
+  const bool one = static_cast<long long>(a.tokens) * p.group * kOneShare <= static_cast<long long>(a.batch) * kBlockM &&
+                   p.group <= Smem<64, true>::kRows;
+  p.tile_tokens = (one ? Smem<64, true>::kRows : kBlockM) / p.group;
+  p.item_tokens = (one ? 1 : 2) * p.tile_tokens;
   p.box_rows = maps::box_rows(a.page_size);
   if (!maps::encode_queries(&p.tm_q, a.q, a.q_n, a.q_h, a.d, p.group, a.tokens, a.h_kv, p.tile_tokens))
     return cudaErrorInvalidValue;
@@ -126,9 +133,15 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   p.part_lse = p.part_o + part_rows() * a.d;
   p.meta = reinterpret_cast<int4*>(p.part_lse + part_rows());
   const int blocks = grid_blocks();
-  if (a.d == 64) return a.out_f32 ? launch<64, true, false>(p, blocks, st) : launch<64, false, false>(p, blocks, st);
-  if (fused) return a.out_f32 ? launch<128, true, true>(p, blocks, st) : launch<128, false, true>(p, blocks, st);
-  return a.out_f32 ? launch<128, true, false>(p, blocks, st) : launch<128, false, false>(p, blocks, st);
+  auto run = [&](auto d, auto fused_copies) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool kFused = decltype(fused_copies)::value;
+    if (one) return a.out_f32 ? launch<D, true, true, kFused>(p, blocks, st) : launch<D, true, false, kFused>(p, blocks, st);
+    return a.out_f32 ? launch<D, false, true, kFused>(p, blocks, st) : launch<D, false, false, kFused>(p, blocks, st);
+  };
+  if (a.d == 64) return run(std::integral_constant<int, 64>{}, std::false_type{});
+  return fused ? run(std::integral_constant<int, 128>{}, std::true_type{})
+               : run(std::integral_constant<int, 128>{}, std::false_type{});
 }
 
 }  // namespace ditattn

@@ -338,3 +338,79 @@ def test_expired_wait_is_reported():
     finally:
         da.inject_stall(False)
     s.check()
+
+
+@pytest.mark.parametrize("limit", [0, 1, 3])
+@pytest.mark.parametrize("Hq,Hkv,D,P,room", [(6, 2, 128, 16, 9000), (6, 2, 128, 64, 4096), (8, 1, 64, 32, 0), (3, 3, 64, 16, 3000)])
+def test_few_tokens(Hq, Hkv, D, P, room, limit):
+    """Steps of few tokens a request: items in turn on the two halves of a block, empty ones and long ones among them."""
+    da.set_grid_limit(limit)
+    rng = np.random.default_rng(limit)
+    old, new = rng.integers(0, 500, 90), rng.integers(0, 6, 90)
+    new[7], old[11] = 150, 2900 if room else 900
+    s = Step(old, new, Hq, Hkv, D, P, spare=3, seed=P, room=room)
+    s.check(True, torch.bfloat16)
+    s.check(False)
+    none = rng.random(90) < 0.3  # requests without a key
+    s.lens_h = np.where(none, 0, s.lens_h)
+    s.lens = dev(s.lens_h)
+    s.check(True)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(40, 1), (64, 1), (33, 1), (96, 2)])
+def test_few_tokens_of_large_groups(Hq, Hkv):
+    for D in (64, 128):
+        for new in ([1], [2], [1] * 20, [0, 3, 0, 0, 1, 0, 0, 0]):
+            Step([300] * len(new), new, Hq, Hkv, D, 32, seed=len(new), room=2048).check()
+
+
+def test_few_tokens_values_that_are_not_finite():
+    new = [3, 1, 0, 5, 2, 1]
+    s = Step([127, 300, 5, 1000, 62, 0], new, 6, 2, 128, 16, room=4096)
+    want = s.run()[0]
+    for b in (0, 3, 4):  # the request's last key: its last token sees it
+        at = int(s.lens_h[b]) - 1
+        s.v[int(s.table[b, at // 16]), 1, at % 16, 9] = math.nan
+        if at % 16 < 15:
+            s.v[int(s.table[b, at // 16]), :, at % 16 + 1:] = math.inf  # behind the length
+    got = s.run()[0]
+    mark = torch.zeros_like(got, dtype=torch.bool)
+    for b in (0, 3, 4):
+        mark[int(s.cu[b + 1]) - 1, 3:, 9] = True
+    assert got[mark].isnan().all() and torch.equal(got[~mark], want[~mark])
+
+
+def test_few_tokens_streams_and_graphs():
+    rng = np.random.default_rng(8)
+    steps = [Step(rng.integers(0, 3000, 40), rng.integers(1, 5, 40), 6, 2, 128, 64, seed=i, room=4096) for i in range(2)]
+    want = [s.run() for s in steps]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in steps]
+    for _ in range(5):  # two calls at once
+        got = [s.run(stream=st) for s, st in zip(steps, side)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    graphs = []
+    for s in steps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = s.run()
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, _ in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for (_, o), w in zip(graphs, want) for a, b in zip(o, w))
+
+
+def test_few_tokens_expired_wait_is_reported():
+    s = Step([300] * 9, [1] * 9, 2, 1, 64, 16, room=2048)
+    try:
+        da.inject_stall(True, 2_000_000)
+        s.run()
+        with pytest.raises(da.DitError) as e:
+            da.check(DEV)
+        assert e.value.status == da.DIT_ERR_TIMEOUT
+    finally:
+        da.inject_stall(False)
+    s.check()
