@@ -640,8 +640,8 @@ cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st) {
       !maps::encode_rows(&p.tm_k, a.k_cache, a.ks, a.d, a.page_size, a.h_kv, a.n_pages, p.box_rows))
     return cudaErrorInvalidValue;
   // Runs of 512 to 4096 keys, whichever would end first if every request filled its row of the table: longer ones cost
-  // less beside their keys, and leave more blocks idle in the last round (2 x 75600 keys, 8 heads, L2 flushed: runs of 4096, 2048,
-  // 1024, 512: 73, 77, 85, 98 us; 27280 keys, 24 heads: 61, 54, 55, 59; of 3584 and 1536 by this rule 73 and 48).
+  // less beside their keys, and leave more blocks idle in the last round (L2 flushed; 2 x 75600 keys, 8 heads, runs of
+  // 4096, 2048, 1024, 512: 73, 77, 85, 98 us; 27280 keys, 24 heads: 61, 54, 55, 59, and of 1536, by this rule, 48).
   long long best = LLONG_MAX;
   for (int keys = 512; keys <= kRunTiles * kTileN; keys += 512) {
     const int pages = std::max(1, keys / a.page_size);
