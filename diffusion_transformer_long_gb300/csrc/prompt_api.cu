@@ -15,7 +15,8 @@ using namespace ditattn::api;
 
 namespace {
 
-constexpr int kMaxRequests = 1 << 30;  // request indexes, a warp's step past the last one too, stay in 32 bits
+// Each block adds the requests' lengths up for itself, 32 at a time: 20 ms at this many.
+constexpr int kMaxRequests = 1 << 20;
 
 // Whether the kernels' 32-bit key indexes reach past a full table row's last tile.
 bool room_counts(int page_size, int max_pages) { return static_cast<long long>(max_pages) * page_size <= 1 << 30; }

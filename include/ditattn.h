@@ -312,7 +312,7 @@ dit_status dit_layout_copy(const void* src, const dit_strides* src_strides, void
  *   cu_new, start_lens, requests : device int32 [requests + 1], [requests] (read): token n of request r (dit_paged_plan's
  *                   cu_new) is at start_lens[r] + n - cu_new[r].  Tokens of no request are left as they are.
  *                   cu_new ascends (else its tokens' positions are unspecified).
- *   B * N, requests : at most 2^30
+ *   B * N         : at most 2^30;  requests : at most 2^20
  */
 dit_status dit_qk_norm_rope(const void* q, const dit_strides* q_strides, void* q_out,
                             const dit_strides* q_out_strides, int H_q, const void* k,
@@ -483,8 +483,8 @@ size_t dit_paged_attn_workspace_bytes(int B, int H_q, int H_kv, int D, int page_
  *                 without a slot then keep their positions and see the keys that were stored.
  *   out         : device [T, H_q, D] of out_dtype, contiguous, 16-byte aligned (written)
  *   lse         : device fp32 [T, H_q] (written), or NULL
- *   T, B        : 1 .. 2^30;  H_q : a multiple of H_kv, at most 128 H_kv;  max_pages * page_size : at most 2^30
- *                 (above either: DIT_ERR_UNSUPPORTED)
+ *   T           : 1 .. 2^30;  B : 1 .. 2^20;  H_q : a multiple of H_kv, at most 128 H_kv;
+ *                 max_pages * page_size : at most 2^30 (above either of these two: DIT_ERR_UNSUPPORTED)
  *   causal      : 0 or 1
  *   scale       : > 0, and finite times log2 e in 32 bits
  *   workspace   : at least dit_paged_prefill_workspace_bytes(D, page_size, max_pages) bytes; NULL where that is 0
@@ -518,8 +518,8 @@ size_t dit_paged_prefill_workspace_bytes(int D, int page_size, int max_pages);
  *   mass      : device fp32 [n_pages, H_kv], contiguous (read)
  *   mass_out  : device fp32 [n_pages, H_kv] (written: the pages of requests with new tokens alone); may be mass
  *               itself.  A page that is in the table more than once is left with any of its sums.
- *   window    : >= 0;  T, B : 1 .. 2^30;  H_q : a multiple of H_kv, at most 256 H_kv;  max_pages * page_size : at
- *               most 2^30 (above either: DIT_ERR_UNSUPPORTED)
+ *   window    : >= 0;  T : 1 .. 2^30;  B : 1 .. 2^20;  H_q : a multiple of H_kv, at most 256 H_kv;
+ *               max_pages * page_size : at most 2^30 (above either of these two: DIT_ERR_UNSUPPORTED)
  *   scale     : > 0, and finite times log2 e in 32 bits
  */
 dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, const float* lse, const void* k_cache,

@@ -190,9 +190,9 @@ def test_binding_refuses_wrong_tensors():
         da.paged_evict(torch.zeros(3, 2), i[None], i, i, i, 16, 2)
 
 
-@pytest.mark.parametrize("B", [(1 << 30) + 1, (1 << 31) - 2])
+@pytest.mark.parametrize("B", [(1 << 20) + 1, (1 << 30) + 1, (1 << 31) - 2])
 def test_request_limit(lib, B):
-    """Request indexes stay in 32 bits in a warp's step past the last one."""
+    """Request indexes stay in 32 bits in a warp's step past the last one, and sums over the requests in milliseconds."""
     assert prefill(lib, B=B) == INVALID and mass(lib, B=B) == INVALID
     assert rope(lib, pos=None, cu=A[8], start=A[9], requests=B, B=1, pairs=(16,)) == INVALID
 
