@@ -299,7 +299,8 @@ dit_status dit_layout_copy(const void* src, const dit_strides* src_strides, void
  *   q, k          : device bf16 [B, H, N, D] views (read); NULL strides: contiguous.  A packed step's [T, H, D] is
  *                   B = 1, N = T.  k may be NULL (H_k = 0, no k_out, no k_weight): queries alone.
  *   q_out, k_out  : device bf16 views of the same shapes (written), of any layout (token-major in, head-major out):
- *                   each may be its input in place (the same view), and shares no element with anything else.
+ *                   each may be its input in place (the same view), and shares no element with anything else (views
+ *                   may interleave, as slices of one allocation do: heads, halves of the tokens, a block for each b).
  *   norm          : 0 or 1; eps >= 0 (read with norm alone)
  *   q_weight, k_weight : device [D] of weight_dtype (read), or NULL (1); NULL without norm
  *   freqs         : device fp32 [n] (read): the angle of each pair per position, so that stretched and
