@@ -116,6 +116,17 @@ bool views_apart(const View& a, const View& b, int B, int N, int D) {
   return grids_apart(g[0], 0, g[1], 0, gap, steps);
 }
 
+// True if two tables of B rows of n ints share none.
+bool rows_apart(const int* a, long long a_stride, const int* b, long long b_stride, int B, int n) {
+  Grid g[2];
+  for (int i = 0; i < 2; ++i) {
+    g[i].run = n;
+    g[i].add(i ? b_stride : a_stride, B);
+  }
+  int steps = kMostSteps;
+  return grids_apart(g[0], 0, g[1], 0, b - a, steps);
+}
+
 }  // namespace
 
 extern "C" {
@@ -376,13 +387,16 @@ dit_status dit_paged_evict(const float* mass, const int* block_table, long long 
                         span(free_pages, 4LL * pool_capacity), span(n_free_out, 4),
                         span(workspace, static_cast<long long>(need))};
   const Range ins[] = {table, span(seq_lens, 4LL * B), span(mass, 4LL * n_pages * H_kv), span(n_free, 4)};
+  // (Rows of the two tables may lie in turn, in one allocation.)
+  const bool tables_apart = rows_apart(block_table, table_stride, table_out, table_out_stride, B, max_pages);
   const bool same[5] = {in_place, seq_lens_out == seq_lens, false, n_free_out == n_free, false};
   const int of[5] = {0, 1, -1, 3, -1};  // the input that an output may be
   for (int i = 0; i < 5; ++i) {
     for (int j = i + 1; j < 5; ++j)
       if (overlap(outs[i], outs[j])) return DIT_ERR_INVALID_ARG;
     for (int j = 0; j < 4; ++j)
-      if (!(same[i] && j == of[i]) && overlap(outs[i], ins[j])) return DIT_ERR_INVALID_ARG;
+      if (!(same[i] && j == of[i]) && overlap(outs[i], ins[j]) && !(i == 0 && j == 0 && tables_apart))
+        return DIT_ERR_INVALID_ARG;
   }
   ditattn::EvictLaunch a{mass,   block_table, table_stride, table_out, table_out_stride, seq_lens,  seq_lens_out, free_pages,
                          n_free, n_free_out,  B,            H_kv,      page_size,        n_pages,   max_pages,    pool_capacity,

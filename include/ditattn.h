@@ -545,7 +545,8 @@ dit_status dit_paged_page_mass(const void* q, const dit_strides* q_strides, cons
  *   free_pages  : device int32 [pool_capacity] (entries from n_free on are written)
  *   keep        : >= 1;  recent : 1 .. keep;  B : 1 .. 8192 (above: DIT_ERR_UNSUPPORTED)
  *   workspace   : at least dit_paged_evict_workspace_bytes(B, max_pages) bytes
- * Outputs must not overlap each other or the inputs, but for the three pairs named.
+ * Outputs must not overlap each other or the inputs, but for the three pairs named; rows of block_table and
+ * table_out may lie in turn in one allocation.
  */
 dit_status dit_paged_evict(const float* mass, const int* block_table, long long table_stride, int* table_out,
                            long long table_out_stride, const int* seq_lens, int* seq_lens_out, int* free_pages,

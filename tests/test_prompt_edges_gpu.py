@@ -3,7 +3,9 @@ import numpy as np
 import pytest
 import torch
 
+import prompt_oracle as po
 from diffusion_transformer_long_gb300 import ditattn as da
+from test_mass_evict_gpu import evict_state
 from test_paged_gpu import rand
 from test_qk_norm_rope_gpu import close, weight
 
@@ -43,3 +45,21 @@ def test_interleaved_views_in_place(inter):
             close(y, old, w, 1e-6, freqs, pairs, pos, inter, 1.0)
             old.copy_(y)
         assert torch.equal(x, before)
+
+
+# ------------------------------------------------------------------ eviction
+
+
+def test_tables_in_one_allocation():
+    """The old and the new table's rows in turn: the result of tables apart."""
+    mass, table, lens, stack, n_free = evict_state([16 * 50, 16 * 60 + 3, 5, 16 * 9], 16, 2)
+    want = po.evict(mass, table, lens, stack, n_free, 16, 10, 2)
+    n = table.shape[1]
+    both = torch.full((4, 2, n + 3), 5, dtype=torch.int32, device=DEV)
+    for i in (0, 1):
+        both.fill_(5)
+        old, new = both[:, i, :n], both[:, 1 - i, :n]
+        old.copy_(table)
+        got_lens, got_free = da.paged_evict(mass, old, lens, stack.clone(), n_free, 16, 10, 2, table_out=new)
+        assert np.array_equal(new.cpu().numpy(), want[0]) and torch.equal(old, table) and (both[:, :, n:] == 5).all()
+        assert np.array_equal(got_lens.cpu().numpy(), want[1]) and int(got_free) == want[3]
