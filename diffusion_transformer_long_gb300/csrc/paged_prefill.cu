@@ -17,6 +17,9 @@ namespace {
 
 // Requests with room for at most this many keys keep their items whole: one launch and no workspace.
 constexpr long long kWholeKeys = 1024;
+// SM clocks that a key tile of an item may take, some five times what it does (2.0 us): with the limit of a single step's
+// wait alone, items of more than 10^8 keys ran out of it.
+constexpr long long kTileClocks = 20000;
 // Items are of one Q tile of 64 rows where the step's rows (tokens x heads of a group) fill at most 1 / kOneShare of a
 // whole tile a request (16 tokens, 24 heads on 8, 64 requests of 100-4096 keys: 128 us, of two tiles 145; 30 tokens, more than
 // one such item a request: 194 and 154).
@@ -129,6 +132,8 @@ cudaError_t launch_paged_prefill(const PrefillLaunch& a, cudaStream_t st) {
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
   stall_injection(&p.stall, &p.wait_limit);
+  // Some waits last a whole item: the epilogue's for its sums, the idle softmax's for the next, the ring's for a place.
+  p.wait_limit += static_cast<long long>(p.max_len / kBlockN) * kTileClocks;
   p.part_o = static_cast<float*>(a.workspace);
   p.part_lse = p.part_o + part_rows() * a.d;
   p.meta = reinterpret_cast<int4*>(p.part_lse + part_rows());

@@ -63,3 +63,27 @@ def test_tables_in_one_allocation():
         got_lens, got_free = da.paged_evict(mass, old, lens, stack.clone(), n_free, 16, 10, 2, table_out=new)
         assert np.array_equal(new.cpu().numpy(), want[0]) and torch.equal(old, table) and (both[:, :, n:] == 5).all()
         assert np.array_equal(got_lens.cpu().numpy(), want[1]) and int(got_free) == want[3]
+
+
+# ------------------------------------------------------------------ attention of new tokens
+
+
+@pytest.mark.parametrize("n", [1, 100, 300])
+def test_items_that_outlast_a_wait(n):
+    """The limit of a wait is one of no progress: an item of 1500 key tiles (over 500 us) under a limit of 100 us a step
+    ends in order.  All pages are one, so that the outputs are the short request's."""
+    P, keys, repeat = 1024, 1024, 190
+    q, k, v = rand(n, 1, 64, seed=1), rand(1, 1, P, 64, seed=2), rand(1, 1, P, 64, seed=3)
+    table = torch.zeros(1, repeat, dtype=torch.int32, device=DEV)
+    cu, want = dev([0, n]), da.paged_prefill_fwd(q, k, v, table[:, :1], dev([keys]), dev([0, n]), causal=False)
+    try:
+        da.set_grid_limit(1)  # (one block has it all)
+        da.inject_stall(False, 200_000)
+        out, lse = da.paged_prefill_fwd(q, k, v, table, dev([repeat * keys]), cu, causal=False)
+        da.check(DEV)
+    finally:
+        da.inject_stall(False)
+        da.set_grid_limit(0)
+    # Sums of 190 times as many equal terms in 32 bits, 2^18 keys: off by at most 2^18 2^-23 of them, twice, in the worst case.
+    assert (out - want[0]).abs().max() <= 2.0 ** -4 * v.abs().max()
+    assert (lse - want[1] - np.log(repeat)).abs().max() <= 2.0 ** -4
