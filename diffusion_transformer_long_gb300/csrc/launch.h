@@ -91,7 +91,7 @@ void set_stall_injection(int enable, long long wait_limit_cycles);
 // Test-only cap on the attention kernel's persistent grid (0 = one CTA per SM).
 void set_grid_limit(int max_ctas);
 
-// What the two test hooks are set to (the paged attention obeys them too).
+// What the two test hooks are set to (the paged operators that wait obey them too).
 int grid_limit();
 void stall_injection(int* enable, long long* wait_limit_cycles);
 

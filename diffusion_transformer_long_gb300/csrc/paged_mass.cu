@@ -54,6 +54,8 @@ struct MassParams {
   int run_pages;  // pages of a run
   int chunk_tokens, box_rows;
   int* status;
+  long long wait_limit;
+  int stall;
   float scale_log2;
 };
 
@@ -259,7 +261,6 @@ constexpr int kManyThreads = 384;
 constexpr int kEpilogue0 = 4;    // warps 4-7 and 8-11: a tensor-memory buffer each
 constexpr int kRunTiles = 32;    // a run's tiles, at most: 256 pieces of 16 keys
 constexpr int kRunCost = 256;    // what a run costs beside its keys, in keys (1.5 us)
-constexpr long long kWaitLimit = 4000000000LL;
 
 template <int D>
 struct ManySmem {
@@ -281,13 +282,13 @@ struct ManySmem {
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint32_t abort_flag) {
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint32_t abort_flag, long long limit) {
   if (ptx::mbar_test_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!ptx::mbar_try_wait(bar, parity)) {
     int stop;
     asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
-    if (stop || clock64() - t0 > kWaitLimit) return false;
+    if (stop || clock64() - t0 > limit) return false;
   }
   return true;
 }
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_mass_many_kernel(const 
   const uint32_t abort_flag = sbase + S::kAbort;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   auto bar = [&](int i) { return sbase + S::kBars + 8u * i; };
-  auto wait = [&](int i, uint32_t parity) { return wait_or_abort(bar(i), parity, abort_flag); };
+  auto wait = [&](int i, uint32_t parity) { return wait_or_abort(bar(i), parity, abort_flag, p.wait_limit); };
   // (lane 0 waits for its warp)
   auto wait_warp = [&](int i, uint32_t parity) {
     bool done = true;
@@ -418,6 +419,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_mass_many_kernel(const 
                              r.rq.row0 + r.token0() + c * p.chunk_tokens, r.h);
         }
         ++loads;
+        if (p.stall) break;
         // Each lane looks up the box that it copies, a tile ahead.
         auto look_up = [&](int j, int& page, int& at) {
           const int key = j * kTileN + box * p.box_rows, col = key / p.page_size;
@@ -442,14 +444,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_mass_many_kernel(const 
           at = next_at;
         }
       }
+      if (p.stall) break;  // test only: the products' first wait for keys will expire
     }
-    if (!ok) {
-      if (lane == 0) raise_abort(p, abort_flag);
+    if (!ok || p.stall) {
+      if (!ok && lane == 0) raise_abort(p, abort_flag);
       // Let every copy land before the block can exit.
-      if (loads > 0) ptx::mbar_wait(bar(S::bQFull), (loads - 1) & 1, kWaitLimit);
+      if (loads > 0) ptx::mbar_wait(bar(S::bQFull), (loads - 1) & 1, p.wait_limit);
       for (int s = 0; s < kRing; ++s) {
         const int n = (it + kRing - 1 - s) / kRing;  // copies into the slot
-        if (n > 0) ptx::mbar_wait(bar(S::bKFull + s), (n - 1) & 1, kWaitLimit);
+        if (n > 0) ptx::mbar_wait(bar(S::bKFull + s), (n - 1) & 1, p.wait_limit);
       }
     }
   } else if (warp == 1) {
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) paged_mass_many_kernel(const 
         if (!ok) {
           raise_abort(p, abort_flag);
           ptx::mma_commit(bar(S::bDrain));
-          ptx::mbar_wait(bar(S::bDrain), 0, kWaitLimit);
+          ptx::mbar_wait(bar(S::bDrain), 0, p.wait_limit);
         }
       }
       ok = __shfl_sync(~0u, ok, 0) != 0;
@@ -625,6 +628,7 @@ cudaError_t launch_paged_mass(const MassLaunch& a, cudaStream_t st) {
   p.window = a.window;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.status = a.status;
+  stall_injection(&p.stall, &p.wait_limit);
   const long long rows = std::min(a.cu_new ? a.window > 0 ? a.window : a.tokens : 1, a.tokens) * static_cast<long long>(p.group);
   if (rows <= kFewRows) {
     p.run_pages = std::max(1, kFewKeys / a.page_size);

@@ -598,7 +598,8 @@ dit_status dit_attn_check(dit_stream stream);
  * after `wait_limit_cycles` SM clocks (<= 0 keeps the default of about two
  * seconds); the kernel then records DIT_ERR_TIMEOUT in the status word and
  * exits cleanly, and dit_attn_check() reports it.  Nothing faults or hangs.
- * dit_paged_attn_fwd withholds its copies and reports in the same way.
+ * dit_paged_attn_fwd, dit_paged_prefill_fwd and dit_paged_page_mass (of more than 16 rows) withhold their copies and
+ * report in the same way.
  * Call with enable = 0 to restore normal operation.  Not thread-safe with
  * concurrent launches from other host threads.
  */

@@ -7,6 +7,7 @@ import prompt_oracle as po
 from diffusion_transformer_long_gb300 import ditattn as da
 from test_mass_evict_gpu import evict_state
 from test_paged_gpu import rand
+from test_prefill_gpu import Step
 from test_qk_norm_rope_gpu import close, weight
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +88,28 @@ def test_items_that_outlast_a_wait(n):
     # Sums of 190 times as many equal terms in 32 bits, 2^18 keys: off by at most 2^18 2^-23 of them, twice, in the worst case.
     assert (out - want[0]).abs().max() <= 2.0 ** -4 * v.abs().max()
     assert (lse - want[1] - np.log(repeat)).abs().max() <= 2.0 ** -4
+
+
+# ------------------------------------------------------------------ page weights
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("old,new", [([300], [40]), ([4000, 0, 700], [100, 30, 1]), ([20000], [300])])
+def test_mass_expired_wait_is_reported(old, new, D):
+    """With the keys' copies withheld every block's wait runs out, also one of several column blocks and runs; the next
+    call is right again."""
+    s = Step(old, new, 6, 2, D, 16)
+    _, lse = s.run()
+    mass = torch.rand(s.n_pages, 2, device=DEV)
+    call = lambda: da.paged_page_mass(s.q, lse, s.k, s.table, s.lens, mass, cu_new=s.cu, mass_out=mass.clone())  # noqa: E731
+    want = call()
+    da.check(DEV)
+    try:
+        da.inject_stall(True, 2_000_000)
+        call()
+        with pytest.raises(da.DitError) as e:
+            da.check(DEV)
+        assert e.value.status == da.DIT_ERR_TIMEOUT
+    finally:
+        da.inject_stall(False)
+    assert torch.equal(call(), want)
