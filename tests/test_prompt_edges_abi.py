@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_prompt_abi import A, INVALID, UNSUPPORTED, evict, lib  # noqa: F401 (lib: a fixture)
+from test_prompt_abi import A, INVALID, UNSUPPORTED, evict, lib, mass, prefill  # noqa: F401 (lib: a fixture)
 
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up device addresses: run where there is no GPU")
 
@@ -15,3 +15,14 @@ def test_evict_takes_tables_in_one_allocation(lib, B):  # noqa: F811
                                    (20, 20, 20), (5, 10, 10), (10, 40, 20), (5, 40, 20), (20, 20, 40)):
         got = evict(lib, B=B, stride=stride, out=A[1] + 4 * at, out_stride=out_stride)
         assert got != UNSUPPORTED and (got == INVALID) == bool(rows(0, stride) & rows(at, out_stride)), (at, stride)
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 8])
+def test_group_limits(lib, Hkv):  # noqa: F811
+    """Page weights of at most 256 heads a group, attention of at most 128."""
+    for cu in (A[5], None):
+        at = dict(Hkv=Hkv, cu=cu, **(dict(T=3, start=None) if cu is None else {}))
+        assert mass(lib, Hq=257 * Hkv, **at) == UNSUPPORTED
+        assert mass(lib, Hq=256 * Hkv, **at) not in (INVALID, UNSUPPORTED)
+    assert prefill(lib, Hq=129 * Hkv, Hkv=Hkv) == UNSUPPORTED
+    assert prefill(lib, Hq=128 * Hkv, Hkv=Hkv) not in (INVALID, UNSUPPORTED)
