@@ -87,7 +87,7 @@ struct KvTile {
 
 struct PrefillParams {
   CUtensorMap tm_q;        // (D, head of the group, token, key/value head)
-  CUtensorMap tm_k, tm_v;  // paged_prefill.cu: encode_cache
+  CUtensorMap tm_k, tm_v;  // maps::encode_rows, or, where kFused, paged_prefill.cu: encode_fused
   const __nv_bfloat16* v_cache;
   Strides vs;
   const int* table;

@@ -748,8 +748,9 @@ def rope_freqs(rot, theta=10000.0, scaling=None, factor=1.0, original_len=4096, 
       "linear"  every position divided by factor
       "ntk"     a larger base, theta * factor^(rot / (rot - 2)): the slowest pair stretched by factor, the fastest not
       "yarn"    pairs that turn less than beta_slow times in original_len positions divided by factor, those that
-                turn more than beta_fast times left, in between in proportion; rot_scale = 0.1 ln(factor) + 1
-    Computed in 64 bits on the host."""
+                turn more than beta_fast times left, in between in proportion to the turns; rot_scale = 0.1 ln(factor) + 1
+    (Many released models ramp in proportion to the pair's index instead: give their tables as freqs.)  rot_scale is 1
+    but for "yarn", and a call that leaves it out attends at another temperature.  Computed in 64 bits on the host."""
     dims = [int(rot)] if isinstance(rot, int) else [int(r) for r in rot]
     if any(r < 2 or r % 2 for r in dims) or not dims:
         raise ValueError("each axis has a positive, even number of channels")
@@ -793,7 +794,7 @@ def _int_array(values):
 
 def qk_norm_rope(q, k=None, positions=None, freqs=None, axis_pairs=None, interleaved=False, rot_scale=1.0, eps=None,
                  q_weight=None, k_weight=None, cu_new=None, start_lens=None, q_out=None, k_out=None, stream=None):
-    """dit_qk_norm_rope: RMS norms of each head of q and k (eps None: none; weights [D], bf16 or fp32, or None) and rotary
+    """dit_qk_norm_rope: RMS norms of each head of q and k by itself (eps None: none; weights [D], bf16 or fp32, or None) and rotary
     positions (freqs None: none), in one pass.  q, k: bf16 views [B, H, N, D], or [T, H, D] of packed tokens.
 
     freqs (fp32 [n]), axis_pairs and rot_scale are rope_freqs'; axis_pairs None: one axis.  Positions, int32: [N] or
@@ -1141,7 +1142,9 @@ def paged_prefill_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_new, start_
     request order (cu_new int32 [B + 1], paged_plan's), over the requests' seq_lens[b] cached tokens, their own
     among them; `causal` False: every token sees all of them.  start_lens (int32 [B]): the position of each
     request's first new token, by default such that they are its last.  Rows of no request are left as
-    they are.  The workspace is allocated with torch unless given.
+    they are.  The workspace is allocated with torch unless given.  The attention's weights are rounded to bf16 whatever the
+    output's type, as the dense attention's are (outputs are off by about 1e-3 of their size; paged_attn_fwd holds all of
+    them with fp32 output).
 
     Returns (out [T, H_q, D] of out_dtype, lse fp32 [T, H_q]); with_lse=False returns (out, None)."""
     dev, index = _check_rows(q, "q", 3)
@@ -1186,7 +1189,8 @@ def paged_page_mass(q, lse, k_cache, block_table, seq_lens, mass, cu_new=None, s
     q bf16 [T, H_q, D] gave it, from their attention's lse fp32 [T, H_q]; pages whose first key is new start from
     nothing.  cu_new (int32 [B + 1]): packed new tokens, of which the last `window` (0: all) of each request count;
     None: one token of each request (T = B).  In place unless mass_out is given, of which only the pages of requests
-    with new tokens are written.  Returns mass_out."""
+    with new tokens are written.  Called in every step, it drops what a page's former owner left; a program that skips steps
+    clears the weights of the pages that they handed out.  The lse is of all pages, not of selected ones.  Returns mass_out."""
     dev, index = _check_rows(q, "q", 3)
     elsewhere = _elsewhere(dev, stream)
     if elsewhere is not None:

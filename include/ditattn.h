@@ -289,13 +289,16 @@ dit_status dit_layout_copy(const void* src, const dit_strides* src_strides, void
 /*
  * Norms of queries and keys for each head and rotary positions, in one pass, before the attention or
  * before the cache (arganzheng.life multi-GPU diffusion parallelism, section 4.1 Ulysses: RoPE sliced with the
- * tokens; valdrada.cn Wan2.2, TP section: QK norms).  For every head x of every token,
+ * tokens).  The norm is of each head by itself; Wan's is over all heads of a token (valdrada.cn Wan2.2, TP section: its
+ * sum of squares is reduced over the ranks that hold them) and is not computed here: such a model norms before this
+ * call, which then turns alone (norm = 0).  For every head x of every token,
  *   z = w x / sqrt(mean_d x_d^2 + eps)                                            (norm; else z = x)
  * and pair i of the first 2 n channels, n the sum of axis_pairs, (2 i, 2 i + 1) where `interleaved`, else
  * (i, i + n), at the angle t = pos_a(i) * freqs[i],
  *   y_first = s (z_first cos t - z_second sin t),  y_second = s (z_first sin t + z_second cos t)
  * with s = rot_scale; the channels behind them are y = z.  In 32 bits, rounded to bf16 once; the angle
- * is taken modulo a turn exactly, whatever the position.  A sum of squares that overflows 32 bits makes its head 0 or NaN.
+ * is taken modulo a turn exactly, whatever the position.  A sum of squares that overflows 32 bits makes its head 0 or NaN;
+ * one of values all below 2^-62 loses digits or vanishes there, which an eps of 1e-30 or more hides.
  *   q, k          : device bf16 [B, H, N, D] views (read); NULL strides: contiguous.  A packed step's [T, H, D] is
  *                   B = 1, N = T.  k may be NULL (H_k = 0, no k_out, no k_weight): queries alone.
  *   q_out, k_out  : device bf16 views of the same shapes (written), of any layout (token-major in, head-major out):
@@ -511,14 +514,18 @@ size_t dit_paged_prefill_workspace_bytes(int D, int page_size, int max_pages);
  *                         group: exp(scale * q_th . k_j - lse_th)
  * Observing are the last `window` new tokens of each request (0: all); they see keys as with `causal` in
  * dit_paged_prefill_fwd, whose lse this takes (dit_paged_attn_fwd's, of single tokens).  A row whose lse is -inf
- * adds nothing; a NaN lse, or score, makes the pages that the row sees NaN.  Rows of no request are not
+ * adds nothing; a NaN lse, or score, makes the pages that the row sees NaN.  The lse is that of an attention over all of a
+ * request's pages: behind one over selected pages the others' weights mean nothing.  Rows of no request are not
  * looked at.  Sums are in 32 bits, in an order that the sizes and lengths alone fix: equal calls give equal bits.
  *   q, k_cache, block_table, seq_lens, start_lens : as dit_paged_prefill_fwd (read)
  *   lse       : device fp32 [T, H_q] (read)
  *   cu_new    : device int32 [B + 1] (read), or NULL: one token of each request, its last (T = B; no start_lens)
  *   mass      : device fp32 [n_pages, H_kv], contiguous (read)
  *   mass_out  : device fp32 [n_pages, H_kv] (written: the pages of requests with new tokens alone); may be mass
- *               itself.  A page that is in the table more than once is left with any of its sums.
+ *               itself.  A page that is in the table more than once is left with any of its sums.  The weight that a
+ *               page's former owner left is dropped by the call in the step in which the page's first key is new, and by
+ *               nothing else: a program that does not call this in every step sets the weights of pages that were handed
+ *               out in the others to 0 itself, or their requests inherit them.
  *   window    : >= 0;  T : 1 .. 2^30;  B : 1 .. 2^20;  H_q : a multiple of H_kv, at most 256 H_kv;
  *               max_pages * page_size : at most 2^30 (above either of these two: DIT_ERR_UNSUPPORTED)
  *   scale     : > 0, and finite times log2 e in 32 bits
