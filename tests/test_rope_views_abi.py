@@ -121,6 +121,49 @@ def test_views_at_random(lib):
     assert min(seen) > 400
 
 
+def test_views_of_different_layouts_at_random(lib):
+    """Queries and keys of unlike strides in one allocation, in place: accepted as long as they share nothing."""
+    rng = random.Random(6)
+    seen = [0, 0]
+    for _ in range(4000):
+        B, N = rng.randint(1, 3), rng.randint(1, 4)
+
+        def some(block):
+            H = rng.randint(1, 4)
+            extent, stride, at = dict(b=B, h=H, n=N), {}, D
+            for x in rng.choice(("bhn", "bnh", "hbn", "nbh"))[::-1]:
+                stride[x] = at
+                at = at * extent[x] + rng.choice((0, 0, D, 3 * D))
+            if rng.random() < 0.5 and stride["b"] <= block:  # a block of its own for each batch
+                stride["b"] = block
+            return V(D * rng.randint(0, 40), stride["b"], stride["h"], stride["n"], H)
+
+        block = D * rng.randint(8, 64)
+        q, k = some(block), some(block)
+        p = [x.pieces(B, N).tolist() for x in (q, k)]
+        if any(len(set(x)) < len(x) for x in p):
+            continue  # (an output that meets itself)
+        good = not set(p[0]) & set(p[1])
+        got = call(lib, q, k, q, k, B, N)
+        assert not got or good, (B, N, q.at, q.strides, q.H, k.at, k.strides, k.H)
+        if got != good:  # refused although apart: an output whose own dimensions do not nest
+            assert any(not nested(v, B, N) for v in (q, k)), (B, N, q.at, q.strides, q.H, k.at, k.strides, k.H)
+        seen[good] += 1
+    assert min(seen) > 400
+
+
+def nested(v, B, N):
+    """Whether each dimension's stride clears what the shorter ones span, as outputs have to."""
+    b, h, n = v.strides
+    at = D
+    for stride, extent in sorted(((b, B), (h, v.H), (n, N))):
+        if extent > 1:
+            if stride < at:
+                return False
+            at += stride * (extent - 1)
+    return True
+
+
 def test_views_that_take_long_to_tell_apart(lib):
     """Layouts that have nothing in common are told apart as far as that goes quickly, and refused else; never accepted
     where they meet."""
